@@ -1,0 +1,241 @@
+// gdn_head_norm_rope: per-head RMS norms of queries and keys, the position
+// rotation and the writing of K and V to their pool rows, in one pass.
+//
+// statecache.py (squad-0.8b, qev_fast), CacheQwen35's attention layers: q and
+// k are RMS-normalised per head, rotated by the token's position (rotary
+// offset of the cached prefix) and k, v appended to the layer's cache.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w;  (y0, y1) -> (y0 cos - y1 sin, y1 cos + y0 sin)
+//
+// Memory-bound: every element is read and written once, 4 bytes for ~8 flops.
+// A head lies over D/8 lanes of a warp, 16 bytes per lane, so a warp load
+// covers 32/(D/8) heads and the norm is a shuffle over the head's lanes. The
+// angles depend on the token only: a warp forms its lanes' cosines and sines
+// once and applies them to all the heads it takes of that token.
+//
+// Angles: positions reach 2^31 while the result needs ~2^-20 of a turn, so the
+// turns pos * inv_freq / (2 pi) modulo 1 are formed in 64-bit fixed point:
+// F = frac(inv_freq / (2 pi)) * 2^64, and pos * F wraps modulo 2^64 exactly as
+// turns wrap modulo 1. The only errors are F's own rounding (2^-54 of a turn
+// from the fp64 division, times |pos| < 2^31) and the final fp32 rounding.
+#include "gdn_launch.h"
+
+namespace gdn {
+namespace rope {
+
+struct Args {
+  int n, hq, hk, rot, axes, adjacent, slices, items;
+  float eps;
+  long long qs, ks, vs, kv_rows;
+  const bf16 *q, *k, *v, *qw, *kw;
+  const int32_t *pos;
+  const double *inv_freq;
+  const uint8_t *axis;
+  const int32_t *kv_index;
+  bf16 *qo, *ko, *vo;
+  unsigned int *status;
+};
+
+__device__ __forceinline__ void unpack8(uint4 u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // vectors a lane has in flight
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ Args A) {
+  constexpr int LPH = D / 8, HPI = 32 / LPH;  // lanes of a head, heads of one warp load
+  __shared__ uint64_t s_freq[D / 2];
+  __shared__ uint8_t s_axis[D / 2];
+  griddep_wait();
+  griddep_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, half = A.rot / 2;
+  if (tid < half) {
+    const double t = A.inv_freq[tid] * 0.15915494309189535;  // turns per position
+    s_freq[tid] = (uint64_t)((t - floor(t)) * 18446744073709551616.0);
+    int a = A.axis ? A.axis[tid] : 0;
+    if (a >= A.axes) {
+      set_status(A.status, GDN_ERR_INDEX);
+      a = 0;
+    }
+    s_axis[tid] = (uint8_t)a;
+  }
+  __syncthreads();
+  const int c = lane % LPH, sub = lane / LPH;  // 16-byte chunk of the head, head of the load
+  const bool rotates = c * 8 < A.rot;
+  // the pair's other channel: in this lane (adjacent pairs) or in lane `other`
+  const bool upper = !A.adjacent && c * 8 >= half;
+  const int other = !rotates || A.adjacent ? lane : lane + (upper ? -1 : 1) * (A.rot / 16);
+  float wq[8], wk[8];
+  const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+  unpack8(A.qw ? reinterpret_cast<const uint4 *>(A.qw)[c] : ones, wq);
+  unpack8(A.kw ? reinterpret_cast<const uint4 *>(A.kw)[c] : ones, wk);
+
+  const long long units = (long long)A.n * A.slices, stride = (long long)gridDim.x * (kThreads / 32);
+  for (long long u = (long long)blockIdx.x * (kThreads / 32) + (tid >> 5); u < units; u += stride) {
+    const long long t = u / A.slices;
+    const int slice = (int)(u - t * A.slices);
+    // loads of one warp: heads q | k | v in rounds of HPI; this slice's rounds
+    const int r0 = (int)((long long)A.items * slice / A.slices), r1 = (int)((long long)A.items * (slice + 1) / A.slices);
+    long long row = A.kv_index ? A.kv_index[t] : t;
+    if (row < -1 || row >= A.kv_rows) {
+      if (lane == 0) set_status(A.status, GDN_ERR_INDEX);
+      row = -1;
+    }
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      cs[e] = 1.0f;
+      sn[e] = 0.0f;
+    }
+    if (rotates) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = A.adjacent ? c * 4 + (e >> 1) : c * 8 + e - (upper ? half : 0);
+        const uint64_t turns = (uint64_t)(int64_t)A.pos[(long long)s_axis[i] * A.n + t] * s_freq[i];
+        sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31: half turns
+      }
+      // the second channel of a pair takes +sin of the first, the first -sin of the second
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (A.adjacent ? !(e & 1) : !upper) sn[e] = -sn[e];
+    }
+    for (int r = r0; r < r1; r += kBatch) {
+      uint4 x[kBatch];
+      const bf16 *src[kBatch];
+      bf16 *dst[kBatch];
+      int kind[kBatch];  // 0 q, 1 k, 2 v, 3 nothing
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int h = (r + j) * HPI + sub;
+        kind[j] = r + j >= r1 ? 3 : h < A.hq ? 0 : h < A.hq + A.hk ? 1 : (h < A.hq + 2 * A.hk && A.v) ? 2 : 3;
+        if ((kind[j] == 1 || kind[j] == 2) && row < 0) kind[j] = 3;
+        const int g = kind[j] == 0 ? h : kind[j] == 1 ? h - A.hq : h - A.hq - A.hk;
+        src[j] = (kind[j] == 0 ? A.q + t * A.qs : kind[j] == 1 ? A.k + t * A.ks : A.v + t * A.vs) + (long long)g * D + c * 8;
+        dst[j] = (kind[j] == 0   ? A.qo + (t * A.hq + g) * D
+                  : kind[j] == 1 ? A.ko + (row * A.hk + g) * D
+                                 : A.vo + (row * A.hk + g) * D) +
+                 c * 8;
+        x[j] = kind[j] < 3 ? *reinterpret_cast<const uint4 *>(src[j]) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        float y[8];
+        unpack8(x[j], y);
+        float ss = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = rsqrtf(ss * (1.0f / D) + A.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= inv * (kind[j] == 0 ? wq[e] : wk[e]);
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float far = __shfl_sync(0xffffffffu, y[e], other);
+          z[e] = fmaf(y[e], cs[e], (A.adjacent ? y[e ^ 1] : far) * sn[e]);
+        }
+        if (kind[j] < 3) *reinterpret_cast<uint4 *>(dst[j]) = kind[j] == 2 ? x[j] : pack8(z);
+      }
+    }
+  }
+}
+
+}  // namespace rope
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" gdn_status gdn_head_norm_rope(const gdn_rope_dims *d, const void *q, const void *k, const void *v,
+                                         const void *q_weight, const void *k_weight, const int32_t *positions,
+                                         const double *inv_freq, const uint8_t *axis, const int32_t *kv_index,
+                                         void *q_out, void *k_out, void *v_out, void *stream) {
+  if (!d) return fail(GDN_ERR_ARG, "dims is NULL");
+  if (d->n_tokens < 0 || d->n_q_heads < 1 || d->n_kv_heads < 1 || d->n_q_heads > 4096 || d->n_kv_heads > 4096)
+    return fail(GDN_ERR_SHAPE, "n_tokens must be >= 0 and head counts in [1, 4096]");
+  const int D = d->head_dim;
+  if (D != 64 && D != 128 && D != 256) return fail(GDN_ERR_SHAPE, "head_dim must be 64, 128 or 256");
+  if (d->rot_dim < 0 || d->rot_dim > D || d->rot_dim % 16 != 0)
+    return fail(GDN_ERR_SHAPE, "rot_dim must be a multiple of 16 in [0, head_dim]");
+  if (d->n_axes < 1 || d->n_axes > 8) return fail(GDN_ERR_SHAPE, "n_axes must be in [1, 8]");
+  if (!(d->eps >= 0.0f)) return fail(GDN_ERR_ARG, "eps must be >= 0");
+  if (d->q_stride % 8 != 0 || d->k_stride % 8 != 0 || d->v_stride % 8 != 0)
+    return fail(GDN_ERR_SHAPE, "token strides must be multiples of 8 elements");
+  if (d->q_stride < (long long)d->n_q_heads * D || d->k_stride < (long long)d->n_kv_heads * D ||
+      (v && d->v_stride < (long long)d->n_kv_heads * D))
+    return fail(GDN_ERR_SHAPE, "token strides must cover the heads");
+  if (d->kv_rows < 0 || (!kv_index && d->kv_rows < d->n_tokens))
+    return fail(GDN_ERR_SHAPE, "kv_rows must hold the tokens");
+  if (d->n_tokens == 0) return GDN_OK;  // empty tensors may have no address
+  GDN_TRY(check_ptr(q, "q"));
+  GDN_TRY(check_ptr(k, "k"));
+  GDN_TRY(check_ptr(q_out, "q_out"));
+  GDN_TRY(check_ptr(k_out, "k_out"));
+  if ((v == nullptr) != (v_out == nullptr)) return fail(GDN_ERR_ARG, "v and v_out must both be given or both be NULL");
+  if (v) {
+    GDN_TRY(check_ptr(v, "v"));
+    GDN_TRY(check_ptr(v_out, "v_out"));
+  }
+  if (q_weight) GDN_TRY(check_ptr(q_weight, "q_weight"));
+  if (k_weight) GDN_TRY(check_ptr(k_weight, "k_weight"));
+  if (d->rot_dim > 0) {
+    GDN_TRY(check_ptr(positions, "positions", 4));
+    GDN_TRY(check_ptr(inv_freq, "inv_freq", 8));
+  }
+  if (kv_index) GDN_TRY(check_ptr(kv_index, "kv_index", 4));
+  const DeviceInfo *dev;
+  GDN_TRY(current_device(&dev));
+  rope::Args A = {};
+  A.n = d->n_tokens;
+  A.hq = d->n_q_heads;
+  A.hk = d->n_kv_heads;
+  A.rot = d->rot_dim;
+  A.axes = d->n_axes;
+  A.adjacent = d->adjacent != 0;
+  A.eps = d->eps;
+  A.qs = d->q_stride;
+  A.ks = d->k_stride;
+  A.vs = d->v_stride;
+  A.kv_rows = d->kv_rows;
+  A.q = static_cast<const bf16 *>(q);
+  A.k = static_cast<const bf16 *>(k);
+  A.v = static_cast<const bf16 *>(v);
+  A.qw = static_cast<const bf16 *>(q_weight);
+  A.kw = static_cast<const bf16 *>(k_weight);
+  A.pos = positions;
+  A.inv_freq = inv_freq;
+  A.axis = axis;
+  A.kv_index = kv_index;
+  A.qo = static_cast<bf16 *>(q_out);
+  A.ko = static_cast<bf16 *>(k_out);
+  A.vo = static_cast<bf16 *>(v_out);
+  A.status = dev->status;
+  const int per_load = 32 / (D / 8);
+  A.items = (A.hq + (v ? 2 : 1) * A.hk + per_load - 1) / per_load;
+  // a token's heads go to several warps where the tokens alone would leave SMs idle
+  const long long want = (long long)dev->sms * 32 / A.n;
+  A.slices = (int)(want < 1 ? 1 : want > A.items ? A.items : want);
+  const long long ctas = ((long long)A.n * A.slices + 7) / 8;
+  const dim3 grid((unsigned)(ctas < dev->sms * 4 ? ctas : dev->sms * 4));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (D == 64) launch_pdl(rope::norm_rope_kernel<64>, grid, dim3(rope::kThreads), 0, st, A);
+  if (D == 128) launch_pdl(rope::norm_rope_kernel<128>, grid, dim3(rope::kThreads), 0, st, A);
+  if (D == 256) launch_pdl(rope::norm_rope_kernel<256>, grid, dim3(rope::kThreads), 0, st, A);
+  return check_launch("head_norm_rope");
+}

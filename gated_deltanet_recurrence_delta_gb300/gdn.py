@@ -21,7 +21,9 @@ STATUS = {0: "GDN_OK", 1: "GDN_ERR_ARG", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_MASK", 
 EXPORTS = ("gdn_decode_step", "gdn_verify_with_checkpoints", "gdn_prefill_chunked",
            "gdn_prefill_workspace_size", "gdn_state_copy", "gdn_check_status", "gdn_last_error",
            "gdn_prefill_chunked_static_scratch", "gdn_commit_accepted", "gdn_decode_step_mxfp8",
-           "gdn_prefill_chunked_ckpt", "gdn_in_proj", "gdn_out_proj", "gdn_copy_overlapped")
+           "gdn_prefill_chunked_ckpt", "gdn_in_proj", "gdn_out_proj", "gdn_copy_overlapped",
+           "gdn_head_norm_rope", "gdn_attn_prefill", "gdn_attn_shared_prefix", "gdn_attn_workspace_size",
+           "gdn_accept_draft")
 MAX_OVERLAPPED_COPIES = 8
 
 
@@ -49,6 +51,18 @@ class InputsMxfp8(ctypes.Structure):
 
 class Copy(ctypes.Structure):
     _fields_ = [("dst", ctypes.c_void_p), ("src", ctypes.c_void_p), ("bytes", ctypes.c_size_t)]
+
+
+class RopeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_q_heads", "n_kv_heads", "head_dim", "rot_dim", "n_axes",
+                                              "adjacent")] + [("eps", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "kv_rows")]
+
+
+class AttnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "n_tokens", "n_groups", "n_q_heads", "n_kv_heads",
+                                              "head_dim")] + [("scale", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "kv_stride", "kv_rows")]
 
 
 _lib = None
@@ -80,12 +94,20 @@ def load_library(path: Path | str | None = None):
     lib.gdn_decode_step_mxfp8.argtypes = [DP, ctypes.POINTER(InputsMxfp8), P, P, P, P]
     lib.gdn_commit_accepted.argtypes = [DP, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P, P, P, P]
     lib.gdn_copy_overlapped.argtypes = [ctypes.POINTER(Copy), ctypes.c_int32, P]
+    lib.gdn_head_norm_rope.argtypes = [ctypes.POINTER(RopeDims)] + [P] * 13
+    AP = ctypes.POINTER(AttnDims)
+    lib.gdn_attn_prefill.argtypes = [AP] + [P] * 8
+    lib.gdn_attn_shared_prefix.argtypes = [AP] + [P] * 11 + [ctypes.c_size_t, P]
+    lib.gdn_attn_workspace_size.argtypes = [AP]
+    lib.gdn_attn_workspace_size.restype = ctypes.c_size_t
+    lib.gdn_accept_draft.argtypes = [ctypes.c_int32] * 3 + [P] * 8
     lib.gdn_check_status.argtypes = [P]
     lib.gdn_last_error.restype = ctypes.c_char_p
     for name in ("gdn_decode_step", "gdn_verify_with_checkpoints", "gdn_prefill_chunked", "gdn_state_copy",
                  "gdn_check_status", "gdn_prefill_chunked_static_scratch", "gdn_commit_accepted",
                  "gdn_decode_step_mxfp8", "gdn_prefill_chunked_ckpt", "gdn_in_proj", "gdn_out_proj",
-                 "gdn_copy_overlapped"):
+                 "gdn_copy_overlapped", "gdn_head_norm_rope", "gdn_attn_prefill", "gdn_attn_shared_prefix",
+                 "gdn_accept_draft"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -249,6 +271,79 @@ def out_proj(o, w_out, y, stream=None):
     V, H = int(o.shape[-1]), int(w_out.shape[0])
     M = o.numel() // V
     _check(load_library().gdn_out_proj(M, H, V, _ptr(o), _ptr(w_out), _ptr(y), _stream(stream)))
+
+
+def _token_stride(x, name):
+    """Elements between the tokens of x [..., heads, head_dim], whose heads lie together and whose tokens are
+    evenly spaced."""
+    shape, st = x.shape, x.stride()
+    if x.dtype != torch.bfloat16 or x.dim() not in (3, 4):
+        raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, head_dim] or [rows, tokens, heads, head_dim]")
+    if st[-1] != 1 or (st[-2] != shape[-1] and shape[-2] > 1) or (
+            x.dim() == 4 and shape[0] > 1 and st[0] != shape[1] * st[1]):
+        raise ValueError(f"{name} must have dense heads and evenly spaced tokens")
+    return st[-3]
+
+
+def make_rope_dims(q, k, rot_dim, n_axes=1, kv_rows=None, adjacent=False, eps=1e-6, v=None) -> RopeDims:
+    """Sizes and token strides of a head_norm_rope call on q [n, Hq, d] and k [n, Hk, d]; v's tokens are spaced as
+    k's unless v is given. kv_rows: rows of the pools (n when they hold the tokens themselves)."""
+    n = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    ks = _token_stride(k, "k")
+    return RopeDims(n, q.shape[-2], k.shape[-2], q.shape[-1], rot_dim, n_axes, int(adjacent), eps,
+                    _token_stride(q, "q"), ks, ks if v is None else _token_stride(v, "v"), n if kv_rows is None else kv_rows)
+
+
+def head_norm_rope(dims: RopeDims, q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out, v_out, axis=None,
+                   kv_index=None, stream=None):
+    """gdn_head_norm_rope: per-head norms of q and k, the rotation by positions int32 [axes, n] with inv_freq fp64
+    [rot_dim/2] (axis uint8 [rot_dim/2]: each pair's position axis), K and V to the rows kv_index int32 [n] of the
+    pools k_out, v_out [kv_rows, Hk, d]."""
+    _check(load_library().gdn_head_norm_rope(
+        ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
+        _ptr(axis), _ptr(kv_index), _ptr(q_out), _ptr(k_out), _ptr(v_out), _stream(stream)))
+
+
+def make_attn_dims(q, k, B, T=1, n_groups=0, scale=None) -> AttnDims:
+    """Sizes and strides of an attention call: q [n, Hq, d] or [B, T, Hq, d], k (and v, spaced alike) the pool
+    [kv_rows, Hk, d]."""
+    n = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    d = q.shape[-1]
+    return AttnDims(B, T, n, n_groups, q.shape[-2], k.shape[-2], d, d ** -0.5 if scale is None else scale,
+                    _token_stride(q, "q"), _token_stride(k, "k"), k.shape[0])
+
+
+def attn_prefill(dims: AttnDims, q, k, v, cu_seqlens, out, kv_start=None, kv_len=None, stream=None):
+    """gdn_attn_prefill: causal attention of packed prompts over their extents of the pools k, v."""
+    _check(load_library().gdn_attn_prefill(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens),
+                                           _ptr(kv_start), _ptr(kv_len), _ptr(out), _stream(stream)))
+
+
+def attn_workspace_size(dims: AttnDims) -> int:
+    """Workspace bytes of attn_shared_prefix."""
+    return int(load_library().gdn_attn_workspace_size(ctypes.byref(dims)))
+
+
+def attn_workspace(dims: AttnDims, device="cuda") -> torch.Tensor:
+    """A workspace tensor for attn_shared_prefix, reusable from call to call on one stream."""
+    return torch.empty(max(attn_workspace_size(dims), 1), dtype=torch.uint8, device=device)
+
+
+def attn_shared_prefix(dims: AttnDims, q, k, v, group_rows, prefix_start, prefix_len, suffix_start, suffix_len, out,
+                       workspace, q_len=None, stream=None):
+    """gdn_attn_shared_prefix: q [B, T, Hq, d] over each group's shared prefix extent and each row's own extent."""
+    _check(load_library().gdn_attn_shared_prefix(
+        ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(group_rows), _ptr(prefix_start), _ptr(prefix_len),
+        _ptr(suffix_start), _ptr(suffix_len), _ptr(q_len), _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+
+
+def accept_draft(tokens, target_probs, draft_probs, uniform, accept_len, next_token, n_tokens=None, stream=None):
+    """gdn_accept_draft: tokens int32 [B, T], target_probs fp32 [B, T, V], draft_probs fp32 [B, T-1, V] or None
+    (certain drafts), uniform fp32 [B, T] -> accept_len, next_token int32 [B]."""
+    B, T, V = target_probs.shape
+    _check(load_library().gdn_accept_draft(B, T, V, _ptr(tokens), _ptr(target_probs), _ptr(draft_probs), _ptr(uniform),
+                                           _ptr(n_tokens), _ptr(accept_len), _ptr(next_token), _stream(stream)))
 
 
 def check_status(stream=None):

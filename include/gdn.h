@@ -364,6 +364,154 @@ typedef struct gdn_copy {
 } gdn_copy;
 gdn_status gdn_copy_overlapped(const gdn_copy *copies, int32_t n, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The full-attention layers that stand between a hybrid stack's GDN layers,
+ * and the acceptance of drafted tokens.
+ *
+ * statecache.py (squad-0.8b, qev_fast), CacheQwen35: the attention layers keep
+ * their keys and values per token, normalise queries and keys per head, rotate
+ * them by the token's position and attend causally over the cached prefix and
+ * the chunk; generate.py (sparkle, mlx_streaming/mtp), accept_prefix /
+ * tree_verify_step: a verify forward scores the drafted tokens of several
+ * paths over one cached prompt and the accepted prefix is committed.
+ *
+ * Keys and values live in two token pools k, v: bf16 [kv_rows][n_kv_heads]
+ * [head_dim], kv_stride elements between rows. A sequence, a shared prefix or
+ * a row's own continuation is an extent of consecutive pool rows (start, len),
+ * as a GDN row is a state slot. Query head h reads key head
+ * h / (n_q_heads / n_kv_heads).
+ * ------------------------------------------------------------------------ */
+
+/* Sizes of a gdn_head_norm_rope call.
+ *   n_tokens          tokens of the call
+ *   n_q_heads, n_kv_heads, head_dim   head_dim one of 64, 128, 256
+ *   rot_dim           channels [0, rot_dim) of a head rotate, a multiple of 16
+ *                     in [0, head_dim]; 0 = norms only
+ *   n_axes            position axes (1 for text; 3 for time, height, width), at most 8
+ *   adjacent          0: channel i is paired with i + rot_dim/2;
+ *                     1: channel 2i is paired with 2i + 1
+ *   eps               x / sqrt(mean(x^2) + eps)
+ *   q_stride, k_stride, v_stride   elements between tokens of the inputs
+ *                     (views into one projection's rows are fine), multiples of 8
+ *   kv_rows           rows of k_out / v_out */
+typedef struct gdn_rope_dims {
+  int32_t n_tokens, n_q_heads, n_kv_heads, head_dim, rot_dim, n_axes, adjacent;
+  float eps;
+  int64_t q_stride, k_stride, v_stride, kv_rows;
+} gdn_rope_dims;
+
+/* Norms of queries and keys per head and the position rotation in one pass,
+ * K and V going straight to their pool rows.
+ *   q, k, v    bf16, token t's heads at t * {q,k,v}_stride; v NULL: no values
+ *   q_weight, k_weight  bf16 [head_dim], or NULL for ones
+ *   positions  int32 [n_axes][n_tokens] (any int32), NULL iff rot_dim == 0
+ *   inv_freq   fp64 [rot_dim/2]: pair i turns by positions[axis[i]] * inv_freq[i]
+ *   axis       uint8 [rot_dim/2], each < n_axes, or NULL (axis 0 for all); a
+ *              value >= n_axes is a device error (GDN_ERR_INDEX) and reads axis 0
+ *   kv_index   int32 [n_tokens]: token t's pool row, -1 = not kept; NULL = t.
+ *              Any other value outside [0, kv_rows) is a device error
+ *              (GDN_ERR_INDEX) and the token's K and V are not written.
+ *              Rows must be distinct.
+ *   q_out      bf16 [n_tokens][n_q_heads][head_dim]
+ *   k_out, v_out  bf16 [kv_rows][n_kv_heads][head_dim]; v_out NULL iff v is
+ * y = x / sqrt(mean x^2 + eps) * w, then a pair (y0, y1) becomes
+ * (y0 cos - y1 sin, y1 cos + y0 sin). fp32 throughout, one rounding to bf16;
+ * the angle is exact to 2^-25 of a turn for every int32 position. An output
+ * may be its own input where the input is dense (and kv_index NULL). */
+gdn_status gdn_head_norm_rope(const gdn_rope_dims *dims, const void *q, const void *k, const void *v,
+                              const void *q_weight, const void *k_weight, const int32_t *positions,
+                              const double *inv_freq, const uint8_t *axis, const int32_t *kv_index, void *q_out,
+                              void *k_out, void *v_out, void *stream);
+
+/* Sizes of an attention call.
+ *   B          sequences (prefill) or rows (shared prefix)
+ *   T          query tokens per row (shared prefix: 1 for decode, the drafted
+ *              tokens for verify, at most 64); unused by prefill
+ *   n_tokens   query tokens in all (shared prefix: B * T)
+ *   n_groups   groups of rows that share a prefix (0: no prefixes); unused by prefill
+ *   n_q_heads, n_kv_heads, head_dim   n_q_heads a multiple of n_kv_heads, at most
+ *              64 query heads per key head; head_dim one of 64, 128, 256
+ *   scale      multiplies q.k before the softmax (head_dim^-0.5 is usual)
+ *   q_stride   elements between query tokens, a multiple of 8
+ *   kv_stride  elements between pool rows of k and of v, a multiple of 8
+ *   kv_rows    rows of the pools */
+typedef struct gdn_attn_dims {
+  int32_t B, T, n_tokens, n_groups, n_q_heads, n_kv_heads, head_dim;
+  float scale;
+  int64_t q_stride, kv_stride, kv_rows;
+} gdn_attn_dims;
+
+/* Causal attention of packed prompts over their cached keys and values.
+ *   q           bf16, token t's heads at t * q_stride
+ *   k, v        the pools
+ *   cu_seqlens  int32 [B+1]: sequence b's queries are tokens [cu[b], cu[b+1])
+ *   kv_start, kv_len  int32 [B]: sequence b's keys are pool rows
+ *               [kv_start, kv_start + kv_len), its own tokens last; both NULL:
+ *               the pools hold the packed tokens themselves (start cu[b], as
+ *               many keys as queries)
+ *   out         bf16 [n_tokens][n_q_heads][head_dim]
+ * Query i of n, over m keys, sees keys j <= m - n + i. A query that sees no
+ * key (m < n) gets zeros. Softmax statistics and accumulators are fp32; the
+ * probabilities enter the second product in bf16. A range of queries or keys
+ * that leaves its tensor is a device error (GDN_ERR_INDEX) and that sequence's
+ * outputs are not written. Values behind a sequence's end are never used,
+ * whatever they hold. */
+gdn_status gdn_attn_prefill(const gdn_attn_dims *dims, const void *q, const void *k, const void *v,
+                            const int32_t *cu_seqlens, const int32_t *kv_start, const int32_t *kv_len, void *out,
+                            void *stream);
+
+/* Attention of rows that share prefixes: a decode step (T = 1) or the verify
+ * of T drafted tokens per row, each prefix read once for all its rows.
+ *   q            bf16 [B][T] tokens, q_stride apart
+ *   group_rows   int32 [n_groups+1], from 0 to B: group g is rows
+ *                [group_rows[g], group_rows[g+1])
+ *   prefix_start, prefix_len  int32 [n_groups]: the group's prefix extent
+ *   suffix_start, suffix_len  int32 [B]: the row's own extent, the call's
+ *                tokens last (their keys are already in the pool)
+ *   q_len        int32 [B] in [0, T], the row's real tokens, or NULL (T each)
+ *   out          bf16 [B][T][n_q_heads][head_dim]
+ *   workspace    gdn_attn_workspace_size(dims) bytes, 256-byte aligned
+ * Token t of a row sees the whole prefix and suffix keys
+ * j <= suffix_len - q_len + t; a token that sees nothing, or with t >= q_len,
+ * gets zeros. Precision and device errors as in gdn_attn_prefill: a bad group
+ * skips its rows, a bad row itself. */
+gdn_status gdn_attn_shared_prefix(const gdn_attn_dims *dims, const void *q, const void *k, const void *v,
+                                  const int32_t *group_rows, const int32_t *prefix_start, const int32_t *prefix_len,
+                                  const int32_t *suffix_start, const int32_t *suffix_len, const int32_t *q_len,
+                                  void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of gdn_attn_shared_prefix (0 on invalid dims). */
+size_t gdn_attn_workspace_size(const gdn_attn_dims *dims);
+
+/* Acceptance of drafted tokens against the target's probabilities, from given
+ * random numbers: the accept lengths that gdn_commit_accepted takes.
+ *   B, T, V       rows, verify tokens per row (1 <= T <= 32), vocabulary
+ *   tokens        int32 [B][T]: the verify call's tokens; token 0 is already
+ *                 kept (not read), tokens 1.. are the drafts
+ *   target_probs  fp32 [B][T][V]: the target's distribution after token t
+ *   draft_probs   fp32 [B][T-1][V]: the distribution that token t+1 was drawn
+ *                 from, or NULL: each draft was certain
+ *   uniform       fp32 [B][T] in [0, 1): uniform[b][t] tests token t+1,
+ *                 uniform[b][T-1] draws the next token
+ *   n_tokens      int32 [B] in [0, T], the row's real verify tokens, or NULL
+ *                 (T each); 0: accept length 0, next token -1
+ *   accept_len    int32 [B]: 1 + the accepted drafts
+ *   next_token    int32 [B]
+ * Draft x = tokens[t+1] is accepted iff uniform * draft(x) < target(x) (draft
+ * 1 where certain); the first refusal ends the row. The next token follows the
+ * inverse distribution function at its random number: of max(target - draft, 0)
+ * at a refusal (of the target where that has no mass), of the target after the
+ * last token; the lowest index whose running sum exceeds the number times the
+ * total. Sums carry about 48 bits. Weights that are negative or NaN count as
+ * zero; a distribution without any mass gives -1. With several candidate paths
+ * per sequence the winner that gdn_commit_accepted picks keeps the target's
+ * distribution only for certain drafts and a one-hot target.
+ * A draft outside [0, V) or a bad n_tokens is a device error (GDN_ERR_INDEX):
+ * the row gets accept length 0 and next token -1. */
+gdn_status gdn_accept_draft(int32_t B, int32_t T, int32_t V, const int32_t *tokens, const float *target_probs,
+                            const float *draft_probs, const float *uniform, const int32_t *n_tokens,
+                            int32_t *accept_len, int32_t *next_token, void *stream);
+
 /* Synchronise `stream`, then return (and clear) a device-detected error
  * recorded on the current device since the last check (GDN_ERR_MASK,
  * GDN_ERR_INDEX, GDN_ERR_TIMEOUT; the lowest code wins when several were
