@@ -1,120 +1,942 @@
-// Causal attention over a pool of cached keys and values: packed prompts
-// (gdn_attn_prefill) and rows that share prefixes (gdn_attn_shared_prefix).
+// Causal attention over a pool of cached keys and values on the tcgen05 tensor
+// cores: packed prompts (gdn_attn_prefill) and rows that share prefixes
+// (gdn_attn_shared_prefix).
 //
 // statecache.py (squad-0.8b, qev_fast), CacheQwen35's attention layers: a
-// chunk's queries attend over the cached prefix and, causally, the chunk.
+// chunk's queries attend over the cached prefix and, causally, the chunk;
+// generate.py (sparkle, mlx_streaming/mtp), tree_verify_step: several drafted
+// paths of one sequence over its one cached prompt.
 //
 //   s_ij = scale q_i . k_j,  o_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i)
 //
-// One warp per (query token, head), one pass over its keys with the running
-// maximum and sum of the softmax.
+// One pass over the keys in blocks of 128 with the running maximum and sum of
+// the softmax. The query heads that share a key head are packed into the rows
+// of one tile: row r of a tile is (token r / G, head r % G), so 128 / G tokens
+// fill the M = 128 of the tensor cores and one kernel serves prompts, drafted
+// tokens and single tokens alike. A CTA has
+//   - one TMA warp: Q tiles, then K and V blocks through a ring of units of
+//     128 keys x min(D, 128) channels, in the order the products take them;
+//   - one MMA warp: S = Q K^T into TMEM, O += P V with P read from TMEM;
+//   - one or two softmax groups of four warps, a thread per row: S from TMEM
+//     to registers, exponentials, P (bf16) back over S.
+// D = 64, 128: two S tiles and two O tiles fill the TMEM's 512 columns, and two
+// softmax groups work in turn with the tensor cores. They take either two query
+// tiles against the same keys, or (one tile of rows only) the even and the odd
+// key blocks, each with its own running maximum, joined at the end.
+// D = 256: one O tile of 256 columns and two S tiles in turn, one group.
+//
+// Running maximum: O is rescaled only where a row's maximum grew by more than
+// 2^8 since the value it is measured against; probabilities then reach 2^8 at
+// most, which fp32 sums and bf16's exponent carry without loss.
+#include <mutex>
+
 #include "gdn_launch.h"
+#include "gdn_umma.cuh"
 
 namespace gdn {
 namespace attn {
 
+constexpr int kMaxCtas = 152;  // CTAs of a shared-prefix call: one per SM
+constexpr int BN = 128;        // keys of a block
+
 struct Args {
   int B, T, n_tokens, n_groups, hq, hk, G;
-  float scale;
-  long long qs, kvs, kv_rows;
-  const bf16 *q, *k, *v;
+  int TQ;           // tokens of one 128-row tile
+  int tile_tokens;  // tokens of one CTA's tiles (TQ, or 2 TQ for two query tiles)
+  int max_tiles;    // prefill: tiles the grid covers
+  float c;          // |scale| log2(e)
+  uint32_t idesc_s; // instruction descriptor of S (the sign of scale)
+  long long kv_rows;
   bf16 *out;
-  const int32_t *cu, *kv_start, *kv_len;                      // prefill
-  const int32_t *group_rows, *prefix_start, *prefix_len;      // shared prefix
+  const int32_t *cu, *kv_start, *kv_len;                  // prefill
+  const int32_t *group_rows, *prefix_start, *prefix_len;  // shared prefix
   const int32_t *suffix_start, *suffix_len, *q_len;
   unsigned int *status;
+  // shared prefix: partial results. A slot of the prefix region holds 2 (D = 256: 1) tiles of prefix_rows rows,
+  // of the suffix region 2 (1) tiles of suffix_rows rows: D fp32 each, then (maximum, sum) pairs.
+  int prefix_rows, suffix_rows;
+  float *prefix_o, *suffix_o;
+  float2 *prefix_ml, *suffix_ml;
+  long long *plan;  // cost per CTA, whether the groups are in order, then per entry (first cost, first line)
 };
 
-// The largest i in [0, n) with a[i] <= x, or -1.
-__device__ __forceinline__ int find_row(const int32_t *a, int n, int x) {
-  int lo = -1, hi = n;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (a[m] <= x) lo = m; else hi = m;
-  }
-  return lo;
-}
-
-struct Extent {
-  long long start;
-  int len;
-};
 __device__ __forceinline__ bool inside(long long start, long long len, long long rows) {
   return start >= 0 && len >= 0 && start + len <= rows;
 }
+__device__ __forceinline__ int blocks_of(int keys) { return keys <= 0 ? 0 : (int)(((long long)keys + BN - 1) / BN); }
+
+// ------------------------------------------------------------ what a CTA does
+// One segment: the query tokens [t0, t0 + ntok) of one key head over the key
+// blocks [b0, b1) of one extent. Token i sees keys below lim0 + step * i.
+struct Seg {
+  int t0, ntok, head, kv0, len, b0, b1, lim0, step;
+  bool pair;  // two query tiles; else one tile, whose blocks alternate between the S tiles
+  int slot;   // of the partial results; prefix and suffix lines are told apart by `own`
+  bool own;
+};
+
+// Entry e of a shared-prefix call: a group's prefix (e < n_groups) or a row's own extent.
+struct Entry {
+  int first, ntok;  // query tokens
+  int kv0, len, lim0, step;
+  int tiles, blocks;
+  bool ok;
+  __device__ long long line_cost() const { return blocks > 0 ? blocks + 1 : 0; }  // + 1: the tile's set-up and store
+  __device__ long long cost(int hk) const { return line_cost() * tiles * hk; }
+};
+
+// The group of row b (-1 without groups); the offsets are in order.
+__device__ __forceinline__ int group_of(const Args &A, int b) {
+  if (A.n_groups == 0) return -1;
+  int lo = 0, hi = A.n_groups;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (A.group_rows[m] <= b) lo = m; else hi = m;
+  }
+  return lo;
+}
+__device__ __forceinline__ Entry entry_at(const Args &A, int e, bool all_ok) {
+  Entry x = {};
+  if (e < A.n_groups) {
+    const int a = all_ok ? A.group_rows[e] : 0, z = all_ok ? A.group_rows[e + 1] : 0;
+    x.kv0 = A.prefix_start[e];
+    x.len = A.prefix_len[e];
+    x.ok = all_ok && inside(x.kv0, x.len, A.kv_rows);
+    x.first = a * A.T;
+    x.ntok = (z - a) * A.T;
+    x.lim0 = x.len;
+  } else {
+    const int b = e - A.n_groups;
+    const int ql = A.q_len ? A.q_len[b] : A.T;
+    x.kv0 = A.suffix_start[b];
+    x.len = A.suffix_len[b];
+    x.ok = all_ok && ql >= 0 && ql <= A.T && inside(x.kv0, x.len, A.kv_rows);
+    x.first = b * A.T;
+    x.ntok = x.ok ? ql : 0;
+    x.lim0 = x.len - ql + 1;
+    x.step = 1;
+  }
+  if (x.ok && x.ntok > 0) {
+    x.tiles = (x.ntok + A.tile_tokens - 1) / A.tile_tokens;
+    x.blocks = blocks_of(x.len);
+  }
+  return x;
+}
+
+// A CTA of a shared-prefix call takes the stretch [pos, end) of all lines' cost
+// laid end to end (a line: one tile of one key head over one extent), so every
+// SM gets the same work whatever the lengths. A line that crosses a border
+// leaves partial results in both CTAs; slot (line + CTA) is unique, since each
+// next segment moves to the next line or the next CTA.
+struct Walk {
+  const Args &A;
+  bool all_ok;
+  int e;
+  Entry x;
+  long long first_cost, first_line, pos, end;
+  int cta;
+  __device__ Walk(const Args &a) : A(a) {}
+  __device__ bool next(Seg &s) {
+    while (pos < end) {
+      const long long lc = x.line_cost();
+      if (pos >= first_cost + x.cost(A.hk)) {  // the next entry
+        first_cost += x.cost(A.hk);
+        first_line += (long long)x.tiles * A.hk;
+        if (++e >= A.n_groups + A.B) return false;
+        x = entry_at(A, e, all_ok);
+        continue;
+      }
+      const long long li = (pos - first_cost) / lc, a = first_cost + li * lc;
+      const long long z = min(end, a + lc);
+      const int tile = (int)(li / A.hk);
+      s.head = (int)(li - (long long)tile * A.hk);
+      s.b0 = (int)max(pos - a - 1, 0LL);
+      s.b1 = (int)(z - a - 1);
+      pos = z;
+      if (s.b1 <= s.b0) continue;
+      s.t0 = x.first + tile * A.tile_tokens;
+      s.ntok = min(A.tile_tokens, x.ntok - tile * A.tile_tokens);
+      s.kv0 = x.kv0;
+      s.len = x.len;
+      s.step = x.step;
+      s.lim0 = x.lim0 + x.step * tile * A.tile_tokens;
+      s.pair = s.ntok > A.TQ;
+      s.own = e >= A.n_groups;
+      s.slot = (int)(first_line + li) + cta;
+      return true;
+    }
+    return false;
+  }
+};
+
+// The block-wide exclusive sum of (a, b) over the threads; totals in ta, tb.
+template <int NT>
+__device__ void block_scan(long long &a, long long &b, long long &ta, long long &tb, long long (*sm)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long ia = a, ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) {
+      ia += x;
+      ib += y;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    sm[warp][0] = ia;
+    sm[warp][1] = ib;
+  }
+  __syncthreads();
+  long long pa = 0, pb = 0;
+  ta = tb = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w == warp) {
+      pa = ta;
+      pb = tb;
+    }
+    ta += sm[w][0];
+    tb += sm[w][1];
+  }
+  a = pa + ia - a;
+  b = pb + ib - b;
+}
+
+struct Start {  // where the CTA's work begins
+  int e, any;
+  long long first_cost, first_line;
+  Seg seg;  // prefill
+};
+
+// Prefill: the CTA's one segment. Tiles are numbered through the sequences; the
+// grid's first CTAs take the last tiles, which see the most keys.
+__device__ bool prefill_seg(const Args &A, Seg &s) {
+  const int lane = threadIdx.x & 31;
+  s.head = blockIdx.x % A.hk;
+  const int want = A.max_tiles - 1 - (int)(blockIdx.x / A.hk);
+  int seen = 0;
+  for (int b0 = 0; b0 < A.B; b0 += 32) {  // a warp looks at 32 sequences at a time
+    const int b = b0 + lane;
+    int a = 0, n = 0;
+    if (b < A.B) {
+      a = A.cu[b];
+      n = A.cu[b + 1] - a;
+      if (a < 0 || n < 0 || (long long)a + n > A.n_tokens) {
+        set_status(A.status, GDN_ERR_INDEX);
+        n = 0;
+      }
+    }
+    const int tiles = (n + A.tile_tokens - 1) / A.tile_tokens;
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, want < seen + incl);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int tile = want - seen - __shfl_sync(0xffffffffu, incl - tiles, l);
+      a = __shfl_sync(0xffffffffu, a, l);
+      n = __shfl_sync(0xffffffffu, n, l);
+      const int q = b0 + l;
+      const long long start = A.kv_start ? A.kv_start[q] : a;
+      const int m = A.kv_len ? A.kv_len[q] : n;
+      if (!inside(start, m, A.kv_rows)) {
+        if (lane == 0) set_status(A.status, GDN_ERR_INDEX);
+        return false;
+      }
+      s.t0 = a + tile * A.tile_tokens;
+      s.ntok = min(A.tile_tokens, n - tile * A.tile_tokens);
+      s.kv0 = (int)start;
+      s.len = m;
+      s.step = 1;
+      s.lim0 = m - n + tile * A.tile_tokens + 1;
+      s.b0 = 0;
+      s.b1 = blocks_of(min(m, s.lim0 + s.ntok - 1));
+      s.pair = s.ntok > A.TQ;
+      s.slot = 0;
+      s.own = false;
+      return true;
+    }
+    seen += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// ------------------------------------------------------------------- kernel
+
+template <int D>
+struct Cfg {
+  static constexpr int NS = D == 256 ? 1 : 2;               // query tiles = softmax groups = O tiles
+  static constexpr int UC = D < 128 ? D : 128;              // channels of a ring unit
+  static constexpr int HB = D / UC;                         // units of a K or V block
+  static constexpr int UB = BN * UC * 2;                    // bytes of a unit
+  static constexpr int NU = D == 64 ? 10 : 5;               // units of the ring
+  static constexpr int QB = 128 * D * 2;                    // bytes of a Q tile
+  static constexpr int kBar = NS * QB + NU * UB;
+  static constexpr int kBytes = kBar + 8 * (2 * NU + 12) + 1024;
+  static constexpr int kThreads = NS * 128 + 128;
+  static constexpr int kO = 256;                            // TMEM column of the first O tile
+};
+
+__device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] B over one K = 16 step; A's rows are the TMEM lanes, two bf16 per column.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t db, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(db), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// 32 columns of this warp's lanes, in flight until tmem_wait_ld().
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two fp32 at once: (x0, x1) * c + a
+__device__ __forceinline__ void fma2(float &x0, float &x1, float c, float a) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mov.b64 z, {%3, %3};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(c), "f"(a));
+}
+__device__ __forceinline__ void add2(float &s0, float &s1, float x0, float x1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(x0), "f"(x1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Every wait is bounded; one that runs out raises the CTA's abort flag, which ends the others.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 0; i < (1u << 22); ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 63 && *abort) return false;
+  }
+  *abort = 1;
+  set_status(status, GDN_ERR_TIMEOUT);
+  return false;
+}
+
+// The same by all lanes of a warp, with one outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *status) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, status));
+}
+
+// Where unit `u` of a segment's K or V block lies in the order of the loads.
+// Two query tiles: K0 V0 K1 V1 ...; one tile: K0 K1 V0 K2 V1 ... (S runs two blocks ahead).
+__device__ __forceinline__ int k_place(bool pair, int j) { return pair ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_place(bool pair, int j, int n) { return pair ? 2 * j + 1 : j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
+
+// The key blocks that query tile q of the segment sees.
+__device__ __forceinline__ int tile_blocks(const Args &A, const Seg &s, int q) {
+  const int last = min(s.ntok, (q + 1) * A.TQ) - 1;  // the tile's last token sees the most keys
+  return max(0, min(s.b1, blocks_of(min(s.len, s.lim0 + s.step * last))) - s.b0);
+}
 
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(128) attn_rows_kernel(const __grid_constant__ Args A) {
-  constexpr int E = D / 32;  // channels of a lane
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args A) {
+  using C = Cfg<D>;
+  constexpr int NS = C::NS, NU = C::NU, HB = C::HB, NT = C::kThreads;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  unsigned char *sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kBar), *empty = full + NU;
+  uint64_t *q_full = empty + NU, *q_empty = q_full + 1, *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2, *handed = o_full + 2;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ Start s_start;
+  __shared__ long long s_scan[NT / 32][2];
+  __shared__ float2 s_ml[NS == 2 && !SHARED ? 128 : 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kMma = NS * 4, kTma = NS * 4 + 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < NU; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(handed, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);  // the four warps of a softmax group
+      mbar_init(&o_full[i], 1);
+    }
+    fence_mbar_init();
+    s_abort = 0;
+  }
+  if (warp == kMma) tmem_alloc(&s_tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  griddep_wait();
+  griddep_trigger();  // after this CTA's TMEM is allocated: a dependent kernel cannot take it first
+
+  // ---- what this CTA does
+  Walk walk(A);
+  Seg one = {};
+  bool any;
+  if (SHARED) {
+    const int n = A.n_groups + A.B;
+    // the groups' offsets run from 0 to B without a step back, or no row is touched (and no slot used)
+    bool broken = A.n_groups > 0 && (A.group_rows[0] != 0 || A.group_rows[A.n_groups] != A.B);
+    for (int g = tid; g < A.n_groups; g += NT) broken = broken || A.group_rows[g] > A.group_rows[g + 1];
+    const bool all_ok = !__syncthreads_or(broken);
+    if (!all_ok && blockIdx.x == 0 && tid == 0) set_status(A.status, GDN_ERR_INDEX);
+    long long total = 0, lines = 0, ta, tb;
+    for (int e0 = 0; e0 < n; e0 += NT) {
+      const int e = e0 + tid;
+      long long a = 0, b = 0;
+      if (e < n) {
+        const Entry x = entry_at(A, e, all_ok);
+        if (!x.ok && blockIdx.x == 0) set_status(A.status, GDN_ERR_INDEX);
+        a = x.cost(A.hk);
+        b = (long long)x.tiles * A.hk;
+      }
+      block_scan<NT>(a, b, ta, tb, s_scan);
+      if (blockIdx.x == 0 && e < n) {  // for the join
+        A.plan[2 + 2 * e] = total + a;
+        A.plan[3 + 2 * e] = lines + b;
+      }
+      total += ta;
+      lines += tb;
+    }
+    const long long share = max((total + gridDim.x - 1) / gridDim.x, 3LL);
+    if (blockIdx.x == 0 && tid == 0) {
+      A.plan[0] = share;
+      A.plan[1] = all_ok;
+    }
+    walk.pos = blockIdx.x * share;
+    walk.end = min(walk.pos + share, total);
+    any = walk.pos < walk.end;
+    if (any) {
+      // the entry that holds pos
+      long long before = 0, before_lines = 0;
+      for (int e0 = 0; e0 < n; e0 += NT) {
+        const int e = e0 + tid;
+        long long a = 0, b = 0;
+        if (e < n) {
+          const Entry x = entry_at(A, e, all_ok);
+          a = x.cost(A.hk);
+          b = (long long)x.tiles * A.hk;
+        }
+        const long long own_cost = a;
+        block_scan<NT>(a, b, ta, tb, s_scan);
+        a += before;
+        if (a <= walk.pos && walk.pos < a + own_cost) {
+          s_start.e = e;
+          s_start.first_cost = a;
+          s_start.first_line = before_lines + b;
+        }
+        before += ta;
+        before_lines += tb;
+        if (walk.pos < before) break;  // the same for every thread
+      }
+      __syncthreads();
+      walk.all_ok = all_ok;
+      walk.e = s_start.e;
+      walk.first_cost = s_start.first_cost;
+      walk.first_line = s_start.first_line;
+      walk.x = entry_at(A, walk.e, all_ok);
+      walk.cta = blockIdx.x;
+    }
+  } else {
+    if (warp == 0) {
+      Seg s = {};
+      const bool got = prefill_seg(A, s);
+      if (lane == 0) {
+        s_start.any = got;
+        s_start.seg = s;
+      }
+    }
+    __syncthreads();
+    any = s_start.any;
+    one = s_start.seg;
+  }
+  bool fresh = true;
+  auto next_seg = [&](Seg &s) -> bool {
+    if (SHARED) return walk.next(s);
+    s = one;
+    const bool f = fresh;
+    fresh = false;
+    return f;
+  };
+
+  if (any) {
+    Seg s;
+    if (warp == kTma) {
+      if (lane == 0) {
+        // ---- loads
+        int u = 0, segs = 0;  // units issued, segments begun
+        bool ok = true;
+        while (ok && next_seg(s)) {
+          const int tiles = s.pair ? 2 : 1;
+          const int n = tile_blocks(A, s, tiles - 1);
+          if (n > 0) {
+            if (segs > 0) ok = wait_or_abort(q_empty, (segs - 1) & 1, &s_abort, A.status);
+            if (!ok) break;
+            ++segs;
+            mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * (D / 64) * A.TQ * A.G * 128));
+            for (int t = 0; t < tiles; ++t)
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(smem_u32(sm) + t * C::QB + c * 128 * 128, &qmap, c * 64, s.head * A.G, s.t0 + t * A.TQ, q_full);
+          }
+          for (int i = 0; ok && i < 2 * n; ++i) {  // K and V blocks in the order of the products
+            bool is_v;
+            int j;
+            if (s.pair) {
+              is_v = i & 1;
+              j = i >> 1;
+            } else {
+              is_v = i == 2 * n - 1 || (i >= 2 && !(i & 1));
+              j = i == 2 * n - 1 ? n - 1 : is_v ? i / 2 - 1 : (i + 1) / 2;
+            }
+            for (int h = 0; h < HB; ++h, ++u) {
+              const int st = u % NU;
+              if (u >= NU && !wait_or_abort(&empty[st], ((u / NU) - 1) & 1, &s_abort, A.status)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(&full[st], C::UB);
+              const uint32_t dst = smem_u32(sm) + NS * C::QB + st * C::UB;
+#pragma unroll
+              for (int c = 0; c < C::UC / 64; ++c)
+                tma_load_3d(dst + c * BN * 128, is_v ? &vmap : &kmap, h * C::UC + c * 64, s.head,
+                            s.kv0 + (s.b0 + j) * BN, &full[st]);
+            }
+          }
+        }
+        // the copies this thread issued have landed before the CTA's memory is released
+        for (int i = max(0, u - NU); i < u; ++i) (void)mbar_wait_bounded(&full[i % NU], (i / NU) & 1);
+        if (segs > 0) (void)mbar_wait_bounded(q_full, (segs - 1) & 1);
+      }
+    } else if (warp == kMma) {
+      // ---- products
+      int base = 0, segs = 0;          // units of earlier segments, segments with keys
+      uint32_t pc[2] = {0, 0};         // P tiles taken from each buffer
+      bool ok = true;
+      const uint32_t q_addr = smem_u32(sm), ring = q_addr + NS * C::QB;
+      const uint32_t idesc_o = idesc_bf16(128, C::UC) | (1u << 16);  // B (V) is read MN-major
+      while (ok && next_seg(s)) {
+        int nb[2];
+        nb[0] = tile_blocks(A, s, 0);
+        nb[1] = s.pair ? tile_blocks(A, s, 1) : 0;
+        const int n = s.pair ? nb[1] : nb[0];
+        if (n == 0) continue;
+        if (!warp_wait(q_full, segs & 1, &s_abort, A.status)) break;
+        ++segs;
+        auto unit_ready = [&](int place, int h) -> uint32_t {  // waits for a unit, returns its address
+          const int g = base + place * HB + h;
+          if (ok) ok = warp_wait(&full[g % NU], (g / NU) & 1, &s_abort, A.status);
+          return ring + (g % NU) * C::UB;
+        };
+        auto release = [&](int place) {
+          for (int h = 0; h < HB; ++h)
+            if (lane == 0) umma_commit(&empty[(base + place * HB + h) % NU]);
+        };
+        // S tile `buf` = query tile q times block j; done: the block's last use, fresh_v: its first
+        auto issue_s = [&](int q, int buf, int j, bool done) {
+          const int place = k_place(s.pair, j);
+#pragma unroll
+          for (int h = 0; h < HB; ++h) {
+            const uint32_t k = unit_ready(place, h);
+            if (!ok) return;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int x = 0; x < C::UC / 16; ++x)
+                umma_f16(tmem + buf * 128, umma_desc(q_addr + q * C::QB + (h * (C::UC / 64) + (x >> 2)) * 128 * 128 + (x & 3) * 32),
+                         umma_desc(k + (x >> 2) * BN * 128 + (x & 3) * 32), A.idesc_s, h > 0 || x > 0);
+            }
+          }
+          if (lane == 0) umma_commit(&s_full[buf]);
+          if (done) release(place);
+        };
+        // O tile o += P tile `buf` times block j
+        auto issue_o = [&](int o, int buf, int j, bool first, bool fresh_v, bool done) {
+          const int place = v_place(s.pair, j, n);
+          if (ok) ok = warp_wait(&p_full[buf], pc[buf] & 1, &s_abort, A.status);
+          if (!ok) return;
+          ++pc[buf];
+          const int valid = s.len - (s.b0 + j) * BN;  // rows past the extent hold anything: 0 * NaN must not enter
+#pragma unroll
+          for (int h = 0; h < HB; ++h) {
+            const uint32_t v = unit_ready(place, h);
+            if (!ok) return;
+            if (valid < BN && fresh_v) {
+              unsigned char *p = sm + (v - q_addr);
+              for (int i = valid * 8 + lane; i < BN * 8; i += 32)
+#pragma unroll
+                for (int c = 0; c < C::UC / 64; ++c)
+                  *reinterpret_cast<uint4 *>(p + c * BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int x = 0; x < BN / 16; ++x)
+                umma_ts(tmem + C::kO + o * D + h * C::UC, tmem + buf * 128 + x * 8, umma_desc_mn(v + x * 2048, BN * 128),
+                        idesc_o, !first || x > 0);
+            }
+          }
+          if (done) release(place);
+        };
+        if (s.pair) {
+          for (int q = 0; q < 2; ++q)
+            if (ok && nb[q] > 0) issue_s(q, q, 0, q == 1);
+          for (int j = 0; ok && j < n; ++j)
+            for (int q = 0; q < 2; ++q) {
+              if (ok && j < nb[q]) {
+                issue_o(q, q, j, j == 0, q == 0 || j >= nb[0], q == 1);
+                if (j + 1 == nb[q] && ok && lane == 0) umma_commit(&o_full[q]);
+              }
+              if (ok && j + 1 < nb[q]) {
+                issue_s(q, q, j + 1, q == 1);
+              }
+            }
+          if (ok && lane == 0) umma_commit(q_empty);
+        } else {
+          issue_s(0, 0, 0, true);
+          if (ok && n > 1) issue_s(0, 1, 1, true);
+          for (int j = 0; ok && j < n; ++j) {
+            const int o = NS == 2 ? (j & 1) : 0;
+            issue_o(o, j & 1, j, NS == 2 ? j < 2 : j == 0, true, true);
+            if (ok && lane == 0 && (NS == 1 || j + 2 >= n)) umma_commit(&o_full[o]);
+            if (ok && j + 2 < n) issue_s(0, j & 1, j + 2, true);
+          }
+          if (ok && lane == 0) umma_commit(q_empty);
+        }
+        base += 2 * n * HB;
+      }
+    } else if (warp < kMma) {
+      // ---- softmax: thread = row of a tile
+      const int grp = warp >> 2, wq = warp & 3, row = (wq << 5) + lane;
+      uint32_t sc[2] = {0, 0}, oc = 0;  // S tiles taken from each buffer, O tiles waited for
+      bool ok = true;
+      while (ok && next_seg(s)) {
+        const int q = s.pair ? grp : 0;
+        const int nb = tile_blocks(A, s, q);
+        const int tok = row / A.G + q * A.TQ, gh = row - (row / A.G) * A.G;
+        const bool real = row < A.TQ * A.G && tok < s.ntok;
+        const int lim = real ? min(s.len, s.lim0 + s.step * tok) : 0x7fffffff;
+        const int j0 = (!s.pair && NS == 2) ? grp : 0, dj = (!s.pair && NS == 2) ? 2 : 1;
+        float top = -INFINITY, sum = 0.0f;  // the maximum that O is measured against (before scaling), the sum
+        const uint32_t o_tmem = tmem_at(tmem, wq, C::kO + (NS == 2 ? grp : 0) * D);
+        for (int j = j0; j < nb; j += dj) {
+          const int buf = NS == 2 ? grp : (j & 1);
+          const uint32_t s_tmem_at = tmem_at(tmem, wq, buf * 128);
+          ok = warp_wait(&s_full[buf], sc[buf] & 1, &s_abort, A.status);
+          if (!ok) break;
+          ++sc[buf];
+          tc_fence_after();
+          float x[128];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32_async(s_tmem_at + 32 * i, x + 32 * i);
+          tmem_wait_ld();
+          const int key0 = (s.b0 + j) * BN;
+          if (__any_sync(0xffffffffu, lim < key0 + BN)) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) x[i] = key0 + i < lim ? x[i] : -INFINITY;
+          }
+          float mx[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(x[k], x[k + 4]);
+#pragma unroll
+          for (int i = 8; i < 128; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(x[i + k], x[i + k + 4]));
+          const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool grew = (m - top) * A.c > 8.0f || top == -INFINITY;
+          float keep = 1.0f;
+          if (grew && m > top) {
+            keep = ex2((top - m) * A.c);  // 0 from -inf
+            top = m;
+          }
+          if (j != j0 && __any_sync(0xffffffffu, keep != 1.0f)) {
+            if (NS == 1) {  // the product before may still be adding to O
+              ok = warp_wait(&o_full[0], (oc + j - 1) & 1, &s_abort, A.status);
+                  if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              float v[32];
+              tmem_ld32_async(o_tmem + i, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] *= keep;
+              tmem_st32(o_tmem + i, reinterpret_cast<const uint32_t *>(v));
+            }
+          }
+          const float shift = top == -INFINITY ? 0.0f : -top * A.c;
+          float sm4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float &a = x[64 * h + 2 * i], &b = x[64 * h + 2 * i + 1];
+              fma2(a, b, A.c, shift);
+              a = ex2(a);
+              b = ex2(b);
+              add2(sm4[2 * (i & 1)], sm4[2 * (i & 1) + 1], a, b);
+              // a probability's rounding to bf16 (2^-9 of itself on average zero) is below the output's own
+              p[i] = pack_bf16(a, b);
+            }
+            tmem_st32(s_tmem_at + 32 * h, p);
+          }
+          sum = sum * keep + ((sm4[0] + sm4[1]) + (sm4[2] + sm4[3]));
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[buf]);
+        }
+        if (!ok) break;
+        const int mine = nb > j0 ? (nb - j0 + dj - 1) / dj : 0;  // blocks this group took
+        if (mine > 0) {
+          const uint32_t ph = NS == 1 ? oc + nb - 1 : oc;
+          ok = warp_wait(&o_full[NS == 2 ? grp : 0], ph & 1, &s_abort, A.status);
+          if (!ok) break;
+          oc += NS == 1 ? nb : 1;
+          tc_fence_after();
+        }
+        // ---- the segment's results
+        if (SHARED) {
+          const int rows = s.own ? A.suffix_rows : A.prefix_rows;
+          const long long r = ((long long)s.slot * NS + grp) * rows + row;
+          if (real)  // a group that took no block says so: (-inf, 0)
+            (s.own ? A.suffix_ml : A.prefix_ml)[r] = make_float2(top == -INFINITY ? -INFINITY : top * A.c, sum);
+          float *dst = (s.own ? A.suffix_o : A.prefix_o) + r * D;
+          if (mine > 0) {
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              float v[32];
+              tmem_ld32_async(o_tmem + i, v);
+              tmem_wait_ld();
+              if (real) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+                  *reinterpret_cast<float4 *>(dst + i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+              }
+            }
+          }
+        } else {
+          const bool split = NS == 2 && !s.pair;  // the groups took alternate blocks of the same rows
+          float *far = reinterpret_cast<float *>(sm + NS * C::QB);
+          float w0 = 1.0f, w1 = 0.0f;
+          if (split) {
+            // group 1 hands its rows over in the ring's memory, which every product has read by then
+            const int n0 = (nb + 1) / 2, n1 = nb / 2;
+            if (grp == 1) {
+              if (n0 > 0) ok = warp_wait(&o_full[0], 0, &s_abort, A.status);
+              if (!ok) break;
+              s_ml[row] = make_float2(top, sum);
+              if (n1 > 0) {
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                  float v[32];
+                  tmem_ld32_async(o_tmem + i, v);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<float4 *>(far + ((i + k) / 4 * 128 + row) * 4) =
+                        make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                }
+              }
+            }
+            if (grp == 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(handed);
+              break;
+            }
+            ok = warp_wait(handed, 0, &s_abort, A.status);
+            if (!ok) break;
+            const float2 o = s_ml[row];
+            if (o.y > 0.0f) {
+              const float m = fmaxf(top, o.x);
+              w0 = sum > 0.0f ? ex2((top - m) * A.c) : 0.0f;
+              w1 = ex2((o.x - m) * A.c);
+              sum = sum * w0 + o.y * w1;
+            }
+          }
+          const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // NaN stays
+          w0 *= inv;
+          w1 *= inv;
+          bf16 *dst = A.out + ((long long)(s.t0 + tok) * A.hq + s.head * A.G + gh) * D;
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            float v[32];
+            if (mine > 0) {
+              tmem_ld32_async(o_tmem + i, v);
+              tmem_wait_ld();
+            }
+            if (real) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = mine > 0 && inv != 0.0f ? v[k] * w0 : 0.0f;
+              if (w1 != 0.0f) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                  const float4 f = *reinterpret_cast<const float4 *>(far + ((i + k) / 4 * 128 + row) * 4);
+                  v[k] = fmaf(f.x, w1, v[k]);
+                  v[k + 1] = fmaf(f.y, w1, v[k + 1]);
+                  v[k + 2] = fmaf(f.z, w1, v[k + 2]);
+                  v[k + 3] = fmaf(f.w, w1, v[k + 3]);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 32; k += 8)
+                *reinterpret_cast<uint4 *>(dst + i + k) =
+                    make_uint4(pack_bf16(v[k], v[k + 1]), pack_bf16(v[k + 2], v[k + 3]), pack_bf16(v[k + 4], v[k + 5]),
+                               pack_bf16(v[k + 6], v[k + 7]));
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) tmem_dealloc(tmem, 512);
+}
+
+// Joins the partial results of a shared-prefix call: one warp per (query token,
+// head), the parts in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args A, int ctas) {
+  constexpr int NS = Cfg<D>::NS, E = D / 32;
   griddep_wait();
   griddep_trigger();
   const int lane = threadIdx.x & 31;
-  if (!SHARED && blockIdx.x == 0)
-    for (int b = threadIdx.x; b < A.B; b += 128)
-      if (A.cu[b] < 0 || A.cu[b] > A.cu[b + 1] || A.cu[b + 1] > A.n_tokens) set_status(A.status, GDN_ERR_INDEX);
   const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int t = (int)(unit / A.hq), h = (int)(unit - (long long)t * A.hq);
-  if (t >= A.n_tokens) return;
-  Extent ext[2] = {{0, 0}, {0, 0}};
-  bool real = true;
-  if (SHARED) {
-    const int b = t / A.T, i = t - b * A.T;
-    if (A.n_groups > 0) {
-      const int g = find_row(A.group_rows, A.n_groups, b);
-      const bool ok = A.group_rows[0] == 0 && A.group_rows[A.n_groups] == A.B && g >= 0 && b < A.group_rows[g + 1];
-      if (!ok || !inside(A.prefix_start[g], A.prefix_len[g], A.kv_rows)) {
-        set_status(A.status, GDN_ERR_INDEX);
-        return;
+  if (t >= A.n_tokens || !A.plan[1]) return;
+  const int b = t / A.T, g = group_of(A, b), head = h / A.G, gh = h - head * A.G;
+  const long long share = A.plan[0];
+  const Entry own = entry_at(A, A.n_groups + b, true);
+  if (!own.ok || (g >= 0 && !inside(A.prefix_start[g], A.prefix_len[g], A.kv_rows))) return;
+  float o[E], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  const bool real = t - own.first < own.ntok;
+  for (int part = 0; real && part < 2; ++part) {
+    if (part == 0 && g < 0) continue;
+    const int e = part == 0 ? g : A.n_groups + b;
+    const Entry x = part == 0 ? entry_at(A, g, true) : own;
+    if (x.blocks == 0) continue;
+    const int ti = t - x.first, tile = ti / A.tile_tokens, i = ti - tile * A.tile_tokens;
+    const bool pair = min(A.tile_tokens, x.ntok - tile * A.tile_tokens) > A.TQ;
+    const long long li = (long long)tile * A.hk + head, lc = x.line_cost();
+    const long long a = A.plan[2 + 2 * e] + li * lc, z = a + lc;
+    const int rows = part == 0 ? A.prefix_rows : A.suffix_rows;
+    const int streams = NS == 2 && !pair ? 2 : 1, s0 = pair ? i / A.TQ : 0, row = (pair ? i % A.TQ : i) * A.G + gh;
+    const float *po = part == 0 ? A.prefix_o : A.suffix_o;
+    const float2 *pml = part == 0 ? A.prefix_ml : A.suffix_ml;
+    const int c0 = (int)(a / share), c1 = (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
+    for (int p0 = 0; p0 < n; p0 += 32) {
+      const int p = p0 + lane;
+      long long r = 0;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (p < n) {
+        const int cta = c0 + p / streams;
+        const long long b0 = max(max(a, cta * share) - a - 1, 0LL), b1 = min(z, (cta + 1) * share) - a - 1;
+        if (b1 > b0) {
+          r = ((A.plan[3 + 2 * e] + li + cta) * NS + s0 + p % streams) * rows + row;
+          ml = pml[r];
+        }
       }
-      ext[0] = {A.prefix_start[g], A.prefix_len[g]};
-    }
-    const int ql = A.q_len ? A.q_len[b] : A.T;
-    if (!inside(A.suffix_start[b], A.suffix_len[b], A.kv_rows) || ql < 0 || ql > A.T) {
-      set_status(A.status, GDN_ERR_INDEX);
-      return;
-    }
-    real = i < ql;
-    ext[1] = {A.suffix_start[b], max(0, A.suffix_len[b] - ql + i + 1)};
-    if (!real) ext[0].len = ext[1].len = 0;
-  } else {
-    const int b = find_row(A.cu, A.B, t);
-    if (b < 0 || t >= A.cu[b + 1]) return;
-    const int n = A.cu[b + 1] - A.cu[b], i = t - A.cu[b];
-    const long long start = A.kv_start ? A.kv_start[b] : A.cu[b];
-    const int m = A.kv_len ? A.kv_len[b] : n;
-    if (A.cu[b] < 0 || A.cu[b + 1] > A.n_tokens || !inside(start, m, A.kv_rows)) {
-      set_status(A.status, GDN_ERR_INDEX);
-      return;
-    }
-    ext[1] = {start, max(0, m - n + i + 1)};
-  }
-  float q[E], o[E], top = -INFINITY, sum = 0.0f;
-  const bf16 *qp = A.q + t * A.qs + (long long)h * D + lane * E;
+      float m = ml.y > 0.0f || ml.y != ml.y ? ml.x : -INFINITY;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = ldbf(qp + e) * A.scale;
-    o[e] = 0.0f;
-  }
-  for (int x = 0; x < 2; ++x) {
-    const long long base = ext[x].start * A.kvs + (long long)(h / A.G) * D + lane * E;
-    for (int j = 0; j < ext[x].len; ++j) {
-      const bf16 *kp = A.k + base + j * A.kvs, *vp = A.v + base + j * A.kvs;
-      float s = 0.0f;
+      for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+      const float best = fmaxf(top, m);
+      const float keep = top == -INFINITY ? 0.0f : ex2(top - best);
+      const float w = ml.y == 0.0f ? 0.0f : ex2(ml.x - best);
+      top = best;
+      sum *= keep;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(q[e], ldbf(kp + e), s);
+      for (int e2 = 0; e2 < E; ++e2) o[e2] *= keep;
+      const int here = min(32, n - p0);
+#pragma unroll 4
+      for (int k = 0; k < here; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k), yk = __shfl_sync(0xffffffffu, ml.y, k);
+        const long long rk = __shfl_sync(0xffffffffu, r, k);
+        if (wk == 0.0f) continue;
+        sum = fmaf(yk, wk, sum);
+        const float *src = po + rk * D + lane * E;
+        float v[E];
+        if (E == 2) {
+          const float2 f = *reinterpret_cast<const float2 *>(src);
+          v[0] = f.x;
+          v[1] = f.y;
+        } else {
 #pragma unroll
-      for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-      const float m = fmaxf(top, s), old = top == m ? 1.0f : __expf(top - m), p = __expf(s - m);
-      top = m;
-      sum = sum * old + p;
+          for (int q = 0; q < E / 4; ++q) {
+            const float4 f = *reinterpret_cast<const float4 *>(src + 4 * q);
+            v[4 * q] = f.x;
+            v[4 * q + 1] = f.y;
+            v[4 * q + 2] = f.z;
+            v[4 * q + 3] = f.w;
+          }
+        }
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(p, ldbf(vp + e), o[e] * old);
+        for (int e2 = 0; e2 < E; ++e2) o[e2] = fmaf(v[e2], wk, o[e2]);
+      }
     }
   }
-  bf16 *op = A.out + ((long long)t * A.hq + h) * D + lane * E;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint32_t p[E / 2];
 #pragma unroll
-  for (int e = 0; e < E; ++e) op[e] = __float2bfloat16_rn(sum > 0.0f ? o[e] / sum : 0.0f);
+  for (int e = 0; e < E / 2; ++e) p[e] = sum == 0.0f ? 0u : pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+  bf16 *dst = A.out + ((long long)t * A.hq + h) * D + lane * E;
+  if (E == 2) *reinterpret_cast<uint32_t *>(dst) = p[0];
+  if (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(p[0], p[E / 2 - 1]);
+  if (E == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1 % (E / 2)], p[2 % (E / 2)], p[3 % (E / 2)]);
 }
+
+// --------------------------------------------------------------------- host
 
 gdn_status check(const gdn_attn_dims *d) {
   if (!d) return fail(GDN_ERR_ARG, "dims is NULL");
@@ -136,7 +958,35 @@ gdn_status check(const gdn_attn_dims *d) {
   return GDN_OK;
 }
 
-Args make_args(const gdn_attn_dims *d, const void *q, const void *k, const void *v, void *out) {
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// [rows][heads][D] with `stride` elements between rows; boxes of 64 channels x box_heads x box_rows, 128-byte swizzle.
+gdn_status encode(CUtensorMap *map, const void *base, int D, int heads, long long rows, long long stride, int box_heads,
+                  int box_rows) {
+  static const EncodeTiled fn = []() -> EncodeTiled {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  if (!fn) return fail(GDN_ERR_CUDA, "attention: cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t es[3] = {1, 1, 1};
+  if (fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return fail(GDN_ERR_CUDA, "attention: cannot encode a tensor map");
+  return GDN_OK;
+}
+
+Args make_args(const gdn_attn_dims *d, void *out, unsigned int *status) {
   Args A = {};
   A.B = d->B;
   A.T = d->T;
@@ -145,27 +995,78 @@ Args make_args(const gdn_attn_dims *d, const void *q, const void *k, const void 
   A.hq = d->n_q_heads;
   A.hk = d->n_kv_heads;
   A.G = d->n_q_heads / d->n_kv_heads;
-  A.scale = d->scale;
-  A.qs = d->q_stride;
-  A.kvs = d->kv_stride;
+  A.TQ = 128 / A.G;
+  A.tile_tokens = (d->head_dim == 256 ? 1 : 2) * A.TQ;
+  // masked scores are -inf: times a scale of exactly zero they would be NaN
+  A.c = fmaxf(fabsf(d->scale) * 1.4426950408889634f, 1e-30f);
+  // kind::f16, bf16 A and B, fp32 D, N = 128, M = 128; bit 13 negates A for a negative scale
+  A.idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24) | (d->scale < 0.0f ? 1u << 13 : 0u);
   A.kv_rows = d->kv_rows;
-  A.q = static_cast<const bf16 *>(q);
-  A.k = static_cast<const bf16 *>(k);
-  A.v = static_cast<const bf16 *>(v);
   A.out = static_cast<bf16 *>(out);
+  A.status = status;
   return A;
 }
 
+template <int D, bool SHARED>
+gdn_status launch_t(const gdn_attn_dims *d, const void *q, const void *k, const void *v, const Args &A, int grid,
+                    cudaStream_t st) {
+  CUtensorMap qm, km, vm;
+  GDN_TRY(encode(&qm, q, D, A.hq, A.n_tokens, d->q_stride, A.G, A.TQ));
+  GDN_TRY(encode(&km, k, D, A.hk, A.kv_rows, d->kv_stride, 1, BN));
+  GDN_TRY(encode(&vm, v, D, A.hk, A.kv_rows, d->kv_stride, 1, BN));
+  const DeviceInfo &dev = device_info();
+  static std::atomic<bool> ready[kMaxDevices];
+  if (!ready[dev.id].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(attn_kernel<D, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes) !=
+        cudaSuccess)
+      return fail(GDN_ERR_CUDA, "attention: cannot reserve shared memory");
+    ready[dev.id].store(true, std::memory_order_release);
+  }
+  launch_pdl(attn_kernel<D, SHARED>, dim3((unsigned)grid), dim3(Cfg<D>::kThreads), Cfg<D>::kBytes, st, qm, km, vm, A);
+  GDN_TRY(check_launch("attention"));
+  if (SHARED) {
+    const long long warps = (long long)A.n_tokens * A.hq;
+    launch_pdl(join_kernel<D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, A, grid);
+  }
+  return check_launch("attention");
+}
+
 template <bool SHARED>
-gdn_status launch(Args &A, int D, cudaStream_t st) {
-  const DeviceInfo *dev;
-  GDN_TRY(current_device(&dev));
-  A.status = dev->status;
-  const dim3 grid((unsigned)(((long long)A.n_tokens * A.hq + 3) / 4));
-  if (D == 64) launch_pdl(attn_rows_kernel<64, SHARED>, grid, dim3(128), 0, st, A);
-  if (D == 128) launch_pdl(attn_rows_kernel<128, SHARED>, grid, dim3(128), 0, st, A);
-  if (D == 256) launch_pdl(attn_rows_kernel<256, SHARED>, grid, dim3(128), 0, st, A);
-  return check_launch(SHARED ? "attn_shared_prefix" : "attn_prefill");
+gdn_status launch(const gdn_attn_dims *d, const void *q, const void *k, const void *v, const Args &A, int grid,
+                  cudaStream_t st) {
+  if (d->head_dim == 64) return launch_t<64, SHARED>(d, q, k, v, A, grid, st);
+  if (d->head_dim == 128) return launch_t<128, SHARED>(d, q, k, v, A, grid, st);
+  return launch_t<256, SHARED>(d, q, k, v, A, grid, st);
+}
+
+// The workspace of a shared-prefix call; base NULL: its size only.
+size_t carve(const gdn_attn_dims *d, Args &A, unsigned char *base) {
+  const int D = d->head_dim, ns = D == 256 ? 1 : 2;
+  const long long prefix_lines = (long long)A.hk * ((long long)d->B * d->T / A.tile_tokens + d->n_groups);
+  const long long own_lines = (long long)A.hk * d->B * ((d->T + A.tile_tokens - 1) / A.tile_tokens);
+  A.prefix_rows = A.TQ * A.G;
+  A.suffix_rows = (d->T < A.TQ ? d->T : A.TQ) * A.G;
+  const long long ps = d->n_groups > 0 ? (prefix_lines + kMaxCtas) * ns * A.prefix_rows : 0;
+  const long long ss = ((d->n_groups > 0 ? prefix_lines : 0) + own_lines + kMaxCtas) * ns * A.suffix_rows;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char *p = base ? base + at : nullptr;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  A.plan = reinterpret_cast<long long *>(take(16 * ((size_t)d->n_groups + d->B + 1)));
+  A.prefix_ml = reinterpret_cast<float2 *>(take((size_t)ps * 8));
+  A.suffix_ml = reinterpret_cast<float2 *>(take((size_t)ss * 8));
+  A.prefix_o = reinterpret_cast<float *>(take((size_t)ps * D * 4));
+  A.suffix_o = reinterpret_cast<float *>(take((size_t)ss * D * 4));
+  return at;
+}
+
+gdn_status check_shared(const gdn_attn_dims *d) {
+  GDN_TRY(check(d));
+  if (d->T < 1 || d->T > 64) return fail(GDN_ERR_SHAPE, "T must be in [1, 64]");
+  if ((long long)d->B * d->T != d->n_tokens) return fail(GDN_ERR_SHAPE, "n_tokens must be B * T");
+  return GDN_OK;
 }
 
 }  // namespace attn
@@ -191,25 +1092,31 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims *d, const void *q, const void *k
     GDN_TRY(check_ptr(kv_start, "kv_start", 4));
     GDN_TRY(check_ptr(kv_len, "kv_len", 4));
   }
-  attn::Args A = attn::make_args(d, q, k, v, out);
+  const DeviceInfo *dev;
+  GDN_TRY(current_device(&dev));
+  attn::Args A = attn::make_args(d, out, dev->status);
   A.cu = cu_seqlens;
   A.kv_start = kv_start;
   A.kv_len = kv_len;
-  return attn::launch<false>(A, d->head_dim, static_cast<cudaStream_t>(stream));
+  // fewer two-tile CTAs than SMs: one tile each, its keys shared between the two groups
+  if ((long long)d->n_tokens * d->n_kv_heads < (long long)dev->sms * A.tile_tokens) A.tile_tokens = A.TQ;
+  const long long tiles = (long long)d->n_tokens / A.tile_tokens + d->B;
+  if (tiles * A.hk > (1LL << 31) - 1) return fail(GDN_ERR_SHAPE, "too many tokens in one call");
+  A.max_tiles = (int)tiles;
+  return attn::launch<false>(d, q, k, v, A, (int)(tiles * A.hk), static_cast<cudaStream_t>(stream));
 }
 
 size_t gdn_attn_workspace_size(const gdn_attn_dims *d) {
-  if (attn::check(d) != GDN_OK) return 0;
-  return 256;
+  if (attn::check_shared(d) != GDN_OK) return 0;
+  attn::Args A = attn::make_args(d, nullptr, nullptr);
+  return attn::carve(d, A, nullptr);
 }
 
 gdn_status gdn_attn_shared_prefix(const gdn_attn_dims *d, const void *q, const void *k, const void *v,
                                   const int32_t *group_rows, const int32_t *prefix_start, const int32_t *prefix_len,
                                   const int32_t *suffix_start, const int32_t *suffix_len, const int32_t *q_len,
                                   void *out, void *workspace, size_t workspace_bytes, void *stream) {
-  GDN_TRY(attn::check(d));
-  if (d->T < 1 || d->T > 64) return fail(GDN_ERR_SHAPE, "T must be in [1, 64]");
-  if ((long long)d->B * d->T != d->n_tokens) return fail(GDN_ERR_SHAPE, "n_tokens must be B * T");
+  GDN_TRY(attn::check_shared(d));
   if (d->B == 0) return GDN_OK;
   GDN_TRY(check_ptr(q, "q"));
   GDN_TRY(check_ptr(k, "k"));
@@ -225,14 +1132,18 @@ gdn_status gdn_attn_shared_prefix(const gdn_attn_dims *d, const void *q, const v
   if (q_len) GDN_TRY(check_ptr(q_len, "q_len", 4));
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < gdn_attn_workspace_size(d))
     return fail(GDN_ERR_WORKSPACE, "workspace missing, not 256-byte aligned, or too small");
-  attn::Args A = attn::make_args(d, q, k, v, out);
+  const DeviceInfo *dev;
+  GDN_TRY(current_device(&dev));
+  attn::Args A = attn::make_args(d, out, dev->status);
+  (void)attn::carve(d, A, static_cast<unsigned char *>(workspace));
   A.group_rows = group_rows;
   A.prefix_start = prefix_start;
   A.prefix_len = prefix_len;
   A.suffix_start = suffix_start;
   A.suffix_len = suffix_len;
   A.q_len = q_len;
-  return attn::launch<true>(A, d->head_dim, static_cast<cudaStream_t>(stream));
+  const int grid = dev->sms < attn::kMaxCtas ? dev->sms : attn::kMaxCtas;
+  return attn::launch<true>(d, q, k, v, A, grid, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
