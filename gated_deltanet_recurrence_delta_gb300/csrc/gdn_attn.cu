@@ -738,7 +738,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (!ok) break;
         const int mine = nb > j0 ? (nb - j0 + dj - 1) / dj : 0;  // blocks this group took
         if (mine > 0) {
+          // D = 256 completes a phase with every product: a parity tells only neighbouring phases apart, and
+          // the last S tile vouches for the products up to two before the last
           const uint32_t ph = NS == 1 ? oc + nb - 1 : oc;
+          if (NS == 1 && nb > 1) ok = warp_wait(&o_full[0], (ph - 1) & 1, &s_abort, A.status);
+          if (!ok) break;
           ok = warp_wait(&o_full[NS == 2 ? grp : 0], ph & 1, &s_abort, A.status);
           if (!ok) break;
           oc += NS == 1 ? nb : 1;
