@@ -17,6 +17,7 @@
 //   - one TMA warp: Q tiles, then K and V blocks through a ring of units of
 //     128 keys x min(D, 128) channels, in the order the products take them;
 //   - one MMA warp: S = Q K^T into TMEM, O += P V with P read from TMEM;
+//   - one warp that clears the rows of V that lie past an extent's end;
 //   - one or two softmax groups of four warps, a thread per row: S from TMEM
 //     to registers, exponentials, P (bf16) back over S.
 // D = 64, 128: two S tiles and two O tiles fill the TMEM's 512 columns, and two
@@ -275,12 +276,12 @@ struct Cfg {
   static constexpr int NU = D == 64 ? 10 : 5;               // units of the ring
   static constexpr int QB = 128 * D * 2;                    // bytes of a Q tile
   static constexpr int kBar = NS * QB + NU * UB;
-  static constexpr int kBytes = kBar + 8 * (2 * NU + 12) + 1024;
+  static constexpr int kBytes = kBar + 8 * (2 * NU + 14) + 1024;
   static constexpr int kThreads = NS * 128 + 128;
   static constexpr int kO = 256;                            // TMEM column of the first O tile
 };
 
-__device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // D[tmem] (+)= A[tmem] B over one K = 16 step; A's rows are the TMEM lanes, two bf16 per column.
@@ -372,6 +373,16 @@ __device__ __forceinline__ int tile_blocks(const Args &A, const Seg &s, int q) {
   return max(0, min(s.b1, blocks_of(min(s.len, s.lim0 + s.step * last))) - s.b0);
 }
 
+// The segment's block whose last rows lie past the extent, if it is among the first n; else -1.
+__device__ __forceinline__ int tail_block(const Seg &s, int n) {
+  return n > 0 && (long long)(s.b0 + n) * BN > s.len ? n - 1 : -1;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -382,14 +393,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char *sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kBar), *empty = full + NU;
-  uint64_t *q_full = empty + NU, *q_empty = q_full + 1, *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2, *handed = o_full + 2;
+  uint64_t *q_full = empty + NU, *q_empty = q_full + 1, *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2, *handed = o_full + 2,
+           *clean = handed + 1, *dirty = clean + 1;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ Start s_start;
   __shared__ long long s_scan[NT / 32][2];
   __shared__ float2 s_ml[NS == 2 && !SHARED ? 128 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kMma = NS * 4, kTma = NS * 4 + 1;
+  constexpr int kMma = NS * 4, kTma = NS * 4 + 1, kClean = NS * 4 + 2;
 
   if (tid == 0) {
     for (int i = 0; i < NU; ++i) {
@@ -399,6 +411,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(handed, 4);
+    mbar_init(clean, 1);
+    mbar_init(dirty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);  // the four warps of a softmax group
@@ -554,101 +568,124 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (segs > 0) (void)mbar_wait_bounded(q_full, (segs - 1) & 1);
       }
     } else if (warp == kMma) {
-      // ---- products
-      int base = 0, segs = 0;          // units of earlier segments, segments with keys
-      uint32_t pc[2] = {0, 0};         // P tiles taken from each buffer
-      bool ok = true;
-      const uint32_t q_addr = smem_u32(sm), ring = q_addr + NS * C::QB;
-      const uint32_t idesc_o = idesc_bf16(128, C::UC) | (1u << 16);  // B (V) is read MN-major
-      while (ok && next_seg(s)) {
-        int nb[2];
-        nb[0] = tile_blocks(A, s, 0);
-        nb[1] = s.pair ? tile_blocks(A, s, 1) : 0;
-        const int n = s.pair ? nb[1] : nb[0];
-        if (n == 0) continue;
-        if (!warp_wait(q_full, segs & 1, &s_abort, A.status)) break;
-        ++segs;
-        auto unit_ready = [&](int place, int h) -> uint32_t {  // waits for a unit, returns its address
-          const int g = base + place * HB + h;
-          if (ok) ok = warp_wait(&full[g % NU], (g / NU) & 1, &s_abort, A.status);
-          return ring + (g % NU) * C::UB;
-        };
-        auto release = [&](int place) {
-          for (int h = 0; h < HB; ++h)
-            if (lane == 0) umma_commit(&empty[(base + place * HB + h) % NU]);
-        };
-        // S tile `buf` = query tile q times block j; done: the block's last use, fresh_v: its first
-        auto issue_s = [&](int q, int buf, int j, bool done) {
-          const int place = k_place(s.pair, j);
+      // ---- products: one thread issues them all
+      if (elect_one()) {
+        int base = 0, segs = 0;  // units of earlier segments, segments with keys
+        uint32_t pc[2] = {0, 0}, cleaned = 0;  // P tiles taken from each buffer, blocks with cleaned tails
+        bool ok = true;
+        const uint64_t q_desc = umma_desc(smem_u32(sm)), k_desc = umma_desc(smem_u32(sm) + NS * C::QB),
+                       v_desc = umma_desc_mn(smem_u32(sm) + NS * C::QB, BN * 128);
+        constexpr uint32_t idesc_o = idesc_bf16(128, C::UC) | (1u << 16);  // B (V) is read MN-major
+        while (ok && next_seg(s)) {
+          const int nb0 = tile_blocks(A, s, 0), nb1 = s.pair ? tile_blocks(A, s, 1) : 0;
+          const int n = s.pair ? nb1 : nb0;
+          if (n == 0) continue;
+          if (!wait_or_abort(q_full, segs & 1, &s_abort, A.status)) break;
+          ++segs;
+          const int tail = tail_block(s, n);  // the block whose V rows past the extent are cleaned first
+          bool handed_over = false;
+          auto unit_ready = [&](int g) {
+            if (ok) ok = wait_or_abort(&full[g % NU], (g / NU) & 1, &s_abort, A.status);
+          };
+          // S tile `buf` = query tile q times block j; done: the block's last use
+          auto issue_s = [&](int q, int buf, int j, bool done) {
+            const int g0 = base + k_place(s.pair, j) * HB;
 #pragma unroll
-          for (int h = 0; h < HB; ++h) {
-            const uint32_t k = unit_ready(place, h);
-            if (!ok) return;
-            tc_fence_after();
-            if (lane == 0) {
+            for (int h = 0; h < HB; ++h) {
+              unit_ready(g0 + h);
+              if (!ok) return;
+              tc_fence_after();
+              const uint64_t a = q_desc + (uint32_t)((q * C::QB + h * (C::UC / 64) * 128 * 128) >> 4);
+              const uint64_t b = k_desc + (uint32_t)(((g0 + h) % NU) * (C::UB >> 4));
 #pragma unroll
-              for (int x = 0; x < C::UC / 16; ++x)
-                umma_f16(tmem + buf * 128, umma_desc(q_addr + q * C::QB + (h * (C::UC / 64) + (x >> 2)) * 128 * 128 + (x & 3) * 32),
-                         umma_desc(k + (x >> 2) * BN * 128 + (x & 3) * 32), A.idesc_s, h > 0 || x > 0);
+              for (int x = 0; x < C::UC / 16; ++x) {
+                const uint32_t step = (uint32_t)(((x >> 2) * 128 * 128 + (x & 3) * 32) >> 4);
+                umma_f16(tmem + buf * 128, a + step, b + step, A.idesc_s, h > 0 || x > 0);
+              }
             }
-          }
-          if (lane == 0) umma_commit(&s_full[buf]);
-          if (done) release(place);
-        };
-        // O tile o += P tile `buf` times block j
-        auto issue_o = [&](int o, int buf, int j, bool first, bool fresh_v, bool done) {
-          const int place = v_place(s.pair, j, n);
-          if (ok) ok = warp_wait(&p_full[buf], pc[buf] & 1, &s_abort, A.status);
-          if (!ok) return;
-          ++pc[buf];
-          const int valid = s.len - (s.b0 + j) * BN;  // rows past the extent hold anything: 0 * NaN must not enter
-#pragma unroll
-          for (int h = 0; h < HB; ++h) {
-            const uint32_t v = unit_ready(place, h);
-            if (!ok) return;
-            if (valid < BN && fresh_v) {
-              unsigned char *p = sm + (v - q_addr);
-              for (int i = valid * 8 + lane; i < BN * 8; i += 32)
-#pragma unroll
-                for (int c = 0; c < C::UC / 64; ++c)
-                  *reinterpret_cast<uint4 *>(p + c * BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
+            umma_commit(&s_full[buf]);
+            if (done)
+              for (int h = 0; h < HB; ++h) umma_commit(&empty[(g0 + h) % NU]);
+          };
+          // O tile o += P tile `buf` times block j
+          auto issue_o = [&](int o, int buf, int j, bool first, bool done) {
+            const int g0 = base + v_place(s.pair, j, n) * HB;
+            if (j == tail) {  // landed: hand the units to the cleaning warp
+              for (int h = 0; h < HB; ++h) unit_ready(g0 + h);
+              if (ok && !handed_over) mbar_arrive(dirty);
+              handed_over = true;
             }
-            tc_fence_after();
-            if (lane == 0) {
+            if (ok) ok = wait_or_abort(&p_full[buf], pc[buf] & 1, &s_abort, A.status);
+            if (!ok) return;
+            ++pc[buf];
+#pragma unroll
+            for (int h = 0; h < HB; ++h) {
+              unit_ready(g0 + h);
+              if (ok && j == tail && h == 0) ok = wait_or_abort(clean, cleaned & 1, &s_abort, A.status);
+              if (!ok) return;
+              tc_fence_after();
+              const uint64_t b = v_desc + (uint32_t)(((g0 + h) % NU) * (C::UB >> 4));
 #pragma unroll
               for (int x = 0; x < BN / 16; ++x)
-                umma_ts(tmem + C::kO + o * D + h * C::UC, tmem + buf * 128 + x * 8, umma_desc_mn(v + x * 2048, BN * 128),
-                        idesc_o, !first || x > 0);
+                umma_ts(tmem + C::kO + o * D + h * C::UC, tmem + buf * 128 + x * 8, b + (uint32_t)(x * 2048 >> 4), idesc_o,
+                        !first || x > 0);
+            }
+            if (done)
+              for (int h = 0; h < HB; ++h) umma_commit(&empty[(g0 + h) % NU]);
+          };
+          if (s.pair) {
+            if (nb0 > 0) issue_s(0, 0, 0, false);
+            if (ok) issue_s(1, 1, 0, true);
+            for (int j = 0; ok && j < n; ++j) {
+              if (j < nb0) {
+                issue_o(0, 0, j, j == 0, false);
+                if (j + 1 == nb0 && ok) umma_commit(&o_full[0]);
+                if (j + 1 < nb0 && ok) issue_s(0, 0, j + 1, false);
+              }
+              if (ok) issue_o(1, 1, j, j == 0, true);
+              if (j + 1 == n && ok) umma_commit(&o_full[1]);
+              if (j + 1 < n && ok) issue_s(1, 1, j + 1, true);
+            }
+          } else {
+            issue_s(0, 0, 0, true);
+            if (ok && n > 1) issue_s(0, 1, 1, true);
+            for (int j = 0; ok && j < n; ++j) {
+              const int o = NS == 2 ? (j & 1) : 0;
+              issue_o(o, j & 1, j, NS == 2 ? j < 2 : j == 0, true);
+              if (ok && (NS == 1 || j + 2 >= n)) umma_commit(&o_full[o]);
+              if (ok && j + 2 < n) issue_s(0, j & 1, j + 2, true);
             }
           }
-          if (done) release(place);
-        };
-        if (s.pair) {
-          for (int q = 0; q < 2; ++q)
-            if (ok && nb[q] > 0) issue_s(q, q, 0, q == 1);
-          for (int j = 0; ok && j < n; ++j)
-            for (int q = 0; q < 2; ++q) {
-              if (ok && j < nb[q]) {
-                issue_o(q, q, j, j == 0, q == 0 || j >= nb[0], q == 1);
-                if (j + 1 == nb[q] && ok && lane == 0) umma_commit(&o_full[q]);
-              }
-              if (ok && j + 1 < nb[q]) {
-                issue_s(q, q, j + 1, q == 1);
-              }
-            }
-          if (ok && lane == 0) umma_commit(q_empty);
-        } else {
-          issue_s(0, 0, 0, true);
-          if (ok && n > 1) issue_s(0, 1, 1, true);
-          for (int j = 0; ok && j < n; ++j) {
-            const int o = NS == 2 ? (j & 1) : 0;
-            issue_o(o, j & 1, j, NS == 2 ? j < 2 : j == 0, true, true);
-            if (ok && lane == 0 && (NS == 1 || j + 2 >= n)) umma_commit(&o_full[o]);
-            if (ok && j + 2 < n) issue_s(0, j & 1, j + 2, true);
+          if (ok) umma_commit(q_empty);
+          if (tail >= 0) ++cleaned;
+          base += 2 * n * HB;
+        }
+      }
+    } else if (warp == kClean) {
+      // ---- V rows past an extent's end hold anything, and 0 * NaN must not enter the product: zeros over them
+      // (lane 0 of the MMA warp says when they have landed: a parity alone does not tell a ring unit's later phases apart)
+      int base = 0;
+      uint32_t cleaned = 0;
+      bool ok = true;
+      while (ok && next_seg(s)) {
+        const int n = tile_blocks(A, s, s.pair ? 1 : 0), tail = tail_block(s, n);
+        if (tail >= 0) {
+          const int g0 = base + v_place(s.pair, tail, n) * HB, valid = s.len - (s.b0 + tail) * BN;
+          ok = warp_wait(dirty, cleaned & 1, &s_abort, A.status);
+          if (!ok) break;
+          ++cleaned;
+          for (int h = 0; h < HB; ++h) {
+            const int g = g0 + h;
+            (void)mbar_try_wait(&full[g % NU], (g / NU) & 1);  // complete: acquires the copy's writes
+            unsigned char *p = sm + NS * C::QB + (g % NU) * C::UB;
+            for (int i = valid * 8 + lane; i < BN * 8; i += 32)
+#pragma unroll
+              for (int c = 0; c < C::UC / 64; ++c)
+                *reinterpret_cast<uint4 *>(p + c * BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
           }
-          if (ok && lane == 0) umma_commit(q_empty);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(clean);
         }
         base += 2 * n * HB;
       }
