@@ -710,33 +710,61 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           if (!ok) break;
           ++sc[buf];
           tc_fence_after();
-          float x[128];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32_async(s_tmem_at + 32 * i, x + 32 * i);
-          tmem_wait_ld();
           const int key0 = (s.b0 + j) * BN;
-          if (__any_sync(0xffffffffu, lim < key0 + BN)) {
+          const bool masked = __any_sync(0xffffffffu, lim < key0 + BN);
+          auto load_scores = [&](float (&x)[128]) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i) x[i] = key0 + i < lim ? x[i] : -INFINITY;
+            for (int i = 0; i < 4; ++i) tmem_ld32_async(s_tmem_at + 32 * i, x + 32 * i);
+            tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 128; ++i) x[i] = key0 + i < lim ? x[i] : -INFINITY;
+            }
+          };
+          if (j == j0) {  // the first block: its maximum is the one to measure against
+            float x[128];
+            load_scores(x);
+            float mx[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(x[k], x[k + 4]);
+#pragma unroll
+            for (int i = 8; i < 128; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(x[i + k], x[i + k + 4]));
+            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           }
-          float mx[4];
+          // Probabilities against the maximum so far, while the block's own maximum is found beside them (one
+          // after the other costs a third more). A row that outgrew it is rare after the first blocks: O is
+          // rescaled and the block's probabilities formed again.
+          uint32_t p[64];
+          float part;
+          while (true) {
+            float x[128];
+            load_scores(x);
+            const float shift = top == -INFINITY ? 0.0f : -top * A.c;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float sm4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(x[k], x[k + 4]);
-#pragma unroll
-          for (int i = 8; i < 128; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(x[i + k], x[i + k + 4]));
-          const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool grew = (m - top) * A.c > 8.0f || top == -INFINITY;
-          float keep = 1.0f;
-          if (grew && m > top) {
-            keep = ex2((top - m) * A.c);  // 0 from -inf
-            top = m;
-          }
-          if (j != j0 && __any_sync(0xffffffffu, keep != 1.0f)) {
+            for (int i = 0; i < 64; ++i) {
+              float &a = x[2 * i], &b = x[2 * i + 1];
+              mx[i & 3] = fmaxf(mx[i & 3], fmaxf(a, b));
+              fma2(a, b, A.c, shift);
+              a = ex2(a);
+              b = ex2(b);
+              add2(sm4[2 * (i & 1)], sm4[2 * (i & 1) + 1], a, b);
+              // a probability's rounding to bf16 (2^-9 of itself, on average zero) is below the output's own
+              p[i] = pack_bf16(a, b);
+            }
+            part = (sm4[0] + sm4[1]) + (sm4[2] + sm4[3]);
+            const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool grew = m > top && ((m - top) * A.c > 8.0f || top == -INFINITY);
+            if (!__any_sync(0xffffffffu, grew)) break;
+            const float keep = grew ? ex2((top - m) * A.c) : 1.0f;  // 0 from -inf
+            if (grew) top = m;
+            sum *= keep;
             if (NS == 1) {  // the product before may still be adding to O
               ok = warp_wait(&o_full[0], (oc + j - 1) & 1, &s_abort, A.status);
-                  if (!ok) break;
+              if (!ok) break;
               tc_fence_after();
             }
 #pragma unroll 1
@@ -749,24 +777,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
               tmem_st32(o_tmem + i, reinterpret_cast<const uint32_t *>(v));
             }
           }
-          const float shift = top == -INFINITY ? 0.0f : -top * A.c;
-          float sm4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float &a = x[64 * h + 2 * i], &b = x[64 * h + 2 * i + 1];
-              fma2(a, b, A.c, shift);
-              a = ex2(a);
-              b = ex2(b);
-              add2(sm4[2 * (i & 1)], sm4[2 * (i & 1) + 1], a, b);
-              // a probability's rounding to bf16 (2^-9 of itself on average zero) is below the output's own
-              p[i] = pack_bf16(a, b);
-            }
-            tmem_st32(s_tmem_at + 32 * h, p);
-          }
-          sum = sum * keep + ((sm4[0] + sm4[1]) + (sm4[2] + sm4[3]));
+          if (!ok) break;
+          tmem_st32(s_tmem_at, p);
+          tmem_st32(s_tmem_at + 32, p + 32);
+          sum += part;
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
