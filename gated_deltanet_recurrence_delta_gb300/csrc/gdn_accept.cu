@@ -11,9 +11,9 @@
 //
 // Memory-bound by the one or two rows of V probabilities the draw is made
 // from. A cluster of CTAs shares one batch row: each sums its slice of the
-// vocabulary, the slice sums meet in distributed shared memory, and the CTA
-// whose slice holds the drawn point finds the index in the one warp's share
-// (an eighth of the slice) that holds it. The drawn index is a comparison of
+// vocabulary, a share for each of its warps, the 64 shares' sums meet in
+// distributed shared memory, and the CTA whose share holds the drawn point
+// finds the index in it. The drawn index is a comparison of
 // running sums, so sums are carried as two floats (~48 bits): plain fp32 sums
 // would move ~1% of the draws to a neighbouring token.
 #include "gdn_launch.h"
@@ -62,6 +62,26 @@ struct Row {
   }
 };
 
+// This lane's part of the mass of tokens [i0, i1): tokens i0 + lane, + 32, ... in batches of kBatch loads of each row.
+constexpr int kBatch = 8;
+template <bool TWO>
+__device__ __forceinline__ double lane_mass(const Row &R, int i0, int i1, int lane) {
+  float hi = 0.0f, lo = 0.0f;
+  int i = i0 + lane;
+  for (; i + 32 * (kBatch - 1) < i1; i += 32 * kBatch) {
+    float p[kBatch], q[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      p[k] = __ldcs(R.p + i + 32 * k);
+      q[k] = TWO ? __ldcs(R.q + i + 32 * k) : i + 32 * k == R.taken ? 3.4e38f : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) add(hi, lo, weight(p[k], q[k]));
+  }
+  for (; i < i1; i += 32) add(hi, lo, R.at(i));
+  return (double)hi + (double)lo;
+}
+
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -71,16 +91,19 @@ __device__ __forceinline__ double ld_cluster(const double *p, uint32_t rank) {
   uint32_t a;
   double v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void cluster_sync_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant__ Args A) {
   __shared__ int s_kept, s_bad, s_pick;
-  __shared__ double s_warp[kWarps], s_total;
+  __shared__ double s_warp[kWarps], s_part[kWarps], s_at, s_spot;
   griddep_wait();
   griddep_trigger();
   uint32_t rank;
@@ -107,11 +130,11 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
     if (lane == 0) {
       s_kept = __ffs(~ok) - 1;  // T <= 32: at most 31 drafts, so a zero bit is there
       s_bad = bad;
-      s_pick = -1;
     }
   }
   __syncthreads();
   const int kept = s_kept;
+  const float u_draw = A.uniform[b * A.T + A.T - 1];
   if (s_bad || n == 0) {  // the same for every CTA of the cluster
     if (rank == 0 && tid == 0) {
       if (s_bad) set_status(A.status, GDN_ERR_INDEX);
@@ -127,79 +150,61 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
   R.taken = refused && !A.draft ? A.tokens[b * A.T + kept + 1] : -1;
 
   // ---- this warp's contiguous share of the row
-  const long long W = (long long)kCluster * kWarps, w = (long long)rank * kWarps + warp;
-  const int i0 = (int)(A.V * w / W), i1 = (int)(A.V * (w + 1) / W);
-  double total = 0.0, before = 0.0, mine = 0.0;
+  constexpr int W = kCluster * kWarps;
+  const int w = (int)rank * kWarps + warp;
+  const int i0 = (int)((long long)A.V * w / W), i1 = (int)((long long)A.V * (w + 1) / W);
   for (int again = 0; again < 2; ++again) {
-    float hi = 0.0f, lo = 0.0f;
-#pragma unroll 8
-    for (int i = i0 + lane; i < i1; i += 32) add(hi, lo, R.at(i));
-    const double s = warp_sum((double)hi + (double)lo);
+    const double s = warp_sum(R.q ? lane_mass<true>(R, i0, i1, lane) : lane_mass<false>(R, i0, i1, lane));
     if (lane == 0) s_warp[warp] = s;
-    __syncthreads();
-    if (tid == 0) {
-      double x = 0.0;
-      for (int j = 0; j < kWarps; ++j) x += s_warp[j];
-      s_total = x;
-    }
     cluster_sync();
-    total = before = 0.0;
-    for (uint32_t r = 0; r < kCluster; ++r) {
-      const double x = ld_cluster(&s_total, r);
-      if (r < rank) before += x;
-      if (r == rank) mine = x;
-      total += x;
+    if (warp == 0) {
+      // the share that holds the drawn point: the first whose running sum
+      // exceeds it, else (the sums' last bits) the last that has any mass.
+      // Two shares to a lane; every CTA finds the same.
+      static_assert(W == 64, "two shares to a lane");
+      const double x0 = ld_cluster(&s_warp[(2 * lane) % kWarps], 2 * lane / kWarps);
+      const double x1 = ld_cluster(&s_warp[(2 * lane + 1) % kWarps], (2 * lane + 1) / kWarps);
+      double incl = x0 + x1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const double total = __shfl_sync(0xffffffffu, incl, 31);
+      const double spot = (double)u_draw * total, before = incl - (x0 + x1);
+      const bool h0 = x0 > 0.0 && before + x0 > spot, h1 = x1 > 0.0 && incl > spot;
+      const unsigned hit = __ballot_sync(0xffffffffu, h0 || h1), mass = __ballot_sync(0xffffffffu, x0 > 0.0 || x1 > 0.0);
+      int pick = -1;
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        pick = 2 * l + (__shfl_sync(0xffffffffu, (int)h0, l) ? 0 : 1);
+      } else if (mass) {
+        const int l = 31 - __clz(mass);
+        pick = 2 * l + (__shfl_sync(0xffffffffu, (int)(x1 > 0.0), l) ? 1 : 0);
+      }
+      const double at = __shfl_sync(0xffffffffu, (pick & 1) ? before + x0 : before, max(pick, 0) / 2);
+      if (lane == 0) {
+        s_pick = pick;
+        s_at = at;
+        s_spot = spot;
+      }
     }
-    if (total > 0.0 || !refused) break;  // the same for every CTA
+    __syncthreads();
+    if (s_pick >= 0 || !refused || again) break;  // the same for every CTA
     cluster_sync();  // every CTA has read the sums that the next pass overwrites
-    R.q = nullptr;  // no mass is left: draw from the target itself
+    R.q = nullptr;   // no mass is left: draw from the target itself
     R.taken = -1;
   }
-
-  // ---- the CTA that holds the drawn point: the first whose running sum
-  // exceeds it, else (the sums' last bits) the last that has any mass
-  const double spot = (double)A.uniform[b * A.T + A.T - 1] * total;
-  int owner = -1, last = -1;
-  {
-    double run = 0.0;
-    for (uint32_t r = 0; r < kCluster; ++r) {
-      const double x = ld_cluster(&s_total, r);
-      run += x;
-      if (x > 0.0) {
-        last = (int)r;
-        if (owner < 0 && run > spot) owner = (int)r;
-      }
-    }
-    if (owner < 0) owner = last;
-  }
+  const int pick = s_pick;
+  const double spot = s_spot, pick_at = s_at;
   if (rank == 0 && tid == 0) {
     A.accept_len[b] = kept + 1;
-    if (owner < 0) A.next[b] = -1;  // no mass at all
+    if (pick < 0) A.next[b] = -1;  // no mass at all
   }
-  if (owner == (int)rank) {
-    // the warp's share, by the same rule
-    double run = before;
-    int pick = -1, tail = -1;
-    double pick_at = 0.0, tail_at = 0.0;
-    for (int j = 0; j < kWarps; ++j) {
-      const double x = s_warp[j];
-      if (x > 0.0) {
-        tail = j;
-        tail_at = run;
-        if (pick < 0 && run + x > spot) {
-          pick = j;
-          pick_at = run;
-        }
-      }
-      run += x;
-    }
-    if (pick < 0) {
-      pick = tail;
-      pick_at = tail_at;
-    }
+  cluster_sync_arrive();  // this CTA no longer reads the others' sums
+  if (pick >= 0 && pick / kWarps == (int)rank) {
     // its tokens, a contiguous run for each thread of the CTA
-    const long long v = (long long)rank * kWarps + pick;
-    const int j0 = (int)(A.V * v / W), j1 = (int)(A.V * (v + 1) / W);
+    const int j0 = (int)((long long)A.V * pick / W), j1 = (int)((long long)A.V * (pick + 1) / W);
     const int per = (j1 - j0 + kThreads - 1) / kThreads;
     const int a = min(j0 + tid * per, j1), z = min(a + per, j1);
     double s = 0.0;
@@ -213,11 +218,10 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
       const double x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    __syncthreads();  // s_warp has been read
-    if (lane == 31) s_warp[warp] = incl;
+    if (lane == 31) s_part[warp] = incl;
     __syncthreads();
     double at = pick_at + incl - s;
-    for (int j = 0; j < warp; ++j) at += s_warp[j];
+    for (int j = 0; j < warp; ++j) at += s_part[j];
     // the lowest token whose running sum exceeds the point, else the last with mass
     int found = 0x7fffffff, heavy = -1;
     for (int i = a; i < z; ++i) {
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
       A.next[b] = found < 0x7fffffff ? found : heavy;
     }
   }
-  cluster_sync();  // no CTA leaves while another reads its sums
+  cluster_sync_wait();  // no CTA leaves while another reads its sums
 }
 
 }  // namespace accept

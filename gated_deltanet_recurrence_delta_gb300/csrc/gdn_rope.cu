@@ -9,7 +9,7 @@
 //
 // Memory-bound: every element is read and written once, 4 bytes for ~8 flops.
 // A head lies over D/8 lanes of a warp, 16 bytes per lane, so a warp load
-// covers 32/(D/8) heads and the norm is a shuffle over the head's lanes. The
+// covers 32/(D/8) heads and the norm is a sum over the head's lanes. The
 // angles depend on the token only: a warp forms its lanes' cosines and sines
 // once and applies them to all the heads it takes of that token.
 //
@@ -55,10 +55,15 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // vectors a lane has in flight
+constexpr int kBatch = 4;  // heads a lane has in flight
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ Args A) {
+// A lane holds 8 channels of a head as two groups of four, lo and hi:
+//   pairs (i, i + rot/2): lane c < rot/8 takes channels 4c.. and rot/2 + 4c..,
+//     so both halves of its four pairs are its own and no shuffle moves them;
+//   adjacent pairs, and channels that do not rotate: channels 8c.. in a row.
+// Either way a lane has four angles.
+template <int D, bool ADJ>
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_constant__ Args A) {
   constexpr int LPH = D / 8, HPI = 32 / LPH;  // lanes of a head, heads of one warp load
   __shared__ uint64_t s_freq[D / 2];
   __shared__ uint8_t s_axis[D / 2];
@@ -76,15 +81,29 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     s_axis[tid] = (uint8_t)a;
   }
   __syncthreads();
-  const int c = lane % LPH, sub = lane / LPH;  // 16-byte chunk of the head, head of the load
+  const int c = lane % LPH, sub = lane / LPH;  // this lane's place in the head, the head's place in the load
   const bool rotates = c * 8 < A.rot;
-  // the pair's other channel: in this lane (adjacent pairs) or in lane `other`
-  const bool upper = !A.adjacent && c * 8 >= half;
-  const int other = !rotates || A.adjacent ? lane : lane + (upper ? -1 : 1) * (A.rot / 16);
-  float wq[8], wk[8];
+  const int lo = !ADJ && rotates ? 4 * c : 8 * c, hi = !ADJ && rotates ? half + 4 * c : 8 * c + 4;
+  auto load = [&](const bf16 *p) {  // 16 bytes of a head
+    uint4 x;
+    if (ADJ) {
+      x = *reinterpret_cast<const uint4 *>(p + lo);
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2 *>(p + lo), b = *reinterpret_cast<const uint2 *>(p + hi);
+      x = make_uint4(a.x, a.y, b.x, b.y);
+    }
+    return x;
+  };
+  auto store = [&](bf16 *p, uint4 x) {
+    if (ADJ) {
+      *reinterpret_cast<uint4 *>(p + lo) = x;
+    } else {
+      *reinterpret_cast<uint2 *>(p + lo) = make_uint2(x.x, x.y);
+      *reinterpret_cast<uint2 *>(p + hi) = make_uint2(x.z, x.w);
+    }
+  };
   const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-  unpack8(A.qw ? reinterpret_cast<const uint4 *>(A.qw)[c] : ones, wq);
-  unpack8(A.kw ? reinterpret_cast<const uint4 *>(A.kw)[c] : ones, wk);
+  const uint4 wq = A.qw ? load(A.qw) : ones, wk = A.kw ? load(A.kw) : ones;
 
   const long long units = (long long)A.n * A.slices, stride = (long long)gridDim.x * (kThreads / 32);
   for (long long u = (long long)blockIdx.x * (kThreads / 32) + (tid >> 5); u < units; u += stride) {
@@ -97,46 +116,36 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       if (lane == 0) set_status(A.status, GDN_ERR_INDEX);
       row = -1;
     }
-    float cs[8], sn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cs[e] = 1.0f;
-      sn[e] = 0.0f;
-    }
+    float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (rotates) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = A.adjacent ? c * 4 + (e >> 1) : c * 8 + e - (upper ? half : 0);
+      for (int e = 0; e < 4; ++e) {
+        const int i = 4 * c + e;
         const uint64_t turns = (uint64_t)(int64_t)A.pos[(long long)s_axis[i] * A.n + t] * s_freq[i];
         sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31: half turns
       }
-      // the second channel of a pair takes +sin of the first, the first -sin of the second
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (A.adjacent ? !(e & 1) : !upper) sn[e] = -sn[e];
     }
     for (int r = r0; r < r1; r += kBatch) {
       uint4 x[kBatch];
-      const bf16 *src[kBatch];
-      bf16 *dst[kBatch];
-      int kind[kBatch];  // 0 q, 1 k, 2 v, 3 nothing
+      // head h of q | k | v: 0 q, 1 k, 2 v, 3 none
+      auto kind_of = [&](int h, bool in) {
+        const int k = !in ? 3 : h < A.hq ? 0 : h < A.hq + A.hk ? 1 : (h < A.hq + 2 * A.hk && A.v) ? 2 : 3;
+        return (k == 1 || k == 2) && row < 0 ? 3 : k;
+      };
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int h = (r + j) * HPI + sub;
-        kind[j] = r + j >= r1 ? 3 : h < A.hq ? 0 : h < A.hq + A.hk ? 1 : (h < A.hq + 2 * A.hk && A.v) ? 2 : 3;
-        if ((kind[j] == 1 || kind[j] == 2) && row < 0) kind[j] = 3;
-        const int g = kind[j] == 0 ? h : kind[j] == 1 ? h - A.hq : h - A.hq - A.hk;
-        src[j] = (kind[j] == 0 ? A.q + t * A.qs : kind[j] == 1 ? A.k + t * A.ks : A.v + t * A.vs) + (long long)g * D + c * 8;
-        dst[j] = (kind[j] == 0   ? A.qo + (t * A.hq + g) * D
-                  : kind[j] == 1 ? A.ko + (row * A.hk + g) * D
-                                 : A.vo + (row * A.hk + g) * D) +
-                 c * 8;
-        x[j] = kind[j] < 3 ? *reinterpret_cast<const uint4 *>(src[j]) : make_uint4(0, 0, 0, 0);
+        const int h = (r + j) * HPI + sub, kind = kind_of(h, r + j < r1);
+        const bf16 *src = kind == 0   ? A.q + t * A.qs + h * D
+                          : kind == 1 ? A.k + t * A.ks + (h - A.hq) * D
+                                      : A.v + t * A.vs + (h - A.hq - A.hk) * D;
+        x[j] = kind < 3 ? load(src) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        float y[8];
+        const int h = (r + j) * HPI + sub, kind = kind_of(h, r + j < r1);
+        float y[8], w[8];
         unpack8(x[j], y);
+        unpack8(kind == 0 ? wq : wk, w);
         float ss = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
@@ -144,14 +153,18 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float inv = rsqrtf(ss * (1.0f / D) + A.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= inv * (kind[j] == 0 ? wq[e] : wk[e]);
+        for (int e = 0; e < 8; ++e) y[e] *= inv * w[e];
         float z[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float far = __shfl_sync(0xffffffffu, y[e], other);
-          z[e] = fmaf(y[e], cs[e], (A.adjacent ? y[e ^ 1] : far) * sn[e]);
+        for (int e = 0; e < 4; ++e) {
+          const int a = ADJ ? 2 * e : e, b = ADJ ? 2 * e + 1 : e + 4;
+          z[a] = y[a] * cs[e] - y[b] * sn[e];
+          z[b] = y[b] * cs[e] + y[a] * sn[e];
         }
-        if (kind[j] < 3) *reinterpret_cast<uint4 *>(dst[j]) = kind[j] == 2 ? x[j] : pack8(z);
+        bf16 *dst = kind == 0   ? A.qo + (t * A.hq + h) * D
+                    : kind == 1 ? A.ko + (row * A.hk + h - A.hq) * D
+                                : A.vo + (row * A.hk + h - A.hq - A.hk) * D;
+        if (kind < 3) store(dst, kind == 2 ? x[j] : pack8(z));
       }
     }
   }
@@ -232,10 +245,11 @@ extern "C" gdn_status gdn_head_norm_rope(const gdn_rope_dims *d, const void *q, 
   const long long want = (long long)dev->sms * 32 / A.n;
   A.slices = (int)(want < 1 ? 1 : want > A.items ? A.items : want);
   const long long ctas = ((long long)A.n * A.slices + 7) / 8;
-  const dim3 grid((unsigned)(ctas < dev->sms * 4 ? ctas : dev->sms * 4));
+  const dim3 grid((unsigned)(ctas < dev->sms * 3 ? ctas : dev->sms * 3));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (D == 64) launch_pdl(rope::norm_rope_kernel<64>, grid, dim3(rope::kThreads), 0, st, A);
-  if (D == 128) launch_pdl(rope::norm_rope_kernel<128>, grid, dim3(rope::kThreads), 0, st, A);
-  if (D == 256) launch_pdl(rope::norm_rope_kernel<256>, grid, dim3(rope::kThreads), 0, st, A);
+  const dim3 block(rope::kThreads);
+  if (D == 64) launch_pdl(A.adjacent ? rope::norm_rope_kernel<64, true> : rope::norm_rope_kernel<64, false>, grid, block, 0, st, A);
+  if (D == 128) launch_pdl(A.adjacent ? rope::norm_rope_kernel<128, true> : rope::norm_rope_kernel<128, false>, grid, block, 0, st, A);
+  if (D == 256) launch_pdl(A.adjacent ? rope::norm_rope_kernel<256, true> : rope::norm_rope_kernel<256, false>, grid, block, 0, st, A);
   return check_launch("head_norm_rope");
 }
