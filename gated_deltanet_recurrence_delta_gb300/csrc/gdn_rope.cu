@@ -11,7 +11,8 @@
 // A head lies over D/8 lanes of a warp, 16 bytes per lane, so a warp load
 // covers 32/(D/8) heads and the norm is a sum over the head's lanes. The
 // angles depend on the token only: a warp forms its lanes' cosines and sines
-// once and applies them to all the heads it takes of that token.
+// once and applies them to all the heads it takes of that token. The next four
+// heads' loads are in flight while four are computed.
 //
 // Angles: positions reach 2^31 while the result needs ~2^-20 of a turn, so the
 // turns pos * inv_freq / (2 pi) modulo 1 are formed in 64-bit fixed point:
@@ -63,7 +64,7 @@ constexpr int kBatch = 4;  // heads a lane has in flight
 //   adjacent pairs, and channels that do not rotate: channels 8c.. in a row.
 // Either way a lane has four angles.
 template <int D, bool ADJ>
-__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const __grid_constant__ Args A) {
   constexpr int LPH = D / 8, HPI = 32 / LPH;  // lanes of a head, heads of one warp load
   __shared__ uint64_t s_freq[D / 2];
   __shared__ uint8_t s_axis[D / 2];
@@ -104,69 +105,120 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_con
   };
   const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
   const uint4 wq = A.qw ? load(A.qw) : ones, wk = A.kw ? load(A.kw) : ones;
+  const int nq = (A.hq + HPI - 1) / HPI, nk = (A.hk + HPI - 1) / HPI;  // rounds of q, of k, of v
 
-  const long long units = (long long)A.n * A.slices, stride = (long long)gridDim.x * (kThreads / 32);
-  for (long long u = (long long)blockIdx.x * (kThreads / 32) + (tid >> 5); u < units; u += stride) {
-    const long long t = u / A.slices;
-    const int slice = (int)(u - t * A.slices);
-    // loads of one warp: heads q | k | v in rounds of HPI; this slice's rounds
-    const int r0 = (int)((long long)A.items * slice / A.slices), r1 = (int)((long long)A.items * (slice + 1) / A.slices);
-    long long row = A.kv_index ? A.kv_index[t] : t;
-    if (row < -1 || row >= A.kv_rows) {
-      if (lane == 0) set_status(A.status, GDN_ERR_INDEX);
-      row = -1;
+  // This warp's batches one after the other: token t, rounds [r, min(r + kBatch, r1)).
+  struct Cursor {
+    unsigned u;
+    int t, r, r1;
+  };
+  const unsigned units = (unsigned)A.n * (unsigned)A.slices, stride = gridDim.x * (kThreads / 32);
+  auto enter = [&](Cursor &x) {  // the first batch of unit u: a token, or a slice of its rounds
+    if (x.u >= units) return;
+    x.t = (int)(x.u / (unsigned)A.slices);
+    const int slice = (int)(x.u - (unsigned)x.t * (unsigned)A.slices);
+    x.r = A.items * slice / A.slices;
+    x.r1 = A.items * (slice + 1) / A.slices;
+  };
+  auto advance = [&](Cursor &x) {
+    x.r += kBatch;
+    if (x.r >= x.r1) {
+      x.u += stride;
+      enter(x);
     }
-    float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (rotates) {
+  };
+  // Round r: heads of one kind (0 q, 1 k, 2 v), this lane's among them
+  auto kind_of = [&](int r) { return r < nq ? 0 : r < nq + nk ? 1 : 2; };
+  auto head_of = [&](int r) { return (r < nq ? r : r < nq + nk ? r - nq : r - nq - nk) * HPI + sub; };
+  auto fetch = [&](const Cursor &x, uint4 (&v)[kBatch]) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = x.r + j, kind = kind_of(r), h = head_of(r);
+      const bf16 *src = kind == 0 ? A.q + x.t * A.qs : kind == 1 ? A.k + x.t * A.ks : A.v + x.t * A.vs;
+      v[j] = r < x.r1 && h < (kind == 0 ? A.hq : A.hk) ? load(src + h * D) : make_uint4(0, 0, 0, 0);
+    }
+  };
+
+  Cursor cur = {blockIdx.x * (kThreads / 32) + (tid >> 5), 0, 0, 0};
+  if (cur.u >= units) return;
+  enter(cur);
+  uint4 x[kBatch], ahead[kBatch];
+  fetch(cur, x);
+  int seen = -1, coef_kind = -1;
+  long long row = 0;
+  float cs[4], sn[4];
+  // z_a = (x_a ca - x_b sb) / rms, z_b = (x_b cb + x_a sa) / rms, with the weights in the coefficients
+  float ca[4], cb[4], sa[4], sb[4];
+  while (cur.u < units) {
+    Cursor next = cur;
+    advance(next);
+    if (next.u < units) fetch(next, ahead);  // in flight while this batch is computed
+    if (cur.t != seen) {
+      seen = cur.t;
+      coef_kind = -1;
+      row = A.kv_index ? A.kv_index[cur.t] : cur.t;
+      if (row < -1 || row >= A.kv_rows) {
+        if (lane == 0) set_status(A.status, GDN_ERR_INDEX);
+        row = -1;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = 4 * c + e;
-        const uint64_t turns = (uint64_t)(int64_t)A.pos[(long long)s_axis[i] * A.n + t] * s_freq[i];
-        sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31: half turns
+        cs[e] = 1.0f;
+        sn[e] = 0.0f;
+      }
+      if (rotates) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * c + e;
+          const uint64_t turns = (uint64_t)(int64_t)A.pos[(long long)s_axis[i] * A.n + cur.t] * s_freq[i];
+          sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31: half turns
+        }
       }
     }
-    for (int r = r0; r < r1; r += kBatch) {
-      uint4 x[kBatch];
-      // head h of q | k | v: 0 q, 1 k, 2 v, 3 none
-      auto kind_of = [&](int h, bool in) {
-        const int k = !in ? 3 : h < A.hq ? 0 : h < A.hq + A.hk ? 1 : (h < A.hq + 2 * A.hk && A.v) ? 2 : 3;
-        return (k == 1 || k == 2) && row < 0 ? 3 : k;
-      };
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int h = (r + j) * HPI + sub, kind = kind_of(h, r + j < r1);
-        const bf16 *src = kind == 0   ? A.q + t * A.qs + h * D
-                          : kind == 1 ? A.k + t * A.ks + (h - A.hq) * D
-                                      : A.v + t * A.vs + (h - A.hq - A.hk) * D;
-        x[j] = kind < 3 ? load(src) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = cur.r + j, kind = kind_of(r), h = head_of(r);
+      if (r >= cur.r1) break;  // the same for the warp
+      if (kind == 2) {
+        if (h < A.hk && row >= 0) store(A.vo + (row * A.hk + h) * D, x[j]);
+        continue;
       }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int h = (r + j) * HPI + sub, kind = kind_of(h, r + j < r1);
-        float y[8], w[8];
-        unpack8(x[j], y);
+      if (kind != coef_kind) {
+        coef_kind = kind;
+        float w[8];
         unpack8(kind == 0 ? wq : wk, w);
-        float ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(ss * (1.0f / D) + A.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= inv * w[e];
-        float z[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int a = ADJ ? 2 * e : e, b = ADJ ? 2 * e + 1 : e + 4;
-          z[a] = y[a] * cs[e] - y[b] * sn[e];
-          z[b] = y[b] * cs[e] + y[a] * sn[e];
+          ca[e] = w[a] * cs[e];
+          cb[e] = w[b] * cs[e];
+          sa[e] = w[a] * sn[e];
+          sb[e] = w[b] * sn[e];
         }
-        bf16 *dst = kind == 0   ? A.qo + (t * A.hq + h) * D
-                    : kind == 1 ? A.ko + (row * A.hk + h - A.hq) * D
-                                : A.vo + (row * A.hk + h - A.hq - A.hk) * D;
-        if (kind < 3) store(dst, kind == 2 ? x[j] : pack8(z));
+      }
+      float y[8], z[8];
+      unpack8(x[j], y);
+      float ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = rsqrtf(ss * (1.0f / D) + A.eps);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int a = ADJ ? 2 * e : e, b = ADJ ? 2 * e + 1 : e + 4;
+        z[a] = (y[a] * ca[e] - y[b] * sb[e]) * inv;
+        z[b] = (y[b] * cb[e] + y[a] * sa[e]) * inv;
+      }
+      if (kind == 0) {
+        if (h < A.hq) store(A.qo + ((long long)cur.t * A.hq + h) * D, pack8(z));
+      } else if (h < A.hk && row >= 0) {
+        store(A.ko + (row * A.hk + h) * D, pack8(z));
       }
     }
+    cur = next;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) x[j] = ahead[j];
   }
 }
 
@@ -240,12 +292,12 @@ extern "C" gdn_status gdn_head_norm_rope(const gdn_rope_dims *d, const void *q, 
   A.vo = static_cast<bf16 *>(v_out);
   A.status = dev->status;
   const int per_load = 32 / (D / 8);
-  A.items = (A.hq + (v ? 2 : 1) * A.hk + per_load - 1) / per_load;
+  A.items = (A.hq + per_load - 1) / per_load + (v ? 2 : 1) * ((A.hk + per_load - 1) / per_load);
   // a token's heads go to several warps where the tokens alone would leave SMs idle
   const long long want = (long long)dev->sms * 32 / A.n;
   A.slices = (int)(want < 1 ? 1 : want > A.items ? A.items : want);
   const long long ctas = ((long long)A.n * A.slices + 7) / 8;
-  const dim3 grid((unsigned)(ctas < dev->sms * 3 ? ctas : dev->sms * 3));
+  const dim3 grid((unsigned)(ctas < dev->sms * 2 ? ctas : dev->sms * 2));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 block(rope::kThreads);
   if (D == 64) launch_pdl(A.adjacent ? rope::norm_rope_kernel<64, true> : rope::norm_rope_kernel<64, false>, grid, block, 0, st, A);
