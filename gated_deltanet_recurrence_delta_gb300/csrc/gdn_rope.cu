@@ -37,22 +37,33 @@ struct Args {
   unsigned int *status;
 };
 
-__device__ __forceinline__ void unpack8(uint4 u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Two fp32 in one register pair, and the paired instructions.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ float2 halves(f2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 unpack2(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t pack2(f2 x) {
+  const float2 v = halves(x);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 constexpr int kThreads = 256;
@@ -105,38 +116,35 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const __grid_con
   };
   const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
   const uint4 wq = A.qw ? load(A.qw) : ones, wk = A.kw ? load(A.kw) : ones;
-  const int nq = (A.hq + HPI - 1) / HPI, nk = (A.hk + HPI - 1) / HPI;  // rounds of q, of k, of v
-
-  // This warp's batches one after the other: token t, rounds [r, min(r + kBatch, r1)).
-  struct Cursor {
+  // A token's batches of up to kBatch loads, each of one kind: q, then k, then v.
+  constexpr int HPB = HPI * kBatch;  // heads of a batch
+  const int bq = (A.hq + HPB - 1) / HPB, bk = (A.hk + HPB - 1) / HPB;
+  struct Cursor {  // batch b of token t, up to b1
     unsigned u;
-    int t, r, r1;
+    int t, b, b1;
   };
   const unsigned units = (unsigned)A.n * (unsigned)A.slices, stride = gridDim.x * (kThreads / 32);
-  auto enter = [&](Cursor &x) {  // the first batch of unit u: a token, or a slice of its rounds
+  auto enter = [&](Cursor &x) {  // the first batch of unit u: a token, or a slice of its batches
     if (x.u >= units) return;
     x.t = (int)(x.u / (unsigned)A.slices);
     const int slice = (int)(x.u - (unsigned)x.t * (unsigned)A.slices);
-    x.r = A.items * slice / A.slices;
-    x.r1 = A.items * (slice + 1) / A.slices;
+    x.b = A.items * slice / A.slices;
+    x.b1 = A.items * (slice + 1) / A.slices;
   };
   auto advance = [&](Cursor &x) {
-    x.r += kBatch;
-    if (x.r >= x.r1) {
+    if (++x.b >= x.b1) {
       x.u += stride;
       enter(x);
     }
   };
-  // Round r: heads of one kind (0 q, 1 k, 2 v), this lane's among them
-  auto kind_of = [&](int r) { return r < nq ? 0 : r < nq + nk ? 1 : 2; };
-  auto head_of = [&](int r) { return (r < nq ? r : r < nq + nk ? r - nq : r - nq - nk) * HPI + sub; };
+  auto kind_of = [&](int b) { return b < bq ? 0 : b < bq + bk ? 1 : 2; };
+  auto head_of = [&](int b) { return (b < bq ? b : b < bq + bk ? b - bq : b - bq - bk) * HPB + sub; };
   auto fetch = [&](const Cursor &x, uint4 (&v)[kBatch]) {
+    const int kind = kind_of(x.b), h = head_of(x.b), heads = kind == 0 ? A.hq : A.hk;
+    const bf16 *src = (kind == 0 ? A.q + x.t * A.qs : kind == 1 ? A.k + x.t * A.ks : A.v + x.t * A.vs) + h * D;
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int r = x.r + j, kind = kind_of(r), h = head_of(r);
-      const bf16 *src = kind == 0 ? A.q + x.t * A.qs : kind == 1 ? A.k + x.t * A.ks : A.v + x.t * A.vs;
-      v[j] = r < x.r1 && h < (kind == 0 ? A.hq : A.hk) ? load(src + h * D) : make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < kBatch; ++j)
+      v[j] = h + j * HPI < heads ? load(src + j * HPI * D) : make_uint4(0, 0, 0, 0);
   };
 
   Cursor cur = {blockIdx.x * (kThreads / 32) + (tid >> 5), 0, 0, 0};
@@ -147,8 +155,9 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const __grid_con
   int seen = -1, coef_kind = -1;
   long long row = 0;
   float cs[4], sn[4];
-  // z_a = (x_a ca - x_b sb) / rms, z_b = (x_b cb + x_a sa) / rms, with the weights in the coefficients
-  float ca[4], cb[4], sa[4], sb[4];
+  // pair k of the results is (own pair k) P_k + (partner) Q_k, over the rms: the weights are in the coefficients.
+  // Adjacent pairs: the partner is the pair itself, swapped; else pair k ^ 2.
+  f2 P[4], Q[4];
   while (cur.u < units) {
     Cursor next = cur;
     advance(next);
@@ -175,45 +184,52 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const __grid_con
         }
       }
     }
+    const int kind = kind_of(cur.b), h0 = head_of(cur.b), heads = kind == 0 ? A.hq : A.hk;
+    bf16 *dst = (kind == 0 ? A.qo + (long long)cur.t * A.hq * D : (kind == 1 ? A.ko : A.vo) + row * A.hk * D) + h0 * D;
+    const bool kept = kind == 0 || row >= 0;
+    if (kind == 2) {
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int r = cur.r + j, kind = kind_of(r), h = head_of(r);
-      if (r >= cur.r1) break;  // the same for the warp
-      if (kind == 2) {
-        if (h < A.hk && row >= 0) store(A.vo + (row * A.hk + h) * D, x[j]);
-        continue;
-      }
+      for (int j = 0; j < kBatch; ++j)
+        if (kept && h0 + j * HPI < heads) store(dst + j * HPI * D, x[j]);
+    } else {
       if (kind != coef_kind) {
         coef_kind = kind;
-        float w[8];
-        unpack8(kind == 0 ? wq : wk, w);
+        const uint4 wv = kind == 0 ? wq : wk;
+        const f2 w[4] = {unpack2(wv.x), unpack2(wv.y), unpack2(wv.z), unpack2(wv.w)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int a = ADJ ? 2 * e : e, b = ADJ ? 2 * e + 1 : e + 4;
-          ca[e] = w[a] * cs[e];
-          cb[e] = w[b] * cs[e];
-          sa[e] = w[a] * sn[e];
-          sb[e] = w[b] * sn[e];
+        for (int k = 0; k < 4; ++k) {
+          // (y0, y1) -> (y0 cos - y1 sin, y1 cos + y0 sin), y = x w
+          if (ADJ) {
+            const float2 v = halves(w[k]);
+            P[k] = mul2(w[k], pair(cs[k], cs[k]));
+            Q[k] = mul2(pair(v.y, v.x), pair(-sn[k], sn[k]));
+          } else {
+            const int e = 2 * (k & 1);
+            P[k] = mul2(w[k], pair(cs[e], cs[e + 1]));
+            Q[k] = mul2(w[k ^ 2], k < 2 ? pair(-sn[e], -sn[e + 1]) : pair(sn[e], sn[e + 1]));
+          }
         }
       }
-      float y[8], z[8];
-      unpack8(x[j], y);
-      float ss = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+      for (int j = 0; j < kBatch; ++j) {
+        const f2 y[4] = {unpack2(x[j].x), unpack2(x[j].y), unpack2(x[j].z), unpack2(x[j].w)};
+        const float2 sq = halves(fma2(y[3], y[3], fma2(y[2], y[2], fma2(y[1], y[1], mul2(y[0], y[0])))));
+        float ss = sq.x + sq.y;
 #pragma unroll
-      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float inv = rsqrtf(ss * (1.0f / D) + A.eps);
+        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = rsqrtf(ss * (1.0f / D) + A.eps);
+        const f2 scale = pair(inv, inv);
+        uint32_t z[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int a = ADJ ? 2 * e : e, b = ADJ ? 2 * e + 1 : e + 4;
-        z[a] = (y[a] * ca[e] - y[b] * sb[e]) * inv;
-        z[b] = (y[b] * cb[e] + y[a] * sa[e]) * inv;
-      }
-      if (kind == 0) {
-        if (h < A.hq) store(A.qo + ((long long)cur.t * A.hq + h) * D, pack8(z));
-      } else if (h < A.hk && row >= 0) {
-        store(A.ko + (row * A.hk + h) * D, pack8(z));
+        for (int k = 0; k < 4; ++k) {
+          f2 far = y[k ^ 2];
+          if (ADJ) {
+            const float2 v = halves(y[k]);
+            far = pair(v.y, v.x);
+          }
+          z[k] = pack2(mul2(fma2(y[k], P[k], mul2(far, Q[k])), scale));
+        }
+        if (kept && h0 + j * HPI < heads) store(dst + j * HPI * D, make_uint4(z[0], z[1], z[2], z[3]));
       }
     }
     cur = next;
@@ -291,8 +307,8 @@ extern "C" gdn_status gdn_head_norm_rope(const gdn_rope_dims *d, const void *q, 
   A.ko = static_cast<bf16 *>(k_out);
   A.vo = static_cast<bf16 *>(v_out);
   A.status = dev->status;
-  const int per_load = 32 / (D / 8);
-  A.items = (A.hq + per_load - 1) / per_load + (v ? 2 : 1) * ((A.hk + per_load - 1) / per_load);
+  const int per_batch = 32 / (D / 8) * rope::kBatch;
+  A.items = (A.hq + per_batch - 1) / per_batch + (v ? 2 : 1) * ((A.hk + per_batch - 1) / per_batch);
   // a token's heads go to several warps where the tokens alone would leave SMs idle
   const long long want = (long long)dev->sms * 32 / A.n;
   A.slices = (int)(want < 1 ? 1 : want > A.items ? A.items : want);
