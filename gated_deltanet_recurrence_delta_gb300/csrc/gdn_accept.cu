@@ -14,7 +14,7 @@
 // vocabulary, a share for each of its warps, the 64 shares' sums meet in
 // distributed shared memory, and the CTA whose share holds the drawn point
 // finds the index in it. The drawn index is a comparison of
-// running sums, so sums are carried as two floats (~48 bits): plain fp32 sums
+// running sums, so sums are carried as two floats (~46 bits): plain fp32 sums
 // would move ~1% of the draws to a neighbouring token.
 #include "gdn_launch.h"
 
@@ -33,24 +33,54 @@ struct Args {
   unsigned int *status;
 };
 
-// The weight of a token: max(p - q, 0), or max(p, 0) without q; exact as hi + lo.
+// The weight of a token, max(p - q, 0), exact as hi + lo. Negative and NaN p
+// count as zero, a NaN q as no more than p. p >= q >= 0 makes the subtraction's
+// error (p - hi) - q exact.
 struct Weight {
   float hi, lo;
 };
 __device__ __forceinline__ Weight weight(float p, float q) {
+  p = fmaxf(p, 0.0f);
+  q = fminf(q, p);
   Weight w;
   w.hi = __fsub_rn(p, q);
-  const float b = __fsub_rn(p, w.hi);  // two-difference
-  w.lo = __fadd_rn(__fsub_rn(p, __fadd_rn(w.hi, b)), __fsub_rn(b, q));
-  if (!(p > q)) w.hi = w.lo = 0.0f;  // NaN counts as zero
+  w.lo = __fsub_rn(__fsub_rn(p, w.hi), q);
   return w;
 }
-// (hi, lo) += w, the rounding of the leading sum kept in lo
-__device__ __forceinline__ void add(float &hi, float &lo, Weight w) {
-  const float s = __fadd_rn(hi, w.hi), z = __fsub_rn(s, hi);
-  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, z)), __fsub_rn(w.hi, z));
-  hi = s;
-  lo = __fadd_rn(lo, __fadd_rn(e, w.lo));
+
+// A number as hi + lo, hi the nearest float: ~48 bits from the fp32 units. (The
+// chip's fp64 units do two operations a cycle per SM: sums in doubles took half
+// the kernel's time.)
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two plus(Two a, Two b) {
+  const float s = __fadd_rn(a.hi, b.hi), z = __fsub_rn(s, a.hi);
+  float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, z)), __fsub_rn(b.hi, z));
+  e = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+  const float h = __fadd_rn(s, e);
+  return {h, __fsub_rn(e, __fsub_rn(h, s))};
+}
+__device__ __forceinline__ bool above(Two a, Two b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+
+// A sum as two floats. hi starts at kBase, above every weight, so that each
+// addition's error w - (s - hi) is exact; lo collects the errors, which are
+// below 2^-22, to about 2^-46.
+constexpr float kBase = 2.0f;
+struct Sum {
+  float hi = kBase, lo = 0.0f;
+  __device__ __forceinline__ void add(Weight w) {
+    const float s = __fadd_rn(hi, w.hi);
+    const float e = __fsub_rn(w.hi, __fsub_rn(s, hi));
+    hi = s;
+    lo = __fadd_rn(lo, __fadd_rn(e, w.lo));
+  }
+  __device__ __forceinline__ Two value() const;
+};
+
+__device__ __forceinline__ Two Sum::value() const {
+  const float h = __fsub_rn(hi, kBase), s = __fadd_rn(h, lo);
+  return {s, __fsub_rn(lo, __fsub_rn(s, h))};
 }
 
 // The row that is drawn from. `taken`: a token whose draft probability is 1.
@@ -58,40 +88,75 @@ struct Row {
   const float *p, *q;
   int taken;
   __device__ __forceinline__ Weight at(int i) const {
-    return weight(p[i], q ? q[i] : i == taken ? 3.4e38f : 0.0f);
+    return weight(p[i], q ? q[i] : i == taken ? __int_as_float(0x7f800000) : 0.0f);
   }
 };
 
-// This lane's part of the mass of tokens [i0, i1): tokens i0 + lane, + 32, ... in batches of kBatch loads of each row.
-constexpr int kBatch = 8;
-template <bool TWO>
-__device__ __forceinline__ double lane_mass(const Row &R, int i0, int i1, int lane) {
-  float hi = 0.0f, lo = 0.0f;
-  int i = i0 + lane;
-  for (; i + 32 * (kBatch - 1) < i1; i += 32 * kBatch) {
-    float p[kBatch], q[kBatch];
+// This lane's part of the mass of tokens [i0, i1). TWO: a draft row beside the
+// target's; VEC: 16-byte loads (both rows' addresses leave the same rest to 16).
+template <bool TWO, bool VEC>
+__device__ __forceinline__ Two lane_mass(const Row &R, int i0, int i1, int lane) {
+  Sum sum[4];
+  if (VEC) {
+    const int a = min(i1, i0 + (int)(((16 - (reinterpret_cast<uintptr_t>(R.p + i0) & 15)) & 15) / 4));
+    if (i0 + lane < a) sum[0].add(R.at(i0 + lane));
+    const int z = a + (i1 - a) / 4 * 4;
+    constexpr int kBatch = 4;  // 16-byte loads of each row in flight
+    int i = a + 4 * lane;
+    for (; i + 128 * (kBatch - 1) < z; i += 128 * kBatch) {
+      float4 p[kBatch], q[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      p[k] = __ldcs(R.p + i + 32 * k);
-      q[k] = TWO ? __ldcs(R.q + i + 32 * k) : i + 32 * k == R.taken ? 3.4e38f : 0.0f;
+      for (int k = 0; k < kBatch; ++k) {
+        p[k] = __ldcs(reinterpret_cast<const float4 *>(R.p + i + 128 * k));
+        if (TWO) q[k] = __ldcs(reinterpret_cast<const float4 *>(R.q + i + 128 * k));
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        sum[0].add(weight(p[k].x, TWO ? q[k].x : 0.0f));
+        sum[1].add(weight(p[k].y, TWO ? q[k].y : 0.0f));
+        sum[2].add(weight(p[k].z, TWO ? q[k].z : 0.0f));
+        sum[3].add(weight(p[k].w, TWO ? q[k].w : 0.0f));
+      }
     }
+    for (; i < z; i += 128)
+      for (int k = 0; k < 4; ++k) sum[k].add(R.at(i + k));
+    if (z + lane < i1) sum[0].add(R.at(z + lane));
+  } else {
+    constexpr int kBatch = 8;
+    int i = i0 + lane;
+    for (; i + 32 * (kBatch - 1) < i1; i += 32 * kBatch) {
+      float p[kBatch], q[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) add(hi, lo, weight(p[k], q[k]));
+      for (int k = 0; k < kBatch; ++k) {
+        p[k] = __ldcs(R.p + i + 32 * k);
+        q[k] = TWO ? __ldcs(R.q + i + 32 * k) : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) sum[k & 3].add(weight(p[k], q[k]));
+    }
+    for (; i < i1; i += 32) sum[0].add(R.at(i));
   }
-  for (; i < i1; i += 32) add(hi, lo, R.at(i));
-  return (double)hi + (double)lo;
+  return plus(plus(sum[0].value(), sum[1].value()), plus(sum[2].value(), sum[3].value()));
 }
-
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ Two warp_sum(Two x) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = 16; o > 0; o >>= 1)
+    x = plus(x, {__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
   return x;
 }
-__device__ __forceinline__ double ld_cluster(const double *p, uint32_t rank) {
+__device__ __forceinline__ Two warp_scan(Two x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Two y = {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
+    if (lane >= o) x = plus(y, x);
+  }
+  return x;
+}
+__device__ __forceinline__ Two ld_cluster(const Two *p, uint32_t rank) {
   uint32_t a;
-  double v;
+  Two v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.hi), "=f"(v.lo) : "r"(a));
   return v;
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -103,7 +168,7 @@ __device__ __forceinline__ void cluster_sync_wait() { asm volatile("barrier.clus
 
 __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant__ Args A) {
   __shared__ int s_kept, s_bad, s_pick;
-  __shared__ double s_warp[kWarps], s_part[kWarps], s_at, s_spot;
+  __shared__ __align__(8) Two s_warp[kWarps], s_part[kWarps], s_at, s_spot;
   griddep_wait();
   griddep_trigger();
   uint32_t rank;
@@ -154,7 +219,15 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
   const int w = (int)rank * kWarps + warp;
   const int i0 = (int)((long long)A.V * w / W), i1 = (int)((long long)A.V * (w + 1) / W);
   for (int again = 0; again < 2; ++again) {
-    const double s = warp_sum(R.q ? lane_mass<true>(R, i0, i1, lane) : lane_mass<false>(R, i0, i1, lane));
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(R.p), qa = reinterpret_cast<uintptr_t>(R.q);
+    Two s;  // the branches are the same for a warp
+    if (R.q)
+      s = (pa & 15) == (qa & 15) ? lane_mass<true, true>(R, i0, i1, lane) : lane_mass<true, false>(R, i0, i1, lane);
+    else if (R.taken < i0 || R.taken >= i1)
+      s = lane_mass<false, true>(R, i0, i1, lane);
+    else  // around the taken token
+      s = plus(lane_mass<false, true>(R, i0, R.taken, lane), lane_mass<false, true>(R, R.taken + 1, i1, lane));
+    s = warp_sum(s);
     if (lane == 0) s_warp[warp] = s;
     cluster_sync();
     if (warp == 0) {
@@ -162,30 +235,29 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
       // exceeds it, else (the sums' last bits) the last that has any mass.
       // Two shares to a lane; every CTA finds the same.
       static_assert(W == 64, "two shares to a lane");
-      const double x0 = ld_cluster(&s_warp[(2 * lane) % kWarps], 2 * lane / kWarps);
-      const double x1 = ld_cluster(&s_warp[(2 * lane + 1) % kWarps], (2 * lane + 1) / kWarps);
-      double incl = x0 + x1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      const double total = __shfl_sync(0xffffffffu, incl, 31);
-      const double spot = (double)u_draw * total, before = incl - (x0 + x1);
-      const bool h0 = x0 > 0.0 && before + x0 > spot, h1 = x1 > 0.0 && incl > spot;
-      const unsigned hit = __ballot_sync(0xffffffffu, h0 || h1), mass = __ballot_sync(0xffffffffu, x0 > 0.0 || x1 > 0.0);
+      const Two x0 = ld_cluster(&s_warp[(2 * lane) % kWarps], 2 * lane / kWarps);
+      const Two x1 = ld_cluster(&s_warp[(2 * lane + 1) % kWarps], (2 * lane + 1) / kWarps);
+      const Two incl = warp_scan(plus(x0, x1), lane);
+      Two before = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+      if (lane == 0) before = {0.0f, 0.0f};
+      const Two mid = plus(before, x0);
+      const float th = __shfl_sync(0xffffffffu, incl.hi, 31), tl = __shfl_sync(0xffffffffu, incl.lo, 31);
+      const double at_mass = (double)u_draw * ((double)th + (double)tl);
+      const Two spot = {(float)at_mass, (float)(at_mass - (double)(float)at_mass)};
+      const bool h0 = x0.hi > 0.0f && above(mid, spot), h1 = x1.hi > 0.0f && above(incl, spot);
+      const unsigned hit = __ballot_sync(0xffffffffu, h0 || h1);
+      const unsigned mass = __ballot_sync(0xffffffffu, x0.hi > 0.0f || x1.hi > 0.0f);
       int pick = -1;
       if (hit) {
         const int l = __ffs(hit) - 1;
         pick = 2 * l + (__shfl_sync(0xffffffffu, (int)h0, l) ? 0 : 1);
       } else if (mass) {
         const int l = 31 - __clz(mass);
-        pick = 2 * l + (__shfl_sync(0xffffffffu, (int)(x1 > 0.0), l) ? 1 : 0);
+        pick = 2 * l + (__shfl_sync(0xffffffffu, (int)(x1.hi > 0.0f), l) ? 1 : 0);
       }
-      const double at = __shfl_sync(0xffffffffu, (pick & 1) ? before + x0 : before, max(pick, 0) / 2);
-      if (lane == 0) {
+      if (lane == max(pick, 0) / 2) {
         s_pick = pick;
-        s_at = at;
+        s_at = (pick & 1) ? mid : before;
         s_spot = spot;
       }
     }
@@ -196,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
     R.taken = -1;
   }
   const int pick = s_pick;
-  const double spot = s_spot, pick_at = s_at;
+  const Two spot = s_spot;
   if (rank == 0 && tid == 0) {
     A.accept_len[b] = kept + 1;
     if (pick < 0) A.next[b] = -1;  // no mass at all
@@ -207,29 +279,26 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
     const int j0 = (int)((long long)A.V * pick / W), j1 = (int)((long long)A.V * (pick + 1) / W);
     const int per = (j1 - j0 + kThreads - 1) / kThreads;
     const int a = min(j0 + tid * per, j1), z = min(a + per, j1);
-    double s = 0.0;
+    Two s = {0.0f, 0.0f};
     for (int i = a; i < z; ++i) {
       const Weight x = R.at(i);
-      s += (double)x.hi + (double)x.lo;
+      s = plus(s, {x.hi, x.lo});
     }
-    double incl = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
+    const Two incl = warp_scan(s, lane);
     if (lane == 31) s_part[warp] = incl;
     __syncthreads();
-    double at = pick_at + incl - s;
-    for (int j = 0; j < warp; ++j) at += s_part[j];
+    Two at = s_at;
+    for (int j = 0; j < warp; ++j) at = plus(at, s_part[j]);
+    const Two ahead = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+    if (lane > 0) at = plus(at, ahead);
     // the lowest token whose running sum exceeds the point, else the last with mass
     int found = 0x7fffffff, heavy = -1;
     for (int i = a; i < z; ++i) {
       const Weight x = R.at(i);
-      at += (double)x.hi + (double)x.lo;
+      at = plus(at, {x.hi, x.lo});
       if (x.hi > 0.0f) {
         heavy = i;
-        if (found == 0x7fffffff && at > spot) found = i;
+        if (found == 0x7fffffff && above(at, spot)) found = i;
       }
     }
     found = __reduce_min_sync(0xffffffffu, found);

@@ -502,7 +502,7 @@ size_t gdn_attn_workspace_size(const gdn_attn_dims *dims);
  * inverse distribution function at its random number: of max(target - draft, 0)
  * at a refusal (of the target where that has no mass), of the target after the
  * last token; the lowest index whose running sum exceeds the number times the
- * total. Sums carry about 48 bits. Weights that are negative or NaN count as
+ * total. Sums carry about 46 bits (of probabilities, which are at most 1). Weights that are negative or NaN count as
  * zero; a distribution without any mass gives -1. With several candidate paths
  * per sequence the winner that gdn_commit_accepted picks keeps the target's
  * distribution only for certain drafts and a one-hot target.

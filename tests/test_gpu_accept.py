@@ -1,7 +1,7 @@
 """gdn_accept_draft against the 64-bit form, token for token, and the commit that it feeds.
 
-Whole numbers have to be equal: the library's sums carry ~48 bits, so a draw can differ from exact arithmetic's only
-where the random number lies within V * 2^-46 of a boundary (1e-9 a draw at the sizes here)."""
+Whole numbers have to be equal: the library's sums carry ~46 bits, so a draw can differ from exact arithmetic's only
+where the random number lies within 2^-44 of one of V boundaries (1e-8 a draw at the sizes here)."""
 import pytest
 import torch
 
