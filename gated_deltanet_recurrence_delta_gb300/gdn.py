@@ -131,8 +131,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# torch.cuda.current_stream() builds a Stream object (3 us); a small call's kernel takes 5
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -273,25 +280,25 @@ def out_proj(o, w_out, y, stream=None):
     _check(load_library().gdn_out_proj(M, H, V, _ptr(o), _ptr(w_out), _ptr(y), _stream(stream)))
 
 
-def _token_stride(x, name):
-    """Elements between the tokens of x [..., heads, head_dim], whose heads lie together and whose tokens are
-    evenly spaced."""
-    shape, st = x.shape, x.stride()
-    if x.dtype != torch.bfloat16 or x.dim() not in (3, 4):
+def _layout(x, name):
+    """(tokens, heads, head_dim, elements between tokens) of a bf16 tensor [tokens, heads, head_dim] or
+    [rows, tokens, heads, head_dim] whose heads lie together and whose tokens are evenly spaced."""
+    if x.dtype is not torch.bfloat16 or x.dim() not in (3, 4):
         raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, head_dim] or [rows, tokens, heads, head_dim]")
-    if st[-1] != 1 or (st[-2] != shape[-1] and shape[-2] > 1) or (
-            x.dim() == 4 and shape[0] > 1 and st[0] != shape[1] * st[1]):
+    *lead, heads, d = x.shape
+    st = x.stride()
+    if st[-1] != 1 or (st[-2] != d and heads > 1) or (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * st[1]):
         raise ValueError(f"{name} must have dense heads and evenly spaced tokens")
-    return st[-3]
+    return (lead[0] if len(lead) == 1 else lead[0] * lead[1]), heads, d, st[-3]
 
 
 def make_rope_dims(q, k, rot_dim, n_axes=1, kv_rows=None, adjacent=False, eps=1e-6, v=None) -> RopeDims:
     """Sizes and token strides of a head_norm_rope call on q [n, Hq, d] and k [n, Hk, d]; v's tokens are spaced as
     k's unless v is given. kv_rows: rows of the pools (n when they hold the tokens themselves)."""
-    n = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
-    ks = _token_stride(k, "k")
-    return RopeDims(n, q.shape[-2], k.shape[-2], q.shape[-1], rot_dim, n_axes, int(adjacent), eps,
-                    _token_stride(q, "q"), ks, ks if v is None else _token_stride(v, "v"), n if kv_rows is None else kv_rows)
+    n, hq, d, qs = _layout(q, "q")
+    _, hk, _, ks = _layout(k, "k")
+    return RopeDims(n, hq, hk, d, rot_dim, n_axes, int(adjacent), eps, qs, ks, ks if v is None else _layout(v, "v")[3],
+                    n if kv_rows is None else kv_rows)
 
 
 def head_norm_rope(dims: RopeDims, q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out, v_out, axis=None,
@@ -307,10 +314,9 @@ def head_norm_rope(dims: RopeDims, q, k, v, q_weight, k_weight, positions, inv_f
 def make_attn_dims(q, k, B, T=1, n_groups=0, scale=None) -> AttnDims:
     """Sizes and strides of an attention call: q [n, Hq, d] or [B, T, Hq, d], k (and v, spaced alike) the pool
     [kv_rows, Hk, d]."""
-    n = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
-    d = q.shape[-1]
-    return AttnDims(B, T, n, n_groups, q.shape[-2], k.shape[-2], d, d ** -0.5 if scale is None else scale,
-                    _token_stride(q, "q"), _token_stride(k, "k"), k.shape[0])
+    n, hq, d, qs = _layout(q, "q")
+    rows, hk, _, ks = _layout(k, "k")
+    return AttnDims(B, T, n, n_groups, hq, hk, d, d ** -0.5 if scale is None else scale, qs, ks, rows)
 
 
 def attn_prefill(dims: AttnDims, q, k, v, cu_seqlens, out, kv_start=None, kv_len=None, stream=None):
