@@ -39,6 +39,7 @@ namespace attn {
 
 constexpr int kMaxCtas = 152;  // CTAs of a shared-prefix call: one per SM
 constexpr int BN = 128;        // keys of a block
+constexpr int kSetup = 2;      // a segment's queries, first latency and stores, in blocks' time
 
 struct Args {
   int B, T, n_tokens, n_groups, hq, hk, G;
@@ -54,7 +55,7 @@ struct Args {
   const int32_t *suffix_start, *suffix_len, *q_len;
   unsigned int *status;
   // shared prefix: partial results. A slot of the prefix region holds 2 (D = 256: 1) tiles of prefix_rows rows,
-  // of the suffix region 2 (1) tiles of suffix_rows rows: D fp32 each, then (maximum, sum) pairs.
+  // of the suffix region 2 (1) tiles of suffix_rows rows: D/4 times 16 bytes of every row, and (maximum, sum) pairs.
   int prefix_rows, suffix_rows;
   float *prefix_o, *suffix_o;
   float2 *prefix_ml, *suffix_ml;
@@ -82,7 +83,7 @@ struct Entry {
   int kv0, len, lim0, step;
   int tiles, blocks;
   bool ok;
-  __device__ long long line_cost() const { return blocks > 0 ? blocks + 1 : 0; }  // + 1: the tile's set-up and store
+  __device__ long long line_cost() const { return blocks > 0 ? blocks + kSetup : 0; }
   __device__ long long cost(int hk) const { return line_cost() * tiles * hk; }
 };
 
@@ -151,8 +152,8 @@ struct Walk {
       const long long z = min(end, a + lc);
       const int tile = (int)(li / A.hk);
       s.head = (int)(li - (long long)tile * A.hk);
-      s.b0 = (int)max(pos - a - 1, 0LL);
-      s.b1 = (int)(z - a - 1);
+      s.b0 = (int)max(pos - a - kSetup, 0LL);
+      s.b1 = (int)(z - a - kSetup);
       pos = z;
       if (s.b1 <= s.b0) continue;
       s.t0 = x.first + tile * A.tile_tokens;
@@ -203,6 +204,7 @@ __device__ void block_scan(long long &a, long long &b, long long &ta, long long 
   b = pb + ib - b;
 }
 
+constexpr int kSegs = 4;  // segments found ahead
 struct Start {  // where the CTA's work begins
   int e, any;
   long long first_cost, first_line;
@@ -276,7 +278,7 @@ struct Cfg {
   static constexpr int NU = D == 64 ? 10 : 5;               // units of the ring
   static constexpr int QB = 128 * D * 2;                    // bytes of a Q tile
   static constexpr int kBar = NS * QB + NU * UB;
-  static constexpr int kBytes = kBar + 8 * (2 * NU + 14) + 1024;
+  static constexpr int kBytes = kBar + 8 * (2 * NU + 13 + 2 * kSegs) + 1024;
   static constexpr int kThreads = NS * 128 + 128;
   static constexpr int kO = 256;                            // TMEM column of the first O tile
 };
@@ -373,6 +375,16 @@ __device__ __forceinline__ int tile_blocks(const Args &A, const Seg &s, int q) {
   return max(0, min(s.b1, blocks_of(min(s.len, s.lim0 + s.step * last))) - s.b0);
 }
 
+// Which query slots a segment's tiles take: two tiles both, one tile each slot in turn, so that the next tile can land
+// while this one is in use.
+struct QSlots {
+  int used[2] = {0, 0}, turn = 0;
+  __device__ __forceinline__ int first(bool pair, int slots) {
+    if (pair || slots == 1) return 0;
+    turn ^= 1;
+    return turn;
+  }
+};
 // The segment's block whose last rows lie past the extent, if it is among the first n; else -1.
 __device__ __forceinline__ int tail_block(const Seg &s, int n) {
   return n > 0 && (long long)(s.b0 + n) * BN > s.len ? n - 1 : -1;
@@ -393,27 +405,32 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char *sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kBar), *empty = full + NU;
-  uint64_t *q_full = empty + NU, *q_empty = q_full + 1, *s_full = q_empty + 1, *p_full = s_full + 2, *o_full = p_full + 2, *handed = o_full + 2,
-           *clean = handed + 1, *dirty = clean + 1;
+  uint64_t *q_full = empty + NU, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *handed = o_full + 2,
+           *clean = handed + 1, *dirty = clean + 1, *seg_full = dirty + 1, *seg_empty = seg_full + kSegs;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ Start s_start;
+  __shared__ Seg s_seg[kSegs];
   __shared__ long long s_scan[NT / 32][2];
   __shared__ float2 s_ml[NS == 2 && !SHARED ? 128 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kMma = NS * 4, kTma = NS * 4 + 1, kClean = NS * 4 + 2;
+  constexpr int kMma = NS * 4, kTma = NS * 4 + 1, kClean = NS * 4 + 2, kQ = NS * 4 + 3;
 
   if (tid == 0) {
     for (int i = 0; i < NU; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], NS * 4 + 3);  // the softmax warps, the loads, the products, the cleaning warp
+    }
     mbar_init(handed, 4);
     mbar_init(clean, 1);
     mbar_init(dirty, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);  // the four warps of a softmax group
       mbar_init(&o_full[i], 1);
@@ -431,7 +448,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
   // ---- what this CTA does
   Walk walk(A);
-  Seg one = {};
   bool any;
   if (SHARED) {
     const int n = A.n_groups + A.B;
@@ -441,6 +457,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const bool all_ok = !__syncthreads_or(broken);
     if (!all_ok && blockIdx.x == 0 && tid == 0) set_status(A.status, GDN_ERR_INDEX);
     long long total = 0, lines = 0, ta, tb;
+    long long my_cost = 0, my_first = 0, my_line = 0;  // of the last entry looked at
     for (int e0 = 0; e0 < n; e0 += NT) {
       const int e = e0 + tid;
       long long a = 0, b = 0;
@@ -450,15 +467,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         a = x.cost(A.hk);
         b = (long long)x.tiles * A.hk;
       }
+      my_cost = a;
       block_scan<NT>(a, b, ta, tb, s_scan);
+      my_first = total + a;
+      my_line = lines + b;
       if (blockIdx.x == 0 && e < n) {  // for the join
-        A.plan[2 + 2 * e] = total + a;
-        A.plan[3 + 2 * e] = lines + b;
+        A.plan[2 + 2 * e] = my_first;
+        A.plan[3 + 2 * e] = my_line;
       }
       total += ta;
       lines += tb;
     }
-    const long long share = max((total + gridDim.x - 1) / gridDim.x, 3LL);
+    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kSetup + 2);
     if (blockIdx.x == 0 && tid == 0) {
       A.plan[0] = share;
       A.plan[1] = all_ok;
@@ -467,27 +487,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     walk.end = min(walk.pos + share, total);
     any = walk.pos < walk.end;
     if (any) {
-      // the entry that holds pos
+      // the entry that holds pos; more entries than threads are gone through again
       long long before = 0, before_lines = 0;
       for (int e0 = 0; e0 < n; e0 += NT) {
         const int e = e0 + tid;
-        long long a = 0, b = 0;
-        if (e < n) {
-          const Entry x = entry_at(A, e, all_ok);
-          a = x.cost(A.hk);
-          b = (long long)x.tiles * A.hk;
+        if (n > NT) {
+          long long a = 0, b = 0;
+          if (e < n) {
+            const Entry x = entry_at(A, e, all_ok);
+            a = x.cost(A.hk);
+            b = (long long)x.tiles * A.hk;
+          }
+          my_cost = a;
+          block_scan<NT>(a, b, ta, tb, s_scan);
+          my_first = before + a;
+          my_line = before_lines + b;
+          before += ta;
+          before_lines += tb;
         }
-        const long long own_cost = a;
-        block_scan<NT>(a, b, ta, tb, s_scan);
-        a += before;
-        if (a <= walk.pos && walk.pos < a + own_cost) {
+        if (my_first <= walk.pos && walk.pos < my_first + my_cost) {
           s_start.e = e;
-          s_start.first_cost = a;
-          s_start.first_line = before_lines + b;
+          s_start.first_cost = my_first;
+          s_start.first_line = my_line;
         }
-        before += ta;
-        before_lines += tb;
-        if (walk.pos < before) break;  // the same for every thread
+        if (n > NT && walk.pos < before) break;  // the same for every thread
       }
       __syncthreads();
       walk.all_ok = all_ok;
@@ -508,36 +531,37 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     __syncthreads();
     any = s_start.any;
-    one = s_start.seg;
   }
-  bool fresh = true;
-  auto next_seg = [&](Seg &s) -> bool {
-    if (SHARED) return walk.next(s);
-    s = one;
-    const bool f = fresh;
-    fresh = false;
-    return f;
+  // The segments one after the other: one thread finds them (its divisions and
+  // loads would cost every other thread registers and time) and hands them on
+  // through a ring of shared memory. A prefill CTA has one.
+  uint32_t seg_count = 0;
+  auto next_seg = [&](Seg &s, bool whole_warp) -> bool {
+    const uint32_t k = seg_count++;
+    if (!SHARED) {
+      s = s_start.seg;
+      return k == 0;
+    }
+    const int i = k % kSegs;
+    const uint32_t phase = (k / kSegs) & 1;
+    if (!(whole_warp ? warp_wait(&seg_full[i], phase, &s_abort, A.status)
+                     : wait_or_abort(&seg_full[i], phase, &s_abort, A.status)))
+      return false;
+    s = s_seg[i];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(&seg_empty[i]);
+    return s.ntok > 0;
   };
 
   if (any) {
     Seg s;
     if (warp == kTma) {
       if (lane == 0) {
-        // ---- loads
-        int u = 0, segs = 0;  // units issued, segments begun
+        // ---- K and V blocks
+        int u = 0;  // units issued
         bool ok = true;
-        while (ok && next_seg(s)) {
-          const int tiles = s.pair ? 2 : 1;
-          const int n = tile_blocks(A, s, tiles - 1);
-          if (n > 0) {
-            if (segs > 0) ok = wait_or_abort(q_empty, (segs - 1) & 1, &s_abort, A.status);
-            if (!ok) break;
-            ++segs;
-            mbar_arrive_expect_tx(q_full, (uint32_t)(tiles * (D / 64) * A.TQ * A.G * 128));
-            for (int t = 0; t < tiles; ++t)
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(smem_u32(sm) + t * C::QB + c * 128 * 128, &qmap, c * 64, s.head * A.G, s.t0 + t * A.TQ, q_full);
-          }
+        while (ok && next_seg(s, false)) {
+          const int n = tile_blocks(A, s, s.pair ? 1 : 0);
           for (int i = 0; ok && i < 2 * n; ++i) {  // K and V blocks in the order of the products
             bool is_v;
             int j;
@@ -565,23 +589,59 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         // the copies this thread issued have landed before the CTA's memory is released
         for (int i = max(0, u - NU); i < u; ++i) (void)mbar_wait_bounded(&full[i % NU], (i / NU) & 1);
-        if (segs > 0) (void)mbar_wait_bounded(q_full, (segs - 1) & 1);
+      }
+    } else if (warp == kQ) {
+      if (lane == 0) {
+        // ---- query tiles: a warp of its own, so that the next segment's keys do not wait for this one's queries
+        QSlots slots;
+        uint32_t found = 0;
+        bool ok = true, more = true;
+        while (ok && more) {
+          more = SHARED ? walk.next(s) : found == 0;
+          if (SHARED) {
+            const int i = found % kSegs;
+            if (found >= kSegs && !wait_or_abort(&seg_empty[i], ((found / kSegs) - 1) & 1, &s_abort, A.status)) break;
+            if (!more) s.ntok = 0;  // the end
+            s_seg[i] = s;
+            mbar_arrive(&seg_full[i]);
+          } else {
+            s = s_start.seg;
+          }
+          ++found;
+          if (!more) break;
+          if (tile_blocks(A, s, s.pair ? 1 : 0) == 0) continue;
+          const int first = slots.first(s.pair, NS), tiles = s.pair ? 2 : 1;
+          for (int t = 0; ok && t < tiles; ++t) {
+            const int q = first + t;
+            if (slots.used[q] > 0) ok = wait_or_abort(&q_empty[q], (slots.used[q] - 1) & 1, &s_abort, A.status);
+            if (!ok) break;
+            ++slots.used[q];
+            mbar_arrive_expect_tx(&q_full[q], (uint32_t)((D / 64) * A.TQ * A.G * 128));
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(smem_u32(sm) + q * C::QB + c * 128 * 128, &qmap, c * 64, s.head * A.G, s.t0 + t * A.TQ, &q_full[q]);
+          }
+        }
+        for (int q = 0; q < NS; ++q)
+          if (slots.used[q] > 0) (void)mbar_wait_bounded(&q_full[q], (slots.used[q] - 1) & 1);
       }
     } else if (warp == kMma) {
       // ---- products: one thread issues them all
       if (elect_one()) {
-        int base = 0, segs = 0;  // units of earlier segments, segments with keys
+        int base = 0;  // units of earlier segments
+        QSlots slots;
         uint32_t pc[2] = {0, 0}, cleaned = 0;  // P tiles taken from each buffer, blocks with cleaned tails
         bool ok = true;
         const uint64_t q_desc = umma_desc(smem_u32(sm)), k_desc = umma_desc(smem_u32(sm) + NS * C::QB),
                        v_desc = umma_desc_mn(smem_u32(sm) + NS * C::QB, BN * 128);
         constexpr uint32_t idesc_o = idesc_bf16(128, C::UC) | (1u << 16);  // B (V) is read MN-major
-        while (ok && next_seg(s)) {
+        while (ok && next_seg(s, false)) {
           const int nb0 = tile_blocks(A, s, 0), nb1 = s.pair ? tile_blocks(A, s, 1) : 0;
           const int n = s.pair ? nb1 : nb0;
           if (n == 0) continue;
-          if (!wait_or_abort(q_full, segs & 1, &s_abort, A.status)) break;
-          ++segs;
+          const int q_first = slots.first(s.pair, NS);
+          for (int q = q_first; ok && q < q_first + (s.pair ? 2 : 1); ++q)
+            ok = wait_or_abort(&q_full[q], slots.used[q]++ & 1, &s_abort, A.status);
+          if (!ok) break;
           const int tail = tail_block(s, n);  // the block whose V rows past the extent are cleaned first
           bool handed_over = false;
           auto unit_ready = [&](int g) {
@@ -647,16 +707,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
               if (j + 1 < n && ok) issue_s(1, 1, j + 1, true);
             }
           } else {
-            issue_s(0, 0, 0, true);
-            if (ok && n > 1) issue_s(0, 1, 1, true);
+            issue_s(q_first, 0, 0, true);
+            if (ok && n > 1) issue_s(q_first, 1, 1, true);
             for (int j = 0; ok && j < n; ++j) {
               const int o = NS == 2 ? (j & 1) : 0;
               issue_o(o, j & 1, j, NS == 2 ? j < 2 : j == 0, true);
               if (ok && (NS == 1 || j + 2 >= n)) umma_commit(&o_full[o]);
-              if (ok && j + 2 < n) issue_s(0, j & 1, j + 2, true);
+              if (ok && j + 2 < n) issue_s(q_first, j & 1, j + 2, true);
             }
           }
-          if (ok) umma_commit(q_empty);
+          for (int q = q_first; ok && q < q_first + (s.pair ? 2 : 1); ++q) umma_commit(&q_empty[q]);
           if (tail >= 0) ++cleaned;
           base += 2 * n * HB;
         }
@@ -667,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       int base = 0;
       uint32_t cleaned = 0;
       bool ok = true;
-      while (ok && next_seg(s)) {
+      while (ok && next_seg(s, true)) {
         const int n = tile_blocks(A, s, s.pair ? 1 : 0), tail = tail_block(s, n);
         if (tail >= 0) {
           const int g0 = base + v_place(s.pair, tail, n) * HB, valid = s.len - (s.b0 + tail) * BN;
@@ -694,11 +754,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const int grp = warp >> 2, wq = warp & 3, row = (wq << 5) + lane;
       uint32_t sc[2] = {0, 0}, oc = 0;  // S tiles taken from each buffer, O tiles waited for
       bool ok = true;
-      while (ok && next_seg(s)) {
+      while (ok && next_seg(s, true)) {
         const int q = s.pair ? grp : 0;
         const int nb = tile_blocks(A, s, q);
         const int tok = row / A.G + q * A.TQ, gh = row - (row / A.G) * A.G;
         const bool real = row < A.TQ * A.G && tok < s.ntok;
+        const bool busy = __any_sync(0xffffffffu, real);  // few query rows leave warps without any
         const int lim = real ? min(s.len, s.lim0 + s.step * tok) : 0x7fffffff;
         const int j0 = (!s.pair && NS == 2) ? grp : 0, dj = (!s.pair && NS == 2) ? 2 : 1;
         float top = -INFINITY, sum = 0.0f;  // the maximum that O is measured against (before scaling), the sum
@@ -709,6 +770,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           ok = warp_wait(&s_full[buf], sc[buf] & 1, &s_abort, A.status);
           if (!ok) break;
           ++sc[buf];
+          if (!busy) {  // its rows of P stay whatever they are: they reach its rows of O only
+            if (lane == 0) mbar_arrive(&p_full[buf]);
+            continue;
+          }
           tc_fence_after();
           const int key0 = (s.b0 + j) * BN;
           const bool masked = __any_sync(0xffffffffu, lim < key0 + BN);
@@ -805,8 +870,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           const long long r = ((long long)s.slot * NS + grp) * rows + row;
           if (real)  // a group that took no block says so: (-inf, 0)
             (s.own ? A.suffix_ml : A.prefix_ml)[r] = make_float2(top == -INFINITY ? -INFINITY : top * A.c, sum);
-          float *dst = (s.own ? A.suffix_o : A.prefix_o) + r * D;
-          if (mine > 0) {
+          // 16 bytes of each row side by side: a warp's stores and the join's loads are contiguous
+          float4 *dst = reinterpret_cast<float4 *>(s.own ? A.suffix_o : A.prefix_o) +
+                        ((long long)s.slot * NS + grp) * rows * (D / 4) + row;
+          if (mine > 0 && busy) {
 #pragma unroll 1
             for (int i = 0; i < D; i += 32) {
               float v[32];
@@ -815,7 +882,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
               if (real) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
-                  *reinterpret_cast<float4 *>(dst + i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                  dst[(i + k) / 4 * rows] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
               }
             }
           }
@@ -898,97 +965,80 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partial results of a shared-prefix call: one warp per (query token,
-// head), the parts in a fixed order.
+// Joins the partial results of a shared-prefix call: a thread takes four
+// channels of one (query token, head) and goes through its parts in order,
+// kParts of them loaded at once.
+constexpr int kParts = 8;
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args A, int ctas) {
-  constexpr int NS = Cfg<D>::NS, E = D / 32;
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args A) {
+  constexpr int NS = Cfg<D>::NS;
   griddep_wait();
   griddep_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(unit / A.hq), h = (int)(unit - (long long)t * A.hq);
+  // items: (token, key head, channel group, head of the group), the last fastest
+  const long long item = (long long)blockIdx.x * 128 + threadIdx.x;
+  const long long th = item / ((D / 4) * A.G);
+  const int in = (int)(item - th * ((D / 4) * A.G)), c = in / A.G, gh = in - c * A.G;
+  const int t = (int)(th / A.hk), head = (int)(th - (long long)t * A.hk);
   if (t >= A.n_tokens || !A.plan[1]) return;
-  const int b = t / A.T, g = group_of(A, b), head = h / A.G, gh = h - head * A.G;
+  const int b = t / A.T, g = group_of(A, b);
   const long long share = A.plan[0];
   const Entry own = entry_at(A, A.n_groups + b, true);
   if (!own.ok || (g >= 0 && !inside(A.prefix_start[g], A.prefix_len[g], A.kv_rows))) return;
-  float o[E], top = -INFINITY, sum = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float top = -INFINITY, sum = 0.0f;
   const bool real = t - own.first < own.ntok;
-  for (int part = 0; real && part < 2; ++part) {
-    if (part == 0 && g < 0) continue;
+  for (int part = g < 0 ? 1 : 0; real && part < 2; ++part) {
     const int e = part == 0 ? g : A.n_groups + b;
     const Entry x = part == 0 ? entry_at(A, g, true) : own;
     if (x.blocks == 0) continue;
     const int ti = t - x.first, tile = ti / A.tile_tokens, i = ti - tile * A.tile_tokens;
     const bool pair = min(A.tile_tokens, x.ntok - tile * A.tile_tokens) > A.TQ;
-    const long long li = (long long)tile * A.hk + head, lc = x.line_cost();
-    const long long a = A.plan[2 + 2 * e] + li * lc, z = a + lc;
+    const long long li = (long long)tile * A.hk + head, a = A.plan[2 + 2 * e] + li * x.line_cost(), z = a + x.line_cost();
     const int rows = part == 0 ? A.prefix_rows : A.suffix_rows;
     const int streams = NS == 2 && !pair ? 2 : 1, s0 = pair ? i / A.TQ : 0, row = (pair ? i % A.TQ : i) * A.G + gh;
-    const float *po = part == 0 ? A.prefix_o : A.suffix_o;
-    const float2 *pml = part == 0 ? A.prefix_ml : A.suffix_ml;
-    const int c0 = (int)(a / share), c1 = (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
-    for (int p0 = 0; p0 < n; p0 += 32) {
-      const int p = p0 + lane;
-      long long r = 0;
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (p < n) {
-        const int cta = c0 + p / streams;
-        const long long b0 = max(max(a, cta * share) - a - 1, 0LL), b1 = min(z, (cta + 1) * share) - a - 1;
-        if (b1 > b0) {
-          r = ((A.plan[3 + 2 * e] + li + cta) * NS + s0 + p % streams) * rows + row;
-          ml = pml[r];
-        }
-      }
-      float m = ml.y > 0.0f || ml.y != ml.y ? ml.x : -INFINITY;
+    const float4 *po = reinterpret_cast<const float4 *>(part == 0 ? A.prefix_o : A.suffix_o) + (long long)c * rows + row;
+    const float2 *pml = (part == 0 ? A.prefix_ml : A.suffix_ml) + row;
+    // the CTAs that took some of the line's blocks
+    const int c0 = (int)((a + kSetup) / share), c1 = (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
+    const long long first = (A.plan[3 + 2 * e] + li + c0) * NS + s0;  // part p is tile first + p (+ p with one stream of two)
+    const int stride = NS / streams;
+    for (int p0 = 0; p0 < n; p0 += kParts) {
+      float2 ml[kParts];
+      float4 v[kParts];
 #pragma unroll
-      for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-      const float best = fmaxf(top, m);
-      const float keep = top == -INFINITY ? 0.0f : ex2(top - best);
-      const float w = ml.y == 0.0f ? 0.0f : ex2(ml.x - best);
-      top = best;
+      for (int k = 0; k < kParts; ++k) {
+        const long long at = (first + (long long)min(p0 + k, n - 1) * stride) * rows;
+        ml[k] = pml[at];
+        v[k] = po[at * (D / 4)];
+        if (p0 + k >= n) ml[k].y = 0.0f;
+      }
+      float m = top;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k)
+        if (ml[k].y != 0.0f) m = fmaxf(m, ml[k].x);
+      const float keep = top == -INFINITY ? 0.0f : ex2(top - m);
+      top = m;
       sum *= keep;
+      o.x *= keep;
+      o.y *= keep;
+      o.z *= keep;
+      o.w *= keep;
 #pragma unroll
-      for (int e2 = 0; e2 < E; ++e2) o[e2] *= keep;
-      const int here = min(32, n - p0);
-#pragma unroll 4
-      for (int k = 0; k < here; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k), yk = __shfl_sync(0xffffffffu, ml.y, k);
-        const long long rk = __shfl_sync(0xffffffffu, r, k);
-        if (wk == 0.0f) continue;
-        sum = fmaf(yk, wk, sum);
-        const float *src = po + rk * D + lane * E;
-        float v[E];
-        if (E == 2) {
-          const float2 f = *reinterpret_cast<const float2 *>(src);
-          v[0] = f.x;
-          v[1] = f.y;
-        } else {
-#pragma unroll
-          for (int q = 0; q < E / 4; ++q) {
-            const float4 f = *reinterpret_cast<const float4 *>(src + 4 * q);
-            v[4 * q] = f.x;
-            v[4 * q + 1] = f.y;
-            v[4 * q + 2] = f.z;
-            v[4 * q + 3] = f.w;
-          }
+      for (int k = 0; k < kParts; ++k)
+        if (ml[k].y != 0.0f) {  // else the part saw no key, and its numbers were not written
+          const float w = ex2(ml[k].x - m);
+          sum = fmaf(ml[k].y, w, sum);
+          o.x = fmaf(v[k].x, w, o.x);
+          o.y = fmaf(v[k].y, w, o.y);
+          o.z = fmaf(v[k].z, w, o.z);
+          o.w = fmaf(v[k].w, w, o.w);
         }
-#pragma unroll
-        for (int e2 = 0; e2 < E; ++e2) o[e2] = fmaf(v[e2], wk, o[e2]);
-      }
     }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint32_t p[E / 2];
-#pragma unroll
-  for (int e = 0; e < E / 2; ++e) p[e] = sum == 0.0f ? 0u : pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-  bf16 *dst = A.out + ((long long)t * A.hq + h) * D + lane * E;
-  if (E == 2) *reinterpret_cast<uint32_t *>(dst) = p[0];
-  if (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(p[0], p[E / 2 - 1]);
-  if (E == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(p[0], p[1 % (E / 2)], p[2 % (E / 2)], p[3 % (E / 2)]);
+  const float inv = 1.0f / sum;
+  uint2 r = make_uint2(0u, 0u);
+  if (sum != 0.0f) r = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  *reinterpret_cast<uint2 *>(A.out + ((long long)t * A.hq + head * A.G + gh) * D + 4 * c) = r;
 }
 
 // --------------------------------------------------------------------- host
@@ -1080,8 +1130,8 @@ gdn_status launch_t(const gdn_attn_dims *d, const void *q, const void *k, const 
   launch_pdl(attn_kernel<D, SHARED>, dim3((unsigned)grid), dim3(Cfg<D>::kThreads), Cfg<D>::kBytes, st, qm, km, vm, A);
   GDN_TRY(check_launch("attention"));
   if (SHARED) {
-    const long long warps = (long long)A.n_tokens * A.hq;
-    launch_pdl(join_kernel<D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, A, grid);
+    const long long items = (long long)A.n_tokens * A.hq * (D / 4);
+    launch_pdl(join_kernel<D>, dim3((unsigned)((items + 127) / 128)), dim3(128), 0, st, A);
   }
   return check_launch("attention");
 }
