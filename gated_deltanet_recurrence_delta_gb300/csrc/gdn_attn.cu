@@ -148,7 +148,9 @@ struct Walk {
         x = entry_at(A, e, all_ok);
         continue;
       }
-      const long long li = (pos - first_cost) / lc, a = first_cost + li * lc;
+      const long long off = pos - first_cost;  // a 64-bit division takes hundreds of cycles
+      const long long li = off < (1LL << 31) ? (long long)((unsigned)off / (unsigned)lc) : off / lc;
+      const long long a = first_cost + li * lc;
       const long long z = min(end, a + lc);
       const int tile = (int)(li / A.hk);
       s.head = (int)(li - (long long)tile * A.hk);
@@ -208,6 +210,7 @@ constexpr int kSegs = 4;  // segments found ahead
 struct Start {  // where the CTA's work begins
   int e, any;
   long long first_cost, first_line;
+  Entry entry;
   Seg seg;  // prefill
 };
 
@@ -300,6 +303,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 // 32 columns of this warp's lanes, in flight until tmem_wait_ld().
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *v) {
@@ -439,6 +445,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     s_abort = 0;
   }
   if (warp == kMma) tmem_alloc(&s_tmem, 512);
+  if (tid == kTma * 32) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -458,14 +469,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (!all_ok && blockIdx.x == 0 && tid == 0) set_status(A.status, GDN_ERR_INDEX);
     long long total = 0, lines = 0, ta, tb;
     long long my_cost = 0, my_first = 0, my_line = 0;  // of the last entry looked at
+    Entry mine = {};
     for (int e0 = 0; e0 < n; e0 += NT) {
       const int e = e0 + tid;
       long long a = 0, b = 0;
       if (e < n) {
-        const Entry x = entry_at(A, e, all_ok);
-        if (!x.ok && blockIdx.x == 0) set_status(A.status, GDN_ERR_INDEX);
-        a = x.cost(A.hk);
-        b = (long long)x.tiles * A.hk;
+        mine = entry_at(A, e, all_ok);
+        if (!mine.ok && blockIdx.x == 0) set_status(A.status, GDN_ERR_INDEX);
+        a = mine.cost(A.hk);
+        b = (long long)mine.tiles * A.hk;
       }
       my_cost = a;
       block_scan<NT>(a, b, ta, tb, s_scan);
@@ -494,9 +506,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (n > NT) {
           long long a = 0, b = 0;
           if (e < n) {
-            const Entry x = entry_at(A, e, all_ok);
-            a = x.cost(A.hk);
-            b = (long long)x.tiles * A.hk;
+            mine = entry_at(A, e, all_ok);
+            a = mine.cost(A.hk);
+            b = (long long)mine.tiles * A.hk;
           }
           my_cost = a;
           block_scan<NT>(a, b, ta, tb, s_scan);
@@ -509,6 +521,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           s_start.e = e;
           s_start.first_cost = my_first;
           s_start.first_line = my_line;
+          s_start.entry = mine;
         }
         if (n > NT && walk.pos < before) break;  // the same for every thread
       }
@@ -517,7 +530,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       walk.e = s_start.e;
       walk.first_cost = s_start.first_cost;
       walk.first_line = s_start.first_line;
-      walk.x = entry_at(A, walk.e, all_ok);
+      walk.x = s_start.entry;
       walk.cta = blockIdx.x;
     }
   } else {
@@ -976,31 +989,36 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
   griddep_trigger();
   // items: (token, key head, channel group, head of the group), the last fastest
   const long long item = (long long)blockIdx.x * 128 + threadIdx.x;
-  const long long th = item / ((D / 4) * A.G);
-  const int in = (int)(item - th * ((D / 4) * A.G)), c = in / A.G, gh = in - c * A.G;
-  const int t = (int)(th / A.hk), head = (int)(th - (long long)t * A.hk);
-  if (t >= A.n_tokens || !A.plan[1]) return;
+  const long long per_token = (long long)(D / 4) * A.hq;
+  const bool few = item < (1LL << 31);
+  const int t = few ? (unsigned)item / (unsigned)per_token : (int)(item / per_token);
+  const int of_token = (int)(item - t * per_token), head = of_token / ((D / 4) * A.G);
+  const int in = of_token - head * ((D / 4) * A.G), c = in / A.G, gh = in - c * A.G;
+  if (t >= A.n_tokens) return;
   const int b = t / A.T, g = group_of(A, b);
-  const long long share = A.plan[0];
-  const Entry own = entry_at(A, A.n_groups + b, true);
-  if (!own.ok || (g >= 0 && !inside(A.prefix_start[g], A.prefix_len[g], A.kv_rows))) return;
+  const long long share = A.plan[0], in_order = A.plan[1];
+  const Entry own = entry_at(A, A.n_groups + b, true), shared = g >= 0 ? entry_at(A, g, true) : own;
+  const long long own_at = A.plan[2 + 2 * (A.n_groups + b)], own_line = A.plan[3 + 2 * (A.n_groups + b)];
+  const long long shared_at = A.plan[2 + 2 * max(g, 0)], shared_line = A.plan[3 + 2 * max(g, 0)];
+  if (!in_order || !own.ok || !shared.ok) return;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float top = -INFINITY, sum = 0.0f;
   const bool real = t - own.first < own.ntok;
   for (int part = g < 0 ? 1 : 0; real && part < 2; ++part) {
-    const int e = part == 0 ? g : A.n_groups + b;
-    const Entry x = part == 0 ? entry_at(A, g, true) : own;
+    const Entry x = part == 0 ? shared : own;
     if (x.blocks == 0) continue;
     const int ti = t - x.first, tile = ti / A.tile_tokens, i = ti - tile * A.tile_tokens;
     const bool pair = min(A.tile_tokens, x.ntok - tile * A.tile_tokens) > A.TQ;
-    const long long li = (long long)tile * A.hk + head, a = A.plan[2 + 2 * e] + li * x.line_cost(), z = a + x.line_cost();
+    const long long li = (long long)tile * A.hk + head, a = (part == 0 ? shared_at : own_at) + li * x.line_cost(), z = a + x.line_cost();
     const int rows = part == 0 ? A.prefix_rows : A.suffix_rows;
     const int streams = NS == 2 && !pair ? 2 : 1, s0 = pair ? i / A.TQ : 0, row = (pair ? i % A.TQ : i) * A.G + gh;
     const float4 *po = reinterpret_cast<const float4 *>(part == 0 ? A.prefix_o : A.suffix_o) + (long long)c * rows + row;
     const float2 *pml = (part == 0 ? A.prefix_ml : A.suffix_ml) + row;
     // the CTAs that took some of the line's blocks
-    const int c0 = (int)((a + kSetup) / share), c1 = (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
-    const long long first = (A.plan[3 + 2 * e] + li + c0) * NS + s0;  // part p is tile first + p (+ p with one stream of two)
+    const bool small = z < (1LL << 31);
+    const int c0 = small ? (unsigned)(a + kSetup) / (unsigned)share : (int)((a + kSetup) / share);
+    const int c1 = small ? (unsigned)(z - 1) / (unsigned)share : (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
+    const long long first = ((part == 0 ? shared_line : own_line) + li + c0) * NS + s0;  // part p is tile first + p (+ p with one stream of two)
     const int stride = NS / streams;
     for (int p0 = 0; p0 < n; p0 += kParts) {
       float2 ml[kParts];
