@@ -25,11 +25,6 @@
 // tiles against the same keys, or (one tile of rows only) the even and the odd
 // key blocks, each with its own running maximum, joined at the end.
 // D = 256: one O tile of 256 columns and two S tiles in turn, one group.
-// Shared prefixes, at most 16 rows (a decode step's own keys): the products are
-// turned round, with the 128 keys as the rows of S and the queries as its 16
-// columns, so that a thread has 16 scores instead of 128 of which one warp's
-// few rows count; P goes through shared memory as the second operand of
-// O^T = V^T P^T, and the four warps agree on a column's maximum.
 //
 // Running maximum: O is rescaled only where a row's maximum grew by more than
 // 2^8 since the value it is measured against; probabilities then reach 2^8 at
@@ -44,17 +39,15 @@ namespace attn {
 
 constexpr int kMaxCtas = 152;  // CTAs of a shared-prefix call: one per SM
 constexpr int BN = 128;        // keys of a block
-constexpr int kN = 16;         // query rows of a narrow tile
 constexpr int kSetup = 2;      // a segment's queries, first latency and stores, in blocks' time
 
 struct Args {
   int B, T, n_tokens, n_groups, hq, hk, G;
   int TQ;           // tokens of one 128-row tile
-  int TN;           // tokens of a narrow tile (0: none)
   int tile_tokens;  // tokens of one CTA's tiles (TQ, or 2 TQ for two query tiles)
   int max_tiles;    // prefill: tiles the grid covers
   float c;          // |scale| log2(e)
-  uint32_t negate;  // instruction descriptor bit for a negative scale
+  uint32_t idesc_s; // instruction descriptor of S (the sign of scale)
   long long kv_rows;
   bf16 *out;
   const int32_t *cu, *kv_start, *kv_len;                  // prefill
@@ -79,7 +72,6 @@ __device__ __forceinline__ int blocks_of(int keys) { return keys <= 0 ? 0 : (int
 // blocks [b0, b1) of one extent. Token i sees keys below lim0 + step * i.
 struct Seg {
   int t0, ntok, head, kv0, len, b0, b1, lim0, step;
-  bool narrow;  // at most kN query rows: keys as the rows of S, queries as its columns
   bool pair;  // two query tiles; else one tile, whose blocks alternate between the S tiles
   int slot;   // of the partial results; prefix and suffix lines are told apart by `own`
   bool own;
@@ -173,7 +165,6 @@ struct Walk {
       s.step = x.step;
       s.lim0 = x.lim0 + x.step * tile * A.tile_tokens;
       s.pair = s.ntok > A.TQ;
-      s.narrow = s.ntok <= A.TN;
       s.own = e >= A.n_groups;
       s.slot = (int)(first_line + li) + cta;
       return true;
@@ -270,7 +261,6 @@ __device__ bool prefill_seg(const Args &A, Seg &s) {
       s.b0 = 0;
       s.b1 = blocks_of(min(m, s.lim0 + s.ntok - 1));
       s.pair = s.ntok > A.TQ;
-      s.narrow = false;
       s.slot = 0;
       s.own = false;
       return true;
@@ -291,7 +281,7 @@ struct Cfg {
   static constexpr int NU = D == 64 ? 10 : 5;               // units of the ring
   static constexpr int QB = 128 * D * 2;                    // bytes of a Q tile
   static constexpr int kBar = NS * QB + NU * UB;
-  static constexpr int kBytes = kBar + 8 * (2 * NU + 15 + 2 * kSegs) + 1024;
+  static constexpr int kBytes = kBar + 8 * (2 * NU + 13 + 2 * kSegs) + 1024;
   static constexpr int kThreads = NS * 128 + 128;
   static constexpr int kO = 256;                            // TMEM column of the first O tile
 };
@@ -328,30 +318,6 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *v) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, float *v) {
-  uint32_t *r = reinterpret_cast<uint32_t *>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float *v) {
-  const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// Where P' tile `buf` of a narrow segment lies in its query slot: the slot's first 16 rows hold the queries, rows 64..
-// of the first 64 channels' block are free. [kN rows][128 keys], two blocks of 64 keys.
-__device__ __forceinline__ constexpr int p_narrow(int buf) { return 64 * 128 + buf * kN * 256; }
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -437,8 +403,7 @@ __device__ __forceinline__ bool elect_one() {
 
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
-    attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qnmap,
-                const __grid_constant__ CUtensorMap kmap,
+    attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args A) {
   using C = Cfg<D>;
   constexpr int NS = C::NS, NU = C::NU, HB = C::HB, NT = C::kThreads;
@@ -447,14 +412,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   unsigned char *sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kBar), *empty = full + NU;
   uint64_t *q_full = empty + NU, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *handed = o_full + 2,
-           *clean = handed + 1, *dirty = clean + 1, *seg_full = dirty + 1, *seg_empty = seg_full + kSegs,
-           *agree = seg_empty + kSegs;
+           *clean = handed + 1, *dirty = clean + 1, *seg_full = dirty + 1, *seg_empty = seg_full + kSegs;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ Start s_start;
   __shared__ Seg s_seg[kSegs];
-  __shared__ __align__(16) float s_col[SHARED ? NS : 1][4][kN];  // narrow tiles: the warps' maxima or sums
-  __shared__ uint32_t s_grew[NS];
   __shared__ long long s_scan[NT / 32][2];
   __shared__ float2 s_ml[NS == 2 && !SHARED ? 128 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -478,16 +440,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);  // the four warps of a softmax group
       mbar_init(&o_full[i], 1);
-      mbar_init(&agree[i], 4);
     }
     fence_mbar_init();
     s_abort = 0;
-    for (int i = 0; i < NS; ++i) s_grew[i] = 0;
   }
   if (warp == kMma) tmem_alloc(&s_tmem, 512);
   if (tid == kTma * 32) {
     prefetch_map(&qmap);
-    if (SHARED) prefetch_map(&qnmap);
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
@@ -670,10 +629,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (slots.used[q] > 0) ok = wait_or_abort(&q_empty[q], (slots.used[q] - 1) & 1, &s_abort, A.status);
             if (!ok) break;
             ++slots.used[q];
-            const bool narrow = SHARED && s.narrow;
-            mbar_arrive_expect_tx(&q_full[q], (uint32_t)((D / 64) * (narrow ? A.TN : A.TQ) * A.G * 128));
+            mbar_arrive_expect_tx(&q_full[q], (uint32_t)((D / 64) * A.TQ * A.G * 128));
             for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(smem_u32(sm) + q * C::QB + c * 128 * 128, narrow ? &qnmap : &qmap, c * 64, s.head * A.G, s.t0 + t * A.TQ, &q_full[q]);
+              tma_load_3d(smem_u32(sm) + q * C::QB + c * 128 * 128, &qmap, c * 64, s.head * A.G, s.t0 + t * A.TQ, &q_full[q]);
           }
         }
         for (int q = 0; q < NS; ++q)
@@ -689,7 +647,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const uint64_t q_desc = umma_desc(smem_u32(sm)), k_desc = umma_desc(smem_u32(sm) + NS * C::QB),
                        v_desc = umma_desc_mn(smem_u32(sm) + NS * C::QB, BN * 128);
         constexpr uint32_t idesc_o = idesc_bf16(128, C::UC) | (1u << 16);  // B (V) is read MN-major
-        const uint32_t idesc_s = idesc_bf16(128, BN) | A.negate;
         while (ok && next_seg(s, false)) {
           const int nb0 = tile_blocks(A, s, 0), nb1 = s.pair ? tile_blocks(A, s, 1) : 0;
           const int n = s.pair ? nb1 : nb0;
@@ -716,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
               for (int x = 0; x < C::UC / 16; ++x) {
                 const uint32_t step = (uint32_t)(((x >> 2) * 128 * 128 + (x & 3) * 32) >> 4);
-                umma_f16(tmem + buf * 128, a + step, b + step, idesc_s, h > 0 || x > 0);
+                umma_f16(tmem + buf * 128, a + step, b + step, A.idesc_s, h > 0 || x > 0);
               }
             }
             umma_commit(&s_full[buf]);
@@ -749,63 +706,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (done)
               for (int h = 0; h < HB; ++h) umma_commit(&empty[(g0 + h) % NU]);
           };
-          // Narrow tiles: S' = K Q^T (rows: keys, columns: queries), O' = V^T P' (rows: channels), P' from shared memory
-          auto issue_s_narrow = [&](int buf, int j) {
-            constexpr uint32_t idesc = idesc_bf16(128, kN);
-            const int g0 = base + k_place(false, j) * HB;
-#pragma unroll
-            for (int h = 0; h < HB; ++h) {
-              unit_ready(g0 + h);
-              if (!ok) return;
-              tc_fence_after();
-              const uint64_t a = k_desc + (uint32_t)(((g0 + h) % NU) * (C::UB >> 4));
-              const uint64_t b = q_desc + (uint32_t)((q_first * C::QB + h * (C::UC / 64) * 128 * 128) >> 4);
-#pragma unroll
-              for (int x = 0; x < C::UC / 16; ++x) {
-                const uint32_t step = (uint32_t)(((x >> 2) * 128 * 128 + (x & 3) * 32) >> 4);
-                umma_f16(tmem + buf * 128, a + step, b + step, idesc | A.negate, h > 0 || x > 0);
-              }
-            }
-            umma_commit(&s_full[buf]);
-            for (int h = 0; h < HB; ++h) umma_commit(&empty[(g0 + h) % NU]);
-          };
-          auto issue_o_narrow = [&](int o, int buf, int j, bool first) {
-            constexpr uint32_t idesc = idesc_bf16(128, kN) | (1u << 15);  // A (V) is read MN-major
-            const int g0 = base + v_place(false, j, n) * HB;
-            if (j == tail) {
-              for (int h = 0; h < HB; ++h) unit_ready(g0 + h);
-              if (ok) mbar_arrive(dirty);
-            }
-            if (ok) ok = wait_or_abort(&p_full[buf], pc[buf] & 1, &s_abort, A.status);
-            if (!ok) return;
-            ++pc[buf];
-            const uint64_t b = q_desc + (uint32_t)((q_first * C::QB + p_narrow(buf)) >> 4);
-#pragma unroll
-            for (int h = 0; h < HB; ++h) {
-              unit_ready(g0 + h);
-              if (ok && j == tail && h == 0) ok = wait_or_abort(clean, cleaned & 1, &s_abort, A.status);
-              if (!ok) return;
-              tc_fence_after();
-              // D = 64: rows 64.. of the product repeat the 64 channels (block stride 0) and are not read
-              const uint64_t a = (D == 64 ? umma_desc_mn(smem_u32(sm) + NS * C::QB, 0) : v_desc) +
-                                 (uint32_t)(((g0 + h) % NU) * (C::UB >> 4));
-#pragma unroll
-              for (int x = 0; x < BN / 16; ++x)
-                umma_f16(tmem + C::kO + o * 64 + h * kN, a + (uint32_t)(x * 2048 >> 4),
-                         b + (uint32_t)(((x >> 2) * kN * 128 + (x & 3) * 32) >> 4), idesc, !first || x > 0);
-            }
-            for (int h = 0; h < HB; ++h) umma_commit(&empty[(g0 + h) % NU]);
-          };
-          if (SHARED && s.narrow) {
-            issue_s_narrow(0, 0);
-            if (ok && n > 1) issue_s_narrow(1, 1);
-            for (int j = 0; ok && j < n; ++j) {
-              const int o = NS == 2 ? (j & 1) : 0;
-              issue_o_narrow(o, j & 1, j, NS == 2 ? j < 2 : j == 0);
-              if (ok && (NS == 1 || j + 2 >= n)) umma_commit(&o_full[o]);
-              if (ok && j + 2 < n) issue_s_narrow(j & 1, j + 2);
-            }
-          } else if (s.pair) {
+          if (s.pair) {
             if (nb0 > 0) issue_s(0, 0, 0, false);
             if (ok) issue_s(1, 1, 0, true);
             for (int j = 0; ok && j < n; ++j) {
@@ -865,156 +766,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       // ---- softmax: thread = row of a tile
       const int grp = warp >> 2, wq = warp & 3, row = (wq << 5) + lane;
       uint32_t sc[2] = {0, 0}, oc = 0;  // S tiles taken from each buffer, O tiles waited for
-      uint32_t ac = 0, gc = 0;          // narrow tiles: exchanges between the four warps, checks for growth
-      QSlots slots;
       bool ok = true;
       while (ok && next_seg(s, true)) {
         const int q = s.pair ? grp : 0;
         const int nb = tile_blocks(A, s, q);
-        const int q_slot = tile_blocks(A, s, s.pair ? 1 : 0) > 0 ? slots.first(s.pair, NS) : 0;
-        if (SHARED && s.narrow) {
-          // thread = key of a block; column n = query row (token n / G, head n % G)
-          float top[kN], sum[kN];
-          int lim[kN];
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            top[i] = -INFINITY;
-            sum[i] = 0.0f;
-            lim[i] = i < s.ntok * A.G ? min(s.len, s.lim0 + s.step * (i / A.G)) : 0;  // other columns see nothing
-          }
-          const uint32_t o_tmem = tmem_at(tmem, wq, C::kO + (NS == 2 ? grp : 0) * 64);
-          // the four warps' values of each column, joined by `op`
-          auto across = [&](float (&x)[kN], auto op) -> bool {
-            if (lane == 0)
-#pragma unroll
-              for (int i = 0; i < kN; i += 4)
-                *reinterpret_cast<float4 *>(&s_col[grp][wq][i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&agree[grp]);
-            if (!warp_wait(&agree[grp], ac++ & 1, &s_abort, A.status)) return false;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) x[i] = op(op(s_col[grp][0][i], s_col[grp][1][i]), op(s_col[grp][2][i], s_col[grp][3][i]));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&agree[grp]);  // read: the next exchange may overwrite them
-            return warp_wait(&agree[grp], ac++ & 1, &s_abort, A.status);
-          };
-          for (int j = NS == 2 ? grp : 0; j < nb; j += NS) {
-            const int buf = j & 1;
-            ok = warp_wait(&s_full[buf], sc[buf] & 1, &s_abort, A.status);
-            if (!ok) break;
-            ++sc[buf];
-            tc_fence_after();
-            const int key = (s.b0 + j) * BN + row;
-            const uint32_t s_at = tmem_at(tmem, wq, buf * 128);
-            unsigned char *p_at = sm + q_slot * C::QB + p_narrow(buf) + (row >> 6) * kN * 128 + (row & 7) * 2;
-            const bool first = j < NS;
-            for (bool agreed = false;; agreed = true) {
-              float x[kN];
-              tmem_ld16_async(s_at, x);
-              tmem_wait_ld();
-              bool grew = false;
-#pragma unroll
-              for (int i = 0; i < kN; ++i) {
-                x[i] = key < lim[i] ? x[i] : -INFINITY;
-                grew = grew || (x[i] - top[i]) * A.c > 8.0f;
-              }
-              if (!agreed && !first) {  // probabilities against the maxima so far, unless a warp saw a column outgrow them
-                grew = __any_sync(0xffffffffu, grew);
-                if (lane == 0) {
-                  if (grew) s_grew[grp] = gc + 1;
-                  mbar_arrive(&agree[grp]);
-                }
-                ok = warp_wait(&agree[grp], ac++ & 1, &s_abort, A.status);
-                if (!ok) break;
-                ++gc;
-                agreed = *reinterpret_cast<volatile uint32_t *>(&s_grew[grp]) != gc;
-              }
-              if (agreed) {
-#pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                  const float p = ex2(fmaf(x[i], A.c, top[i] == -INFINITY ? 0.0f : -top[i] * A.c));
-                  sum[i] += p;
-                  *reinterpret_cast<bf16 *>(p_at + i * 128 + ((((row & 63) >> 3) ^ (i & 7)) << 4)) = __float2bfloat16_rn(p);
-                }
-                break;
-              }
-              float m[kN];
-#pragma unroll
-              for (int i = 0; i < kN; ++i) m[i] = warp_max(x[i]);
-              ok = across(m, [](float a, float b) { return fmaxf(a, b); });
-              if (!ok) break;
-              if (!first && NS == 1) {
-                ok = warp_wait(&o_full[0], (oc + j - 1) & 1, &s_abort, A.status);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              float keep[kN];
-#pragma unroll
-              for (int i = 0; i < kN; ++i) {
-                keep[i] = m[i] > top[i] ? ex2((top[i] - m[i]) * A.c) : 1.0f;
-                top[i] = fmaxf(top[i], m[i]);
-                sum[i] *= keep[i];
-              }
-              if (!first) {
-#pragma unroll 1
-                for (int h = 0; h < HB; ++h) {
-                  float v[kN];
-                  tmem_ld16_async(o_tmem + h * kN, v);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < kN; ++i) v[i] *= keep[i];
-                  tmem_st16(o_tmem + h * kN, v);
-                }
-                tmem_wait_st();
-              }
-            }
-            if (!ok) break;
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[buf]);
-          }
-          if (!ok) break;
-          const int mine = nb > (NS == 2 ? grp : 0) ? (nb - (NS == 2 ? grp : 0) + NS - 1) / NS : 0;
-          if (mine > 0) {
-            const uint32_t ph = NS == 1 ? oc + nb - 1 : oc;
-            if (NS == 1 && nb > 1) ok = warp_wait(&o_full[0], (ph - 1) & 1, &s_abort, A.status);
-            if (ok) ok = warp_wait(&o_full[NS == 2 ? grp : 0], ph & 1, &s_abort, A.status);
-            if (!ok) break;
-            oc += NS == 1 ? nb : 1;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-            ok = across(sum, [](float a, float b) { return a + b; });
-            if (!ok) break;
-          }
-          const int rows = s.own ? A.suffix_rows : A.prefix_rows;
-          const long long tile = (long long)s.slot * NS + grp;
-          if (wq == 0 && lane < s.ntok * A.G) {
-            float2 ml = make_float2(-INFINITY, 0.0f);
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-              if (lane == i && mine > 0) ml = make_float2(top[i] == -INFINITY ? -INFINITY : top[i] * A.c, sum[i]);
-            (s.own ? A.suffix_ml : A.prefix_ml)[tile * rows + lane] = ml;
-          }
-          if (mine > 0) {
-            float *dst = (s.own ? A.suffix_o : A.prefix_o) + tile * rows * D;
-#pragma unroll 1
-            for (int h = 0; h < HB; ++h) {
-              float v[kN];
-              tmem_ld16_async(o_tmem + h * kN, v);
-              tmem_wait_ld();
-              const int d = h * 128 + row;
-              if (d < D)
-#pragma unroll
-                for (int i = 0; i < kN; ++i)
-                  if (i < s.ntok * A.G) dst[((d >> 2) * rows + i) * 4 + (d & 3)] = v[i];
-            }
-          }
-          continue;
-        }
         const int tok = row / A.G + q * A.TQ, gh = row - (row / A.G) * A.G;
         const bool real = row < A.TQ * A.G && tok < s.ntok;
         const bool busy = __any_sync(0xffffffffu, real);  // few query rows leave warps without any
@@ -1260,7 +1015,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     const float4 *po = reinterpret_cast<const float4 *>(part == 0 ? A.prefix_o : A.suffix_o) + (long long)c * rows + row;
     const float2 *pml = (part == 0 ? A.prefix_ml : A.suffix_ml) + row;
     // the CTAs that took some of the line's blocks
-    const bool small = z < (1LL << 31) && share < (1LL << 31);
+    const bool small = z < (1LL << 31);
     const int c0 = small ? (unsigned)(a + kSetup) / (unsigned)share : (int)((a + kSetup) / share);
     const int c1 = small ? (unsigned)(z - 1) / (unsigned)share : (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
     const long long first = ((part == 0 ? shared_line : own_line) + li + c0) * NS + s0;  // part p is tile first + p (+ p with one stream of two)
@@ -1364,11 +1119,11 @@ Args make_args(const gdn_attn_dims *d, void *out, unsigned int *status) {
   A.hk = d->n_kv_heads;
   A.G = d->n_q_heads / d->n_kv_heads;
   A.TQ = 128 / A.G;
-  A.TN = kN / A.G;
   A.tile_tokens = (d->head_dim == 256 ? 1 : 2) * A.TQ;
   // masked scores are -inf: times a scale of exactly zero they would be NaN
   A.c = fmaxf(fabsf(d->scale) * 1.4426950408889634f, 1e-30f);
-  A.negate = d->scale < 0.0f ? 1u << 13 : 0u;
+  // kind::f16, bf16 A and B, fp32 D, N = 128, M = 128; bit 13 negates A for a negative scale
+  A.idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24) | (d->scale < 0.0f ? 1u << 13 : 0u);
   A.kv_rows = d->kv_rows;
   A.out = static_cast<bf16 *>(out);
   A.status = status;
@@ -1378,9 +1133,8 @@ Args make_args(const gdn_attn_dims *d, void *out, unsigned int *status) {
 template <int D, bool SHARED>
 gdn_status launch_t(const gdn_attn_dims *d, const void *q, const void *k, const void *v, const Args &A, int grid,
                     cudaStream_t st) {
-  CUtensorMap qm, qn, km, vm;
+  CUtensorMap qm, km, vm;
   GDN_TRY(encode(&qm, q, D, A.hq, A.n_tokens, d->q_stride, A.G, A.TQ));
-  GDN_TRY(encode(&qn, q, D, A.hq, A.n_tokens, d->q_stride, A.G, A.TN > 0 ? A.TN : 1));  // narrow tiles
   GDN_TRY(encode(&km, k, D, A.hk, A.kv_rows, d->kv_stride, 1, BN));
   GDN_TRY(encode(&vm, v, D, A.hk, A.kv_rows, d->kv_stride, 1, BN));
   const DeviceInfo &dev = device_info();
@@ -1391,7 +1145,7 @@ gdn_status launch_t(const gdn_attn_dims *d, const void *q, const void *k, const 
       return fail(GDN_ERR_CUDA, "attention: cannot reserve shared memory");
     ready[dev.id].store(true, std::memory_order_release);
   }
-  launch_pdl(attn_kernel<D, SHARED>, dim3((unsigned)grid), dim3(Cfg<D>::kThreads), Cfg<D>::kBytes, st, qm, qn, km, vm, A);
+  launch_pdl(attn_kernel<D, SHARED>, dim3((unsigned)grid), dim3(Cfg<D>::kThreads), Cfg<D>::kBytes, st, qm, km, vm, A);
   GDN_TRY(check_launch("attention"));
   if (SHARED) {
     const long long items = (long long)A.n_tokens * A.hq * (D / 4);
