@@ -39,6 +39,7 @@ namespace attn {
 
 constexpr int kMaxCtas = 152;  // CTAs of a shared-prefix call: one per SM
 constexpr int BN = 128;        // keys of a block
+constexpr int kOwnKeys = 2048;
 constexpr int kSetup = 2;      // a segment's queries, first latency and stores, in blocks' time
 
 struct Args {
@@ -46,9 +47,10 @@ struct Args {
   int TQ;           // tokens of one 128-row tile
   int tile_tokens;  // tokens of one CTA's tiles (TQ, or 2 TQ for two query tiles)
   int max_tiles;    // prefill: tiles the grid covers
-  float c;          // |scale| log2(e)
+  float c, c_signed;  // |scale| log2(e), and with the sign
   uint32_t idesc_s; // instruction descriptor of S (the sign of scale)
-  long long kv_rows;
+  long long kv_rows, qs, kvs;
+  const bf16 *q, *k, *v;  // for the join's own loads
   bf16 *out;
   const int32_t *cu, *kv_start, *kv_len;                  // prefill
   const int32_t *group_rows, *prefix_start, *prefix_len;  // shared prefix
@@ -59,6 +61,7 @@ struct Args {
   int prefix_rows, suffix_rows;
   float *prefix_o, *suffix_o;
   float2 *prefix_ml, *suffix_ml;
+  int own_keys;     // rows with at most so many keys of their own have them attended in the join (0: none)
   long long *plan;  // cost per CTA, whether the groups are in order, then per entry (first cost, first line)
 };
 
@@ -120,7 +123,7 @@ __device__ __forceinline__ Entry entry_at(const Args &A, int e, bool all_ok) {
   }
   if (x.ok && x.ntok > 0) {
     x.tiles = (x.ntok + A.tile_tokens - 1) / A.tile_tokens;
-    x.blocks = blocks_of(x.len);
+    x.blocks = e >= A.n_groups && x.len <= A.own_keys ? 0 : blocks_of(x.len);
   }
   return x;
 }
@@ -978,13 +981,62 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partial results of a shared-prefix call: a thread takes four
-// channels of one (query token, head) and goes through its parts in order,
-// kParts of them loaded at once.
+// One part of a row's result: the maximum (in powers of two), the sum and four channels.
+struct Part {
+  float top, sum;
+  float4 o;
+  __device__ __forceinline__ void add(float m, float l, float4 v) {
+    if (l == 0.0f) return;  // saw no key; its channels were not written
+    const float best = fmaxf(top, m), a = top == -INFINITY ? 0.0f : ex2(top - best), w = ex2(m - best);
+    top = best;
+    sum = fmaf(l, w, sum * a);
+    o.x = fmaf(v.x, w, o.x * a);
+    o.y = fmaf(v.y, w, o.y * a);
+    o.z = fmaf(v.z, w, o.z * a);
+    o.w = fmaf(v.w, w, o.w * a);
+  }
+};
+
+// Adds the partial results that the attention kernel left of one entry for channels 4c.. of (token t, head), in
+// order, kParts of them loaded at once.
 constexpr int kParts = 8;
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args A) {
+__device__ __forceinline__ void add_line(const Args &A, Part &P, const Entry &x, int e, bool own, int t, int head, int gh,
+                                         int c, long long share) {
   constexpr int NS = Cfg<D>::NS;
+  if (x.blocks == 0) return;
+  const int ti = t - x.first, tile = ti / A.tile_tokens, i = ti - tile * A.tile_tokens;
+  const bool pair = min(A.tile_tokens, x.ntok - tile * A.tile_tokens) > A.TQ;
+  const long long li = (long long)tile * A.hk + head, a = A.plan[2 + 2 * e] + li * x.line_cost(), z = a + x.line_cost();
+  const int rows = own ? A.suffix_rows : A.prefix_rows;
+  const int streams = NS == 2 && !pair ? 2 : 1, s0 = pair ? i / A.TQ : 0, row = (pair ? i % A.TQ : i) * A.G + gh;
+  const float4 *po = reinterpret_cast<const float4 *>(own ? A.suffix_o : A.prefix_o) + (long long)c * rows + row;
+  const float2 *pml = (own ? A.suffix_ml : A.prefix_ml) + row;
+  // the CTAs that took some of the line's blocks
+  const bool small = z < (1LL << 31) && share < (1LL << 31);
+  const int c0 = small ? (unsigned)(a + kSetup) / (unsigned)share : (int)((a + kSetup) / share);
+  const int c1 = small ? (unsigned)(z - 1) / (unsigned)share : (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
+  const long long first = (A.plan[3 + 2 * e] + li + c0) * NS + s0;
+  const int stride = NS / streams;
+  for (int p0 = 0; p0 < n; p0 += kParts) {
+    float2 ml[kParts];
+    float4 v[kParts];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const long long at = (first + (long long)min(p0 + k, n - 1) * stride) * rows;
+      ml[k] = pml[at];
+      v[k] = po[at * (D / 4)];
+    }
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      if (p0 + k < n) P.add(ml[k].x, ml[k].y, v[k]);
+  }
+}
+
+// Joins the partial results of a shared-prefix call: a thread takes four
+// channels of one (query token, head).
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args A) {
   griddep_wait();
   griddep_trigger();
   // items: (token, key head, channel group, head of the group), the last fastest
@@ -998,65 +1050,191 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
   const int b = t / A.T, g = group_of(A, b);
   const long long share = A.plan[0], in_order = A.plan[1];
   const Entry own = entry_at(A, A.n_groups + b, true), shared = g >= 0 ? entry_at(A, g, true) : own;
-  const long long own_at = A.plan[2 + 2 * (A.n_groups + b)], own_line = A.plan[3 + 2 * (A.n_groups + b)];
-  const long long shared_at = A.plan[2 + 2 * max(g, 0)], shared_line = A.plan[3 + 2 * max(g, 0)];
   if (!in_order || !own.ok || !shared.ok) return;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float top = -INFINITY, sum = 0.0f;
-  const bool real = t - own.first < own.ntok;
-  for (int part = g < 0 ? 1 : 0; real && part < 2; ++part) {
-    const Entry x = part == 0 ? shared : own;
-    if (x.blocks == 0) continue;
-    const int ti = t - x.first, tile = ti / A.tile_tokens, i = ti - tile * A.tile_tokens;
-    const bool pair = min(A.tile_tokens, x.ntok - tile * A.tile_tokens) > A.TQ;
-    const long long li = (long long)tile * A.hk + head, a = (part == 0 ? shared_at : own_at) + li * x.line_cost(), z = a + x.line_cost();
-    const int rows = part == 0 ? A.prefix_rows : A.suffix_rows;
-    const int streams = NS == 2 && !pair ? 2 : 1, s0 = pair ? i / A.TQ : 0, row = (pair ? i % A.TQ : i) * A.G + gh;
-    const float4 *po = reinterpret_cast<const float4 *>(part == 0 ? A.prefix_o : A.suffix_o) + (long long)c * rows + row;
-    const float2 *pml = (part == 0 ? A.prefix_ml : A.suffix_ml) + row;
-    // the CTAs that took some of the line's blocks
-    const bool small = z < (1LL << 31);
-    const int c0 = small ? (unsigned)(a + kSetup) / (unsigned)share : (int)((a + kSetup) / share);
-    const int c1 = small ? (unsigned)(z - 1) / (unsigned)share : (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
-    const long long first = ((part == 0 ? shared_line : own_line) + li + c0) * NS + s0;  // part p is tile first + p (+ p with one stream of two)
-    const int stride = NS / streams;
-    for (int p0 = 0; p0 < n; p0 += kParts) {
-      float2 ml[kParts];
-      float4 v[kParts];
+  Part P = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  if (t - own.first < own.ntok) {
+    if (g >= 0) add_line<D>(A, P, shared, g, false, t, head, gh, c, share);
+    add_line<D>(A, P, own, A.n_groups + b, true, t, head, gh, c, share);
+  }
+  const float inv = 1.0f / P.sum;
+  uint2 r = make_uint2(0u, 0u);
+  if (P.sum != 0.0f) r = make_uint2(pack_bf16(P.o.x * inv, P.o.y * inv), pack_bf16(P.o.z * inv, P.o.w * inv));
+  *reinterpret_cast<uint2 *>(A.out + ((long long)t * A.hq + head * A.G + gh) * D + 4 * c) = r;
+}
+
+// The join of rows with few query rows per key head (T G <= 8: decode steps),
+// which attends over the row's own keys itself: a tile of the tensor cores
+// would hold 4 rows of 128 and cost 4 us of latencies for 1 us of bytes. One
+// CTA per (row, key head); its warps take kLoads loads of keys in turn, 16
+// bytes of a key to a lane and D/8 lanes to a key, for kRows query rows each.
+// None of this reads what the kernel before wrote, so it runs before the wait
+// for it, on the SMs which that kernel leaves; only then the parts are joined.
+// Memory-bound by the keys and values (fp32 arithmetic: 4 rows and 128
+// channels take ~100 instructions for 2 keys, 1 KB).
+constexpr int kRows = 4, kLoads = 4, kJoinWarps = 8;
+
+__device__ __forceinline__ unsigned long long f2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_of(unsigned long long x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long f2_bf16(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) join_rows_kernel(const __grid_constant__ Args A) {
+  constexpr int NS = Cfg<D>::NS, LK = D / 8, KL = 32 / LK;  // lanes of a key, keys of a load
+  __shared__ __align__(16) float s_o[kJoinWarps][kRows][D];
+  __shared__ float2 s_ml[kJoinWarps][kRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane / LK, chunk = lane % LK;
+  const int b = blockIdx.x / A.hk, head = blockIdx.x - b * A.hk, R = A.T * A.G;
+  const int half = R > kRows ? 2 : 1, rb = warp % half, part = warp / half, parts = kJoinWarps / half;
+  const Entry own = entry_at(A, A.n_groups + b, true);
+  const bool here = own.ok && own.len <= A.own_keys;
+
+  // ---- the row's own keys: query rows rb * kRows + r, key loads part, part + parts, ...
+  float top[kRows], sum[kRows];
+  unsigned long long o[kRows][4];
 #pragma unroll
-      for (int k = 0; k < kParts; ++k) {
-        const long long at = (first + (long long)min(p0 + k, n - 1) * stride) * rows;
-        ml[k] = pml[at];
-        v[k] = po[at * (D / 4)];
-        if (p0 + k >= n) ml[k].y = 0.0f;
+  for (int r = 0; r < kRows; ++r) {
+    top[r] = -INFINITY;
+    sum[r] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[r][k] = f2(0.0f, 0.0f);
+  }
+  if (here && own.ntok > 0) {
+    unsigned long long q[kRows][4];
+    int lim[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int row = rb * kRows + r, t = row / A.G;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      lim[r] = row < R && t < own.ntok ? min(own.len, own.lim0 + t) : 0;
+      if (lim[r] > 0)
+        v = *reinterpret_cast<const uint4 *>(A.q + (long long)(own.first + t) * A.qs + (long long)(head * A.G + row - t * A.G) * D + chunk * 8);
+      const unsigned long long c = f2(A.c_signed, A.c_signed), zero = f2(0.0f, 0.0f);
+      q[r][0] = f2_fma(f2_bf16(v.x), c, zero);
+      q[r][1] = f2_fma(f2_bf16(v.y), c, zero);
+      q[r][2] = f2_fma(f2_bf16(v.z), c, zero);
+      q[r][3] = f2_fma(f2_bf16(v.w), c, zero);
+    }
+    const bf16 *kp = A.k + (long long)own.kv0 * A.kvs + (long long)head * D + chunk * 8;
+    const bf16 *vp = A.v + (long long)own.kv0 * A.kvs + (long long)head * D + chunk * 8;
+    for (int j0 = part * kLoads * KL; j0 < own.len; j0 += parts * kLoads * KL) {
+      uint4 kv[kLoads], vv[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int j = j0 + i * KL + sub;
+        const bool in = j < own.len;
+        kv[i] = in ? __ldcs(reinterpret_cast<const uint4 *>(kp + (long long)j * A.kvs)) : make_uint4(0, 0, 0, 0);
+        vv[i] = in ? __ldcs(reinterpret_cast<const uint4 *>(vp + (long long)j * A.kvs)) : make_uint4(0, 0, 0, 0);
       }
-      float m = top;
+      float s[kLoads][kRows];
+      bool grew = false;
 #pragma unroll
-      for (int k = 0; k < kParts; ++k)
-        if (ml[k].y != 0.0f) m = fmaxf(m, ml[k].x);
-      const float keep = top == -INFINITY ? 0.0f : ex2(top - m);
-      top = m;
-      sum *= keep;
-      o.x *= keep;
-      o.y *= keep;
-      o.z *= keep;
-      o.w *= keep;
+      for (int i = 0; i < kLoads; ++i) {
+        const unsigned long long k0 = f2_bf16(kv[i].x), k1 = f2_bf16(kv[i].y), k2 = f2_bf16(kv[i].z), k3 = f2_bf16(kv[i].w);
+        const int j = j0 + i * KL + sub;
 #pragma unroll
-      for (int k = 0; k < kParts; ++k)
-        if (ml[k].y != 0.0f) {  // else the part saw no key, and its numbers were not written
-          const float w = ex2(ml[k].x - m);
-          sum = fmaf(ml[k].y, w, sum);
-          o.x = fmaf(v[k].x, w, o.x);
-          o.y = fmaf(v[k].y, w, o.y);
-          o.z = fmaf(v[k].z, w, o.z);
-          o.w = fmaf(v[k].w, w, o.w);
+        for (int r = 0; r < kRows; ++r) {
+          const float2 x = f2_of(f2_fma(q[r][3], k3, f2_fma(q[r][2], k2, f2_fma(q[r][1], k1, f2_fma(q[r][0], k0, f2(0.0f, 0.0f))))));
+          float y = x.x + x.y;
+#pragma unroll
+          for (int w = LK / 2; w > 0; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+          s[i][r] = j < lim[r] ? y : -INFINITY;
+          grew = grew || s[i][r] - top[r] > 8.0f;
         }
+      }
+      if (__any_sync(0xffffffffu, grew)) {  // as above: the maximum moves only when a row outgrew it by 2^8
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          float m = top[r];
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) m = fmaxf(m, s[i][r]);
+#pragma unroll
+          for (int w = 16; w >= LK; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+          const float keep = m > top[r] ? ex2(top[r] - m) : 1.0f;
+          top[r] = m;
+          sum[r] *= keep;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[r][k] = f2_fma(o[r][k], f2(keep, keep), f2(0.0f, 0.0f));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const unsigned long long v0 = f2_bf16(vv[i].x), v1 = f2_bf16(vv[i].y), v2 = f2_bf16(vv[i].z), v3 = f2_bf16(vv[i].w);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const float p = ex2(s[i][r] - (top[r] == -INFINITY ? 0.0f : top[r]));
+          sum[r] += p;
+          const unsigned long long pp = f2(p, p);
+          o[r][0] = f2_fma(v0, pp, o[r][0]);
+          o[r][1] = f2_fma(v1, pp, o[r][1]);
+          o[r][2] = f2_fma(v2, pp, o[r][2]);
+          o[r][3] = f2_fma(v3, pp, o[r][3]);
+        }
+      }
     }
   }
-  const float inv = 1.0f / sum;
-  uint2 r = make_uint2(0u, 0u);
-  if (sum != 0.0f) r = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  *reinterpret_cast<uint2 *>(A.out + ((long long)t * A.hq + head * A.G + gh) * D + 4 * c) = r;
+  // the warp's keys of a load, joined (they share the maximum), to shared memory
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = f2_of(o[r][k]);
+      v[2 * k] = x.x;
+      v[2 * k + 1] = x.y;
+    }
+#pragma unroll
+    for (int w = 16; w >= LK; w >>= 1) {
+      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], w);
+    }
+    if (sub == 0) {
+      *reinterpret_cast<float4 *>(&s_o[warp][r][chunk * 8]) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(&s_o[warp][r][chunk * 8 + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    if (lane == 0) s_ml[warp][r] = make_float2(top[r], sum[r]);
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_trigger();
+
+  // ---- the parts of four channels of a query row: this CTA's warps', then the prefix's (or the row's, from the kernel before)
+  const int g = group_of(A, b);
+  const Entry shared = g >= 0 ? entry_at(A, g, true) : own;
+  const long long share = A.plan[0], in_order = A.plan[1];
+  if (!in_order || !own.ok || !shared.ok) return;
+  for (int item = tid; item < R * (D / 4); item += kJoinWarps * 32) {
+    const int c = item / R, row = item - c * R, t = row / A.G, gh = row - t * A.G;
+    Part P = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+    if (t < own.ntok) {
+      for (int w = 0; here && w < parts; ++w) {
+        const int ww = w * half + row / kRows;
+        const float2 ml = s_ml[ww][row % kRows];
+        P.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(&s_o[ww][row % kRows][4 * c]));
+      }
+      for (int x = g < 0 ? 1 : 0; x < 2; ++x)
+        add_line<D>(A, P, x == 0 ? shared : own, x == 0 ? g : A.n_groups + b, x == 1, own.first + t, head, gh, c, share);
+    }
+    uint2 r = make_uint2(0u, 0u);
+    const float inv = 1.0f / P.sum;
+    if (P.sum != 0.0f) r = make_uint2(pack_bf16(P.o.x * inv, P.o.y * inv), pack_bf16(P.o.z * inv, P.o.w * inv));
+    *reinterpret_cast<uint2 *>(A.out + ((long long)(own.first + t) * A.hq + head * A.G + gh) * D + 4 * c) = r;
+  }
 }
 
 // --------------------------------------------------------------------- host
@@ -1122,6 +1300,7 @@ Args make_args(const gdn_attn_dims *d, void *out, unsigned int *status) {
   A.tile_tokens = (d->head_dim == 256 ? 1 : 2) * A.TQ;
   // masked scores are -inf: times a scale of exactly zero they would be NaN
   A.c = fmaxf(fabsf(d->scale) * 1.4426950408889634f, 1e-30f);
+  A.c_signed = d->scale * 1.4426950408889634f;
   // kind::f16, bf16 A and B, fp32 D, N = 128, M = 128; bit 13 negates A for a negative scale
   A.idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24) | (d->scale < 0.0f ? 1u << 13 : 0u);
   A.kv_rows = d->kv_rows;
@@ -1149,7 +1328,10 @@ gdn_status launch_t(const gdn_attn_dims *d, const void *q, const void *k, const 
   GDN_TRY(check_launch("attention"));
   if (SHARED) {
     const long long items = (long long)A.n_tokens * A.hq * (D / 4);
-    launch_pdl(join_kernel<D>, dim3((unsigned)((items + 127) / 128)), dim3(128), 0, st, A);
+    if (A.own_keys > 0)
+      launch_pdl(join_rows_kernel<D>, dim3((unsigned)(A.B * A.hk)), dim3(kJoinWarps * 32), 0, st, A);
+    else
+      launch_pdl(join_kernel<D>, dim3((unsigned)((items + 127) / 128)), dim3(128), 0, st, A);
   }
   return check_launch("attention");
 }
@@ -1265,6 +1447,12 @@ gdn_status gdn_attn_shared_prefix(const gdn_attn_dims *d, const void *q, const v
   A.suffix_start = suffix_start;
   A.suffix_len = suffix_len;
   A.q_len = q_len;
+  A.q = static_cast<const bf16 *>(q);
+  A.k = static_cast<const bf16 *>(k);
+  A.v = static_cast<const bf16 *>(v);
+  A.qs = d->q_stride;
+  A.kvs = d->kv_stride;
+  A.own_keys = d->T * A.G <= 2 * attn::kRows && (long long)d->B * A.hk < (1LL << 31) ? attn::kOwnKeys : 0;
   const int grid = dev->sms < attn::kMaxCtas ? dev->sms : attn::kMaxCtas;
   return attn::launch<true>(d, q, k, v, A, grid, static_cast<cudaStream_t>(stream));
 }
