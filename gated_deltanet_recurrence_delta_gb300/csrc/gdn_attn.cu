@@ -1065,13 +1065,13 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
 // The join of rows with few query rows per key head (T G <= 8: decode steps),
 // which attends over the row's own keys itself: a tile of the tensor cores
 // would hold 4 rows of 128 and cost 4 us of latencies for 1 us of bytes. One
-// CTA per (row, key head); its warps take kLoads loads of keys in turn, 16
-// bytes of a key to a lane and D/8 lanes to a key, for kRows query rows each.
+// CTA per (row, key head). Each warp copies tiles of 2048 / D keys (4 KB) and
+// their values to two stages of its own (cp.async); for the scores D / 64 lanes
+// share a key and hold a partial product of every query row, for the values a
+// lane owns D / 32 channels: ~30 instructions a key for 4 rows of 128 channels.
 // None of this reads what the kernel before wrote, so it runs before the wait
 // for it, on the SMs which that kernel leaves; only then the parts are joined.
-// Memory-bound by the keys and values (fp32 arithmetic: 4 rows and 128
-// channels take ~100 instructions for 2 keys, 1 KB).
-constexpr int kRows = 4, kLoads = 4, kJoinWarps = 8;
+constexpr int kJoinWarps = 4, kJoinStages = 2;
 
 __device__ __forceinline__ unsigned long long f2(float a, float b) {
   unsigned long long r;
@@ -1092,128 +1092,186 @@ __device__ __forceinline__ unsigned long long f2_bf16(uint32_t w) {
   return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32, 2) join_rows_kernel(const __grid_constant__ Args A) {
-  constexpr int NS = Cfg<D>::NS, LK = D / 8, KL = 32 / LK;  // lanes of a key, keys of a load
-  __shared__ __align__(16) float s_o[kJoinWarps][kRows][D];
-  __shared__ float2 s_ml[kJoinWarps][kRows];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane / LK, chunk = lane % LK;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.commit_group;\ncp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D, int RB>  // RB: query rows held, 4 or 8
+struct JoinSmem {
+  static constexpr int KT = 2048 / D;          // keys of a tile
+  static constexpr int kTile = 4096;           // bytes of its keys, and of its values
+  static constexpr int kRing = kJoinWarps * kJoinStages * 2 * kTile;
+  static constexpr int kQ = kRing;             // fp32 [RB][D]
+  static constexpr int kP = kQ + RB * D * 4;   // fp32 [warps][KT][RB]
+  static constexpr int kMl = kP + kJoinWarps * KT * RB * 4;  // float2 [warps][RB]
+  static constexpr int kBytes = kMl + kJoinWarps * RB * 8;
+  static_assert(kJoinWarps * RB * D * 4 <= kRing, "the warps' results fit over the ring");
+};
+
+template <int D, int RB>
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) join_rows_kernel(const __grid_constant__ Args A) {
+  using S = JoinSmem<D, RB>;
+  constexpr int LPK = D / 64, KT = S::KT, VC = D / 32;  // lanes of a key, keys of a tile, channels of a lane
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  float *s_q = reinterpret_cast<float *>(smem_raw + S::kQ);
+  float2 *s_ml = reinterpret_cast<float2 *>(smem_raw + S::kMl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / A.hk, head = blockIdx.x - b * A.hk, R = A.T * A.G;
-  const int half = R > kRows ? 2 : 1, rb = warp % half, part = warp / half, parts = kJoinWarps / half;
   const Entry own = entry_at(A, A.n_groups + b, true);
   const bool here = own.ok && own.len <= A.own_keys;
 
-  // ---- the row's own keys: query rows rb * kRows + r, key loads part, part + parts, ...
-  float top[kRows], sum[kRows];
-  unsigned long long o[kRows][4];
+  float top[RB], sum[RB], o[RB][VC];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
+  for (int r = 0; r < RB; ++r) {
     top[r] = -INFINITY;
     sum[r] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[r][k] = f2(0.0f, 0.0f);
+    for (int k = 0; k < VC; ++k) o[r][k] = 0.0f;
   }
   if (here && own.ntok > 0) {
-    unsigned long long q[kRows][4];
-    int lim[kRows];
+    unsigned char *ring = smem_raw + warp * kJoinStages * 2 * S::kTile;
+    float *s_p = reinterpret_cast<float *>(smem_raw + S::kP) + warp * KT * RB;
+    const bf16 *kp = A.k + (long long)own.kv0 * A.kvs + (long long)head * D;
+    const bf16 *vp = A.v + (long long)own.kv0 * A.kvs + (long long)head * D;
+    const int tiles = (own.len + KT - 1) / KT, mine = (tiles - warp + kJoinWarps - 1) / kJoinWarps;
+    auto fetch = [&](int i) {  // this warp's i-th tile
+      if (i < mine) {
+        const int j0 = (warp + i * kJoinWarps) * KT;
+        const uint32_t k_dst = smem_u32(ring) + (i % kJoinStages) * 2 * S::kTile, v_dst = k_dst + S::kTile;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int row = rb * kRows + r, t = row / A.G;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      lim[r] = row < R && t < own.ntok ? min(own.len, own.lim0 + t) : 0;
-      if (lim[r] > 0)
-        v = *reinterpret_cast<const uint4 *>(A.q + (long long)(own.first + t) * A.qs + (long long)(head * A.G + row - t * A.G) * D + chunk * 8);
-      const unsigned long long c = f2(A.c_signed, A.c_signed), zero = f2(0.0f, 0.0f);
-      q[r][0] = f2_fma(f2_bf16(v.x), c, zero);
-      q[r][1] = f2_fma(f2_bf16(v.y), c, zero);
-      q[r][2] = f2_fma(f2_bf16(v.z), c, zero);
-      q[r][3] = f2_fma(f2_bf16(v.w), c, zero);
-    }
-    const bf16 *kp = A.k + (long long)own.kv0 * A.kvs + (long long)head * D + chunk * 8;
-    const bf16 *vp = A.v + (long long)own.kv0 * A.kvs + (long long)head * D + chunk * 8;
-    for (int j0 = part * kLoads * KL; j0 < own.len; j0 += parts * kLoads * KL) {
-      uint4 kv[kLoads], vv[kLoads];
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int j = j0 + i * KL + sub;
-        const bool in = j < own.len;
-        kv[i] = in ? __ldcs(reinterpret_cast<const uint4 *>(kp + (long long)j * A.kvs)) : make_uint4(0, 0, 0, 0);
-        vv[i] = in ? __ldcs(reinterpret_cast<const uint4 *>(vp + (long long)j * A.kvs)) : make_uint4(0, 0, 0, 0);
+        for (int x = 0; x < 8; ++x) {
+          const int at = x * 32 + lane, key = at / (D / 8), c = at % (D / 8), j = j0 + key;
+          const bool in = j < own.len;  // rows past the end arrive as zeros
+          const long long src = (long long)(in ? j : 0) * A.kvs + c * 8;
+          cp_async16(k_dst + key * D * 2 + ((c ^ ((key * LPK) & 7)) << 4), kp + src, in);
+          cp_async16(v_dst + at * 16, vp + src, in);
+        }
       }
-      float s[kLoads][kRows];
+    };
+    fetch(0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    // the queries, scaled, once for the CTA
+    for (int x = tid; x < RB * D / 8; x += kJoinWarps * 32) {
+      const int row = x / (D / 8), c = x % (D / 8), t = row / A.G;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row < R && t < own.ntok)
+        v = *reinterpret_cast<const uint4 *>(A.q + (long long)(own.first + t) * A.qs +
+                                             (long long)(head * A.G + row - t * A.G) * D + c * 8);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<float2 *>(s_q + row * D + c * 8 + 2 * k) =
+            make_float2(__uint_as_float(w[k] << 16) * A.c_signed, __uint_as_float(w[k] & 0xffff0000u) * A.c_signed);
+    }
+    __syncthreads();
+    int lim[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) lim[r] = r < R && r / A.G < own.ntok ? min(own.len, own.lim0 + r / A.G) : 0;
+    const int key = lane / LPK, part = lane % LPK;
+    for (int i = 0; i < mine; ++i) {
+      fetch(i + 1);
+      cp_async_wait<1>();  // tile i has landed
+      __syncwarp();
+      const unsigned char *kt = ring + (i % kJoinStages) * 2 * S::kTile, *vt = kt + S::kTile;
+      unsigned long long acc[RB];
+#pragma unroll
+      for (int r = 0; r < RB; ++r) acc[r] = f2(0.0f, 0.0f);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int c = x * LPK + part;
+        const uint4 u = *reinterpret_cast<const uint4 *>(kt + key * D * 2 + ((c ^ ((key * LPK) & 7)) << 4));
+        const unsigned long long k0 = f2_bf16(u.x), k1 = f2_bf16(u.y), k2 = f2_bf16(u.z), k3 = f2_bf16(u.w);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const ulonglong2 qa = *reinterpret_cast<const ulonglong2 *>(s_q + r * D + c * 8);
+          const ulonglong2 qb = *reinterpret_cast<const ulonglong2 *>(s_q + r * D + c * 8 + 4);
+          acc[r] = f2_fma(qa.x, k0, f2_fma(qa.y, k1, f2_fma(qb.x, k2, f2_fma(qb.y, k3, acc[r]))));
+        }
+      }
+      const int j = (warp + i * kJoinWarps) * KT + key;
+      float sc[RB];
       bool grew = false;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const unsigned long long k0 = f2_bf16(kv[i].x), k1 = f2_bf16(kv[i].y), k2 = f2_bf16(kv[i].z), k3 = f2_bf16(kv[i].w);
-        const int j = j0 + i * KL + sub;
+      for (int r = 0; r < RB; ++r) {
+        const float2 x = f2_of(acc[r]);
+        float y = x.x + x.y;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const float2 x = f2_of(f2_fma(q[r][3], k3, f2_fma(q[r][2], k2, f2_fma(q[r][1], k1, f2_fma(q[r][0], k0, f2(0.0f, 0.0f))))));
-          float y = x.x + x.y;
-#pragma unroll
-          for (int w = LK / 2; w > 0; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-          s[i][r] = j < lim[r] ? y : -INFINITY;
-          grew = grew || s[i][r] - top[r] > 8.0f;
-        }
+        for (int w = LPK / 2; w > 0; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+        sc[r] = j < lim[r] ? y : -INFINITY;
+        grew = grew || sc[r] - top[r] > 8.0f;
       }
       if (__any_sync(0xffffffffu, grew)) {  // as above: the maximum moves only when a row outgrew it by 2^8
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          float m = top[r];
+        for (int r = 0; r < RB; ++r) {
+          float m = fmaxf(top[r], sc[r]);
 #pragma unroll
-          for (int i = 0; i < kLoads; ++i) m = fmaxf(m, s[i][r]);
-#pragma unroll
-          for (int w = 16; w >= LK; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+          for (int w = 16; w >= LPK; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
           const float keep = m > top[r] ? ex2(top[r] - m) : 1.0f;
           top[r] = m;
           sum[r] *= keep;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[r][k] = f2_fma(o[r][k], f2(keep, keep), f2(0.0f, 0.0f));
+          for (int k = 0; k < VC; ++k) o[r][k] *= keep;
         }
       }
+      float pr[RB];
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const unsigned long long v0 = f2_bf16(vv[i].x), v1 = f2_bf16(vv[i].y), v2 = f2_bf16(vv[i].z), v3 = f2_bf16(vv[i].w);
+      for (int r = 0; r < RB; ++r) {
+        pr[r] = ex2(sc[r] - (top[r] == -INFINITY ? 0.0f : top[r]));
+        if (part == 0) sum[r] += pr[r];
+      }
+      if (part == 0)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const float p = ex2(s[i][r] - (top[r] == -INFINITY ? 0.0f : top[r]));
-          sum[r] += p;
-          const unsigned long long pp = f2(p, p);
-          o[r][0] = f2_fma(v0, pp, o[r][0]);
-          o[r][1] = f2_fma(v1, pp, o[r][1]);
-          o[r][2] = f2_fma(v2, pp, o[r][2]);
-          o[r][3] = f2_fma(v3, pp, o[r][3]);
+        for (int r = 0; r < RB; r += 4)
+          *reinterpret_cast<float4 *>(s_p + key * RB + r) = make_float4(pr[r], pr[r + 1], pr[r + 2], pr[r + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int kk = 0; kk < KT; ++kk) {
+        float v[VC];
+        const unsigned char *at = vt + kk * D * 2 + lane * VC * 2;
+        uint32_t w[VC / 2];
+        if (VC == 2) w[0] = *reinterpret_cast<const uint32_t *>(at);
+        if (VC == 4) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(at);
+        if (VC == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(at);
+#pragma unroll
+        for (int k = 0; k < VC / 2; ++k) {
+          v[2 * k] = __uint_as_float(w[k] << 16);
+          v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+#pragma unroll
+        for (int r4 = 0; r4 < RB; r4 += 4) {
+          const float4 p4 = *reinterpret_cast<const float4 *>(s_p + kk * RB + r4);
+          const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int k = 0; k < VC; ++k) o[r4 + r][k] = fmaf(p[r], v[k], o[r4 + r][k]);
         }
       }
+      __syncwarp();  // the stage and the probabilities may be overwritten
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
-  // the warp's keys of a load, joined (they share the maximum), to shared memory
+  __syncthreads();  // every warp is done with the ring: its memory takes the results, fp32 [warps][RB][D]
+  float *s_o = reinterpret_cast<float *>(smem_raw);
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    float v[8];
+  for (int r = 0; r < RB; ++r) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 x = f2_of(o[r][k]);
-      v[2 * k] = x.x;
-      v[2 * k + 1] = x.y;
-    }
+    for (int w = 16; w > 0; w >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], w);
+    if (lane == 0) s_ml[warp * RB + r] = make_float2(top[r], sum[r]);
+    float *dst = s_o + (warp * RB + r) * D + lane * VC;
 #pragma unroll
-    for (int w = 16; w >= LK; w >>= 1) {
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], w);
-    }
-    if (sub == 0) {
-      *reinterpret_cast<float4 *>(&s_o[warp][r][chunk * 8]) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4 *>(&s_o[warp][r][chunk * 8 + 4]) = make_float4(v[4], v[5], v[6], v[7]);
-    }
-    if (lane == 0) s_ml[warp][r] = make_float2(top[r], sum[r]);
+    for (int k = 0; k < VC; ++k) dst[k] = o[r][k];
   }
   __syncthreads();
   griddep_wait();
   griddep_trigger();
 
-  // ---- the parts of four channels of a query row: this CTA's warps', then the prefix's (or the row's, from the kernel before)
+  // ---- the parts of four channels of a query row: the warps', then the prefix's (and the row's own, if the kernel
+  // before took it)
   const int g = group_of(A, b);
   const Entry shared = g >= 0 ? entry_at(A, g, true) : own;
   const long long share = A.plan[0], in_order = A.plan[1];
@@ -1222,19 +1280,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_rows_kernel(const __g
     const int c = item / R, row = item - c * R, t = row / A.G, gh = row - t * A.G;
     Part P = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
     if (t < own.ntok) {
-      for (int w = 0; here && w < parts; ++w) {
-        const int ww = w * half + row / kRows;
-        const float2 ml = s_ml[ww][row % kRows];
-        P.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(&s_o[ww][row % kRows][4 * c]));
+      for (int w = 0; here && w < kJoinWarps; ++w) {
+        const float2 ml = s_ml[w * RB + row];
+        P.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(s_o + (w * RB + row) * D + 4 * c));
       }
-      for (int x = g < 0 ? 1 : 0; x < 2; ++x)
-        add_line<D>(A, P, x == 0 ? shared : own, x == 0 ? g : A.n_groups + b, x == 1, own.first + t, head, gh, c, share);
+      if (g >= 0) add_line<D>(A, P, shared, g, false, own.first + t, head, gh, c, share);
+      add_line<D>(A, P, own, A.n_groups + b, true, own.first + t, head, gh, c, share);
     }
     uint2 r = make_uint2(0u, 0u);
     const float inv = 1.0f / P.sum;
     if (P.sum != 0.0f) r = make_uint2(pack_bf16(P.o.x * inv, P.o.y * inv), pack_bf16(P.o.z * inv, P.o.w * inv));
     *reinterpret_cast<uint2 *>(A.out + ((long long)(own.first + t) * A.hq + head * A.G + gh) * D + 4 * c) = r;
   }
+}
+
+template <int D, int RB>
+gdn_status launch_join_rows(const Args &A, cudaStream_t st) {
+  constexpr int bytes = JoinSmem<D, RB>::kBytes;
+  const DeviceInfo &dev = device_info();
+  static std::atomic<bool> ready[kMaxDevices];
+  if (!ready[dev.id].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(join_rows_kernel<D, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return fail(GDN_ERR_CUDA, "attention: cannot reserve shared memory");
+    ready[dev.id].store(true, std::memory_order_release);
+  }
+  launch_pdl(join_rows_kernel<D, RB>, dim3((unsigned)(A.B * A.hk)), dim3(kJoinWarps * 32), bytes, st, A);
+  return check_launch("attention");
 }
 
 // --------------------------------------------------------------------- host
@@ -1328,10 +1399,8 @@ gdn_status launch_t(const gdn_attn_dims *d, const void *q, const void *k, const 
   GDN_TRY(check_launch("attention"));
   if (SHARED) {
     const long long items = (long long)A.n_tokens * A.hq * (D / 4);
-    if (A.own_keys > 0)
-      launch_pdl(join_rows_kernel<D>, dim3((unsigned)(A.B * A.hk)), dim3(kJoinWarps * 32), 0, st, A);
-    else
-      launch_pdl(join_kernel<D>, dim3((unsigned)((items + 127) / 128)), dim3(128), 0, st, A);
+    if (A.own_keys > 0) return A.T * A.G <= 4 ? launch_join_rows<D, 4>(A, st) : launch_join_rows<D, 8>(A, st);
+    launch_pdl(join_kernel<D>, dim3((unsigned)((items + 127) / 128)), dim3(128), 0, st, A);
   }
   return check_launch("attention");
 }
@@ -1452,7 +1521,7 @@ gdn_status gdn_attn_shared_prefix(const gdn_attn_dims *d, const void *q, const v
   A.v = static_cast<const bf16 *>(v);
   A.qs = d->q_stride;
   A.kvs = d->kv_stride;
-  A.own_keys = d->T * A.G <= 2 * attn::kRows && (long long)d->B * A.hk < (1LL << 31) ? attn::kOwnKeys : 0;
+  A.own_keys = d->T * A.G <= 8 && (long long)d->B * A.hk < (1LL << 31) ? attn::kOwnKeys : 0;
   const int grid = dev->sms < attn::kMaxCtas ? dev->sms : attn::kMaxCtas;
   return attn::launch<true>(d, q, k, v, A, grid, static_cast<cudaStream_t>(stream));
 }
