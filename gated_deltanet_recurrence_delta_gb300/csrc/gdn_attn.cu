@@ -1062,209 +1062,185 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
   *reinterpret_cast<uint2 *>(A.out + ((long long)t * A.hq + head * A.G + gh) * D + 4 * c) = r;
 }
 
-// The join of rows with few query rows per key head (T G <= 8: decode steps),
-// which attends over the row's own keys itself: a tile of the tensor cores
-// would hold 4 rows of 128 and cost 4 us of latencies for 1 us of bytes. One
-// CTA per (row, key head). Each warp copies tiles of 2048 / D keys (4 KB) and
-// their values to two stages of its own (cp.async); for the scores D / 64 lanes
-// share a key and hold a partial product of every query row, for the values a
-// lane owns D / 32 channels: ~30 instructions a key for 4 rows of 128 channels.
+// The join of rows with few query rows per key head (T G <= 16: decode steps,
+// short verifies), which attends over the row's own keys itself. A tile of
+// tcgen05 has 128 rows: with 4 of them real, a segment of the kernel above took
+// 4 us of latencies for 1 us of bytes. Here a CTA of four warps takes one (row,
+// key head); each warp copies tiles of 16 keys and values to stages of its own
+// (cp.async) and multiplies them with the 16-row products of the warp-level
+// tensor instruction, whose fragments stay in registers from the scores to the
+// values. The job is bytes, not products: ~6 instructions a key of 512 bytes
+// (on the fp32 units ~60, which bounded it at half the memory rate).
 // None of this reads what the kernel before wrote, so it runs before the wait
 // for it, on the SMs which that kernel leaves; only then the parts are joined.
-constexpr int kJoinWarps = 4, kJoinStages = 2;
-
-__device__ __forceinline__ unsigned long long f2(float a, float b) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 f2_of(unsigned long long x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b, unsigned long long c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ unsigned long long f2_bf16(uint32_t w) {
-  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
+constexpr int kJoinWarps = 4, kRows = 16, kTileKeys = 16;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.commit_group;\ncp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// c[16][8] += a[16][16] b[16][8]
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int RB>  // RB: query rows held, 4 or 8
+template <int D>
 struct JoinSmem {
-  static constexpr int KT = 2048 / D;          // keys of a tile
-  static constexpr int kTile = 4096;           // bytes of its keys, and of its values
-  static constexpr int kRing = kJoinWarps * kJoinStages * 2 * kTile;
-  static constexpr int kQ = kRing;             // fp32 [RB][D]
-  static constexpr int kP = kQ + RB * D * 4;   // fp32 [warps][KT][RB]
-  static constexpr int kMl = kP + kJoinWarps * KT * RB * 4;  // float2 [warps][RB]
-  static constexpr int kBytes = kMl + kJoinWarps * RB * 8;
-  static_assert(kJoinWarps * RB * D * 4 <= kRing, "the warps' results fit over the ring");
+  static constexpr int kTile = kTileKeys * D * 2;             // bytes of a tile's keys, and of its values
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kWarp = kStages * 2 * kTile;           // a warp's ring
+  static constexpr int kMl = kJoinWarps * kWarp;              // float2 [warps][kRows]
+  static constexpr int kBytes = kMl + kJoinWarps * kRows * 8;
+  static_assert(kRows * D * 4 <= kWarp, "a warp's results fit over its ring");
 };
 
-template <int D, int RB>
-__global__ void __launch_bounds__(kJoinWarps * 32, 3) join_rows_kernel(const __grid_constant__ Args A) {
-  using S = JoinSmem<D, RB>;
-  constexpr int LPK = D / 64, KT = S::KT, VC = D / 32;  // lanes of a key, keys of a tile, channels of a lane
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) join_rows_kernel(const __grid_constant__ Args A) {
+  using S = JoinSmem<D>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  float *s_q = reinterpret_cast<float *>(smem_raw + S::kQ);
   float2 *s_ml = reinterpret_cast<float2 *>(smem_raw + S::kMl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / A.hk, head = blockIdx.x - b * A.hk, R = A.T * A.G;
   const Entry own = entry_at(A, A.n_groups + b, true);
   const bool here = own.ok && own.len <= A.own_keys;
+  unsigned char *ring = smem_raw + warp * S::kWarp;
 
-  float top[RB], sum[RB], o[RB][VC];
+  // this thread's rows of a product: lane / 4 and lane / 4 + 8
+  float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+  float o[D / 8][4];
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    top[r] = -INFINITY;
-    sum[r] = 0.0f;
+  for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-    for (int k = 0; k < VC; ++k) o[r][k] = 0.0f;
-  }
+    for (int k = 0; k < 4; ++k) o[n][k] = 0.0f;
   if (here && own.ntok > 0) {
-    unsigned char *ring = smem_raw + warp * kJoinStages * 2 * S::kTile;
-    float *s_p = reinterpret_cast<float *>(smem_raw + S::kP) + warp * KT * RB;
     const bf16 *kp = A.k + (long long)own.kv0 * A.kvs + (long long)head * D;
     const bf16 *vp = A.v + (long long)own.kv0 * A.kvs + (long long)head * D;
-    const int tiles = (own.len + KT - 1) / KT, mine = (tiles - warp + kJoinWarps - 1) / kJoinWarps;
-    auto fetch = [&](int i) {  // this warp's i-th tile
+    const int tiles = (own.len + kTileKeys - 1) / kTileKeys, mine = (tiles - warp + kJoinWarps - 1) / kJoinWarps;
+    auto fetch = [&](int i) {  // this warp's i-th tile; 16-byte chunk c of key j at place c ^ (j % 8)
       if (i < mine) {
-        const int j0 = (warp + i * kJoinWarps) * KT;
-        const uint32_t k_dst = smem_u32(ring) + (i % kJoinStages) * 2 * S::kTile, v_dst = k_dst + S::kTile;
+        const int j0 = (warp + i * kJoinWarps) * kTileKeys;
+        const uint32_t dst = smem_u32(ring) + (i % S::kStages) * 2 * S::kTile;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int at = x * 32 + lane, key = at / (D / 8), c = at % (D / 8), j = j0 + key;
-          const bool in = j < own.len;  // rows past the end arrive as zeros
-          const long long src = (long long)(in ? j : 0) * A.kvs + c * 8;
-          cp_async16(k_dst + key * D * 2 + ((c ^ ((key * LPK) & 7)) << 4), kp + src, in);
-          cp_async16(v_dst + at * 16, vp + src, in);
+        for (int x = 0; x < D / 16; ++x) {
+          const int at = x * 32 + lane, key = at / (D / 8), c = at % (D / 8);
+          const bool in = j0 + key < own.len;  // rows past the end arrive as zeros
+          const long long src = (long long)(in ? j0 + key : 0) * A.kvs + c * 8;
+          const uint32_t to = dst + key * D * 2 + ((c ^ (key & 7)) << 4);
+          cp_async16(to, kp + src, in);
+          cp_async16(to + S::kTile, vp + src, in);
         }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(0);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    // the queries, scaled, once for the CTA
-    for (int x = tid; x < RB * D / 8; x += kJoinWarps * 32) {
-      const int row = x / (D / 8), c = x % (D / 8), t = row / A.G;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < R && t < own.ntok)
-        v = *reinterpret_cast<const uint4 *>(A.q + (long long)(own.first + t) * A.qs +
-                                             (long long)(head * A.G + row - t * A.G) * D + c * 8);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<float2 *>(s_q + row * D + c * 8 + 2 * k) =
-            make_float2(__uint_as_float(w[k] << 16) * A.c_signed, __uint_as_float(w[k] & 0xffff0000u) * A.c_signed);
+    for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
+    // query fragments: rows lane / 4 (+ 8), channels 2 (lane % 4) (+ 8) of each 16
+    uint32_t q[D / 16][4];
+    int lim[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = lane / 4 + 8 * h, t = row / A.G;
+      const bool in = row < R && t < own.ntok;
+      lim[h] = in ? min(own.len, own.lim0 + t) : 0;
+      const bf16 *src = A.q + (long long)(own.first + (in ? t : 0)) * A.qs +
+                        (long long)(head * A.G + (in ? row - t * A.G : 0)) * D + 2 * (lane & 3);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][h] = in ? *reinterpret_cast<const uint32_t *>(src + 16 * k) : 0u;
+        q[k][h + 2] = in ? *reinterpret_cast<const uint32_t *>(src + 16 * k + 8) : 0u;
+      }
     }
-    __syncthreads();
-    int lim[RB];
-#pragma unroll
-    for (int r = 0; r < RB; ++r) lim[r] = r < R && r / A.G < own.ntok ? min(own.len, own.lim0 + r / A.G) : 0;
-    const int key = lane / LPK, part = lane % LPK;
+    const int m = lane >> 3, mr = lane & 7;  // the matrix of an ldmatrix that this lane addresses, and its row
     for (int i = 0; i < mine; ++i) {
-      fetch(i + 1);
-      cp_async_wait<1>();  // tile i has landed
+      fetch(i + S::kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");  // tile i has landed
       __syncwarp();
-      const unsigned char *kt = ring + (i % kJoinStages) * 2 * S::kTile, *vt = kt + S::kTile;
-      unsigned long long acc[RB];
+      const uint32_t kt = smem_u32(ring) + (i % S::kStages) * 2 * S::kTile, vt = kt + S::kTile;
+      float sc[2][4] = {};  // keys 0-7 and 8-15: rows lane / 4 and + 8, keys 2 (lane % 4) and + 1
 #pragma unroll
-      for (int r = 0; r < RB; ++r) acc[r] = f2(0.0f, 0.0f);
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t f[4];
+        ldmatrix4(f, kt + ((m >> 1) * 8 + mr) * D * 2 + (((2 * k + (m & 1)) ^ mr) << 4));
+        mma16816(sc[0], q[k], f[0], f[1]);
+        mma16816(sc[1], q[k], f[2], f[3]);
+      }
+      const int j = (warp + i * kJoinWarps) * kTileKeys + 2 * (lane & 3);
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int c = x * LPK + part;
-        const uint4 u = *reinterpret_cast<const uint4 *>(kt + key * D * 2 + ((c ^ ((key * LPK) & 7)) << 4));
-        const unsigned long long k0 = f2_bf16(u.x), k1 = f2_bf16(u.y), k2 = f2_bf16(u.z), k3 = f2_bf16(u.w);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const ulonglong2 qa = *reinterpret_cast<const ulonglong2 *>(s_q + r * D + c * 8);
-          const ulonglong2 qb = *reinterpret_cast<const ulonglong2 *>(s_q + r * D + c * 8 + 4);
-          acc[r] = f2_fma(qa.x, k0, f2_fma(qa.y, k1, f2_fma(qb.x, k2, f2_fma(qb.y, k3, acc[r]))));
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float &x = sc[n][2 * h + e];
+            x = j + 8 * n + e < lim[h] ? x * A.c_signed : -INFINITY;
+            mx[h] = fmaxf(mx[h], x);
+          }
+      // as above: the maximum moves only when a row outgrew it by 2^8
+      if (__any_sync(0xffffffffu, mx[0] - top[0] > 8.0f || mx[1] - top[1] > 8.0f)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float best = fmaxf(top[h], mx[h]);
+          best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+          best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+          const float keep = best > top[h] ? ex2(top[h] - best) : 1.0f;
+          top[h] = best;
+          sum[h] *= keep;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[n][2 * h] *= keep;
+            o[n][2 * h + 1] *= keep;
+          }
         }
       }
-      const int j = (warp + i * kJoinWarps) * KT + key;
-      float sc[RB];
-      bool grew = false;
+      uint32_t p[4];
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        const float2 x = f2_of(acc[r]);
-        float y = x.x + x.y;
+      for (int h = 0; h < 2; ++h) {
+        const float shift = top[h] == -INFINITY ? 0.0f : top[h];
 #pragma unroll
-        for (int w = LPK / 2; w > 0; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-        sc[r] = j < lim[r] ? y : -INFINITY;
-        grew = grew || sc[r] - top[r] > 8.0f;
-      }
-      if (__any_sync(0xffffffffu, grew)) {  // as above: the maximum moves only when a row outgrew it by 2^8
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          float m = fmaxf(top[r], sc[r]);
-#pragma unroll
-          for (int w = 16; w >= LPK; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-          const float keep = m > top[r] ? ex2(top[r] - m) : 1.0f;
-          top[r] = m;
-          sum[r] *= keep;
-#pragma unroll
-          for (int k = 0; k < VC; ++k) o[r][k] *= keep;
+        for (int n = 0; n < 2; ++n) {
+          const float a = ex2(sc[n][2 * h] - shift), e = ex2(sc[n][2 * h + 1] - shift);
+          sum[h] += a + e;
+          p[h + 2 * n] = pack_bf16(a, e);
         }
       }
-      float pr[RB];
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        pr[r] = ex2(sc[r] - (top[r] == -INFINITY ? 0.0f : top[r]));
-        if (part == 0) sum[r] += pr[r];
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t f[4];
+        ldmatrix4_trans(f, vt + ((m & 1) * 8 + mr) * D * 2 + (((2 * n + (m >> 1)) ^ mr) << 4));
+        mma16816(o[2 * n], p, f[0], f[1]);
+        mma16816(o[2 * n + 1], p, f[2], f[3]);
       }
-      if (part == 0)
-#pragma unroll
-        for (int r = 0; r < RB; r += 4)
-          *reinterpret_cast<float4 *>(s_p + key * RB + r) = make_float4(pr[r], pr[r + 1], pr[r + 2], pr[r + 3]);
-      __syncwarp();
-#pragma unroll
-      for (int kk = 0; kk < KT; ++kk) {
-        float v[VC];
-        const unsigned char *at = vt + kk * D * 2 + lane * VC * 2;
-        uint32_t w[VC / 2];
-        if (VC == 2) w[0] = *reinterpret_cast<const uint32_t *>(at);
-        if (VC == 4) *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(at);
-        if (VC == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(at);
-#pragma unroll
-        for (int k = 0; k < VC / 2; ++k) {
-          v[2 * k] = __uint_as_float(w[k] << 16);
-          v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
-#pragma unroll
-        for (int r4 = 0; r4 < RB; r4 += 4) {
-          const float4 p4 = *reinterpret_cast<const float4 *>(s_p + kk * RB + r4);
-          const float p[4] = {p4.x, p4.y, p4.z, p4.w};
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int k = 0; k < VC; ++k) o[r4 + r][k] = fmaf(p[r], v[k], o[r4 + r][k]);
-        }
-      }
-      __syncwarp();  // the stage and the probabilities may be overwritten
+      __syncwarp();  // the stage may be overwritten
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
   }
-  __syncthreads();  // every warp is done with the ring: its memory takes the results, fp32 [warps][RB][D]
-  float *s_o = reinterpret_cast<float *>(smem_raw);
+  // the warp's results over its ring: fp32 [kRows][D]
+  float *s_o = reinterpret_cast<float *>(ring);
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
+  for (int h = 0; h < 2; ++h) {
+    const int row = lane / 4 + 8 * h;
+    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+    if ((lane & 3) == 0) s_ml[warp * kRows + row] = make_float2(top[h], sum[h]);
+    if (row < R)
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], w);
-    if (lane == 0) s_ml[warp * RB + r] = make_float2(top[r], sum[r]);
-    float *dst = s_o + (warp * RB + r) * D + lane * VC;
-#pragma unroll
-    for (int k = 0; k < VC; ++k) dst[k] = o[r][k];
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2 *>(s_o + row * D + 8 * n + 2 * (lane & 3)) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
   }
   __syncthreads();
   griddep_wait();
@@ -1281,8 +1257,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) join_rows_kernel(const __g
     Part P = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
     if (t < own.ntok) {
       for (int w = 0; here && w < kJoinWarps; ++w) {
-        const float2 ml = s_ml[w * RB + row];
-        P.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(s_o + (w * RB + row) * D + 4 * c));
+        const float2 ml = s_ml[w * kRows + row];
+        P.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(smem_raw + w * S::kWarp + (row * D + 4 * c) * 4));
       }
       if (g >= 0) add_line<D>(A, P, shared, g, false, own.first + t, head, gh, c, share);
       add_line<D>(A, P, own, A.n_groups + b, true, own.first + t, head, gh, c, share);
@@ -1294,17 +1270,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) join_rows_kernel(const __g
   }
 }
 
-template <int D, int RB>
+template <int D>
 gdn_status launch_join_rows(const Args &A, cudaStream_t st) {
-  constexpr int bytes = JoinSmem<D, RB>::kBytes;
+  constexpr int bytes = JoinSmem<D>::kBytes;
   const DeviceInfo &dev = device_info();
   static std::atomic<bool> ready[kMaxDevices];
   if (!ready[dev.id].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(join_rows_kernel<D, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(join_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
       return fail(GDN_ERR_CUDA, "attention: cannot reserve shared memory");
     ready[dev.id].store(true, std::memory_order_release);
   }
-  launch_pdl(join_rows_kernel<D, RB>, dim3((unsigned)(A.B * A.hk)), dim3(kJoinWarps * 32), bytes, st, A);
+  launch_pdl(join_rows_kernel<D>, dim3((unsigned)(A.B * A.hk)), dim3(kJoinWarps * 32), bytes, st, A);
   return check_launch("attention");
 }
 
@@ -1399,7 +1375,7 @@ gdn_status launch_t(const gdn_attn_dims *d, const void *q, const void *k, const 
   GDN_TRY(check_launch("attention"));
   if (SHARED) {
     const long long items = (long long)A.n_tokens * A.hq * (D / 4);
-    if (A.own_keys > 0) return A.T * A.G <= 4 ? launch_join_rows<D, 4>(A, st) : launch_join_rows<D, 8>(A, st);
+    if (A.own_keys > 0) return launch_join_rows<D>(A, st);
     launch_pdl(join_kernel<D>, dim3((unsigned)((items + 127) / 128)), dim3(128), 0, st, A);
   }
   return check_launch("attention");
@@ -1521,7 +1497,7 @@ gdn_status gdn_attn_shared_prefix(const gdn_attn_dims *d, const void *q, const v
   A.v = static_cast<const bf16 *>(v);
   A.qs = d->q_stride;
   A.kvs = d->kv_stride;
-  A.own_keys = d->T * A.G <= 8 && (long long)d->B * A.hk < (1LL << 31) ? attn::kOwnKeys : 0;
+  A.own_keys = d->T * A.G <= attn::kRows && (long long)d->B * A.hk < (1LL << 31) ? attn::kOwnKeys : 0;
   const int grid = dev->sms < attn::kMaxCtas ? dev->sms : attn::kMaxCtas;
   return attn::launch<true>(d, q, k, v, A, grid, static_cast<cudaStream_t>(stream));
 }
