@@ -288,9 +288,6 @@ struct Cfg {
   static constexpr int kBytes = kBar + 8 * (2 * NU + 14 + 2 * kSegs) + 1024;
   static constexpr int kThreads = NS * 128 + 128;
   static constexpr int kO = 256;                            // TMEM column of the first O tile
-  // two softmax groups: registers of a thread at launch, and after the four other warps gave some to the eight
-  static constexpr int kRegs = 168, kRegsOther = 104, kRegsSoftmax = 200;
-  static_assert(2 * kRegsSoftmax + kRegsOther == 3 * kRegs, "what the groups take is what was launched");
 };
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
@@ -601,10 +598,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
   if (any) {
     Seg s;
-    // A row's 128 scores and what surrounds them take more registers than an even share of the SM's leaves: the four
-    // other warps give some to the softmax groups.
-    if (warp >= NS * 4) {
-    if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kTma) {
       if (lane == 0) {
         // ---- K and V blocks
@@ -839,10 +832,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         base += 2 * n * HB;
       }
-    }
-    } else {
+    } else if (warp < kMma) {
       // ---- softmax: thread = row of a tile
-      if (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
       const int grp = warp >> 2, wq = warp & 3, row = (wq << 5) + lane;
       uint32_t sc[2] = {0, 0}, oc = 0;  // S tiles taken from each buffer, O tiles waited for
       bool ok = true;
@@ -1445,11 +1436,6 @@ gdn_status launch_t(const gdn_attn_dims *d, const void *q, const void *k, const 
     if (cudaFuncSetAttribute(attn_kernel<D, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kBytes) !=
         cudaSuccess)
       return fail(GDN_ERR_CUDA, "attention: cannot reserve shared memory");
-    // sharing out more registers than were launched would wait forever
-    cudaFuncAttributes at;
-    if (cudaFuncGetAttributes(&at, attn_kernel<D, SHARED>) != cudaSuccess ||
-        (Cfg<D>::NS == 2 && at.numRegs != Cfg<D>::kRegs))
-      return fail(GDN_ERR_CUDA, "attention: the kernel was not built with the registers that it shares out");
     ready[dev.id].store(true, std::memory_order_release);
   }
   launch_pdl(attn_kernel<D, SHARED>, dim3((unsigned)grid), dim3(Cfg<D>::kThreads), Cfg<D>::kBytes, st, qm, km, vm, A);
