@@ -47,7 +47,6 @@ struct Args {
   int TQ;           // tokens of one 128-row tile
   int tile_tokens;  // tokens of one CTA's tiles (TQ, or 2 TQ for two query tiles)
   int max_tiles;    // prefill: tiles the grid covers
-  bool steal;       // prefill: a CTA goes on with tiles of CTAs not yet launched
   float c, c_signed;  // |scale| log2(e), and with the sign
   uint32_t idesc_s; // instruction descriptor of S (the sign of scale)
   long long kv_rows, qs, kvs;
@@ -218,12 +217,12 @@ struct Start {  // where the CTA's work begins
   Seg seg;  // prefill
 };
 
-// Prefill: the segment of one unit, by a whole warp. Tiles are numbered through
-// the sequences; the first units are the last tiles, which see the most keys.
-__device__ bool prefill_seg(const Args &A, int unit, Seg &s) {
+// Prefill: the CTA's one segment. Tiles are numbered through the sequences; the
+// grid's first CTAs take the last tiles, which see the most keys.
+__device__ bool prefill_seg(const Args &A, Seg &s) {
   const int lane = threadIdx.x & 31;
-  s.head = unit % A.hk;
-  const int want = A.max_tiles - 1 - unit / A.hk;
+  s.head = blockIdx.x % A.hk;
+  const int want = A.max_tiles - 1 - (int)(blockIdx.x / A.hk);
   int seen = 0;
   for (int b0 = 0; b0 < A.B; b0 += 32) {  // a warp looks at 32 sequences at a time
     const int b = b0 + lane;
@@ -264,7 +263,7 @@ __device__ bool prefill_seg(const Args &A, int unit, Seg &s) {
       s.lim0 = m - n + tile * A.tile_tokens + 1;
       s.b0 = 0;
       s.b1 = blocks_of(min(m, s.lim0 + s.ntok - 1));
-      s.pair = A.steal ? A.tile_tokens > A.TQ : s.ntok > A.TQ;
+      s.pair = s.ntok > A.TQ;
       s.slot = 0;
       s.own = false;
       return true;
@@ -285,7 +284,7 @@ struct Cfg {
   static constexpr int NU = D == 64 ? 10 : 5;               // units of the ring
   static constexpr int QB = 128 * D * 2;                    // bytes of a Q tile
   static constexpr int kBar = NS * QB + NU * UB;
-  static constexpr int kBytes = kBar + 8 * (2 * NU + 14 + 2 * kSegs) + 1024;
+  static constexpr int kBytes = kBar + 8 * (2 * NU + 13 + 2 * kSegs) + 1024;
   static constexpr int kThreads = NS * 128 + 128;
   static constexpr int kO = 256;                            // TMEM column of the first O tile
 };
@@ -381,30 +380,8 @@ __device__ __forceinline__ int v_place(bool pair, int j, int n) { return pair ? 
 
 // The key blocks that query tile q of the segment sees.
 __device__ __forceinline__ int tile_blocks(const Args &A, const Seg &s, int q) {
-  if (q * A.TQ >= s.ntok) return 0;
   const int last = min(s.ntok, (q + 1) * A.TQ) - 1;  // the tile's last token sees the most keys
   return max(0, min(s.b1, blocks_of(min(s.len, s.lim0 + s.step * last))) - s.b0);
-}
-
-// Asks for a CTA of this grid that has not started; 16 bytes of answer complete on `bar`.
-__device__ __forceinline__ void try_cancel(uint4 *answer, uint64_t *bar) {
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                   smem_u32(answer)),
-               "r"(smem_u32(bar))
-               : "memory");
-}
-// Whether there was one, and its number along x.
-__device__ __forceinline__ uint32_t canceled(const uint4 *answer, uint32_t &cta) {
-  uint32_t yes, x;
-  asm volatile(
-      "{\n .reg .b128 a;\n .reg .pred p;\n ld.shared.b128 a, [%2];\n"
-      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
-      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, a;\n}"
-      : "=r"(yes), "=r"(x)
-      : "r"(smem_u32(answer))
-      : "memory");
-  cta = x;
-  return yes;
 }
 
 // Which query slots a segment's tiles take: two tiles both, one tile each slot in turn, so that the next tile can land
@@ -427,11 +404,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// The key blocks that the segment loads.
-__device__ __forceinline__ int seg_blocks(const Args &A, const Seg &s) {
-  return s.pair ? max(tile_blocks(A, s, 0), tile_blocks(A, s, 1)) : tile_blocks(A, s, 0);
-}
-
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -443,13 +415,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   unsigned char *sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::kBar), *empty = full + NU;
   uint64_t *q_full = empty + NU, *q_empty = q_full + 2, *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *handed = o_full + 2,
-           *clean = handed + 1, *dirty = clean + 1, *seg_full = dirty + 1, *seg_empty = seg_full + kSegs,
-           *stolen = seg_empty + kSegs;
+           *clean = handed + 1, *dirty = clean + 1, *seg_full = dirty + 1, *seg_empty = seg_full + kSegs;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ Start s_start;
   __shared__ Seg s_seg[kSegs];
-  __shared__ uint4 s_cancel;
   __shared__ long long s_scan[NT / 32][2];
   __shared__ float2 s_ml[NS == 2 && !SHARED ? 128 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -464,7 +434,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], NS * 4 + 3);  // the softmax warps, the loads, the products, the cleaning warp
     }
-    mbar_init(stolen, 1);
     mbar_init(handed, 4);
     mbar_init(clean, 1);
     mbar_init(dirty, 1);
@@ -570,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   } else {
     if (warp == 0) {
       Seg s = {};
-      const bool got = prefill_seg(A, blockIdx.x, s);
+      const bool got = prefill_seg(A, s);
       if (lane == 0) {
         s_start.any = got;
         s_start.seg = s;
@@ -585,6 +554,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   uint32_t seg_count = 0;
   auto next_seg = [&](Seg &s, bool whole_warp) -> bool {
     const uint32_t k = seg_count++;
+    if (!SHARED) {
+      s = s_start.seg;
+      return k == 0;
+    }
     const int i = k % kSegs;
     const uint32_t phase = (k / kSegs) & 1;
     if (!(whole_warp ? warp_wait(&seg_full[i], phase, &s_abort, A.status)
@@ -604,7 +577,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         int u = 0;  // units issued
         bool ok = true;
         while (ok && next_seg(s, false)) {
-          const int n = seg_blocks(A, s);
+          const int n = tile_blocks(A, s, s.pair ? 1 : 0);
           for (int i = 0; ok && i < 2 * n; ++i) {  // K and V blocks in the order of the products
             bool is_v;
             int j;
@@ -634,68 +607,39 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         for (int i = max(0, u - NU); i < u; ++i) (void)mbar_wait_bounded(&full[i % NU], (i / NU) & 1);
       }
     } else if (warp == kQ) {
-      // ---- segments and their query tiles: a warp of its own, so that the next segment's keys do not wait for this
-      // one's queries
-      Seg w = {};
-      QSlots slots;
-      uint32_t found = 0;
-      bool ok = true;
-      auto publish = [&](bool more) {  // lane 0
-        const int i = found % kSegs;
-        if (found >= kSegs) ok = wait_or_abort(&seg_empty[i], ((found / kSegs) - 1) & 1, &s_abort, A.status);
-        if (!ok) return;
-        if (!more) w.ntok = 0;  // the end
-        s_seg[i] = w;
-        mbar_arrive(&seg_full[i]);
-        ++found;
-        if (!more || seg_blocks(A, w) == 0) return;
-        const int first = slots.first(w.pair, NS), tiles = w.pair ? 2 : 1;
-        for (int t = 0; ok && t < tiles; ++t) {
-          const int q = first + t;
-          if (slots.used[q] > 0) ok = wait_or_abort(&q_empty[q], (slots.used[q] - 1) & 1, &s_abort, A.status);
-          if (!ok) break;
-          ++slots.used[q];
-          mbar_arrive_expect_tx(&q_full[q], (uint32_t)((D / 64) * A.TQ * A.G * 128));
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(smem_u32(sm) + q * C::QB + c * 128 * 128, &qmap, c * 64, w.head * A.G, w.t0 + t * A.TQ, &q_full[q]);
-        }
-      };
-      if (SHARED) {
-        if (lane == 0)
-          for (bool more = true; ok && more;) {
-            more = walk.next(w);
-            publish(more);
+      if (lane == 0) {
+        // ---- query tiles: a warp of its own, so that the next segment's keys do not wait for this one's queries
+        QSlots slots;
+        uint32_t found = 0;
+        bool ok = true, more = true;
+        while (ok && more) {
+          more = SHARED ? walk.next(s) : found == 0;
+          if (SHARED) {
+            const int i = found % kSegs;
+            if (found >= kSegs && !wait_or_abort(&seg_empty[i], ((found / kSegs) - 1) & 1, &s_abort, A.status)) break;
+            if (!more) s.ntok = 0;  // the end
+            s_seg[i] = s;
+            mbar_arrive(&seg_full[i]);
+          } else {
+            s = s_start.seg;
           }
-      } else {
-        // The grid has a CTA for every tile. One that runs takes over tiles whose CTAs have not started, so that
-        // its next tile's loads run under this one's last products; it does so when this tile has been begun, no
-        // earlier, which leaves the balance to the hardware's order (longest first).
-        w = s_start.seg;
-        bool got = true;
-        for (uint32_t round = 0;; ++round) {
-          if (lane == 0 && got) {
-            publish(true);
-            const uint32_t k = found - 1;
-            if (ok) ok = wait_or_abort(&seg_empty[k % kSegs], (k / kSegs) & 1, &s_abort, A.status);
-          }
-          uint32_t more = 0, unit = 0;
-          if (lane == 0 && ok && A.steal) {
-            mbar_arrive_expect_tx(stolen, 16);
-            try_cancel(&s_cancel, stolen);
-            ok = wait_or_abort(stolen, round & 1, &s_abort, A.status);
-            if (ok) more = canceled(&s_cancel, unit);
-            fence_proxy_async_smem();  // read before the next answer is written
-          }
-          more = __shfl_sync(0xffffffffu, more, 0);
-          unit = __shfl_sync(0xffffffffu, unit, 0);
+          ++found;
           if (!more) break;
-          got = prefill_seg(A, (int)unit, w);
+          if (tile_blocks(A, s, s.pair ? 1 : 0) == 0) continue;
+          const int first = slots.first(s.pair, NS), tiles = s.pair ? 2 : 1;
+          for (int t = 0; ok && t < tiles; ++t) {
+            const int q = first + t;
+            if (slots.used[q] > 0) ok = wait_or_abort(&q_empty[q], (slots.used[q] - 1) & 1, &s_abort, A.status);
+            if (!ok) break;
+            ++slots.used[q];
+            mbar_arrive_expect_tx(&q_full[q], (uint32_t)((D / 64) * A.TQ * A.G * 128));
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(smem_u32(sm) + q * C::QB + c * 128 * 128, &qmap, c * 64, s.head * A.G, s.t0 + t * A.TQ, &q_full[q]);
+          }
         }
-        if (lane == 0 && ok) publish(false);
-      }
-      if (lane == 0)
         for (int q = 0; q < NS; ++q)
           if (slots.used[q] > 0) (void)mbar_wait_bounded(&q_full[q], (slots.used[q] - 1) & 1);
+      }
     } else if (warp == kMma) {
       // ---- products: one thread issues them all
       if (elect_one()) {
@@ -708,7 +652,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         constexpr uint32_t idesc_o = idesc_bf16(128, C::UC) | (1u << 16);  // B (V) is read MN-major
         while (ok && next_seg(s, false)) {
           const int nb0 = tile_blocks(A, s, 0), nb1 = s.pair ? tile_blocks(A, s, 1) : 0;
-          const int n = max(nb0, nb1);
+          const int n = s.pair ? nb1 : nb0;
           if (n == 0) continue;
           const int q_first = slots.first(s.pair, NS);
           for (int q = q_first; ok && q < q_first + (s.pair ? 2 : 1); ++q)
@@ -765,41 +709,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (done)
               for (int h = 0; h < HB; ++h) umma_commit(&empty[(g0 + h) % NU]);
           };
-          // the query slot is free once the last product that reads it is done
-          auto q_done = [&](int q) {
-            if (ok) umma_commit(&q_empty[q]);
-          };
-          if (s.pair) {  // the last tile that takes a block (tile 1 where it does) releases it
-            if (nb0 > 0) issue_s(0, 0, 0, nb1 == 0);
-            if (nb0 <= 1) q_done(0);
-            if (nb1 > 0 && ok) issue_s(1, 1, 0, true);
-            if (nb1 <= 1) q_done(1);
+          if (s.pair) {
+            if (nb0 > 0) issue_s(0, 0, 0, false);
+            if (ok) issue_s(1, 1, 0, true);
             for (int j = 0; ok && j < n; ++j) {
               if (j < nb0) {
-                issue_o(0, 0, j, j == 0, j >= nb1);
+                issue_o(0, 0, j, j == 0, false);
                 if (j + 1 == nb0 && ok) umma_commit(&o_full[0]);
-                if (j + 1 < nb0 && ok) issue_s(0, 0, j + 1, j + 1 >= nb1);
-                if (j + 2 == nb0) q_done(0);
+                if (j + 1 < nb0 && ok) issue_s(0, 0, j + 1, false);
               }
-              if (j < nb1) {
-                if (ok) issue_o(1, 1, j, j == 0, true);
-                if (j + 1 == nb1 && ok) umma_commit(&o_full[1]);
-                if (j + 1 < nb1 && ok) issue_s(1, 1, j + 1, true);
-                if (j + 2 == nb1) q_done(1);
-              }
+              if (ok) issue_o(1, 1, j, j == 0, true);
+              if (j + 1 == n && ok) umma_commit(&o_full[1]);
+              if (j + 1 < n && ok) issue_s(1, 1, j + 1, true);
             }
           } else {
             issue_s(q_first, 0, 0, true);
             if (ok && n > 1) issue_s(q_first, 1, 1, true);
-            if (n <= 2) q_done(q_first);
             for (int j = 0; ok && j < n; ++j) {
               const int o = NS == 2 ? (j & 1) : 0;
               issue_o(o, j & 1, j, NS == 2 ? j < 2 : j == 0, true);
               if (ok && (NS == 1 || j + 2 >= n)) umma_commit(&o_full[o]);
               if (ok && j + 2 < n) issue_s(q_first, j & 1, j + 2, true);
-              if (j + 3 == n) q_done(q_first);
             }
           }
+          for (int q = q_first; ok && q < q_first + (s.pair ? 2 : 1); ++q) umma_commit(&q_empty[q]);
           if (tail >= 0) ++cleaned;
           base += 2 * n * HB;
         }
@@ -811,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       uint32_t cleaned = 0;
       bool ok = true;
       while (ok && next_seg(s, true)) {
-        const int n = seg_blocks(A, s), tail = tail_block(s, n);
+        const int n = tile_blocks(A, s, s.pair ? 1 : 0), tail = tail_block(s, n);
         if (tail >= 0) {
           const int g0 = base + v_place(s.pair, tail, n) * HB, valid = s.len - (s.b0 + tail) * BN;
           ok = warp_wait(dirty, cleaned & 1, &s_abort, A.status);
@@ -1517,11 +1450,9 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims *d, const void *q, const void *k
   A.kv_len = kv_len;
   // fewer two-tile CTAs than SMs: one tile each, its keys shared between the two groups
   if ((long long)d->n_tokens * d->n_kv_heads < (long long)dev->sms * A.tile_tokens) A.tile_tokens = A.TQ;
-  const bool split = d->head_dim != 256 && A.tile_tokens == A.TQ;
   const long long tiles = (long long)d->n_tokens / A.tile_tokens + d->B;
   if (tiles * A.hk > (1LL << 31) - 1) return fail(GDN_ERR_SHAPE, "too many tokens in one call");
   A.max_tiles = (int)tiles;
-  A.steal = !split && tiles * A.hk > dev->sms;
   return attn::launch<false>(d, q, k, v, A, (int)(tiles * A.hk), static_cast<cudaStream_t>(stream));
 }
 
