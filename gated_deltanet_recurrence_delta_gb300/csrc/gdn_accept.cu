@@ -122,7 +122,7 @@ __device__ __forceinline__ Two lane_mass(const Row &R, int i0, int i1, int lane)
       for (int k = 0; k < 4; ++k) sum[k].add(R.at(i + k));
     if (z + lane < i1) sum[0].add(R.at(z + lane));
   } else {
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 16;
     int i = i0 + lane;
     for (; i + 32 * (kBatch - 1) < i1; i += 32 * kBatch) {
       float p[kBatch], q[kBatch];

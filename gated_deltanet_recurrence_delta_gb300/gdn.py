@@ -124,11 +124,7 @@ def _check(code: int):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 # torch.cuda.current_stream() builds a Stream object (3 us); a small call's kernel takes 5
@@ -138,7 +134,7 @@ _device = getattr(torch._C, "_cuda_getDevice", None)
 
 def _stream(stream):
     if stream is None:
-        if _raw_stream is not None and _device is not None and torch.cuda.is_initialized():
+        if _raw_stream is not None and _device is not None:
             return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
