@@ -40,7 +40,8 @@ namespace attn {
 constexpr int kMaxCtas = 152;  // CTAs of a shared-prefix call: one per SM
 constexpr int BN = 128;        // keys of a block
 constexpr int kOwnKeys = 2048;
-constexpr int kSetup = 2;      // a segment's queries, first latency and stores, in blocks' time
+constexpr int kLeast = 2;      // blocks of a CTA's stretch at least
+constexpr int kSetup = 4;      // a segment's queries, first latency and stores, in blocks' time
 
 struct Args {
   int B, T, n_tokens, n_groups, hq, hk, G;
@@ -468,16 +469,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // the groups' offsets run from 0 to B without a step back, or no row is touched (and no slot used)
     bool broken = A.n_groups > 0 && (A.group_rows[0] != 0 || A.group_rows[A.n_groups] != A.B);
     for (int g = tid; g < A.n_groups; g += NT) broken = broken || A.group_rows[g] > A.group_rows[g + 1];
+    Entry mine = entry_at(A, min(tid, n - 1), true);  // this thread's first entry, its loads beside the offsets'
     const bool all_ok = !__syncthreads_or(broken);
     if (!all_ok && blockIdx.x == 0 && tid == 0) set_status(A.status, GDN_ERR_INDEX);
     long long total = 0, lines = 0, ta, tb;
     long long my_cost = 0, my_first = 0, my_line = 0;  // of the last entry looked at
-    Entry mine = {};
     for (int e0 = 0; e0 < n; e0 += NT) {
       const int e = e0 + tid;
       long long a = 0, b = 0;
       if (e < n) {
-        mine = entry_at(A, e, all_ok);
+        if (e0 > 0 || !all_ok) mine = entry_at(A, e, all_ok);
         if (!mine.ok && blockIdx.x == 0) set_status(A.status, GDN_ERR_INDEX);
         a = mine.cost(A.hk);
         b = (long long)mine.tiles * A.hk;
@@ -493,7 +494,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       total += ta;
       lines += tb;
     }
-    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kSetup + 2);
+    const long long up = total + gridDim.x - 1;  // a 64-bit division takes hundreds of cycles
+    const long long share = max(up < (1LL << 31) ? (long long)((unsigned)up / gridDim.x) : up / gridDim.x, (long long)kSetup + kLeast);
     if (blockIdx.x == 0 && tid == 0) {
       A.plan[0] = share;
       A.plan[1] = all_ok;
@@ -997,17 +999,23 @@ struct Part {
   }
 };
 
+// Where an entry's lines begin in the plan.
+struct Place {
+  long long cost, line;
+};
+__device__ __forceinline__ Place place_of(const Args &A, int e) { return {A.plan[2 + 2 * e], A.plan[3 + 2 * e]}; }
+
 // Adds the partial results that the attention kernel left of one entry for channels 4c.. of (token t, head), in
 // order, kParts of them loaded at once.
 constexpr int kParts = 8;
 template <int D>
-__device__ __forceinline__ void add_line(const Args &A, Part &P, const Entry &x, int e, bool own, int t, int head, int gh,
-                                         int c, long long share) {
+__device__ __forceinline__ void add_line(const Args &A, Part &P, const Entry &x, Place at_line, bool own, int t, int head,
+                                         int gh, int c, long long share) {
   constexpr int NS = Cfg<D>::NS;
   if (x.blocks == 0) return;
   const int ti = t - x.first, tile = ti / A.tile_tokens, i = ti - tile * A.tile_tokens;
   const bool pair = min(A.tile_tokens, x.ntok - tile * A.tile_tokens) > A.TQ;
-  const long long li = (long long)tile * A.hk + head, a = A.plan[2 + 2 * e] + li * x.line_cost(), z = a + x.line_cost();
+  const long long li = (long long)tile * A.hk + head, a = at_line.cost + li * x.line_cost(), z = a + x.line_cost();
   const int rows = own ? A.suffix_rows : A.prefix_rows;
   const int streams = NS == 2 && !pair ? 2 : 1, s0 = pair ? i / A.TQ : 0, row = (pair ? i % A.TQ : i) * A.G + gh;
   const float4 *po = reinterpret_cast<const float4 *>(own ? A.suffix_o : A.prefix_o) + (long long)c * rows + row;
@@ -1016,7 +1024,7 @@ __device__ __forceinline__ void add_line(const Args &A, Part &P, const Entry &x,
   const bool small = z < (1LL << 31) && share < (1LL << 31);
   const int c0 = small ? (unsigned)(a + kSetup) / (unsigned)share : (int)((a + kSetup) / share);
   const int c1 = small ? (unsigned)(z - 1) / (unsigned)share : (int)((z - 1) / share), n = (c1 - c0 + 1) * streams;
-  const long long first = (A.plan[3 + 2 * e] + li + c0) * NS + s0;
+  const long long first = (at_line.line + li + c0) * NS + s0;
   const int stride = NS / streams;
   for (int p0 = 0; p0 < n; p0 += kParts) {
     float2 ml[kParts];
@@ -1049,12 +1057,13 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
   if (t >= A.n_tokens) return;
   const int b = t / A.T, g = group_of(A, b);
   const long long share = A.plan[0], in_order = A.plan[1];
+  const Place own_at = place_of(A, A.n_groups + b), shared_at = place_of(A, max(g, 0));
   const Entry own = entry_at(A, A.n_groups + b, true), shared = g >= 0 ? entry_at(A, g, true) : own;
   if (!in_order || !own.ok || !shared.ok) return;
   Part P = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (t - own.first < own.ntok) {
-    if (g >= 0) add_line<D>(A, P, shared, g, false, t, head, gh, c, share);
-    add_line<D>(A, P, own, A.n_groups + b, true, t, head, gh, c, share);
+    if (g >= 0) add_line<D>(A, P, shared, shared_at, false, t, head, gh, c, share);
+    add_line<D>(A, P, own, own_at, true, t, head, gh, c, share);
   }
   const float inv = 1.0f / P.sum;
   uint2 r = make_uint2(0u, 0u);
@@ -1115,6 +1124,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_rows_kernel(const __g
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / A.hk, head = blockIdx.x - b * A.hk, R = A.T * A.G;
   const Entry own = entry_at(A, A.n_groups + b, true);
+  const int g = group_of(A, b);
+  const Entry shared = g >= 0 ? entry_at(A, g, true) : own;
   const bool here = own.ok && own.len <= A.own_keys;
   unsigned char *ring = smem_raw + warp * S::kWarp;
 
@@ -1248,9 +1259,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_rows_kernel(const __g
 
   // ---- the parts of four channels of a query row: the warps', then the prefix's (and the row's own, if the kernel
   // before took it)
-  const int g = group_of(A, b);
-  const Entry shared = g >= 0 ? entry_at(A, g, true) : own;
   const long long share = A.plan[0], in_order = A.plan[1];
+  const Place own_at = place_of(A, A.n_groups + b), shared_at = place_of(A, max(g, 0));
   if (!in_order || !own.ok || !shared.ok) return;
   for (int item = tid; item < R * (D / 4); item += kJoinWarps * 32) {
     const int c = item / R, row = item - c * R, t = row / A.G, gh = row - t * A.G;
@@ -1260,8 +1270,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_rows_kernel(const __g
         const float2 ml = s_ml[w * kRows + row];
         P.add(ml.x, ml.y, *reinterpret_cast<const float4 *>(smem_raw + w * S::kWarp + (row * D + 4 * c) * 4));
       }
-      if (g >= 0) add_line<D>(A, P, shared, g, false, own.first + t, head, gh, c, share);
-      add_line<D>(A, P, own, A.n_groups + b, true, own.first + t, head, gh, c, share);
+      if (g >= 0) add_line<D>(A, P, shared, shared_at, false, own.first + t, head, gh, c, share);
+      add_line<D>(A, P, own, own_at, true, own.first + t, head, gh, c, share);
     }
     uint2 r = make_uint2(0u, 0u);
     const float inv = 1.0f / P.sum;
