@@ -70,19 +70,6 @@ gdn_status current_device(const DeviceInfo **out) {
 
 const DeviceInfo &device_info() { return table().info[t_device]; }
 
-gdn_status check_ptr(const void *p, const char *name, size_t align) {
-  static thread_local char buf[160];
-  if (!p) {
-    snprintf(buf, sizeof buf, "%s is NULL", name);
-    return fail(GDN_ERR_ARG, buf);
-  }
-  if (!aligned(p, align)) {
-    snprintf(buf, sizeof buf, "%s is not %zu-byte aligned", name, align);
-    return fail(GDN_ERR_ARG, buf);
-  }
-  return GDN_OK;
-}
-
 }  // namespace gdn
 
 using namespace gdn;
@@ -105,6 +92,25 @@ gdn_status check_dims(const gdn_dims *d, bool /*packed_ok*/) {
     return fail(GDN_ERR_ARG, "scale must be a number and eps values >= 0");
   return GDN_OK;
 }
+
+gdn_status check_ptr(const void *p, const char *name, size_t align = 16) {
+  static thread_local char buf[160];
+  if (!p) {
+    snprintf(buf, sizeof buf, "%s is NULL", name);
+    return fail(GDN_ERR_ARG, buf);
+  }
+  if (!aligned(p, align)) {
+    snprintf(buf, sizeof buf, "%s is not %zu-byte aligned", name, align);
+    return fail(GDN_ERR_ARG, buf);
+  }
+  return GDN_OK;
+}
+
+#define GDN_TRY(x)                      \
+  do {                                  \
+    const gdn_status _s = (x);          \
+    if (_s != GDN_OK) return _s;        \
+  } while (0)
 
 gdn_status check_inputs(const gdn_inputs *in, bool packed_ok) {
   if (!in) return fail(GDN_ERR_ARG, "inputs is NULL");

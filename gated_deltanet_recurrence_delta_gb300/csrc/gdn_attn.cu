@@ -29,9 +29,20 @@
 // Running maximum: O is rescaled only where a row's maximum grew by more than
 // 2^8 since the value it is measured against; probabilities then reach 2^8 at
 // most, which fp32 sums and bf16's exponent carry without loss.
-#include <mutex>
-
-#include "gdn_launch.h"
+//
+// What bounds it. A 128 x 128 x 128 product takes 512 cycles, the softmax of a
+// 128 x 128 tile ~1200 of one group (512 of them the exponentials' own), so two
+// groups keep up with two S and two O products, 2048 cycles for two tiles and
+// a block; measured 2900, as S reads both operands from shared memory at its
+// full rate while the copies write there too. One prompt of 8192 tokens, 32/8
+// heads, D = 128: 380 us, 1450 TFLOP/s or 75% of the measured bf16 rate; 512
+// tokens after 7680 (128 of 152 SMs have a tile): 55 us, 63%; 32 packed prompts
+// of 16 to 2048 tokens, D = 256: 355 us, 45%, a third of it the start and end of
+// each CTA (5 blocks on average between them). Steps that carried it: one
+// elected thread issues the products (all lanes waiting and lane 0 issuing
+// cost 700 cycles a block: 512 -> 404 us); the block's maximum found beside its
+// probabilities instead of before them (404 -> 377 us).
+#include "gdn_check.h"
 #include "gdn_umma.cuh"
 
 namespace gdn {
@@ -39,9 +50,13 @@ namespace attn {
 
 constexpr int kMaxCtas = 152;  // CTAs of a shared-prefix call: one per SM
 constexpr int BN = 128;        // keys of a block
+// Rows with T G <= 16 queries per key head have at most so many keys of their own attended in the join: 64 rows of
+// ~550 keys 81 -> 75 us, 45 rows of ~350 26 -> 18 us against segments here; longer extents are better split over SMs.
 constexpr int kOwnKeys = 2048;
 constexpr int kLeast = 2;      // blocks of a CTA's stretch at least
-constexpr int kSetup = 4;      // a segment's queries, first latency and stores, in blocks' time
+// a segment's queries, first latency and stores, in blocks' time: 1, 2, 4 gave 29.4, 27.7, 27.2 us for 8 x 8 verify
+// tokens over 8192 keys (D = 256) and 22, 18.3, 17.4 us for 45 rows in 7 groups
+constexpr int kSetup = 4;
 
 struct Args {
   int B, T, n_tokens, n_groups, hq, hk, G;
@@ -1082,6 +1097,8 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
 // (on the fp32 units ~60, which bounded it at half the memory rate).
 // None of this reads what the kernel before wrote, so it runs before the wait
 // for it, on the SMs which that kernel leaves; only then the parts are joined.
+// 64 rows x 8 key heads, ~550 keys of 128 channels each: 37 us (147 MB of keys
+// and values, 4 TB/s; ~7 us of each CTA are latencies at its start and join).
 constexpr int kJoinWarps = 4, kRows = 16, kTileKeys = 16;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
@@ -1426,6 +1443,9 @@ gdn_status check_shared(const gdn_attn_dims *d) {
   GDN_TRY(check(d));
   if (d->T < 1 || d->T > 64) return fail(GDN_ERR_SHAPE, "T must be in [1, 64]");
   if ((long long)d->B * d->T != d->n_tokens) return fail(GDN_ERR_SHAPE, "n_tokens must be B * T");
+  if ((long long)d->B * d->n_kv_heads > (1LL << 31) - 1 ||
+      (long long)d->n_tokens * d->n_q_heads * (d->head_dim / 4) / 128 >= (1LL << 31) - 1)
+    return fail(GDN_ERR_SHAPE, "too many rows in one call");
   return GDN_OK;
 }
 

@@ -10,12 +10,6 @@ namespace gdn {
 
 constexpr int kMaxDevices = 64;
 
-#define GDN_TRY(x)                      \
-  do {                                  \
-    const gdn_status _s = (x);          \
-    if (_s != GDN_OK) return _s;        \
-  } while (0)
-
 struct DeviceInfo {
   int id;
   int sms;                 // streaming multiprocessors
@@ -30,8 +24,6 @@ const DeviceInfo &device_info();
 
 // Record `msg` as this thread's last error and return `code`.
 gdn_status fail(gdn_status code, const char *msg);
-// GDN_OK, or GDN_ERR_ARG when `p` (named `name` in the message) is NULL or not aligned.
-gdn_status check_ptr(const void *p, const char *name, size_t align = 16);
 // GDN_OK, or GDN_ERR_CUDA with the launch error of `what`.
 gdn_status check_launch(const char *what);
 
