@@ -107,6 +107,8 @@ def test_shared_refuses_bad_tokens_and_workspaces(lib):
     assert _shared(lib, B=0, n_tokens=0, n_groups=0) == "GDN_OK"
     assert _prefill(lib, B=0, n_groups=0) == "GDN_OK" and _prefill(lib, n_tokens=0) == "GDN_OK"
     assert _prefill(lib, scale=float("nan")) == "GDN_ERR_ARG"
+    huge = dict(B=1 << 24, T=64, n_tokens=1 << 30, n_q_heads=64, n_kv_heads=1, q_stride=4096)
+    assert _shared(lib, **huge) == "GDN_ERR_SHAPE"  # more than a grid holds
 
 
 @pytest.mark.parametrize("kw", [dict(B=-1), dict(B=(1 << 20) + 1), dict(T=0), dict(T=33), dict(V=0), dict(V=(1 << 30) + 1)])
