@@ -63,6 +63,7 @@ struct Args {
   int TQ;           // tokens of one 128-row tile
   int tile_tokens;  // tokens of one CTA's tiles (TQ, or 2 TQ for two query tiles)
   int max_tiles;    // prefill: tiles the grid covers
+  bool out32;       // out is 32-byte aligned
   float c, c_signed;  // |scale| log2(e), and with the sign
   uint32_t idesc_s; // instruction descriptor of S (the sign of scale)
   long long kv_rows, qs, kvs;
@@ -349,6 +350,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// 32 bytes of one row: each lane of a warp has another row, and the memory pipe takes as long for 16.
+__device__ __forceinline__ void st_32bytes(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -982,11 +989,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                   v[k + 3] = fmaf(f.w, w1, v[k + 3]);
                 }
               }
+              uint32_t w[16];
 #pragma unroll
-              for (int k = 0; k < 32; k += 8)
-                *reinterpret_cast<uint4 *>(dst + i + k) =
-                    make_uint4(pack_bf16(v[k], v[k + 1]), pack_bf16(v[k + 2], v[k + 3]), pack_bf16(v[k + 4], v[k + 5]),
-                               pack_bf16(v[k + 6], v[k + 7]));
+              for (int k = 0; k < 16; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+              if (A.out32) {
+                st_32bytes(dst + i, w);
+                st_32bytes(dst + i + 16, w + 8);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  *reinterpret_cast<uint4 *>(dst + i + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+              }
             }
           }
         }
@@ -1379,6 +1392,7 @@ Args make_args(const gdn_attn_dims *d, void *out, unsigned int *status) {
   A.idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24) | (d->scale < 0.0f ? 1u << 13 : 0u);
   A.kv_rows = d->kv_rows;
   A.out = static_cast<bf16 *>(out);
+  A.out32 = reinterpret_cast<uintptr_t>(out) % 32 == 0;
   A.status = status;
   return A;
 }
