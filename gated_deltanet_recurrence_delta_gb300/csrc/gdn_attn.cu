@@ -243,10 +243,12 @@ __device__ bool prefill_seg(const Args &A, Seg &s) {
   int seen = 0;
   for (int b0 = 0; b0 < A.B; b0 += 32) {  // a warp looks at 32 sequences at a time
     const int b = b0 + lane;
-    int a = 0, n = 0;
+    int a = 0, n = 0, kv0 = 0, m = 0;
     if (b < A.B) {
       a = A.cu[b];
       n = A.cu[b + 1] - a;
+      kv0 = A.kv_start ? A.kv_start[b] : a;
+      m = A.kv_len ? A.kv_len[b] : n;
       if (a < 0 || n < 0 || (long long)a + n > A.n_tokens) {
         set_status(A.status, GDN_ERR_INDEX);
         n = 0;
@@ -265,9 +267,8 @@ __device__ bool prefill_seg(const Args &A, Seg &s) {
       const int tile = want - seen - __shfl_sync(0xffffffffu, incl - tiles, l);
       a = __shfl_sync(0xffffffffu, a, l);
       n = __shfl_sync(0xffffffffu, n, l);
-      const int q = b0 + l;
-      const long long start = A.kv_start ? A.kv_start[q] : a;
-      const int m = A.kv_len ? A.kv_len[q] : n;
+      const long long start = __shfl_sync(0xffffffffu, kv0, l);
+      m = __shfl_sync(0xffffffffu, m, l);
       if (!inside(start, m, A.kv_rows)) {
         if (lane == 0) set_status(A.status, GDN_ERR_INDEX);
         return false;
@@ -970,35 +971,42 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           w1 *= inv;
           bf16 *dst = A.out + ((long long)(s.t0 + tok) * A.hq + s.head * A.G + gh) * D;
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            float v[32];
+          for (int i = 0; i < D; i += 64) {
+            float v[64];
             if (mine > 0) {
               tmem_ld32_async(o_tmem + i, v);
+              tmem_ld32_async(o_tmem + i + 32, v + 32);
               tmem_wait_ld();
             }
             if (real) {
+              if (mine == 0 || inv == 0.0f) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = mine > 0 && inv != 0.0f ? v[k] * w0 : 0.0f;
+                for (int k = 0; k < 64; ++k) v[k] = 0.0f;
+              }
               if (w1 != 0.0f) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
+                for (int k = 0; k < 64; k += 4) {
                   const float4 f = *reinterpret_cast<const float4 *>(far + ((i + k) / 4 * 128 + row) * 4);
-                  v[k] = fmaf(f.x, w1, v[k]);
-                  v[k + 1] = fmaf(f.y, w1, v[k + 1]);
-                  v[k + 2] = fmaf(f.z, w1, v[k + 2]);
-                  v[k + 3] = fmaf(f.w, w1, v[k + 3]);
+                  v[k] = fmaf(v[k], w0, f.x * w1);
+                  v[k + 1] = fmaf(v[k + 1], w0, f.y * w1);
+                  v[k + 2] = fmaf(v[k + 2], w0, f.z * w1);
+                  v[k + 3] = fmaf(v[k + 3], w0, f.w * w1);
                 }
-              }
-              uint32_t w[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
-              if (A.out32) {
-                st_32bytes(dst + i, w);
-                st_32bytes(dst + i + 16, w + 8);
               } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  *reinterpret_cast<uint4 *>(dst + i + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                for (int k = 0; k < 64; ++k) v[k] *= w0;
+              }
+              uint32_t w[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                if (A.out32) {
+                  st_32bytes(dst + i + 2 * k, w + k);
+                } else {
+                  *reinterpret_cast<uint4 *>(dst + i + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                  *reinterpret_cast<uint4 *>(dst + i + 2 * k + 8) = make_uint4(w[k + 4], w[k + 5], w[k + 6], w[k + 7]);
+                }
               }
             }
           }
