@@ -1343,7 +1343,7 @@ gdn_status check(const gdn_attn_dims *d) {
     return fail(GDN_ERR_SHAPE, "n_q_heads must be a multiple of n_kv_heads, at most 64 per key head");
   if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
     return fail(GDN_ERR_SHAPE, "head_dim must be 64, 128 or 256");
-  if (d->scale != d->scale) return fail(GDN_ERR_ARG, "scale must be a number");
+  if (!(fabsf(d->scale) <= 3.0e38f)) return fail(GDN_ERR_ARG, "scale must be finite");
   if (d->q_stride % 8 != 0 || d->kv_stride % 8 != 0)
     return fail(GDN_ERR_SHAPE, "token strides must be multiples of 8 elements");
   if (d->q_stride < (long long)d->n_q_heads * d->head_dim || d->kv_stride < (long long)d->n_kv_heads * d->head_dim)

@@ -279,13 +279,15 @@ def out_proj(o, w_out, y, stream=None):
 def _layout(x, name):
     """(tokens, heads, head_dim, elements between tokens) of a bf16 tensor [tokens, heads, head_dim] or
     [rows, tokens, heads, head_dim] whose heads lie together and whose tokens are evenly spaced."""
-    if x.dtype is not torch.bfloat16 or x.dim() not in (3, 4):
+    shape, st = x.shape, x.stride()
+    rank = len(shape)
+    if x.dtype is not torch.bfloat16 or not 3 <= rank <= 4:
         raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, head_dim] or [rows, tokens, heads, head_dim]")
-    *lead, heads, d = x.shape
-    st = x.stride()
-    if st[-1] != 1 or (st[-2] != d and heads > 1) or (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * st[1]):
+    heads, d = shape[-2], shape[-1]
+    n = shape[0] if rank == 3 else shape[0] * shape[1]
+    if st[-1] != 1 or (st[-2] != d and heads > 1) or (rank == 4 and shape[0] > 1 and st[0] != shape[1] * st[1]):
         raise ValueError(f"{name} must have dense heads and evenly spaced tokens")
-    return (lead[0] if len(lead) == 1 else lead[0] * lead[1]), heads, d, st[-3]
+    return n, heads, d, st[-3]
 
 
 def make_rope_dims(q, k, rot_dim, n_axes=1, kv_rows=None, adjacent=False, eps=1e-6, v=None) -> RopeDims:

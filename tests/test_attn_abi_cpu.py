@@ -106,7 +106,8 @@ def test_shared_refuses_bad_tokens_and_workspaces(lib):
     assert _shared(lib, dict(size=need - 1)) == "GDN_ERR_WORKSPACE"
     assert _shared(lib, B=0, n_tokens=0, n_groups=0) == "GDN_OK"
     assert _prefill(lib, B=0, n_groups=0) == "GDN_OK" and _prefill(lib, n_tokens=0) == "GDN_OK"
-    assert _prefill(lib, scale=float("nan")) == "GDN_ERR_ARG"
+    for scale in ("nan", "inf", "-inf"):
+        assert _prefill(lib, scale=float(scale)) == "GDN_ERR_ARG" and _shared(lib, scale=float(scale)) == "GDN_ERR_ARG"
     huge = dict(B=1 << 24, T=64, n_tokens=1 << 30, n_q_heads=64, n_kv_heads=1, q_stride=4096)
     assert _shared(lib, **huge) == "GDN_ERR_SHAPE"  # more than a grid holds
 
