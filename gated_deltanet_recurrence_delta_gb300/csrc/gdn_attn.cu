@@ -490,9 +490,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   if (SHARED) {
     const int n = A.n_groups + A.B;
     // the groups' offsets run from 0 to B without a step back, or no row is touched (and no slot used)
-    bool broken = A.n_groups > 0 && (A.group_rows[0] != 0 || A.group_rows[A.n_groups] != A.B);
-    for (int g = tid; g < A.n_groups; g += NT) broken = broken || A.group_rows[g] > A.group_rows[g + 1];
-    Entry mine = entry_at(A, min(tid, n - 1), true);  // this thread's first entry, its loads beside the offsets'
+    Entry mine = entry_at(A, min(tid, n - 1), true);  // this thread's first entry: its loads run beside the offsets' own
+    bool broken = false;
+    if (A.n_groups > 0) {
+      const int from = A.group_rows[0], to = A.group_rows[A.n_groups];  // two loads in flight at once
+      broken = (from != 0) | (to != A.B);
+      for (int g = tid; g < A.n_groups; g += NT) broken |= A.group_rows[g] > A.group_rows[g + 1];
+    }
     const bool all_ok = !__syncthreads_or(broken);
     if (!all_ok && blockIdx.x == 0 && tid == 0) set_status(A.status, GDN_ERR_INDEX);
     long long total = 0, lines = 0, ta, tb;
