@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             ok = warp_wait(handed, 0, &s_abort, A.status);
             if (!ok) break;
             const float2 o = s_ml[row];
-            if (o.y > 0.0f) {
+            if (o.y != 0.0f) {  // a sum of zero saw no key; a NaN counts
               const float m = fmaxf(top, o.x);
               w0 = sum > 0.0f ? ex2((top - m) * A.c) : 0.0f;
               w1 = ex2((o.x - m) * A.c);
