@@ -27,7 +27,9 @@ class AttentionLayers:
 
     weights: one dict per layer with the bf16 norms q_norm, k_norm [head_dim] (or None). inv_freq: fp64 [rot_dim/2]
     (device). prompt_rows: the pool rows [0, prompt_rows) hold shared prompts, packed; row b's own extent starts at
-    prompt_rows + b * room, whose room holds its continuation and a step's T tokens (keys past it are not kept)."""
+    prompt_rows + b * room, whose room holds its continuation and a step's T tokens. Of a step's tokens a row takes as
+    many as its room still holds (room_for); the others are no tokens of it: no key is kept, their outputs are zeros. A
+    row without room for one token is a device error (GDN_ERR_INDEX, gdn.check_status) and stays as it is."""
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, weights, inv_freq, prompt_rows, n_rows, room, device="cuda"):
         self.hq, self.hk, self.d = n_q_heads, n_kv_heads, head_dim
@@ -63,13 +65,20 @@ class AttentionLayers:
         dims = gdn.make_attn_dims(q_buf, self.k_pool[layer], B=cu_seqlens.numel() - 1)
         gdn.attn_prefill(dims, q_buf, self.k_pool[layer], self.v_pool[layer], cu_seqlens, out, kv_start, kv_len, stream)
 
+    def room_for(self, B, T):
+        """int32 [B]: how many of a step's T tokens fit each row's room, gdn.accept_draft's n_tokens."""
+        return (self.room - self.own_len[:B]).clamp(0, T)
+
     def step(self, layer, qkv, group_rows, prompt_start, prompt_len, q_buf, out, stream=None):
         """A layer's decode (T = 1) or verify (T drafted tokens) of the rows [B][T]: qkv bf16 [B, T, (hq + 2 hk) d].
         The tokens stand behind the row's own keys (own_len, which advance() moves afterwards) at position
         prompt_len of the row's group + place in its own extent."""
         B, T = q_buf.shape[0], q_buf.shape[1]
         place = self.own_len[:B, None] + torch.arange(T, dtype=torch.int32, device=self.device)
-        at = torch.where(place < self.room, self.own_start[:B, None] + place, -1).to(torch.int32).flatten()
+        real = self.room_for(B, T)
+        past = (real == 0)[:, None] * (self.kv_rows + 1) - 1  # -1: not kept; a full row: past the pool, and so reported
+        at = torch.where(place < self.room, self.own_start[:B, None] + place, past).to(torch.int32).flatten()
+        own_len = (self.own_len[:B] + T).clamp(max=self.room)
         group = torch.bucketize(torch.arange(B, dtype=torch.int32, device=self.device), group_rows[1:], right=True)
         positions = (prompt_len[group][:, None] + place).to(torch.int32).reshape(1, -1)
         self._norm_rope(layer, qkv.flatten(0, 1), positions, at, q_buf, stream)
@@ -78,7 +87,7 @@ class AttentionLayers:
         if key not in self.workspace:
             self.workspace[key] = gdn.attn_workspace(dims, self.device)
         gdn.attn_shared_prefix(dims, q_buf, self.k_pool[layer], self.v_pool[layer], group_rows, prompt_start, prompt_len,
-                               self.own_start[:B], self.own_len[:B] + T, out, self.workspace[key], stream=stream)
+                               self.own_start[:B], own_len, out, self.workspace[key], real, stream)
 
     def advance(self, accept_len):
         """Every layer's caches keep the accepted tokens of the step: the next step overwrites the others."""
@@ -94,11 +103,14 @@ def speculative_step(stack, attention, acts, qkv, state_idx, prompts, tokens, ta
     AttentionLayers.step), prompts: (group_rows, prompt_start, prompt_len); tokens, target_probs, draft_probs,
     uniform: gdn.accept_draft's; buffers: dict with gdn_out, ckpt_state, ckpt_conv (LayerStack.verify), q, attn_out
     [n_layers][B][T][hq][d], accept_len, next_token int32 [B].
+    A row whose room holds fewer than T tokens takes part with those (AttentionLayers.room_for); a full row accepts 0,
+    draws -1, keeps its states and is reported.
     The target's probabilities come from the layers' outputs; here they are given."""
     b = buffers
     stack.verify(acts, state_idx, b["gdn_out"], b["ckpt_state"], b["ckpt_conv"])
     for layer in range(attention.n_layers):
         attention.step(layer, qkv[layer], *prompts, b["q"], b["attn_out"][layer])
-    gdn.accept_draft(tokens, target_probs, draft_probs, uniform, b["accept_len"], b["next_token"])
+    gdn.accept_draft(tokens, target_probs, draft_probs, uniform, b["accept_len"], b["next_token"],
+                     attention.room_for(*tokens.shape))
     stack.commit(1, b["accept_len"], state_idx, b["ckpt_state"], b["ckpt_conv"])
     attention.advance(b["accept_len"])
