@@ -17,9 +17,21 @@ GDN layers.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import gdn
+
+
+def _on(stream):
+    """The context in which torch's own operations and allocations belong to `stream` (a stream or its handle; None: the
+    current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 class AttentionLayers:
@@ -29,7 +41,10 @@ class AttentionLayers:
     (device). prompt_rows: the pool rows [0, prompt_rows) hold shared prompts, packed; row b's own extent starts at
     prompt_rows + b * room, whose room holds its continuation and a step's T tokens. Of a step's tokens a row takes as
     many as its room still holds (room_for); the others are no tokens of it: no key is kept, their outputs are zeros. A
-    row without room for one token is a device error (GDN_ERR_INDEX, gdn.check_status) and stays as it is."""
+    row without room for one token is a device error (GDN_ERR_INDEX, gdn.check_status) and stays as it is.
+
+    A call given a stream does all its work on it, its index arithmetic too; calls on several streams are ordered by the
+    caller (the pools and the rows' lengths are one set; each stream has workspaces of its own)."""
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, weights, inv_freq, prompt_rows, n_rows, room, device="cuda"):
         self.hq, self.hk, self.d = n_q_heads, n_kv_heads, head_dim
@@ -73,6 +88,10 @@ class AttentionLayers:
         """A layer's decode (T = 1) or verify (T drafted tokens) of the rows [B][T]: qkv bf16 [B, T, (hq + 2 hk) d].
         The tokens stand behind the row's own keys (own_len, which advance() moves afterwards) at position
         prompt_len of the row's group + place in its own extent."""
+        with _on(stream):
+            self._step(layer, qkv, group_rows, prompt_start, prompt_len, q_buf, out, stream)
+
+    def _step(self, layer, qkv, group_rows, prompt_start, prompt_len, q_buf, out, stream):
         B, T = q_buf.shape[0], q_buf.shape[1]
         place = self.own_len[:B, None] + torch.arange(T, dtype=torch.int32, device=self.device)
         real = self.room_for(B, T)
@@ -83,15 +102,16 @@ class AttentionLayers:
         positions = (prompt_len[group][:, None] + place).to(torch.int32).reshape(1, -1)
         self._norm_rope(layer, qkv.flatten(0, 1), positions, at, q_buf, stream)
         dims = gdn.make_attn_dims(q_buf, self.k_pool[layer], B=B, T=T, n_groups=prompt_start.numel())
-        key = (B, T, prompt_start.numel())
+        key = (B, T, prompt_start.numel(), gdn._stream(stream))
         if key not in self.workspace:
             self.workspace[key] = gdn.attn_workspace(dims, self.device)
         gdn.attn_shared_prefix(dims, q_buf, self.k_pool[layer], self.v_pool[layer], group_rows, prompt_start, prompt_len,
                                self.own_start[:B], own_len, out, self.workspace[key], real, stream)
 
-    def advance(self, accept_len):
+    def advance(self, accept_len, stream=None):
         """Every layer's caches keep the accepted tokens of the step: the next step overwrites the others."""
-        self.own_len[:accept_len.numel()] += accept_len
+        with _on(stream):
+            self.own_len[:accept_len.numel()] += accept_len
 
 
 def speculative_step(stack, attention, acts, qkv, state_idx, prompts, tokens, target_probs, draft_probs, uniform, buffers):

@@ -1,4 +1,4 @@
-"""AttentionLayers and speculative_step on the GPU where a row's room ends.
+"""AttentionLayers and speculative_step on the GPU where a row's room ends, and on a stream of their own.
 
 Bar of the attention outputs: attn_plain.attend's on the queries, keys and values that the pools and buffers hold (bit
 for bit what the kernels read); whole numbers, copied states and repeated calls are equal."""
@@ -130,3 +130,41 @@ def test_speculative_steps_until_the_room_is_full():
             assert n > 0 or int(buf["next_token"][b]) == -1
         assert att.own_len.tolist() == own
     assert own == [10, 10, 10]
+
+
+# -------------------------------------------------------------------- streams
+
+@pytest.mark.parametrize("held", ["side", "current"])
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_steps_on_a_stream_of_their_own(held, as_handle):
+    """The stream's work, or the current stream's, lies milliseconds behind; memory that a step gave back is reused at
+    once. Both steps give what they give on the current stream."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    B, T, prompts = 5, 3, (_ints([0, 2, 5]), _ints([0, 20]), _ints([20, 30]))
+    qkv = [_rand(g, B, T, (HQ + 2 * HK) * D) for _ in range(2)]
+    accept = _ints([1, 3, 2, 1, 2])
+    start = [2, 0, 7, 1, 4]
+    results = []
+    for stream in (None, torch.cuda.Stream()):
+        g.manual_seed(4)
+        att = _layers(g, B, 20, 50)
+        att.own_len.copy_(_ints(start))
+        q = torch.empty((B, T, HQ, D), dtype=torch.bfloat16, device="cuda")
+        outs = [torch.full_like(q, 7.0) for _ in range(2)]
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream if held == "side" else torch.cuda.current_stream()):
+                torch.cuda._sleep(10_000_000)
+        on = stream if stream is None or not as_handle else stream.cuda_stream
+        for x, out in zip(qkv, outs):
+            att.step(0, x, *prompts, q, out, stream=on)
+            if stream is not None:  # small blocks that the step freed, if they are the current stream's
+                for n in (1, B, B * T, 4 * B * T):
+                    torch.full((n,), 1 << 20, dtype=torch.int32, device="cuda")
+            att.advance(accept, stream=on)
+        gdn.check_status(stream)
+        torch.cuda.synchronize()
+        results.append((*outs, att.k_pool, att.v_pool, att.own_len))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert results[1][-1].tolist() == [x + 2 * y for x, y in zip(start, accept.tolist())]

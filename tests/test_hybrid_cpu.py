@@ -97,3 +97,56 @@ def test_a_speculative_step_accepts_no_more_than_the_room_holds(calls):
     for name, c in calls:
         if name == "attn":
             assert bool((c.len <= 10).all())
+
+
+# -------------------------------------------------------------------- streams
+
+class _Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_everything_a_step_does_is_on_its_stream(calls, monkeypatch, as_handle):
+    """The index arithmetic, the workspace and the library's calls of a step given a stream: nothing on another one, and
+    no workspace shared between streams."""
+    import contextlib
+
+    from torch.utils._python_dispatch import TorchDispatchMode
+    current, stray = [0], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream.cuda_stream)
+        yield
+        current.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", _Stream)
+    held = []
+    monkeypatch.setattr(gdn, "attn_shared_prefix",
+                        lambda *a, q_len=None, stream=None: held.append((a[10], gdn._stream(a[12] if len(a) > 12 else stream))))
+
+    class Watch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            views = ("select", "slice", "view", "unsqueeze", "split", "expand", "reshape", "alias", "detach", "t.")
+            name = func.name().split("::")[1]
+            if current[-1] != 77 and not name.startswith(views):
+                stray.append(name)
+            return func(*args, **(kwargs or {}))
+
+    att = _layers(n_rows=3, room=20)
+    prompts = (_ints(0, 3), _ints(0), _ints(100))
+    qkv = torch.zeros((3, 2, (HQ + 2 * HK) * D), dtype=torch.bfloat16)
+    q, out, got = torch.zeros((3, 2, HQ, D), dtype=torch.bfloat16), torch.zeros((3, 2, HQ, D)), _ints(1, 2, 1)
+    side = 77 if as_handle else _Stream(77)
+    with Watch():
+        att.step(0, qkv, *prompts, q, out, stream=side)
+        assert stray == [], f"on another stream than the step's: {stray}"
+        att.advance(got, stream=side)
+        assert stray == [], f"on another stream than the step's: {stray}"
+    assert att.own_len.tolist() == [1, 2, 1]
+    att.step(0, qkv, *prompts, q, out)
+    att.step(0, qkv, *prompts, q, out, stream=side)
+    assert [h for _, h in held] == [77, 0, 77]
+    assert held[0][0] is held[2][0] and held[0][0] is not held[1][0]
