@@ -87,7 +87,8 @@ class AttentionLayers:
     def step(self, layer, qkv, group_rows, prompt_start, prompt_len, q_buf, out, stream=None):
         """A layer's decode (T = 1) or verify (T drafted tokens) of the rows [B][T]: qkv bf16 [B, T, (hq + 2 hk) d].
         The tokens stand behind the row's own keys (own_len, which advance() moves afterwards) at position
-        prompt_len of the row's group + place in its own extent."""
+        prompt_len of the row's group + place in its own extent. Rows without shared prompts: group_rows, prompt_start
+        and prompt_len None (or empty)."""
         with _on(stream):
             self._step(layer, qkv, group_rows, prompt_start, prompt_len, q_buf, out, stream)
 
@@ -98,11 +99,15 @@ class AttentionLayers:
         past = (real == 0)[:, None] * (self.kv_rows + 1) - 1  # -1: not kept; a full row: past the pool, and so reported
         at = torch.where(place < self.room, self.own_start[:B, None] + place, past).to(torch.int32).flatten()
         own_len = (self.own_len[:B] + T).clamp(max=self.room)
-        group = torch.bucketize(torch.arange(B, dtype=torch.int32, device=self.device), group_rows[1:], right=True)
-        positions = (prompt_len[group][:, None] + place).to(torch.int32).reshape(1, -1)
+        n_groups = 0 if prompt_start is None else prompt_start.numel()
+        positions = place
+        if n_groups > 0:
+            group = torch.bucketize(torch.arange(B, dtype=torch.int32, device=self.device), group_rows[1:], right=True)
+            positions = (prompt_len[group][:, None] + place).to(torch.int32)
+        positions = positions.reshape(1, -1)
         self._norm_rope(layer, qkv.flatten(0, 1), positions, at, q_buf, stream)
-        dims = gdn.make_attn_dims(q_buf, self.k_pool[layer], B=B, T=T, n_groups=prompt_start.numel())
-        key = (B, T, prompt_start.numel(), gdn._stream(stream))
+        dims = gdn.make_attn_dims(q_buf, self.k_pool[layer], B=B, T=T, n_groups=n_groups)
+        key = (B, T, n_groups, gdn._stream(stream))
         if key not in self.workspace:
             self.workspace[key] = gdn.attn_workspace(dims, self.device)
         gdn.attn_shared_prefix(dims, q_buf, self.k_pool[layer], self.v_pool[layer], group_rows, prompt_start, prompt_len,

@@ -1,4 +1,5 @@
-"""AttentionLayers and speculative_step on the GPU where a row's room ends, and on a stream of their own.
+"""AttentionLayers and speculative_step on the GPU where a row's room ends, on a stream of their own, and without
+shared prompts.
 
 Bar of the attention outputs: attn_plain.attend's on the queries, keys and values that the pools and buffers hold (bit
 for bit what the kernels read); whole numbers, copied states and repeated calls are equal."""
@@ -168,3 +169,26 @@ def test_steps_on_a_stream_of_their_own(held, as_handle):
     for a, b in zip(*results):
         assert torch.equal(a, b)
     assert results[1][-1].tolist() == [x + 2 * y for x, y in zip(start, accept.tolist())]
+
+
+# ---------------------------------------------------- rows without a prompt
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_rows_without_a_shared_prompt(T):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    att = _layers(g, 4, 300, 0)
+    own = [0, 130, 7, 300 - T]
+    att.own_len.copy_(_ints(own))
+    qkv, q = _rand(g, 4, T, (HQ + 2 * HK) * D), torch.empty((4, T, HQ, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    att.step(0, qkv, None, None, None, q, out)
+    gdn.check_status()
+    _check_rows(att, 0, q, out, [(0, 0)] * 4, own, [T] * 4)
+    xq, xk, xv = att._split(qkv.flatten(0, 1))
+    pos = torch.cat([o + torch.arange(T) for o in own]).int().cuda()[None]
+    at = torch.cat([300 * b + own[b] + torch.arange(T) for b in range(4)]).cuda()
+    for got, x, w in ((q.flatten(0, 1), xq, "q_norm"), (att.k_pool[0][at], xk, "k_norm")):
+        ref = attn_plain.norm_rope(x, att.weights[0][w], pos, att.inv_freq, None, ROT, False, 1e-6)
+        bar = 2.0 ** -8 * ref.abs() + 2.0 ** -19 * ref.abs().amax(-1, keepdim=True)
+        assert float(((got.double() - ref).abs() - bar).max()) <= 0
+    assert torch.equal(att.v_pool[0][at], xv)

@@ -150,3 +150,17 @@ def test_everything_a_step_does_is_on_its_stream(calls, monkeypatch, as_handle):
     att.step(0, qkv, *prompts, q, out, stream=side)
     assert [h for _, h in held] == [77, 0, 77]
     assert held[0][0] is held[2][0] and held[0][0] is not held[1][0]
+
+
+# ---------------------------------------------------- rows without a prompt
+
+@pytest.mark.parametrize("prompts", [(None, None, None), (_ints(0), _ints(), _ints())])
+def test_rows_without_a_shared_prompt(calls, prompts):
+    """Ordinary decode: positions count from the row's own first key, and the call has no groups."""
+    att = _layers(n_rows=3, room=20, prompt_rows=0)
+    att.own_len.copy_(_ints(0, 5, 18))
+    _step(att, 3, 2, prompts)
+    rope, attn = calls[0][1], calls[1][1]
+    assert rope.positions.tolist() == [[0, 1, 5, 6, 18, 19]]
+    assert rope.kv_index.tolist() == [0, 1, 25, 26, 58, 59]
+    assert attn.n_groups == 0 and attn.start.tolist() == [0, 20, 40] and attn.len.tolist() == [2, 7, 20]
