@@ -42,6 +42,8 @@
 // elected thread issues the products (all lanes waiting and lane 0 issuing
 // cost 700 cycles a block: 512 -> 404 us); the block's maximum found beside its
 // probabilities instead of before them (404 -> 377 us).
+#include <float.h>
+
 #include "gdn_check.h"
 #include "gdn_umma.cuh"
 
@@ -50,6 +52,7 @@ namespace attn {
 
 constexpr int kMaxCtas = 152;  // CTAs of a shared-prefix call: one per SM
 constexpr int BN = 128;        // keys of a block
+constexpr float kLog2e = 1.4426950408889634f;
 // Rows with T G <= 16 queries per key head have at most so many keys of their own attended in the join: 64 rows of
 // ~550 keys 81 -> 75 us, 45 rows of ~350 26 -> 18 us against segments here; longer extents are better split over SMs.
 constexpr int kOwnKeys = 2048;
@@ -1347,7 +1350,7 @@ gdn_status check(const gdn_attn_dims *d) {
     return fail(GDN_ERR_SHAPE, "n_q_heads must be a multiple of n_kv_heads, at most 64 per key head");
   if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
     return fail(GDN_ERR_SHAPE, "head_dim must be 64, 128 or 256");
-  if (!(fabsf(d->scale) <= 3.0e38f)) return fail(GDN_ERR_ARG, "scale must be finite");
+  if (!(fabsf(d->scale) * kLog2e <= FLT_MAX)) return fail(GDN_ERR_ARG, "scale, and scale * log2(e), must be finite");
   if (d->q_stride % 8 != 0 || d->kv_stride % 8 != 0)
     return fail(GDN_ERR_SHAPE, "token strides must be multiples of 8 elements");
   if (d->q_stride < (long long)d->n_q_heads * d->head_dim || d->kv_stride < (long long)d->n_kv_heads * d->head_dim)
@@ -1398,8 +1401,8 @@ Args make_args(const gdn_attn_dims *d, void *out, unsigned int *status) {
   A.TQ = 128 / A.G;
   A.tile_tokens = (d->head_dim == 256 ? 1 : 2) * A.TQ;
   // masked scores are -inf: times a scale of exactly zero they would be NaN
-  A.c = fmaxf(fabsf(d->scale) * 1.4426950408889634f, 1e-30f);
-  A.c_signed = d->scale * 1.4426950408889634f;
+  A.c = fmaxf(fabsf(d->scale) * kLog2e, 1e-30f);
+  A.c_signed = d->scale * kLog2e;
   // kind::f16, bf16 A and B, fp32 D, N = 128, M = 128; bit 13 negates A for a negative scale
   A.idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24) | (d->scale < 0.0f ? 1u << 13 : 0u);
   A.kv_rows = d->kv_rows;

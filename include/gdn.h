@@ -431,7 +431,8 @@ gdn_status gdn_head_norm_rope(const gdn_rope_dims *dims, const void *q, const vo
  *   n_groups   groups of rows that share a prefix (0: no prefixes); unused by prefill
  *   n_q_heads, n_kv_heads, head_dim   n_q_heads a multiple of n_kv_heads, at most
  *              64 query heads per key head; head_dim one of 64, 128, 256
- *   scale      multiplies q.k before the softmax (head_dim^-0.5 is usual); finite
+ *   scale      multiplies q.k before the softmax (head_dim^-0.5 is usual);
+ *              |scale| log2(e) finite (scale q.k log2(e) is held in fp32)
  *   q_stride   elements between query tokens, a multiple of 8
  *   kv_stride  elements between pool rows of k and of v, a multiple of 8
  *   kv_rows    rows of the pools */
