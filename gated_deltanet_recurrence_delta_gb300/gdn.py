@@ -290,6 +290,12 @@ def _layout(x, name):
     return n, heads, d, st[-3]
 
 
+def _spaced(x, stride, name):
+    """Refuses a tensor [.., tokens, heads, head_dim] whose tokens are not `stride` elements apart, as the sizes say."""
+    if isinstance(x, torch.Tensor) and x.ndim >= 3 and x.stride(-3) != stride and x.shape[-3] > 1:
+        raise ValueError(f"{name}'s tokens are {x.stride(-3)} elements apart, the sizes say {stride}")
+
+
 def make_rope_dims(q, k, rot_dim, n_axes=1, kv_rows=None, adjacent=False, eps=1e-6, v=None) -> RopeDims:
     """Sizes and token strides of a head_norm_rope call on q [n, Hq, d] and k [n, Hk, d]; v's tokens are spaced as
     k's unless v is given. kv_rows: rows of the pools (n when they hold the tokens themselves)."""
@@ -304,6 +310,7 @@ def head_norm_rope(dims: RopeDims, q, k, v, q_weight, k_weight, positions, inv_f
     """gdn_head_norm_rope: per-head norms of q and k, the rotation by positions int32 [axes, n] with inv_freq fp64
     [rot_dim/2] (axis uint8 [rot_dim/2]: each pair's position axis), K and V to the rows kv_index int32 [n] of the
     pools k_out, v_out [kv_rows, Hk, d]."""
+    _spaced(v, dims.v_stride, "v")
     _check(load_library().gdn_head_norm_rope(
         ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
         _ptr(axis), _ptr(kv_index), _ptr(q_out), _ptr(k_out), _ptr(v_out), _stream(stream)))
@@ -319,6 +326,8 @@ def make_attn_dims(q, k, B, T=1, n_groups=0, scale=None) -> AttnDims:
 
 def attn_prefill(dims: AttnDims, q, k, v, cu_seqlens, out, kv_start=None, kv_len=None, stream=None):
     """gdn_attn_prefill: causal attention of packed prompts over their extents of the pools k, v."""
+    _spaced(k, dims.kv_stride, "k")
+    _spaced(v, dims.kv_stride, "v")
     _check(load_library().gdn_attn_prefill(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens),
                                            _ptr(kv_start), _ptr(kv_len), _ptr(out), _stream(stream)))
 
@@ -336,6 +345,8 @@ def attn_workspace(dims: AttnDims, device="cuda") -> torch.Tensor:
 def attn_shared_prefix(dims: AttnDims, q, k, v, group_rows, prefix_start, prefix_len, suffix_start, suffix_len, out,
                        workspace, q_len=None, stream=None):
     """gdn_attn_shared_prefix: q [B, T, Hq, d] over each group's shared prefix extent and each row's own extent."""
+    _spaced(k, dims.kv_stride, "k")
+    _spaced(v, dims.kv_stride, "v")
     _check(load_library().gdn_attn_shared_prefix(
         ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(group_rows), _ptr(prefix_start), _ptr(prefix_len),
         _ptr(suffix_start), _ptr(suffix_len), _ptr(q_len), _ptr(out), _ptr(workspace),
