@@ -1,5 +1,5 @@
-"""AttentionLayers and speculative_step on the GPU where a row's room ends, on a stream of their own, and without
-shared prompts.
+"""AttentionLayers and speculative_step on the GPU where a row's room ends, on a stream of their own, without shared
+prompts, and in every layer of a stack.
 
 Bar of the attention outputs: attn_plain.attend's on the queries, keys and values that the pools and buffers hold (bit
 for bit what the kernels read); whole numbers, copied states and repeated calls are equal."""
@@ -192,3 +192,37 @@ def test_rows_without_a_shared_prompt(T):
         bar = 2.0 ** -8 * ref.abs() + 2.0 ** -19 * ref.abs().amax(-1, keepdim=True)
         assert float(((got.double() - ref).abs() - bar).max()) <= 0
     assert torch.equal(att.v_pool[0][at], xv)
+
+
+# --------------------------------------------------------------- every layer
+
+def test_every_layer_of_a_speculative_step():
+    """Each layer's output in speculative_step is that layer's own step, bit for bit, and that one is right."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    B, T, V, L, s = 4, 3, 40, 3, I.TINY
+    att = _layers(g, B, 60, 200, L)
+    weights = [{n: t.cuda() for n, t in I.decode_batch(seed=x, B=1, shape=s).items()
+                if n in ("A_log", "dt_bias", "conv_w", "norm_w")} for x in range(2)]
+    stack = LayerStack(s, weights, n_slots=B)
+    own = [0, 17, 40, 57]
+    att.own_len.copy_(_ints(own))
+    prompts, prompt = (_ints([0, 1, 4]), _ints([0, 90]), _ints([90, 110])), [(0, 90)] + [(90, 110)] * 3
+    qkv = [_rand(g, B, T, (HQ + 2 * HK) * D) for _ in range(L)]
+    q = torch.empty((B, T, HQ, D), dtype=torch.bfloat16, device="cuda")
+    alone = [torch.full_like(q, 7.0) for _ in range(L)]
+    for layer in range(L):
+        att.step(layer, qkv[layer], *prompts, q, alone[layer])
+        gdn.check_status()
+        _check_rows(att, layer, q, alone[layer], prompt, own, [T] * B)
+    target = torch.softmax(torch.randn((B, T, V), generator=g, device="cuda"), -1)
+    buf = dict(gdn_out=torch.empty((2, B, T, s.nv, s.dv), dtype=torch.bfloat16, device="cuda"),
+               ckpt_state=torch.empty((2, B, T, s.nv, s.dk, s.dv), device="cuda"),
+               ckpt_conv=torch.empty((2, B, T, s.Kc, s.C), dtype=torch.bfloat16, device="cuda"), q=q,
+               attn_out=torch.full((L, *q.shape), 7.0, dtype=torch.bfloat16, device="cuda"),
+               accept_len=_ints([0] * B), next_token=_ints([0] * B))
+    speculative_step(stack, att, stack.static_acts(B, T), qkv, torch.arange(B, dtype=torch.int32, device="cuda"), prompts,
+                     torch.zeros((B, T), dtype=torch.int32, device="cuda"), target, None,
+                     torch.rand((B, T), generator=g, device="cuda"), buf)
+    gdn.check_status()
+    for layer in range(L):
+        assert torch.equal(buf["attn_out"][layer], alone[layer]), f"layer {layer}"
