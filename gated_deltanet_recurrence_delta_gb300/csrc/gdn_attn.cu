@@ -35,9 +35,9 @@
 // groups keep up with two S and two O products, 2048 cycles for two tiles and
 // a block; measured 2900, as S reads both operands from shared memory at its
 // full rate while the copies write there too. One prompt of 8192 tokens, 32/8
-// heads, D = 128: 380 us, 1450 TFLOP/s or 75% of the measured bf16 rate; 512
+// heads, D = 128: 379 us, 1450 TFLOP/s or 75% of the measured bf16 rate; 512
 // tokens after 7680 (128 of 152 SMs have a tile): 55 us, 63%; 32 packed prompts
-// of 16 to 2048 tokens, D = 256: 355 us, 45%, a third of it the start and end of
+// of 16 to 2048 tokens, D = 256: 340 us, 46%, half of it the start and end of
 // each CTA (5 blocks on average between them). Steps that carried it: one
 // elected thread issues the products (all lanes waiting and lane 0 issuing
 // cost 700 cycles a block: 512 -> 404 us); the block's maximum found beside its
@@ -53,8 +53,15 @@ namespace attn {
 constexpr int kMaxCtas = 152;  // CTAs of a shared-prefix call: one per SM
 constexpr int BN = 128;        // keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
-// Rows with T G <= 16 queries per key head have at most so many keys of their own attended in the join: 64 rows of
-// ~550 keys 81 -> 75 us, 45 rows of ~350 26 -> 18 us against segments here; longer extents are better split over SMs.
+// Rows with T G <= 16 queries per key head have at most so many keys of their own attended in the join, longer extents
+// as lines split over the SMs. Join against lines, us a call with L2 flushed, all rows of one length:
+//   keys of a row                              64      256      512     1024     1536     2048
+//   64 rows, 8 key heads of 128               16/43   25/39    37/49    61/76    82/98  100/117
+//   64 rows, 4 key heads of 256               18/40   27/41    41/53    64/81   84/102  101/121
+//   8 rows, 4 key heads of 256                12/36   14/27    18/29    25/33    31/35    37/37
+//   1 row, 4 key heads of 256                 10/32   12/27    16/28    23/31    29/32    35/33
+//   1 row, 8 key heads of 128                 10/29   12/19    14/21    21/24    25/23    30/23
+// So the join is the faster one up to here but for a call of one row, whose few CTAs lose up to a third at the end.
 constexpr int kOwnKeys = 2048;
 constexpr int kLeast = 2;      // blocks of a CTA's stretch at least
 // a segment's queries, first latency and stores, in blocks' time: 1, 2, 4 gave 29.4, 27.7, 27.2 us for 8 x 8 verify
@@ -865,7 +872,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
               a = ex2(a);
               b = ex2(b);
               add2(sm4[2 * (i & 1)], sm4[2 * (i & 1) + 1], a, b);
-              // a probability's rounding to bf16 (2^-9 of itself, on average zero) is below the output's own
+              // a probability's rounding to bf16 is at most 2^-8 of itself, as the output's own is, and on average
+              // zero: outputs are 2.0e-3 to 2.3e-3 off in place of 1.6e-3 (relative 2-norm), and the product runs at
+              // bf16's rate; the sum is of the unrounded values
               p[i] = pack_bf16(a, b);
             }
             part = (sm4[0] + sm4[1]) + (sm4[2] + sm4[3]);

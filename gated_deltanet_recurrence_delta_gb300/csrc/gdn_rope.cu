@@ -8,11 +8,12 @@
 //   y = x / sqrt(mean(x^2) + eps) * w;  (y0, y1) -> (y0 cos - y1 sin, y1 cos + y0 sin)
 //
 // Memory-bound: every element is read and written once, 4 bytes for ~8 flops.
-// 8192 tokens, 16 + 4 + 4 heads of 256: 38 us, 5.3 TB/s or 77% of the measured
-// copy rate; 4095 video tokens, 32 + 8 + 8 heads of 128: 20.8 us, 72%; 64 tokens:
-// 3.1 us of latency. Issue slots come next to bytes, so pairs of channels go
-// through paired fp32 instructions with the weights folded into the rotation
-// (48 -> 38 us).
+// 8192 tokens, 16 + 4 + 4 heads of 256: 38.4 us, 5.3 TB/s or 79% of the measured
+// copy rate; 4095 video tokens, 32 + 8 + 8 heads of 128: 20.8 us, 73%; 64 tokens:
+// 3.1 us of latency on the device. What keeps it from the copy rate is latency:
+// 126 registers leave two CTAs an SM, 22% of its warps, which wait for their
+// loads; issue slots are at 47%. Pairs of channels go through paired fp32
+// instructions with the weights folded into the rotation (48 -> 38 us).
 // A head lies over D/8 lanes of a warp, 16 bytes per lane, so a warp load
 // covers 32/(D/8) heads and the norm is a sum over the head's lanes. The
 // angles depend on the token only: a warp forms its lanes' cosines and sines

@@ -456,7 +456,7 @@ typedef struct gdn_attn_dims {
  * probabilities enter the second product in bf16. A range of queries or keys
  * that leaves its tensor is a device error (GDN_ERR_INDEX) and that sequence's
  * outputs are not written. Pool rows outside a sequence's extent are never
- * used, whatever they hold; inside it a value that is not finite may also reach
+ * used, whatever they hold; inside it a row of v that is not finite may also reach
  * queries up to a few hundred tokens before it (0 * NaN within a block of 128
  * keys and the tile of queries that meets it). */
 gdn_status gdn_attn_prefill(const gdn_attn_dims *dims, const void *q, const void *k, const void *v,
