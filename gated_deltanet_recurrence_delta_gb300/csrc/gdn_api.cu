@@ -407,6 +407,7 @@ gdn_status gdn_check_status(void *stream) {
         case GDN_ERR_MASK: return fail(GDN_ERR_MASK, "a mask row was not ones followed by zeros (row skipped)");
         case GDN_ERR_INDEX: return fail(GDN_ERR_INDEX, "a slot index or row range was out of bounds (row skipped)");
         case GDN_ERR_TIMEOUT: return fail(GDN_ERR_TIMEOUT, "a bounded wait inside a kernel expired");
+        case GDN_ERR_FULL: return fail(GDN_ERR_FULL, "a row of the paged cache found no page (it took no tokens)");
         default: return fail(static_cast<gdn_status>(code), "device error");
       }
     }

@@ -1,0 +1,221 @@
+// gdn_kv4_store / gdn_kv4_load: tokens' keys and values into 4-bit pages, and
+// back to bf16.
+//
+// Per 16 channels x of a token's head, y = x 2^-exp:
+//   s = e4m3(max|y| / 7, in [2^-9, 240]),  u = 8 + rint(y / s) in [1, 15]
+//
+// Memory-bound: 4 bytes a channel pair in, 9/8 out. A lane takes the 16
+// channels of one scale: 32 bytes of bf16, 8 bytes of codes, one scale. A warp
+// takes 8 groups of 4 tokens, so that a token's 8 code pieces and key scales
+// are contiguous, and the value scales of neighbouring tokens (which lie
+// together, [d/16][64]) meet in one sector.
+//
+// The quotient is rounded exactly without a division per channel. y has 8
+// significant bits, s at most 4: y/s is either k + 1/2 exactly or at least 2^-10
+// from it (y and (k + 1/2) s are both whole multiples of y's last place, which
+// is at least 2^-10 s where |y| > 0.4 s). y times the reciprocal of s is off by
+// less than 2^-19 (|y/s| < 8), so rounding it to multiples of 2^-16 gives k + 1/2
+// exactly where the quotient is, and stays on the right side elsewhere; then it
+// is rounded to whole numbers, ties to even. max|y| / 7 is a true division: its
+// ties (max|y| = 7 times a number of 5 bits) are exact in fp32.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "gdn_check.h"
+#include "gdn_kv4.cuh"
+
+namespace gdn {
+namespace kv4 {
+
+constexpr int kThreads = 256;
+
+struct Args {
+  int n, hk, groups;  // tokens, heads, scales of a token (hk d / 16)
+  long long rows;     // of the pool
+  long long ks, vs;
+  float k_mul, v_mul;  // 2^-exp (store), 2^exp (load)
+  bf16 *k, *v;
+  const int32_t *index;
+  uint8_t *pool;
+  unsigned int *status;
+};
+
+// This lane's token, kind (K or V) and group; false where there is none.
+struct Place {
+  int t, kind, group;
+};
+__device__ __forceinline__ bool place_of(const Args &A, Place &p) {
+  const int lane = threadIdx.x & 31;
+  const int octets = (A.groups + 7) / 8;
+  long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int octet = (int)(w % octets);
+  w /= octets;
+  p.kind = (int)(w & 1);
+  const long long t = (w >> 1) * 4 + (lane >> 3);
+  p.group = octet * 8 + (lane & 7);
+  if (t >= A.n || p.group >= A.groups) return false;
+  p.t = (int)t;
+  return true;
+}
+
+// The token's pool row, or -1.
+__device__ __forceinline__ long long row_of(const Args &A, int t) {
+  const long long r = A.index[t];
+  if (r < -1 || r >= A.rows) {
+    set_status(A.status, GDN_ERR_INDEX);
+    return -1;
+  }
+  return r;
+}
+
+// The block of the group's head; the 8 bytes of its codes and its scale byte.
+template <int D>
+__device__ __forceinline__ void addresses(const Args &A, const Place &p, long long row, uint8_t *&codes, uint8_t *&scale) {
+  constexpr int G = D / kGroup;
+  const int head = p.group / G, g = p.group % G, token = (int)(row % kPage);
+  uint8_t *block = A.pool + ((row / kPage) * A.hk + head) * (long long)block_bytes(D);
+  codes = block + codes_at(D, p.kind) + swizzle(token * (D / 2) + g * 8);
+  scale = block + scales_at(D, p.kind) + (p.kind == 0 ? token * G + g : g * kPage + token);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__ Args A) {
+  griddep_wait();
+  griddep_trigger();
+  Place p;
+  if (!place_of(A, p)) return;
+  const long long row = row_of(A, p.t);
+  const bf16 *src = (p.kind == 0 ? A.k + p.t * A.ks : A.v + p.t * A.vs) + p.group * kGroup;
+  uint32_t w[8];
+  *reinterpret_cast<uint4 *>(w) = __ldcs(reinterpret_cast<const uint4 *>(src));
+  *reinterpret_cast<uint4 *>(w + 4) = __ldcs(reinterpret_cast<const uint4 *>(src) + 1);
+  if (row < 0) return;
+  uint32_t top2 = 0;  // the largest magnitude's bits: an infinity or NaN is at least 0x7f80
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, w[i] & 0x7fff7fffu);
+  const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+  const float mul = p.kind == 0 ? A.k_mul : A.v_mul;
+  const float amax = __uint_as_float(top << 16) * mul;
+  const float wide = fminf(fmaxf(__fdiv_rn(amax, 7.0f), 0.001953125f), 240.0f);
+  __nv_fp8_storage_t byte = __nv_cvt_float_to_fp8(wide, __NV_SATFINITE, __NV_E4M3);
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)));
+  const float r = mul * (1.0f / s);
+  uint32_t code[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float x = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    float q = __fsub_rn(__fmaf_rn(x, r, 192.0f), 192.0f);  // multiples of 2^-16 (beyond +-64 coarser, and clamped)
+    q = fminf(fmaxf(q, -7.0f), 7.0f);
+    const uint32_t u = __float_as_uint(__fadd_rn(q, 12582912.0f + 8.0f)) & 15u;  // 1.5 * 2^23: whole numbers, ties to even
+    code[i / 8] |= u << (4 * (i % 8));
+  }
+  if (top >= 0x7f80u) {
+    byte = 0x7f;  // e4m3 NaN: the group reads back as NaN
+    code[0] = code[1] = 0x99999999u;
+  }
+  uint8_t *codes, *scale;
+  addresses<D>(A, p, row, codes, scale);
+  *reinterpret_cast<uint2 *>(codes) = make_uint2(code[0], code[1]);
+  *scale = byte;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ Args A) {
+  griddep_wait();
+  griddep_trigger();
+  Place p;
+  if (!place_of(A, p)) return;
+  const long long row = row_of(A, p.t);
+  if (row < 0) return;
+  uint8_t *codes, *scale;
+  addresses<D>(A, p, row, codes, scale);
+  const uint2 code = __ldcs(reinterpret_cast<const uint2 *>(codes));
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(*scale, __NV_E4M3))) * (p.kind == 0 ? A.k_mul : A.v_mul);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t c = (i < 4 ? code.x : code.y) >> (8 * (i % 4));
+    const float a = (float)((int)(c & 15) - 8) * s, b = (float)((int)(c >> 4 & 15) - 8) * s;
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  bf16 *dst = (p.kind == 0 ? A.k + p.t * A.ks : A.v + p.t * A.vs) + p.group * kGroup;
+  *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  *(reinterpret_cast<uint4 *>(dst) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// The checks of both calls; A.n stays 0 where there is nothing to do.
+gdn_status arguments(const gdn_kv4_dims *d, const void *k, const void *v, const int32_t *kv_index, const void *pool,
+                     bool store, Args &A) {
+  if (!d) return fail(GDN_ERR_ARG, "dims is NULL");
+  if (d->n_tokens < 0 || d->n_kv_heads < 1 || d->n_kv_heads > 4096)
+    return fail(GDN_ERR_SHAPE, "n_tokens must be >= 0 and n_kv_heads in [1, 4096]");
+  const int D = d->head_dim;
+  if (D != 64 && D != 128 && D != 256) return fail(GDN_ERR_SHAPE, "head_dim must be 64, 128 or 256");
+  if (d->n_pages < 0 || d->n_pages >= (1 << 25)) return fail(GDN_ERR_SHAPE, "n_pages must be in [0, 2^25)");
+  if (d->k_exp < -32 || d->k_exp > 32 || d->v_exp < -32 || d->v_exp > 32)
+    return fail(GDN_ERR_SHAPE, "k_exp and v_exp must be in [-32, 32]");
+  if (d->k_stride % 8 != 0 || d->v_stride % 8 != 0)
+    return fail(GDN_ERR_SHAPE, "token strides must be multiples of 8 elements");
+  const long long width = (long long)d->n_kv_heads * D;
+  if (d->k_stride < width || d->v_stride < width) return fail(GDN_ERR_SHAPE, "token strides must cover the heads");
+  if (d->k_stride >= (1LL << 32) || d->v_stride >= (1LL << 32))
+    return fail(GDN_ERR_SHAPE, "token strides must be below 2^32 elements");
+  const long long warps = ((long long)d->n_tokens + 3) / 4 * 2 * ((width / kGroup + 7) / 8);
+  if ((warps + 7) / 8 > 0x7fffffffLL) return fail(GDN_ERR_SHAPE, "more tokens and heads than a grid holds");
+  A = {};
+  if (d->n_tokens == 0) return GDN_OK;  // empty tensors may have no address
+  GDN_TRY(check_ptr(k, "k"));
+  GDN_TRY(check_ptr(v, "v"));
+  GDN_TRY(check_ptr(kv_index, "kv_index", 4));
+  if (d->n_pages > 0) GDN_TRY(check_ptr(pool, "pool"));
+  const DeviceInfo *dev;
+  GDN_TRY(current_device(&dev));
+  A.n = d->n_tokens;
+  A.hk = d->n_kv_heads;
+  A.groups = (int)(width / kGroup);
+  A.rows = (long long)d->n_pages * kPage;
+  A.ks = d->k_stride;
+  A.vs = d->v_stride;
+  A.k_mul = ldexpf(1.0f, store ? -d->k_exp : d->k_exp);
+  A.v_mul = ldexpf(1.0f, store ? -d->v_exp : d->v_exp);
+  A.k = static_cast<bf16 *>(const_cast<void *>(k));
+  A.v = static_cast<bf16 *>(const_cast<void *>(v));
+  A.index = kv_index;
+  A.pool = static_cast<uint8_t *>(const_cast<void *>(pool));
+  A.status = dev->status;
+  return GDN_OK;
+}
+
+void launch(const Args &A, int D, bool store, void *stream) {
+  const long long warps = ((long long)A.n + 3) / 4 * 2 * ((A.groups + 7) / 8);
+  const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))), block(kThreads);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (D == 64) launch_pdl(store ? store_kernel<64> : load_kernel<64>, grid, block, 0, st, A);
+  if (D == 128) launch_pdl(store ? store_kernel<128> : load_kernel<128>, grid, block, 0, st, A);
+  if (D == 256) launch_pdl(store ? store_kernel<256> : load_kernel<256>, grid, block, 0, st, A);
+}
+
+}  // namespace kv4
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" gdn_status gdn_kv4_store(const gdn_kv4_dims *dims, const void *k, const void *v, const int32_t *kv_index,
+                                    void *pool, void *stream) {
+  kv4::Args A;
+  GDN_TRY(kv4::arguments(dims, k, v, kv_index, pool, true, A));
+  if (A.n == 0) return GDN_OK;
+  kv4::launch(A, dims->head_dim, true, stream);
+  return check_launch("kv4_store");
+}
+
+extern "C" gdn_status gdn_kv4_load(const gdn_kv4_dims *dims, const void *pool, const int32_t *kv_index, void *k, void *v,
+                                   void *stream) {
+  kv4::Args A;
+  GDN_TRY(kv4::arguments(dims, k, v, kv_index, pool, false, A));
+  if (A.n == 0) return GDN_OK;
+  kv4::launch(A, dims->head_dim, false, stream);
+  return check_launch("kv4_load");
+}

@@ -17,14 +17,17 @@ _PKG = Path(__file__).resolve().parent
 LIB_PATH = _PKG / "_build" / "libgdn.so"
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_ARG", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_MASK", 4: "GDN_ERR_INDEX",
-          5: "GDN_ERR_CUDA", 6: "GDN_ERR_WORKSPACE", 7: "GDN_ERR_TIMEOUT"}
+          5: "GDN_ERR_CUDA", 6: "GDN_ERR_WORKSPACE", 7: "GDN_ERR_TIMEOUT", 8: "GDN_ERR_FULL"}
 EXPORTS = ("gdn_decode_step", "gdn_verify_with_checkpoints", "gdn_prefill_chunked",
            "gdn_prefill_workspace_size", "gdn_state_copy", "gdn_check_status", "gdn_last_error",
            "gdn_prefill_chunked_static_scratch", "gdn_commit_accepted", "gdn_decode_step_mxfp8",
            "gdn_prefill_chunked_ckpt", "gdn_in_proj", "gdn_out_proj", "gdn_copy_overlapped",
            "gdn_head_norm_rope", "gdn_attn_prefill", "gdn_attn_shared_prefix", "gdn_attn_workspace_size",
-           "gdn_accept_draft")
+           "gdn_accept_draft", "gdn_kv4_store", "gdn_kv4_load", "gdn_attn_kv4", "gdn_attn_kv4_workspace_size",
+           "gdn_beam_select", "gdn_beam_workspace_size", "gdn_cache_fork", "gdn_slots_copy")
 MAX_OVERLAPPED_COPIES = 8
+MAX_SLOT_POOLS = 4
+PAGE_TOKENS = 64
 
 
 class GdnError(RuntimeError):
@@ -65,6 +68,30 @@ class AttnDims(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("q_stride", "kv_stride", "kv_rows")]
 
 
+class Kv4Dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_kv_heads", "head_dim", "n_pages", "k_exp", "v_exp")] + [
+        (n, ctypes.c_int64) for n in ("k_stride", "v_stride")]
+
+
+class AttnKv4Dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "n_q_heads", "n_kv_heads", "head_dim", "n_pages", "max_pages",
+                                              "k_exp", "v_exp")] + [("scale", ctypes.c_float), ("q_stride", ctypes.c_int64)]
+
+
+class BeamDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_groups", "beams", "vocab", "half", "eos")] + [
+        ("row_stride", ctypes.c_int64)]
+
+
+class ForkDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_rows", "T", "max_pages", "n_pages")]
+
+
+class SlotPool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("base", "src", "dst")] + [("slot_bytes", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("n", "n_layers", "n_slots")]
+
+
 _lib = None
 
 
@@ -101,13 +128,24 @@ def load_library(path: Path | str | None = None):
     lib.gdn_attn_workspace_size.argtypes = [AP]
     lib.gdn_attn_workspace_size.restype = ctypes.c_size_t
     lib.gdn_accept_draft.argtypes = [ctypes.c_int32] * 3 + [P] * 8
+    lib.gdn_kv4_store.argtypes = [ctypes.POINTER(Kv4Dims)] + [P] * 5
+    lib.gdn_kv4_load.argtypes = [ctypes.POINTER(Kv4Dims)] + [P] * 5
+    lib.gdn_attn_kv4.argtypes = [ctypes.POINTER(AttnKv4Dims)] + [P] * 7 + [ctypes.c_size_t, P]
+    lib.gdn_attn_kv4_workspace_size.argtypes = [ctypes.POINTER(AttnKv4Dims)]
+    lib.gdn_attn_kv4_workspace_size.restype = ctypes.c_size_t
+    lib.gdn_beam_select.argtypes = [ctypes.POINTER(BeamDims)] + [P] * 8 + [ctypes.c_size_t, P]
+    lib.gdn_beam_workspace_size.argtypes = [ctypes.POINTER(BeamDims)]
+    lib.gdn_beam_workspace_size.restype = ctypes.c_size_t
+    lib.gdn_cache_fork.argtypes = [ctypes.POINTER(ForkDims)] + [P] * 15
+    lib.gdn_slots_copy.argtypes = [ctypes.POINTER(SlotPool), ctypes.c_int32, P]
     lib.gdn_check_status.argtypes = [P]
     lib.gdn_last_error.restype = ctypes.c_char_p
     for name in ("gdn_decode_step", "gdn_verify_with_checkpoints", "gdn_prefill_chunked", "gdn_state_copy",
                  "gdn_check_status", "gdn_prefill_chunked_static_scratch", "gdn_commit_accepted",
                  "gdn_decode_step_mxfp8", "gdn_prefill_chunked_ckpt", "gdn_in_proj", "gdn_out_proj",
                  "gdn_copy_overlapped", "gdn_head_norm_rope", "gdn_attn_prefill", "gdn_attn_shared_prefix",
-                 "gdn_accept_draft"):
+                 "gdn_accept_draft", "gdn_kv4_store", "gdn_kv4_load", "gdn_attn_kv4", "gdn_beam_select",
+                 "gdn_cache_fork", "gdn_slots_copy"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -361,6 +399,130 @@ def accept_draft(tokens, target_probs, draft_probs, uniform, accept_len, next_to
     B, T, V = target_probs.shape
     _check(load_library().gdn_accept_draft(B, T, V, _ptr(tokens), _ptr(target_probs), _ptr(draft_probs), _ptr(uniform),
                                            _ptr(n_tokens), _ptr(accept_len), _ptr(next_token), _stream(stream)))
+
+
+def _page_pool(pool, heads, d):
+    """Pages of a pool uint8 [n_pages, heads, 72 d]."""
+    if pool.dtype is not torch.uint8 or pool.dim() != 3 or tuple(pool.shape[1:]) != (heads, 72 * d) or not pool.is_contiguous():
+        raise ValueError(f"the pool must be a dense uint8 tensor [n_pages, {heads}, {72 * d}]")
+    return pool.shape[0]
+
+
+def _table(page_table, rows=None):
+    """Entries of a line of a page table int32 [rows, max_pages]."""
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous() or (
+            rows is not None and page_table.shape[0] != rows):
+        raise ValueError("page tables must be dense int32 tensors [rows, max_pages]")
+    return page_table.shape[1]
+
+
+def kv4_pool(n_pages, n_kv_heads, head_dim, device="cuda") -> torch.Tensor:
+    """A pool of n_pages pages of 64 tokens, uint8 [n_pages, n_kv_heads, 72 head_dim]."""
+    return torch.zeros((n_pages, n_kv_heads, 72 * head_dim), dtype=torch.uint8, device=device)
+
+
+def make_kv4_dims(k, pool, v=None, k_exp=0, v_exp=0) -> Kv4Dims:
+    """Sizes of a kv4_store / kv4_load call on k [n, Hk, d]; v's tokens are spaced as k's unless v is given."""
+    n, hk, d, ks = _layout(k, "k")
+    return Kv4Dims(n, hk, d, _page_pool(pool, hk, d), k_exp, v_exp, ks, ks if v is None else _layout(v, "v")[3])
+
+
+def kv4_store(dims: Kv4Dims, k, v, kv_index, pool, stream=None):
+    """gdn_kv4_store: k, v bf16 [n, Hk, d] into the pool rows kv_index int32 [n] (-1: not kept), 4 bits each."""
+    _spaced(k, dims.k_stride, "k")
+    _spaced(v, dims.v_stride, "v")
+    _check(load_library().gdn_kv4_store(ctypes.byref(dims), _ptr(k), _ptr(v), _ptr(kv_index), _ptr(pool), _stream(stream)))
+
+
+def kv4_load(dims: Kv4Dims, pool, kv_index, k, v, stream=None):
+    """gdn_kv4_load: pool rows kv_index int32 [n] to k, v bf16 [n, Hk, d], exactly as attn_kv4 uses them."""
+    _spaced(k, dims.k_stride, "k")
+    _spaced(v, dims.v_stride, "v")
+    _check(load_library().gdn_kv4_load(ctypes.byref(dims), _ptr(pool), _ptr(kv_index), _ptr(k), _ptr(v), _stream(stream)))
+
+
+def make_attn_kv4_dims(q, pool, page_table, scale=None, k_exp=0, v_exp=0) -> AttnKv4Dims:
+    """Sizes of an attn_kv4 call: q [B, T, Hq, d], one layer's pool, page_table int32 [B, max_pages]."""
+    if q.dim() != 4:
+        raise ValueError("q must be [rows, tokens, heads, head_dim]")
+    one = q.shape[1] == 1 and q.stride(1) != q.stride(0)  # the stride of a dimension of one token says nothing
+    _, hq, d, qs = _layout(q[:, 0] if one else q, "q")
+    hk = pool.shape[1] if pool.dim() == 3 else 0
+    return AttnKv4Dims(q.shape[0], q.shape[1], hq, hk, d, _page_pool(pool, hk, d), _table(page_table, q.shape[0]), k_exp,
+                       v_exp, d ** -0.5 if scale is None else scale, qs)
+
+
+def attn_kv4_workspace_size(dims: AttnKv4Dims) -> int:
+    """Workspace bytes of attn_kv4."""
+    return int(load_library().gdn_attn_kv4_workspace_size(ctypes.byref(dims)))
+
+
+def attn_kv4_workspace(dims: AttnKv4Dims, device="cuda") -> torch.Tensor:
+    """A workspace tensor for attn_kv4, reusable from call to call on one stream."""
+    return torch.empty(max(attn_kv4_workspace_size(dims), 1), dtype=torch.uint8, device=device)
+
+
+def attn_kv4(dims: AttnKv4Dims, q, pool, page_table, kv_len, out, workspace, q_len=None, stream=None):
+    """gdn_attn_kv4: q [B, T, Hq, d] over the pages of each row, kv_len int32 [B] tokens of it."""
+    _check(load_library().gdn_attn_kv4(
+        ctypes.byref(dims), _ptr(q), _ptr(pool), _ptr(page_table), _ptr(kv_len), _ptr(q_len), _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+
+
+def make_beam_dims(logits, eos=-1) -> BeamDims:
+    """Sizes of a beam_select call on logits [groups, beams, V], fp32 or bf16, rows evenly spaced."""
+    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.dim() != 3:
+        raise ValueError("logits must be fp32 or bf16 [groups, beams, vocab]")
+    (g, w, v), st = logits.shape, logits.stride()
+    stride = st[1] if w > 1 else st[0] if g > 1 else v
+    if (v > 1 and st[2] != 1) or (g > 1 and w > 1 and st[0] != w * st[1]):
+        raise ValueError("logits must have dense rows, evenly spaced")
+    return BeamDims(g, w, v, int(logits.dtype is torch.bfloat16), -1 if eos is None else eos, stride)
+
+
+def beam_workspace(logits) -> torch.Tensor:
+    """A workspace tensor for beam_select on logits of this shape, reusable from call to call on one stream."""
+    n = int(load_library().gdn_beam_workspace_size(ctypes.byref(make_beam_dims(logits))))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=logits.device)
+
+
+def beam_select(logits, scores, parent, token, new_scores, workspace, done=None, new_done=None, eos=-1, stream=None):
+    """gdn_beam_select: the best continuations of each group's beams; logits [groups, beams, V], scores fp32 and done
+    uint8 [groups, beams] -> parent (row numbers), token int32, new_scores, new_done [groups, beams]."""
+    dims = make_beam_dims(logits, eos)
+    _check(load_library().gdn_beam_select(
+        ctypes.byref(dims), _ptr(logits), _ptr(scores), _ptr(done), _ptr(parent), _ptr(token), _ptr(new_scores),
+        _ptr(new_done), _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        _stream(stream)))
+
+
+def cache_fork(page_table, kv_len, page_table_out, kv_len_out, kv_index, page_src, page_dst, n_pages, parent=None,
+               n_new=None, pinned=None, state_idx=None, state_idx_out=None, state_src=None, state_dst=None, stream=None):
+    """gdn_cache_fork: rows become copies of the rows parent int32 [R] and take n_new tokens (kv_index int32 [R, T]);
+    page_src / page_dst and state_src / state_dst int32 [R] are slots_copy's."""
+    rows = page_table.shape[0]
+    width = _table(page_table)
+    if _table(page_table_out, rows) != width:
+        raise ValueError("page_table and page_table_out must have one shape")
+    T = 0 if kv_index is None else kv_index.shape[1]
+    dims = ForkDims(rows, T, width, n_pages)
+    _check(load_library().gdn_cache_fork(
+        ctypes.byref(dims), _ptr(parent), _ptr(n_new), _ptr(page_table), _ptr(kv_len), _ptr(pinned), _ptr(page_table_out),
+        _ptr(kv_len_out), _ptr(kv_index), _ptr(page_src), _ptr(page_dst), _ptr(state_idx), _ptr(state_idx_out),
+        _ptr(state_src), _ptr(state_dst), _stream(stream)))
+
+
+def slots_copy(pools, stream=None):
+    """gdn_slots_copy: pools (at most MAX_SLOT_POOLS) of (tensor [n_layers, n_slots, ...], src, dst int32 [n]): in every
+    layer slot src[i] is copied to slot dst[i]; -1 skips a pair."""
+    arr = (SlotPool * max(1, len(pools)))()
+    for a, (x, src, dst) in zip(arr, pools):
+        if not x.is_contiguous() or x.dim() < 2 or src.numel() != dst.numel():
+            raise ValueError("a pool must be a dense tensor [n_layers, n_slots, ...], src and dst of one length")
+        layers, n = x.shape[0], x.shape[1]
+        a.base, a.src, a.dst, a.n, a.n_layers, a.n_slots = _ptr(x), _ptr(src), _ptr(dst), src.numel(), layers, n
+        a.slot_bytes = x.numel() // max(1, layers * n) * x.element_size()
+    _check(load_library().gdn_slots_copy(arr, len(pools), _stream(stream)))
 
 
 def check_status(stream=None):

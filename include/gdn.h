@@ -72,7 +72,8 @@ typedef enum gdn_status {
   GDN_ERR_INDEX = 4,     /* (device) a slot index is outside [0, n_slots) */
   GDN_ERR_CUDA = 5,      /* a CUDA runtime call failed */
   GDN_ERR_WORKSPACE = 6, /* workspace missing or smaller than required */
-  GDN_ERR_TIMEOUT = 7    /* (device) a bounded wait inside a kernel expired */
+  GDN_ERR_TIMEOUT = 7,   /* (device) a bounded wait inside a kernel expired */
+  GDN_ERR_FULL = 8       /* (device) a row of the paged cache found no page */
 } gdn_status;
 
 /* Dimensions of one call.
@@ -515,9 +516,221 @@ gdn_status gdn_accept_draft(int32_t B, int32_t T, int32_t V, const int32_t *toke
                             const float *draft_probs, const float *uniform, const int32_t *n_tokens,
                             int32_t *accept_len, int32_t *next_token, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Beam search over a paged cache held in 4 bits: a cache in which a row grows
+ * page by page instead of in an extent of fixed room, rows that part later
+ * share the pages of what they have in common, and the step that re-parents
+ * rows after each selection.
+ *
+ * statecache.py (squad-0.8b, qev_fast), CacheQwen35: a row's cache is a state
+ * per GDN layer and the keys and values of its tokens per attention layer, and
+ * rows continue from a shared prefix; generate.py (sparkle,
+ * mlx_streaming/mtp): several candidate paths of one prompt, of which some are
+ * kept. No counterpart on the pages for the 4-bit pages and the beams' scores.
+ *
+ * A page holds GDN_PAGE_TOKENS tokens of every key head of one layer; a pool is
+ * uint8 [n_pages][n_kv_heads][72 * head_dim] per layer. Pool row r is token
+ * r % 64 of page r / 64. The block of one head, in bytes from its start:
+ *   [0, 32 d)      the keys' codes, 64 rows of d/2 bytes
+ *   [32 d, 64 d)   the values' codes
+ *   [64 d, 68 d)   the keys' scales [64][d/16]
+ *   [68 d, 72 d)   the values' scales [d/16][64]
+ * Channel 2i of a token is the low half of its row's byte i, channel 2i+1 the
+ * high half. Inside a block of codes the bits 4-6 of a byte's offset are xored
+ * with its bits 7-9 (the attention kernel's shared-memory reads are then free
+ * of bank conflicts although a block arrives as one bulk copy). A code u stands
+ * for (u - 8) * s * 2^exp, s the e4m3 scale of its 16 channels; store writes
+ * u in [1, 15]. Every such number has at most 7 significant bits: it is exact
+ * in bf16 and in fp16.
+ *
+ * A row of the cache is a line of a page table, int32 [rows][max_pages], and a
+ * length: token i of the row is row i % 64 of page table[row][i / 64]. Entries
+ * from ceil(length / 64) on are never used. All layers share the table.
+ * ------------------------------------------------------------------------ */
+#define GDN_PAGE_TOKENS 64
+
+/* Sizes of gdn_kv4_store and gdn_kv4_load.
+ *   n_tokens, n_kv_heads, head_dim   head_dim one of 64, 128, 256
+ *   n_pages          pages of the pool, at most 2^25 - 1
+ *   k_exp, v_exp     the pool's exponents, in [-32, 32]
+ *   k_stride, v_stride   elements between tokens of k and v, multiples of 8 */
+typedef struct gdn_kv4_dims {
+  int32_t n_tokens, n_kv_heads, head_dim, n_pages, k_exp, v_exp;
+  int64_t k_stride, v_stride;
+} gdn_kv4_dims;
+
+/* Tokens' keys and values into their pool rows.
+ *   k, v      bf16, token t's heads at t * {k,v}_stride (views into one
+ *             projection's rows are fine)
+ *   kv_index  int32 [n_tokens]: token t's pool row, -1 = not kept; any other
+ *             value outside [0, 64 n_pages) is a device error (GDN_ERR_INDEX)
+ *             and the token is not kept. Rows must be distinct.
+ *   pool      uint8 [n_pages][n_kv_heads][72 head_dim]
+ * Per 16 channels x of a token's head, y = x 2^-exp:
+ *   s = e4m3(max(2^-9, min(240, max|y| / 7))),  u = 8 + max(-7, min(7, rint(y / s)))
+ * both rounded to the nearest, ties to even, exactly: every call gives the same
+ * bytes. Magnitudes above 1680 * 2^exp saturate; below 2^-10 * 2^exp they
+ * become zero. 16 channels of which one is not finite read back as NaN. */
+gdn_status gdn_kv4_store(const gdn_kv4_dims *dims, const void *k, const void *v, const int32_t *kv_index, void *pool,
+                         void *stream);
+
+/* Pool rows back to bf16 (exactly the numbers that gdn_attn_kv4 uses): the
+ * cached tokens of a row whose next chunk runs through gdn_attn_prefill.
+ * Token t's heads go to t * {k,v}_stride of k and v; kv_index as above, a token
+ * with -1 (or a bad row) keeps what k and v held. Rows may repeat. */
+gdn_status gdn_kv4_load(const gdn_kv4_dims *dims, const void *pool, const int32_t *kv_index, void *k, void *v,
+                        void *stream);
+
+/* Sizes of a gdn_attn_kv4 call.
+ *   B, T             rows, query tokens per row (1 for decode, the drafted tokens
+ *                    for verify, at most 64)
+ *   n_q_heads, n_kv_heads, head_dim   n_q_heads a multiple of n_kv_heads, at most
+ *                    64 query heads per key head; head_dim one of 64, 128, 256
+ *   n_pages          pages of the pool, at most 2^25 - 1
+ *   max_pages        entries of a page table's line
+ *   k_exp, v_exp     the pool's exponents, in [-32, 32]
+ *   scale            multiplies q.k before the softmax; finite, and so is
+ *                    |scale| 2^k_exp log2(e)
+ *   q_stride         elements between query tokens, a multiple of 8 */
+typedef struct gdn_attn_kv4_dims {
+  int32_t B, T, n_q_heads, n_kv_heads, head_dim, n_pages, max_pages, k_exp, v_exp;
+  float scale;
+  int64_t q_stride;
+} gdn_attn_kv4_dims;
+
+/* Attention of decode (T = 1) or verify rows over their pages.
+ *   q           bf16 [B][T] tokens, q_stride apart
+ *   pool        one layer's pages
+ *   page_table  int32 [B][max_pages]
+ *   kv_len      int32 [B]: the row's tokens, the call's own last (their keys are
+ *               in the pool already); 0: the row's outputs are zeros
+ *   q_len       int32 [B] in [0, T], the row's real tokens, or NULL (T each)
+ *   out         bf16 [B][T][n_q_heads][head_dim]
+ *   workspace   gdn_attn_kv4_workspace_size(dims) bytes, 256-byte aligned; its
+ *               contents need not be preserved, and calls that may overlap (on
+ *               several streams) need one each
+ * Token t sees keys j <= kv_len - q_len + t; a token that sees nothing, or with
+ * t >= q_len, gets zeros. Keys and values enter the products exactly, queries
+ * in fp16 relative to their head's largest channel (error below 2^-25 of it),
+ * probabilities in fp16; statistics and accumulators are fp32. A length outside
+ * [0, 64 max_pages], a q_len outside [0, T] or a page outside [0, n_pages) is a
+ * device error (GDN_ERR_INDEX): outputs of that row are not written. What the
+ * last page holds behind the row's tokens is never used, whatever it is; values
+ * that are not finite within a row may also reach its earlier tokens of the call. */
+gdn_status gdn_attn_kv4(const gdn_attn_kv4_dims *dims, const void *q, const void *pool, const int32_t *page_table,
+                        const int32_t *kv_len, const int32_t *q_len, void *out, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of gdn_attn_kv4 on the current device (0 on invalid dims). */
+size_t gdn_attn_kv4_workspace_size(const gdn_attn_kv4_dims *dims);
+
+/* Sizes of a gdn_beam_select call.
+ *   n_groups, beams  beams per group in [1, 32]
+ *   vocab            in [1, 2^24]
+ *   half             0: fp32 logits, 1: bf16 logits
+ *   eos              the token that finishes a beam, in [0, vocab), or -1: none
+ *   row_stride       elements between two beams' logits, at least vocab */
+typedef struct gdn_beam_dims {
+  int32_t n_groups, beams, vocab, half, eos;
+  int64_t row_stride;
+} gdn_beam_dims;
+
+/* The best continuations of each group's beams, one pass over the logits.
+ *   logits      [n_groups * beams] rows, row_stride apart
+ *   scores      fp32 [n_groups][beams]: the beams' log-probabilities so far
+ *               (-inf: no beam yet, as at the first step for all but one)
+ *   done        uint8 [n_groups][beams], nonzero for finished beams, or NULL
+ *   parent      int32 [n_groups][beams]: the ROW (group * beams + beam) continued,
+ *               as gdn_cache_fork takes it
+ *   token       int32 [n_groups][beams]
+ *   new_scores  fp32 [n_groups][beams], best first
+ *   new_done    uint8 [n_groups][beams]: finished before or now; NULL iff done is
+ *   workspace   gdn_beam_workspace_size(dims) bytes, 256-byte aligned
+ * Candidates: score + logit - log sum exp(logits) for every token of a beam that
+ * is not finished; the beam itself, with token eos and its score unchanged, for
+ * a finished one (its logits are not read). Candidates that are -inf or NaN (a
+ * row whose logits hold NaN or +inf, or nothing finite, has no others) do not
+ * count. The group's `beams` best are taken, ties to the lowest beam, then to
+ * the lowest token. Where there are fewer, the places left over get their own
+ * row as parent, token -1, score -inf and done 0. Sums of exponentials are
+ * fp32, the candidates' scores 64-bit, new_scores rounded once. new_scores and
+ * new_done may be the arrays scores and done. */
+gdn_status gdn_beam_select(const gdn_beam_dims *dims, const void *logits, const float *scores, const uint8_t *done,
+                           int32_t *parent, int32_t *token, float *new_scores, uint8_t *new_done, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of gdn_beam_select (0 on invalid dims). */
+size_t gdn_beam_workspace_size(const gdn_beam_dims *dims);
+
+/* Sizes of a gdn_cache_fork call.
+ *   n_rows     rows of the cache, at most 1024
+ *   T          the most tokens a row takes now, in [0, 2^20]
+ *   max_pages  entries of a page table's line
+ *   n_pages    pages of the pools, at most 2^20 */
+typedef struct gdn_fork_dims {
+  int32_t n_rows, T, max_pages, n_pages;
+} gdn_fork_dims;
+
+/* Rows of the cache become copies of other rows, and get room for the tokens
+ * they take next: the bookkeeping, on the device. Nothing but these arrays is
+ * kept between calls: a page is free when no row and no pin names it.
+ *   parent      int32 [n_rows]: row r continues row parent[r]; -1: row r is
+ *               emptied; NULL: every row continues itself
+ *   n_new       int32 [n_rows] in [0, T]: the tokens row r takes, or NULL (T each)
+ *   page_table, kv_len  int32 [n_rows][max_pages], [n_rows]: before the call
+ *   pinned      uint8 [n_pages], nonzero for pages that others hold (a shared
+ *               prompt kept for later rows): never taken and never written; or NULL
+ *   page_table_out, kv_len_out  after it; other buffers than page_table, kv_len.
+ *               Entries behind a row's pages are left as they were.
+ *   kv_index    int32 [n_rows][T]: the pool rows of the tokens taken
+ *               (gdn_kv4_store), -1 behind n_new; NULL iff T is 0
+ *   page_src, page_dst  int32 [n_rows]: the page that row r's last page is to be
+ *               copied from and to before anything is stored (gdn_slots_copy); -1: none
+ *   state_idx   int32 [n_rows], the rows' distinct GDN state slots before the
+ *               call, or NULL (then the next three are NULL too)
+ *   state_idx_out, state_src, state_dst  int32 [n_rows]: the slots after it (the
+ *               same set) and the copies that this takes; -1: none
+ * Row r gets its parent's L tokens and pages, shared. If it takes tokens and its
+ * last page is partly filled, that page stays with the row that has the most
+ * tokens among those that hold it (ties: the lowest row), unless it is pinned;
+ * every other row that takes tokens gets a copy. New pages are the
+ * lowest-numbered free ones, in the order of the rows, for a row its copy first.
+ * A row whose pages do not exist any more (none free, or more than max_pages)
+ * takes no tokens (kv_len_out = L, kv_index -1), which is a device error
+ * (GDN_ERR_FULL). A page that several rows hold stands at the same place in
+ * all of them, as copies of a row have it. The lowest child of a row keeps that
+ * row's state slot; other children, and emptied rows, take the slots of rows
+ * without children, in order. A parent outside [-1, n_rows), a length outside
+ * [0, 64 max_pages], an n_new outside [0, T] or a used page outside
+ * [0, n_pages) is a device error (GDN_ERR_INDEX), taken as -1, 0, 0, and a page
+ * that nothing is copied from. */
+gdn_status gdn_cache_fork(const gdn_fork_dims *dims, const int32_t *parent, const int32_t *n_new,
+                          const int32_t *page_table, const int32_t *kv_len, const uint8_t *pinned,
+                          int32_t *page_table_out, int32_t *kv_len_out, int32_t *kv_index, int32_t *page_src,
+                          int32_t *page_dst, const int32_t *state_idx, int32_t *state_idx_out, int32_t *state_src,
+                          int32_t *state_dst, void *stream);
+
+/* Copies of slots within pools, in every layer, all in one launch: the pages,
+ * states and conv tails that gdn_cache_fork asks for.
+ *   pools  array of n_pools (at most GDN_MAX_SLOT_POOLS) descriptors:
+ *          base     [n_layers][n_slots][slot_bytes], slot_bytes a multiple of 16
+ *          src, dst DEVICE int32 [n]: in every layer slot src[i] goes to slot
+ *                   dst[i]; src[i] = -1 skips pair i
+ * A slot outside [0, n_slots) is a device error (GDN_ERR_INDEX) and the pair is
+ * skipped. No slot may be the destination of two pairs, nor the source of one
+ * and the destination of another. n * n_layers of a pool at most 2^20. */
+#define GDN_MAX_SLOT_POOLS 4
+typedef struct gdn_slot_pool {
+  void *base;
+  const int32_t *src, *dst;
+  int64_t slot_bytes;
+  int32_t n, n_layers, n_slots;
+} gdn_slot_pool;
+gdn_status gdn_slots_copy(const gdn_slot_pool *pools, int32_t n_pools, void *stream);
+
 /* Synchronise `stream`, then return (and clear) a device-detected error
  * recorded on the current device since the last check (GDN_ERR_MASK,
- * GDN_ERR_INDEX, GDN_ERR_TIMEOUT; the lowest code wins when several were
+ * GDN_ERR_INDEX, GDN_ERR_TIMEOUT, GDN_ERR_FULL; the lowest code wins when several were
  * recorded), GDN_ERR_CUDA if the stream reports a CUDA error, else GDN_OK. */
 gdn_status gdn_check_status(void *stream);
 
