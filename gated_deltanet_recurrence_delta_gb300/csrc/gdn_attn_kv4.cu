@@ -15,10 +15,10 @@
 //   - Scores S^T = K Q^T: a lane holds a quarter of two keys' channels. The order
 //     of the channels in the product is free, so the eight codes of a 32-bit word
 //     go where they come out: nibble i and i + 4 form a pair. (w << 2) and (w >> 6)
-//     put two nibbles each at the mantissa's bits 2 and 6; with the exponent of 1
-//     that is 1 + u/256 and 1 + u/16, and one paired fp16 multiply-add with
-//     (256 s, -264 s) or (16 s, -24 s) gives (u - 8) s exactly (s has 4 significant
-//     bits, 264 = 33 * 8): 10 instructions for 8 numbers.
+//     put two nibbles each at the mantissa's bits 2 and 6; with the exponents of 256
+//     and 16 that is 256 + u and 16 + u, and one paired fp16 multiply-add with s and
+//     -264 s or -24 s gives (u - 8) s exactly (s has 4 significant bits, 264 = 33 * 8):
+//     10 instructions for 8 numbers.
 //   - Output O^T = V^T P^T: a lane holds 4 keys of an eighth of the channels;
 //     byte permutes put two keys' nibbles of one channel into one register. The
 //     probabilities move from the scores' layout to the operand's by 8x8
@@ -149,24 +149,28 @@ __device__ __forceinline__ __half2 e4m3x2(uint32_t w) {
   return half2_of(h);
 }
 
-// The multipliers and addends of a pair of scales.
+// A pair of scales, and what they make of the bias and the exponents.
 struct Scale {
-  __half2 m16, a16, m256, a256;
-  __device__ __forceinline__ explicit Scale(__half2 s) {
-    m16 = __hmul2(s, __float2half2_rn(16.0f));
-    a16 = __hmul2(s, __float2half2_rn(-24.0f));
-    m256 = __hmul2(s, __float2half2_rn(256.0f));
-    a256 = __hmul2(s, __float2half2_rn(-264.0f));
+  __half2 s, at2, at6;
+  __device__ __forceinline__ explicit Scale(__half2 x) : s(x) {
+    at2 = __hmul2(x, __float2half2_rn(-264.0f));
+    at6 = __hmul2(x, __float2half2_rn(-24.0f));
   }
 };
-// Nibble i of each half of w, times its scale, in v[i].
+__device__ __forceinline__ __half2 field(uint32_t x, uint32_t mask, uint32_t exponent) {  // (x & mask) | exponent
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(exponent));
+  return half2_of(y);
+}
+// Nibble i of each half of w, times its scale, in v[i]: at the mantissa's bit 2 of 256 it is 256 + u, at bit 6 of 16
+// it is 16 + u.
 __device__ __forceinline__ void unpack(uint32_t w, const Scale &s, uint32_t (&v)[4]) {
   const uint32_t x = w << 2, y = w >> 6;
-  constexpr uint32_t one = 0x3c003c00u, m2 = 0x003c003cu, m6 = 0x03c003c0u;
-  v[0] = bits(__hfma2(half2_of((x & m2) | one), s.m256, s.a256));
-  v[1] = bits(__hfma2(half2_of((x & m6) | one), s.m16, s.a16));
-  v[2] = bits(__hfma2(half2_of((y & m2) | one), s.m256, s.a256));
-  v[3] = bits(__hfma2(half2_of((y & m6) | one), s.m16, s.a16));
+  constexpr uint32_t e2 = 0x5c005c00u, e6 = 0x4c004c00u, m2 = 0x003c003cu, m6 = 0x03c003c0u;
+  v[0] = bits(__hfma2(field(x, m2, e2), s.s, s.at2));
+  v[1] = bits(__hfma2(field(x, m6, e6), s.s, s.at6));
+  v[2] = bits(__hfma2(field(y, m2, e2), s.s, s.at2));
+  v[3] = bits(__hfma2(field(y, m6, e6), s.s, s.at6));
 }
 
 // Where key r of a warp's 16 (as rows of the first product) stands among its tokens, so that the shared-memory reads
@@ -190,7 +194,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
   __shared__ int s_b, s_n;
   __shared__ long long s_list[2 * kThreads];  // where the share's blocks stand in the pool; -1: no such page
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&s_full[i], 1);
@@ -259,10 +264,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
   if (s_b < 0) return;
 
   // ---- the blocks of the share: entry e is page e of it
-  const long long count = share.x1 - share.x;
+  const long long x0 = share.x;
+  const uint32_t count = (uint32_t)(share.x1 - x0);  // pages of the share
   Share walk = share;
-  auto list = [&](long long e0) {  // entries [e0, e0 + kThreads)
-    walk.x = share.x1 - count + e0 + tid;
+  auto list = [&](uint32_t e0) {  // entries [e0, e0 + kThreads)
+    walk.x = x0 + e0 + tid;
     Segment at;
     long long block = -1;
     if (walk.x < walk.x1) {
@@ -272,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
     }
     s_list[(e0 + tid) % (2 * kThreads)] = block;
   };
-  auto copy = [&](long long e, int stage) {  // one thread; the stage is empty
+  auto copy = [&](uint32_t e, int stage) {  // one thread; the stage is empty
     const long long block = s_list[e % (2 * kThreads)];
     s_bad[stage] = block < 0;
     if (block < 0) {
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
   list(0);
   __syncthreads();
   if (tid == 0)
-    for (int e = 0; e < S::kStages - 2 && e < count; ++e) copy(e, e);
+    for (uint32_t e = 0; e < S::kStages - 2 && e < count; ++e) copy(e, e);
 
   // ---- the products
   const int row = lane >> 2, t = lane & 3;  // the lane's place in the operands
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
   Segment g;
   int stage = 0;
   uint32_t parity = 0;  // of the ring's round
-  long long done = 0;   // pages of the share
+  uint32_t done = 0;    // pages of the share
   bool dead = false;
   while (next_segment(A, units, share, g)) {
     int ql;
@@ -756,6 +762,8 @@ gdn_status check_dims(const gdn_attn_kv4_dims *d) {
     return fail(GDN_ERR_SHAPE, "k_exp and v_exp must be in [-32, 32]");
   if (d->q_stride % 8 != 0 || d->q_stride < (long long)d->n_q_heads * D || d->q_stride >= (1LL << 32))
     return fail(GDN_ERR_SHAPE, "q_stride must be a multiple of 8 elements that covers the heads, below 2^32");
+  if ((double)d->B * d->T * d->n_q_heads * d->max_pages > 1099511627776.0)
+    return fail(GDN_ERR_SHAPE, "B * T * n_q_heads * max_pages must be at most 2^40");
   if (!(fabs(ldexp((double)d->scale, d->k_exp) * 1.4426950408889634) <= 3.4e38))
     return fail(GDN_ERR_ARG, "|scale| 2^k_exp log2(e) must be finite");
   return GDN_OK;

@@ -541,7 +541,8 @@ gdn_status gdn_accept_draft(int32_t B, int32_t T, int32_t V, const int32_t *toke
  * of bank conflicts although a block arrives as one bulk copy). A code u stands
  * for (u - 8) * s * 2^exp, s the e4m3 scale of its 16 channels; store writes
  * u in [1, 15]. Every such number has at most 7 significant bits: it is exact
- * in bf16 and in fp16.
+ * in bf16 and in fp16. (Scales above 240, which store never writes, are not
+ * supported by gdn_attn_kv4.)
  *
  * A row of the cache is a line of a page table, int32 [rows][max_pages], and a
  * length: token i of the row is row i % 64 of page table[row][i / 64]. Entries
@@ -587,7 +588,8 @@ gdn_status gdn_kv4_load(const gdn_kv4_dims *dims, const void *pool, const int32_
  *   n_q_heads, n_kv_heads, head_dim   n_q_heads a multiple of n_kv_heads, at most
  *                    64 query heads per key head; head_dim one of 64, 128, 256
  *   n_pages          pages of the pool, at most 2^25 - 1
- *   max_pages        entries of a page table's line
+ *   max_pages        entries of a page table's line; B T n_q_heads max_pages at
+ *                    most 2^40
  *   k_exp, v_exp     the pool's exponents, in [-32, 32]
  *   scale            multiplies q.k before the softmax; finite, and so is
  *                    |scale| 2^k_exp log2(e)
