@@ -12,29 +12,29 @@
 // memory, where a tile of 128 keys in fp16 would be written and read again for at
 // most 8 useful columns out of a decode step's handful of queries.
 //
-//   - Scores S^T = K Q^T: a lane holds a quarter of two keys' channels. The order
-//     of the channels in the product is free, so the eight codes of a 32-bit word
-//     go where they come out: nibble i and i + 4 form a pair. (w << 2) and (w >> 6)
-//     put two nibbles each at the mantissa's bits 2 and 6; with the exponents of 256
-//     and 16 that is 256 + u and 16 + u, and one paired fp16 multiply-add with s and
-//     -264 s or -24 s gives (u - 8) s exactly (s has 4 significant bits, 264 = 33 * 8):
-//     10 instructions for 8 numbers.
-//   - Output O^T = V^T P^T: a lane holds 4 keys of an eighth of the channels;
-//     byte permutes put two keys' nibbles of one channel into one register. The
-//     probabilities move from the scores' layout to the operand's by 8x8
-//     transposes between lanes.
+//   - Scores S^T = K Q^T: a warp takes 16 or 32 keys of a page; a lane holds a
+//     quarter of two keys' channels. The order of the channels in the product is
+//     free, so the eight codes of a 32-bit word go where they come out: nibble i
+//     and i + 4 form a pair. (w << 2) and (w >> 6) put two nibbles each at the
+//     mantissa's bits 2 and 6; with the exponents of 256 and 16 that is 256 + u and
+//     16 + u, and one paired fp16 multiply-add with s and -264 s or -24 s gives
+//     (u - 8) s exactly (s has 4 significant bits, 264 = 33 * 8): 10 instructions
+//     for 8 numbers.
+//   - Output O^T = V^T P^T: a warp takes a share of the channels for all 64 keys,
+//     so that a row's output is one warp's alone; the probabilities go through
+//     shared memory, moved from the scores' layout to the operand's by 8x8
+//     transposes between lanes. A lane holds 4 keys of 8 channels; byte permutes put
+//     two keys' nibbles of one channel into one register.
 //   - The running maximum is a reference that is only moved when a score exceeds
-//     it by 2^8 (fp16 holds the probabilities up to there): most tiles need one
-//     vote and no exchange between lanes.
+//     it by 2^8 (fp16 holds the probabilities up to there): the barrier that hands
+//     the probabilities over also says whether any did.
 //
-// A page's block of one head is contiguous: one bulk copy into a ring of stages.
-// The warps issue them in turn, two pages behind the slowest, from a list of the
-// share's blocks that all threads write 128 at a time (a fifth warp for the copies
-// would take a quarter of the registers of an SM's partition). Four warps take 16
-// keys of a page each, with statistics and accumulators of their own that meet at
-// the end of a segment. The (row, key head, query tile, page) sequence is dealt out
-// in equal shares to a CTA each, so a share may begin and end inside a row: a second
-// kernel joins those rows' parts.
+// A page's block of one head is contiguous: one bulk copy into a ring of stages. At
+// a page's barrier all warps have left the page before it, so its stage is filled
+// again right behind it. The (row, key head, query tile, page) sequence is dealt out
+// in equal shares to a CTA each, a unit's set-up counting as kSetup pages, so a share
+// may begin and end inside a unit: of the CTAs that hold parts of one, the last to
+// finish joins them.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -46,15 +46,14 @@ namespace attn_kv4 {
 
 using namespace kv4;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 640;
-constexpr float kNone = -3.0e38f;              // a reference below every score
-constexpr float kLag = 8.0f;                   // scores may exceed the reference by 2^8
-constexpr int kLeast = 2;                      // pages that are worth a CTA
-
-struct Header {  // of the row part that a CTA's share begins and does not end
-  int b, unit, last, pad;  // last: the CTA that ends it; -1: none
-};
+constexpr int kMaxCtas = 1536;
+constexpr float kNone = -3.0e38f;  // a reference below every score
+constexpr float kLag = 8.0f;       // scores may exceed the reference by 2^8
+constexpr int kSetup = 2;          // pages that a unit's queries and output are worth
+constexpr int kLeast = 2;          // pages that are worth a CTA
+constexpr int kMostParts = 64;     // of a unit, on the average
+constexpr int kFan = 16;           // parts that are joined at a time
+constexpr int kMargin = 16;        // positions that the copies may be ahead
 
 struct Args {
   int B, T, hq, hk, G, n_pages, max_pages, tiles;  // tiles: query tiles of a key head
@@ -64,25 +63,29 @@ struct Args {
   const uint8_t *pool;
   const int32_t *table, *kv_len, *q_len;
   bf16 *out;
-  Header *header;  // [gridDim.x]
-  float *stats;    // [2 gridDim.x][columns][2]: reference, sum; a NaN reference: the row is bad
-  float *part;     // [2 gridDim.x][columns / 8][D / 64][8][64]
+  int *count;    // [2][2 kMaxCtas]: parts of a group, groups of a unit that are done; zero between calls
+  float *stats;  // [2 gridDim.x][columns][2]: reference, sum; a NaN reference: the row is bad
+  float *part;   // [2 gridDim.x][columns][D]
   unsigned int *status;
 };
 
 template <int D, int NT>
 struct Shape {
-  static constexpr int N = 8 * NT;              // query columns
-  static constexpr bool kQRegs = NT * D <= 128; // the queries stay in registers
-  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 4 : 6;
+  static constexpr int W = D == 256 ? 4 : 2;     // warps
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kSubs = 4 / W;            // 16 keys each that a warp scores
+  static constexpr int N = 8 * NT;               // query columns
+  static constexpr bool kQRegs = NT == 1;        // the queries stay in registers
+  static constexpr int kStages = 3;
   static constexpr int kBlock = block_bytes(D);
-  static constexpr int kSteps = D / 16;         // products of 16 channels
-  static constexpr int kMeetD = D == 128 ? 128 : 64;  // channels of the warps' meeting at a time
-  static constexpr int kPad = kMeetD + 4;
-  static constexpr int kMeet = kWarps * 8 * kPad * 4;
+  static constexpr int kSteps = D / 16;          // products of 16 channels
+  static constexpr int kSlice = D / W;           // channels of a warp's output
+  static constexpr int kMt = kSlice / 16;        // tiles of 16 of them
+  static constexpr int kP = 2 * 4 * NT * 32 * 8;
   static constexpr int kQ = kQRegs ? 0 : kSteps * NT * 32 * 8;
-  static constexpr int kBytes = kStages * kBlock + kMeet + kQ;
-  static constexpr int kCtas = NT * D >= 512 ? 2 : NT > 1 || D > 128 ? 3 : 4;  // on an SM, as the accumulators' registers allow
+  static constexpr int kBytes = kStages * kBlock + kP + kQ;
+  // on an SM, as shared memory and registers allow
+  static constexpr int kCtas = D == 256 ? (NT == 1 ? 3 : NT == 2 ? 3 : 2) : D == 128 ? (NT == 1 ? 7 : NT == 2 ? 6 : 4) : (NT == 1 ? 10 : NT == 2 ? 8 : 5);
 };
 
 // A row's tokens of the cache, -1 where its numbers are bad.
@@ -91,37 +94,56 @@ __device__ __forceinline__ int row_len(const Args &A, int b, int &ql) {
   ql = A.q_len ? A.q_len[b] : A.T;
   return len < 0 || len > (long long)A.max_pages * kPage || ql < 0 || ql > A.T ? -1 : len;
 }
-__device__ __forceinline__ int row_pages(const Args &A, int b) {
+// Positions of each of a row's units: its pages and the set-up, none for a row without tokens.
+__device__ __forceinline__ int row_cost(const Args &A, int b) {
   int ql;
-  return (max(row_len(A, b, ql), 0) + kPage - 1) / kPage;
+  const int len = row_len(A, b, ql);
+  return len > 0 ? (len + kPage - 1) / kPage + kSetup : 0;
 }
 
-// This CTA's share: X in [x0, x1) of the sequence of all rows' units' pages.
-struct Share {
-  long long x, x1, row0;  // row0: where row b begins
-  int b, n;               // the row, its pages
-};
-// One row's part of the share: pages [p, p + count) of `unit`; moves on.
-struct Segment {
-  int b, unit, p, count, n;
-  long long end;  // where the unit ends
-};
-__device__ __forceinline__ bool next_segment(const Args &A, int units, Share &s, Segment &g) {
-  if (s.x >= s.x1) return false;
-  while (s.x >= s.row0 + (long long)s.n * units) {  // rows without pages are passed over
-    s.row0 += (long long)s.n * units;
-    s.n = row_pages(A, ++s.b);
+// A walk over positions [x, x1) of the sequence of all rows' units.
+struct Walk {
+  int x, x1, row0;  // row0: where row b begins
+  int b, cost;      // the row, the positions of each of its units
+  __device__ __forceinline__ void find_row(const Args &A, int units) {
+    while (x >= row0 + cost * units) {  // rows without tokens are passed over
+      row0 += cost * units;
+      cost = row_cost(A, ++b);
+    }
   }
-  const long long at = s.x - s.row0;
-  g.b = s.b;
-  g.n = s.n;
-  g.unit = (int)(at / s.n);
-  g.p = (int)(at - (long long)g.unit * s.n);
-  g.count = (int)min((long long)(s.n - g.p), s.x1 - s.x);
-  g.end = s.row0 + (long long)(g.unit + 1) * s.n;
-  s.x += g.count;
-  return true;
+};
+// One unit's part of a share: pages [p, p + count), the first at position x.
+struct Segment {
+  int b, unit, p, count, x;
+  int first, end;  // the unit's first page's position, and behind its last
+};
+__device__ __forceinline__ bool next_segment(const Args &A, int units, Walk &w, Segment &g) {
+  while (w.x < w.x1) {
+    w.find_row(A, units);
+    g.b = w.b;
+    g.unit = (w.x - w.row0) / w.cost;
+    g.first = w.row0 + g.unit * w.cost + kSetup;
+    g.end = g.first - kSetup + w.cost;
+    g.x = max(w.x, g.first);
+    const int to = min(g.end, w.x1);
+    w.x = to;
+    g.p = g.x - g.first;
+    g.count = to - g.x;
+    if (g.count > 0) return true;
+  }
+  return false;
 }
+
+// How `total` positions are dealt out to `used` CTAs.
+struct Deal {
+  int used, base, rem;
+  __device__ __forceinline__ Deal(int total, int n) : used(n), base(n > 0 ? total / n : 0), rem(n > 0 ? total - base * n : 0) {}
+  __device__ __forceinline__ int start(int cta) const { return cta * base + min(cta, rem); }
+  __device__ __forceinline__ int owner(int x) const {
+    const int y = x - rem * (base + 1);
+    return y < 0 ? x / (base + 1) : rem + y / base;
+  }
+};
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -173,34 +195,29 @@ __device__ __forceinline__ void unpack(uint32_t w, const Scale &s, uint32_t (&v)
   v[3] = bits(__hfma2(field(y, m6, e6), s.s, s.at6));
 }
 
-// Where key r of a warp's 16 (as rows of the first product) stands among its tokens, so that the shared-memory reads
-// of the second product's lanes, keys 2t, 2t + 1, 2t + 8 and 2t + 9, fall on different banks.
-template <int D>
-__device__ __forceinline__ constexpr int key_of(int r) {
-  return D == 256 ? r : 4 * ((r & 7) >> 1) + (r & 1) + (r >> 3) * 2;
-}
+// Where key r of 16 (as rows of the first product) stands among its tokens: a lane of the second product, with keys
+// 2t, 2t + 1, 2t + 8 and 2t + 9, then holds four tokens in a row, whose scales are one word.
+__device__ __forceinline__ constexpr int key_of(int r) { return 4 * ((r & 7) >> 1) + (r & 1) + (r >> 3) * 2; }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) attn_kernel(const __grid_constant__ Args A) {
   using S = Shape<D, NT>;
+  constexpr int W = S::W, kThreads = S::kThreads;
+  constexpr long long kNoPage = -1, kNothing = -2;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *ring = smem;
-  float *s_meet = reinterpret_cast<float *>(smem + S::kStages * S::kBlock);
-  uint2 *s_q = reinterpret_cast<uint2 *>(smem + S::kStages * S::kBlock + S::kMeet);
-  __shared__ __align__(8) uint64_t s_full[S::kStages], s_empty[S::kStages];
-  __shared__ int s_bad[S::kStages];   // the stage's page does not exist
-  __shared__ float s_ref[kWarps][S::N], s_sum[kWarps][S::N];
-  __shared__ long long s_scan[kWarps], s_row0;
-  __shared__ int s_b, s_n;
-  __shared__ long long s_list[2 * kThreads];  // where the share's blocks stand in the pool; -1: no such page
+  uint2 *s_p = reinterpret_cast<uint2 *>(smem + S::kStages * S::kBlock);  // [2][4][NT][32]
+  uint2 *s_q = s_p + S::kP / 8;                                          // [kSteps][NT][32]
+  __shared__ __align__(8) uint64_t s_full[S::kStages];
+  __shared__ long long s_list[2 * kThreads];  // the blocks of the share's positions
+  __shared__ int s_bad[S::kStages];           // the stage's page does not exist
+  __shared__ float s_top[W][S::N], s_sum[W][S::N];
+  __shared__ int s_scan[W], s_rows[W], s_at[3], s_last;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], kWarps);
-    }
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&s_full[i], 1);
     fence_mbar_init();
   }
   griddep_wait();
@@ -210,42 +227,94 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
   const int units = A.hk * A.tiles, N = gridDim.x, cta = blockIdx.x;
   const int per = (A.B + kThreads - 1) / kThreads;
   const int r0 = min(A.B, tid * per), r1 = min(A.B, r0 + per);
-  long long mine = 0;
-  for (int b = r0; b < r1; ++b) mine += row_pages(A, b);
-  long long upto = mine;
+  int mine = 0, rows = 0;
+  for (int b = r0; b < r1; ++b) {
+    const int c = row_cost(A, b);
+    mine += c;
+    rows += c > 0;
+  }
+  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += y;
   }
-  if (lane == 31) s_scan[warp] = upto;
-  if (tid == 0) s_b = -1;
+  rows = __reduce_add_sync(0xffffffffu, rows);
+  if (lane == 31) {
+    s_scan[warp] = upto;
+    s_rows[warp] = rows;
+  }
+  if (tid == 0) s_at[0] = -1;
   __syncthreads();
-  long long total = 0;
+  int total = 0;
+  rows = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) upto += s_scan[w];
     total += s_scan[w];
+    rows += s_rows[w];
   }
-  const long long all = total * units;
-  const int used = (int)min((long long)N, (all + kLeast - 1) / kLeast);  // CTAs that get a share
-  Share share;
-  share.x = cta < used ? all * cta / used : 0;
-  share.x1 = cta < used ? all * (cta + 1) / used : 0;
-  if (share.x < share.x1) {
-    long long row0 = upto - mine;
-    if (share.x >= row0 * units && share.x < upto * units) {
-      for (int b = r0; b < r1; ++b) {
-        const int n = row_pages(A, b);
-        if (share.x < (row0 + n) * units) {
-          s_b = b;
-          s_n = n;
-          s_row0 = row0 * units;
-          break;
-        }
-        row0 += n;
+  total *= units;
+  const Deal deal(total, min(min(N, total / kLeast), (int)min((long long)rows * units * kMostParts, (long long)N)));
+  Walk share;
+  share.x = cta < deal.used ? deal.start(cta) : 0;
+  share.x1 = cta < deal.used ? deal.start(cta + 1) : 0;
+  if (share.x < share.x1 && share.x >= (upto - mine) * units && share.x < upto * units) {
+    int row0 = (upto - mine) * units;
+    for (int b = r0; b < r1; ++b) {
+      const int c = per == 1 ? mine : row_cost(A, b);
+      if (share.x < row0 + c * units) {
+        s_at[0] = b;
+        s_at[1] = c;
+        s_at[2] = row0;
+        break;
+      }
+      row0 += c * units;
+    }
+  }
+  __syncthreads();
+  const int x0 = share.x, x1 = share.x1;
+  share.b = s_at[0];
+  share.cost = s_at[1];
+  share.row0 = s_at[2];
+
+  // ---- the blocks of the share, kThreads positions at a time
+  Walk walk = share;
+  auto list = [&](int i0) {
+    long long block = kNothing;
+    walk.x = x0 + i0 + tid;
+    if (walk.x < x1) {
+      walk.find_row(A, units);
+      const int unit = (walk.x - walk.row0) / walk.cost, p = walk.x - walk.row0 - unit * walk.cost - kSetup;
+      if (p >= 0) {
+        const int page = A.table[(long long)walk.b * A.max_pages + p];
+        block = page >= 0 && page < A.n_pages ? (long long)page * A.hk + unit / A.tiles : kNoPage;
       }
     }
+    s_list[(i0 + tid) % (2 * kThreads)] = block;
+  };
+  int ahead = 0;      // thread 0: the position whose block is copied next
+  bool dead = false;  // a wait has run out: no copy is started any more
+  auto copy = [&](int stage) {  // thread 0; the stage is free
+    long long block = kNothing;
+    if (dead) return;
+    while (block == kNothing && x0 + ahead < x1) block = s_list[ahead++ % (2 * kThreads)];
+    if (block == kNothing) return;
+    s_bad[stage] = block < 0;
+    if (block < 0) {
+      set_status(A.status, GDN_ERR_INDEX);
+      mbar_arrive(&s_full[stage]);
+    } else {
+      mbar_arrive_expect_tx(&s_full[stage], S::kBlock);
+      bulk_g2s(ring + stage * S::kBlock, A.pool + block * S::kBlock, S::kBlock, &s_full[stage]);
+    }
+  };
+  const bool any_share = s_at[0] >= 0;
+  if (any_share) {
+    list(0);
+    __syncthreads();
+    if (tid == 0)
+      for (int i = 0; i < S::kStages - 1; ++i) copy(i);
   }
   // ---- rows without keys: zeros, dealt out evenly
   for (int b = (int)((long long)A.B * cta / N); b < (int)((long long)A.B * (cta + 1) / N); ++b) {
@@ -256,148 +325,93 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
     uint4 *o = reinterpret_cast<uint4 *>(A.out + (long long)b * A.T * A.hq * D);
     for (int i = tid; i < A.T * A.hq * D / 8; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
   }
-  if (tid == 0) A.header[cta].last = -1;
-  __syncthreads();
-  share.b = s_b;
-  share.n = s_n;
-  share.row0 = s_row0;
-  if (s_b < 0) return;
-
-  // ---- the blocks of the share: entry e is page e of it
-  const long long x0 = share.x;
-  const uint32_t count = (uint32_t)(share.x1 - x0);  // pages of the share
-  Share walk = share;
-  auto list = [&](uint32_t e0) {  // entries [e0, e0 + kThreads)
-    walk.x = x0 + e0 + tid;
-    Segment at;
-    long long block = -1;
-    if (walk.x < walk.x1) {
-      next_segment(A, units, walk, at);
-      const int page = A.table[(long long)at.b * A.max_pages + at.p];
-      if (page >= 0 && page < A.n_pages) block = (long long)page * A.hk + at.unit / A.tiles;
-    }
-    s_list[(e0 + tid) % (2 * kThreads)] = block;
-  };
-  auto copy = [&](uint32_t e, int stage) {  // one thread; the stage is empty
-    const long long block = s_list[e % (2 * kThreads)];
-    s_bad[stage] = block < 0;
-    if (block < 0) {
-      set_status(A.status, GDN_ERR_INDEX);
-      mbar_arrive(&s_full[stage]);
-    } else {
-      mbar_arrive_expect_tx(&s_full[stage], S::kBlock);
-      bulk_g2s(ring + stage * S::kBlock, A.pool + block * S::kBlock, S::kBlock, &s_full[stage]);
-    }
-  };
-  list(0);
-  __syncthreads();
-  if (tid == 0)
-    for (uint32_t e = 0; e < S::kStages - 2 && e < count; ++e) copy(e, e);
+  if (!any_share) return;
 
   // ---- the products
   const int row = lane >> 2, t = lane & 3;  // the lane's place in the operands
-  const int k_a = key_of<D>(row), k_b = key_of<D>(row + 8);
+  const int k_a = key_of(row), k_b = key_of(row + 8);
   Segment g;
-  int stage = 0;
+  int stage = 0, buf = 0, listed = kThreads;  // listed: positions whose blocks are known
   uint32_t parity = 0;  // of the ring's round
-  uint32_t done = 0;    // pages of the share
-  bool dead = false;
   while (next_segment(A, units, share, g)) {
     int ql;
     const int len = row_len(A, g.b, ql);
     const int head = g.unit / A.tiles, col0 = (g.unit - head * A.tiles) * S::N, cols = A.T * A.G;
     // ---- the queries: column `row` of tile j, channels t D/4 .. of it
     uint2 qf[S::kQRegs ? S::kSteps * NT : 1];
-    float f[NT][2];      // scale of columns 2t, 2t + 1
-    int sees[NT][2], least = len;  // keys that they see; the fewest of the tile
+    float f[NT][2];    // scale of columns 2t, 2t + 1
+    int sees[NT][2];   // keys that they see
+    if (!S::kQRegs) __syncthreads();  // the last unit's queries are used no more
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float mul = A.scale;
-      {
-        const int c = col0 + 8 * j + row;
-        const bool real = c < cols;
-        const int tok = real ? c / A.G : 0;
-        const bf16 *q = A.q + ((long long)g.b * A.T + tok) * A.qs + (head * A.G + (real ? c - tok * A.G : 0)) * D + t * (D / 4);
-        uint32_t x[D / 8];
+      const int c = col0 + 8 * j + row;
+      const bool real = c < cols;
+      const int tok = real ? c / A.G : 0;
+      const bf16 *q = A.q + ((long long)g.b * A.T + tok) * A.qs + (head * A.G + (real ? c - tok * A.G : 0)) * D + t * (D / 4);
+      uint32_t x[D / 8];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 y = real ? *(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0, 0, 0, 0);
-          x[4 * i] = y.x;
-          x[4 * i + 1] = y.y;
-          x[4 * i + 2] = y.z;
-          x[4 * i + 3] = y.w;
-        }
-        uint32_t top2 = 0;
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 y = real ? *(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0, 0, 0, 0);
+        x[4 * i] = y.x;
+        x[4 * i + 1] = y.y;
+        x[4 * i + 2] = y.z;
+        x[4 * i + 3] = y.w;
+      }
+      uint32_t top2 = 0;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) top2 = __vmaxu2(top2, x[i] & 0x7fff7fffu);
-        uint32_t top = max(top2 & 0xffffu, top2 >> 16) >> 7;  // the largest channel's exponent field
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max(1, min(253, (int)top));  // 2^(e - 127) and its inverse are both normal
-        const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-        mul *= __uint_as_float((uint32_t)e << 23);
-        if (S::kQRegs || j % kWarps == warp) {
+      for (int i = 0; i < D / 8; ++i) top2 = __vmaxu2(top2, x[i] & 0x7fff7fffu);
+      uint32_t top = max(top2 & 0xffffu, top2 >> 16) >> 7;  // the largest channel's exponent field
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = max(1, min(253, (int)top));  // 2^(e - 127) and its inverse are both normal
+      const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+      mul *= __uint_as_float((uint32_t)e << 23);
+      if (S::kQRegs || j % W == warp) {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {  // 8 channels, two products
-            const uint32_t *y = x + 4 * i;
-            float ch[8];
+        for (int i = 0; i < D / 32; ++i) {  // 8 channels, two products
+          const uint32_t *y = x + 4 * i;
+          float ch[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              ch[2 * k] = __uint_as_float(y[k] << 16) * down;
-              ch[2 * k + 1] = __uint_as_float(y[k] & 0xffff0000u) * down;
-            }
-            uint2 b[2];
+          for (int k = 0; k < 4; ++k) {
+            ch[2 * k] = __uint_as_float(y[k] << 16) * down;
+            ch[2 * k + 1] = __uint_as_float(y[k] & 0xffff0000u) * down;
+          }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              b[k].x = bits(__floats2half2_rn(ch[2 * k], ch[2 * k + 4]));
-              b[k].y = bits(__floats2half2_rn(ch[2 * k + 1], ch[2 * k + 5]));
-              if constexpr (S::kQRegs)
-                qf[(2 * i + k) * NT + j] = b[k];
-              else
-                s_q[((2 * i + k) * NT + j) * 32 + lane] = b[k];
-            }
+          for (int k = 0; k < 2; ++k) {
+            uint2 b;
+            b.x = bits(__floats2half2_rn(ch[2 * k], ch[2 * k + 4]));
+            b.y = bits(__floats2half2_rn(ch[2 * k + 1], ch[2 * k + 5]));
+            if constexpr (S::kQRegs)
+              qf[(2 * i + k) * NT + j] = b;
+            else
+              s_q[((2 * i + k) * NT + j) * 32 + lane] = b;
           }
         }
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         f[j][k] = __shfl_sync(0xffffffffu, mul, 4 * (2 * t + k));
-        const int c = col0 + 8 * j + 2 * t + k, tok = c / A.G;
-        sees[j][k] = c < cols && tok < ql ? min(len, max(0, len - ql + tok + 1)) : 0;
+        const int c2 = col0 + 8 * j + 2 * t + k, tok2 = c2 / A.G;
+        sees[j][k] = c2 >= cols ? len : tok2 < ql ? max(0, len - ql + tok2 + 1) : 0;  // a column of nobody's sees all
       }
     }
-    // the tile's first token sees the fewest keys, unless columns or tokens are missing
-    const int tok0 = col0 / A.G, tok1 = (min(cols, col0 + S::N) - 1) / A.G;
-    least = col0 + S::N <= cols && tok1 < ql ? max(0, len - ql + tok0 + 1) : 0;
+    // the tile's first token sees the fewest keys, unless tokens are missing
+    const int least = (min(cols, col0 + S::N) - 1) / A.G < ql ? max(0, len - ql + col0 / A.G + 1) : 0;
     if (!S::kQRegs) __syncthreads();
 
-    float acc[D / 16][NT][4], ref[NT][2], sum[NT][2];
+    float acc[S::kMt][NT][4], ref[NT][2], sum[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       ref[j][0] = ref[j][1] = kNone;
       sum[j][0] = sum[j][1] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
+      for (int i = 0; i < S::kMt; ++i) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
     }
     bool bad = false;
 
-    for (int i = 0; i < g.count; ++i, ++done) {
-      const int key0 = (g.p + i) * kPage + warp * 16;  // the warp's first key
-      if (done % kThreads == kThreads - 16) {
-        list(done + 16);
-        __syncthreads();
-      }
-      if ((int)(done % kWarps) == warp && lane == 0 && done + S::kStages - 2 < count && !dead) {
-        // the stage that all warps left two pages ago (fresh ones in the first round)
-        const int to = stage >= 2 ? stage - 2 : stage + S::kStages - 2;
-        if (done + S::kStages - 2 >= S::kStages && !mbar_wait_bounded(&s_empty[to], stage >= 2 ? parity : parity ^ 1)) {
-          set_status(A.status, GDN_ERR_TIMEOUT);
-          dead = true;
-        } else {
-          copy(done + S::kStages - 2, to);
-        }
-      }
-      __syncwarp();
+    for (int i = 0; i < g.count; ++i) {
+      const int key0 = (g.p + i) * kPage;  // the page's first key
       if (!dead && !mbar_wait_bounded(&s_full[stage], parity)) {
         if (lane == 0) set_status(A.status, GDN_ERR_TIMEOUT);
         dead = true;
@@ -405,41 +419,52 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
       dead = __any_sync(0xffffffffu, dead);
       bad |= dead || s_bad[stage];
       const uint8_t *block = ring + stage * S::kBlock;
-      if (!bad && key0 < len) {
-        float s[NT][4];
+
+      // ---- scores
+      float s[S::kSubs][NT][4];
+      const int sub0 = warp * S::kSubs;  // the warp's first 16 keys
+      const bool work = !bad && key0 + 16 * sub0 < len;
+      if (work) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
-        const int ka = warp * 16 + k_a, kb = warp * 16 + k_b;
-        // ---- scores: a chunk of up to 32 channels (16 bytes) of each key at a time
+        for (int u = 0; u < S::kSubs; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) s[u][j][0] = s[u][j][1] = s[u][j][2] = s[u][j][3] = 0.0f;
+        // a chunk of up to 32 channels (16 bytes) of each key at a time
         constexpr int CH = D < 128 ? 16 : 32, CHUNKS = D / 4 / CH;
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-          uint32_t wa[CH / 8], wb[CH / 8];
+          uint32_t wa[S::kSubs][CH / 8], wb[S::kSubs][CH / 8];
+          __half2 sa[S::kSubs], sb[S::kSubs];
           const int byte = t * (D / 8) + c * 16;
-          __half2 sa, sb;
-          if constexpr (D == 64) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(block + swizzle(ka * 32 + byte));
-            const uint2 y = *reinterpret_cast<const uint2 *>(block + swizzle(kb * 32 + byte));
-            wa[0] = x.x, wa[1] = x.y, wb[0] = y.x, wb[1] = y.y;
-            sa = e4m3x2(block[scales_at(D, 0) + ka * 4 + t] * 0x101u);
-            sb = e4m3x2(block[scales_at(D, 0) + kb * 4 + t] * 0x101u);
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4 *>(block + swizzle(ka * (D / 2) + byte));
-            const uint4 y = *reinterpret_cast<const uint4 *>(block + swizzle(kb * (D / 2) + byte));
-            wa[0] = x.x, wa[1] = x.y, wa[2] = x.z, wa[3] = x.w;
-            wb[0] = y.x, wb[1] = y.y, wb[2] = y.z, wb[3] = y.w;
-            const int at = t * (D / 64) + c * 2;
-            sa = e4m3x2(*reinterpret_cast<const unsigned short *>(block + scales_at(D, 0) + ka * (D / 16) + at));
-            sb = e4m3x2(*reinterpret_cast<const unsigned short *>(block + scales_at(D, 0) + kb * (D / 16) + at));
+#pragma unroll
+          for (int u = 0; u < S::kSubs; ++u) {
+            const int ka = (sub0 + u) * 16 + k_a, kb = (sub0 + u) * 16 + k_b;
+            if constexpr (D == 64) {
+              const uint2 x = *reinterpret_cast<const uint2 *>(block + swizzle(ka * 32 + byte));
+              const uint2 y = *reinterpret_cast<const uint2 *>(block + swizzle(kb * 32 + byte));
+              wa[u][0] = x.x, wa[u][1] = x.y, wb[u][0] = y.x, wb[u][1] = y.y;
+              sa[u] = e4m3x2(block[scales_at(D, 0) + ka * 4 + t] * 0x101u);
+              sb[u] = e4m3x2(block[scales_at(D, 0) + kb * 4 + t] * 0x101u);
+            } else {
+              const uint4 x = *reinterpret_cast<const uint4 *>(block + swizzle(ka * (D / 2) + byte));
+              const uint4 y = *reinterpret_cast<const uint4 *>(block + swizzle(kb * (D / 2) + byte));
+              wa[u][0] = x.x, wa[u][1] = x.y, wa[u][2] = x.z, wa[u][3] = x.w;
+              wb[u][0] = y.x, wb[u][1] = y.y, wb[u][2] = y.z, wb[u][3] = y.w;
+              const uint8_t *at = block + scales_at(D, 0) + t * (D / 64) + c * 2;
+              sa[u] = e4m3x2(*reinterpret_cast<const unsigned short *>(at + ka * (D / 16)));
+              sb[u] = e4m3x2(*reinterpret_cast<const unsigned short *>(at + kb * (D / 16)));
+            }
           }
 #pragma unroll
           for (int gr = 0; gr < CH / 16; ++gr) {
-            const Scale za(gr ? __high2half2(sa) : __low2half2(sa)), zb(gr ? __high2half2(sb) : __low2half2(sb));
 #pragma unroll
             for (int w = 2 * gr; w < 2 * gr + 2; ++w) {
-              uint32_t va[4], vb[4];
-              unpack(wa[w], za, va);
-              unpack(wb[w], zb, vb);
+              uint32_t va[S::kSubs][4], vb[S::kSubs][4];
+#pragma unroll
+              for (int u = 0; u < S::kSubs; ++u) {
+                unpack(wa[u][w], Scale(gr ? __high2half2(sa[u]) : __low2half2(sa[u])), va[u]);
+                unpack(wb[u][w], Scale(gr ? __high2half2(sb[u]) : __low2half2(sb[u])), vb[u]);
+              }
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const int step = c * (CH / 4) + 2 * w + k;
@@ -450,299 +475,285 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) attn_kernel(con
                     b = qf[step * NT + j];
                   else
                     b = s_q[(step * NT + j) * 32 + lane];
-                  mma(s[j], va[2 * k], vb[2 * k], va[2 * k + 1], vb[2 * k + 1], b.x, b.y);
+#pragma unroll
+                  for (int u = 0; u < S::kSubs; ++u)
+                    mma(s[u][j], va[u][2 * k], vb[u][2 * k], va[u][2 * k + 1], vb[u][2 * k + 1], b.x, b.y);
                 }
               }
             }
           }
         }
-        // ---- probabilities
-        const bool edge = key0 + 16 > least;
-        const int ja = key0 + k_a, jb = key0 + k_b;
-        bool over = false;
-        float y[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            y[j][k] = fmaf(s[j][k], f[j][k & 1], -ref[j][k & 1]);
-            if (edge && (k < 2 ? ja : jb) >= sees[j][k & 1]) y[j][k] = -INFINITY;
-            over |= y[j][k] > kLag;
-          }
-        }
-        if (__any_sync(0xffffffffu, over)) {  // the references move to the columns' maxima so far
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            float fade[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float top = kNone;
-              if (!edge || ja < sees[j][k]) top = fmaxf(top, s[j][k] * f[j][k]);
-              if (!edge || jb < sees[j][k]) top = fmaxf(top, s[j][k + 2] * f[j][k]);
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              top = fmaxf(top, ref[j][k]);
-              fade[k] = ex2(ref[j][k] - top);
-              ref[j][k] = top;
-              sum[j][k] *= fade[k];
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              y[j][k] = fmaf(s[j][k], f[j][k & 1], -ref[j][k & 1]);
-              if (edge && (k < 2 ? ja : jb) >= sees[j][k & 1]) y[j][k] = -INFINITY;
-            }
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) acc[m][j][k] *= fade[k & 1];
-          }
-        }
-        uint32_t p[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[j][k] = ex2(y[j][k]);
-          sum[j][0] += y[j][0] + y[j][2];
-          sum[j][1] += y[j][1] + y[j][3];
-          p[j][0] = transpose(bits(__floats2half2_rn(y[j][0], y[j][1])));
-          p[j][1] = transpose(bits(__floats2half2_rn(y[j][2], y[j][3])));
-        }
-        // ---- output: a word of 8 channels of 4 keys at a time
-        const uint8_t *codes = block + codes_at(D, 1), *scales = block + scales_at(D, 1);
-        int kv[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) kv[k] = warp * 16 + key_of<D>(2 * t + (k & 1) + (k >> 1) * 8);
-        uint32_t wv[4][D / 64];
+      }
+      // ---- probabilities, to the warps that need them
+      uint2 *to = s_p + buf * (4 * NT * 32);
+      const bool edge = key0 + 64 > least;
+      auto exponents = [&](int u, int j, float (&y)[4]) {
+        const int ja = key0 + (sub0 + u) * 16 + k_a, jb = key0 + (sub0 + u) * 16 + k_b;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint8_t *at = codes + swizzle(kv[k] * (D / 2) + row * (D / 16));
-          if constexpr (D == 64) {
-            wv[k][0] = *reinterpret_cast<const uint32_t *>(at);
-          } else if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(at);
-            wv[k][0] = x.x, wv[k][1] = x.y;
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4 *>(at);
-            wv[k][0] = x.x, wv[k][1] = x.y, wv[k][2] = x.z, wv[k][3] = x.w;
-          }
+          y[k] = fmaf(s[u][j][k], f[j][k & 1], -ref[j][k & 1]);
+          if (edge && (k < 2 ? ja : jb) >= sees[j][k & 1]) y[k] = -INFINITY;
         }
-        constexpr int GR = D == 256 ? 2 : 1;  // scales of the lane's channels
+      };
+      float add[NT][2];  // the lane's share of the sums
+      auto hand_over = [&] {
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-          uint32_t e;  // 4 keys' scales
-          if constexpr (D == 256) {
-            const uint8_t *at = scales + (2 * row + gr) * kPage + warp * 16 + 2 * t;
-            e = *reinterpret_cast<const unsigned short *>(at) | (uint32_t)*reinterpret_cast<const unsigned short *>(at + 8) << 16;
-          } else {
-            e = *reinterpret_cast<const uint32_t *>(scales + (D == 64 ? row >> 1 : row) * kPage + warp * 16 + 4 * t);
+        for (int j = 0; j < NT; ++j) add[j][0] = add[j][1] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < S::kSubs; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float y[4];
+            exponents(u, j, y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = ex2(y[k]);
+            add[j][0] += y[0] + y[2];
+            add[j][1] += y[1] + y[3];
+            uint2 p;
+            p.x = transpose(bits(__floats2half2_rn(y[0], y[1])));
+            p.y = transpose(bits(__floats2half2_rn(y[2], y[3])));
+            to[((sub0 + u) * NT + j) * 32 + lane] = p;
           }
-          if (key0 + 16 > len) {  // what the page holds behind the row's tokens may be anything
+      };
+      bool over = false;
+      if (work) {
+#pragma unroll
+        for (int u = 0; u < S::kSubs; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float y[4];
+            exponents(u, j, y);
+            over |= fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > kLag;
+          }
+        over = __any_sync(0xffffffffu, over);
+        if (!over) hand_over();
+      }
+      const bool moved = __syncthreads_or(over);
+      if (tid == 0) copy(stage == 0 ? S::kStages - 1 : stage - 1);  // all warps have left the page before
+      if (moved) {  // the references move to the columns' maxima so far
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = ref[j][k];
+            if (work) {
+#pragma unroll
+              for (int u = 0; u < S::kSubs; ++u) {
+                const int ja = key0 + (sub0 + u) * 16 + k_a, jb = key0 + (sub0 + u) * 16 + k_b;
+                if (!edge || ja < sees[j][k]) top = fmaxf(top, s[u][j][k] * f[j][k]);
+                if (!edge || jb < sees[j][k]) top = fmaxf(top, s[u][j][k + 2] * f[j][k]);
+              }
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+            if (row == 0) s_top[warp][8 * j + 2 * t + k] = top;
+          }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float fade[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = s_top[0][8 * j + 2 * t + k];
+#pragma unroll
+            for (int w = 1; w < W; ++w) top = fmaxf(top, s_top[w][8 * j + 2 * t + k]);
+            fade[k] = ex2(ref[j][k] - top);
+            ref[j][k] = top;
+          }
+#pragma unroll
+          for (int m = 0; m < S::kMt; ++m)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[m][j][k] *= fade[k & 1];
+          sum[j][0] *= fade[0];
+          sum[j][1] *= fade[1];
+        }
+        if (work) hand_over();
+        __syncthreads();
+      }
+      if (work) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          sum[j][0] += add[j][0];
+          sum[j][1] += add[j][1];
+        }
+      }
+      // ---- output: the warp's channels of 16 keys at a time
+      if (!bad) {
+        const uint8_t *codes = block + codes_at(D, 1);
+        constexpr int LB = D / (16 * W);  // a lane's bytes of a key's row: 8 channels, or 4
+        const uint8_t *scales = block + scales_at(D, 1) + (warp * S::kSlice + row * (S::kSlice / 8)) / kGroup * kPage;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          if (key0 + 16 * ks >= len) break;
+          uint2 p[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) p[j] = to[(ks * NT + j) * 32 + lane];
+          uint32_t wv[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint8_t *at = codes + swizzle((16 * ks + 4 * t + k) * (D / 2) + warp * (D / 2 / W) + row * LB);
+            if constexpr (LB == 4)
+              wv[k] = *reinterpret_cast<const uint32_t *>(at);
+            else
+              wv[k] = *reinterpret_cast<const unsigned short *>(at);
+          }
+          uint32_t e = *reinterpret_cast<const uint32_t *>(scales + 16 * ks + 4 * t);  // 4 keys' scales
+          if (key0 + 16 * ks + 16 > len) {  // what the page holds behind the row's tokens may be anything
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (key0 - warp * 16 + kv[k] >= len) e &= ~(0xffu << (8 * k));
+              if (key0 + 16 * ks + 4 * t + k >= len) e &= ~(0xffu << (8 * k));
           }
           const Scale z0(e4m3x2(e)), z1(e4m3x2(e >> 16));
 #pragma unroll
-          for (int w = gr * (D / 64 / GR); w < (gr + 1) * (D / 64 / GR); ++w) {
+          for (int h = 0; h < LB / 2; ++h) {
+            uint32_t v0[4], v1[4];
+            unpack(__byte_perm(wv[0], wv[1], h ? 0x7632 : 0x5410), z0, v0);
+            unpack(__byte_perm(wv[2], wv[3], h ? 0x7632 : 0x5410), z1, v1);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v0[4], v1[4];
-              unpack(__byte_perm(wv[0][w], wv[1][w], h ? 0x7632 : 0x5410), z0, v0);
-              unpack(__byte_perm(wv[2][w], wv[3][w], h ? 0x7632 : 0x5410), z1, v1);
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                  mma(acc[4 * w + 2 * h + k][j], v0[2 * k], v0[2 * k + 1], v1[2 * k], v1[2 * k + 1], p[j][0], p[j][1]);
-            }
+              for (int j = 0; j < NT; ++j)
+                mma(acc[2 * h + k][j], v0[2 * k], v0[2 * k + 1], v1[2 * k], v1[2 * k + 1], p[j].x, p[j].y);
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[stage]);
+      buf ^= 1;
       if (++stage == S::kStages) {
         stage = 0;
         parity ^= 1;
       }
+      if (g.x + i - x0 >= listed - kMargin && x0 + listed < x1) {  // the same for all threads
+        list(listed);
+        listed += kThreads;
+        __syncthreads();
+      }
     }
 
-    // ---- the four warps meet: 8 columns, kMeetD channels at a time
-    const bool whole = g.p == 0 && g.p + g.count == g.n;
-    const int slot = 2 * cta + (g.p == 0);
+    // ---- the sums over all warps' keys
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) sum[j][k] += __shfl_xor_sync(0xffffffffu, sum[j][k], o);
-        if (row == 0) {
-          s_ref[warp][8 * j + 2 * t + k] = bad ? __int_as_float(0x7fffffff) : ref[j][k];
-          s_sum[warp][8 * j + 2 * t + k] = sum[j][k];
-        }
+        if (row == 0) s_sum[warp][8 * j + 2 * t + k] = sum[j][k];
       }
-    }
-    __syncthreads();
+    bad = __syncthreads_or(bad);
+    const int ch = warp * S::kSlice + row * (S::kSlice / 8);  // the lane's first channel
+    const bool whole = g.p == 0 && g.x + g.count == g.end;
+    if (whole && bad) continue;
+    const int slot = 2 * cta + (g.p == 0);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float own[2];  // 2^(reference - the warps' largest)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float top = kNone;
+        const int c = 8 * j + 2 * t + k, col = col0 + c;
+        float all = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ref[w][8 * j + 2 * t + k]);
-        own[k] = ex2(ref[j][k] - top);
-      }
-      const int c = tid >> 4, part = tid & 15;  // the column and channels that this thread finishes
-      float top = kNone, total_sum = 0.0f;
-      bool lost = false;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        lost |= s_ref[w][8 * j + c] != s_ref[w][8 * j + c];
-        top = fmaxf(top, s_ref[w][8 * j + c]);
-      }
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) total_sum += s_sum[w][8 * j + c] * ex2(s_ref[w][8 * j + c] - top);
-#pragma unroll
-      for (int h = 0; h < D / S::kMeetD; ++h) {
-        constexpr int ROWS = 8 * S::kMeetD / D;  // a lane holds the D/8 channels from row D/8 on
-        if (row / ROWS == h) {
-          const int d0 = row % ROWS * (D / 8);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int m = 0; m < D / 16; m += 2)
-              *reinterpret_cast<float4 *>(s_meet + (warp * 8 + 2 * t + k) * S::kPad + d0 + 2 * m) =
-                  make_float4(acc[m][j][k] * own[k], acc[m][j][k + 2] * own[k], acc[m + 1][j][k] * own[k],
-                              acc[m + 1][j][k + 2] * own[k]);
-        }
-        __syncthreads();
-        constexpr int PER = S::kMeetD / 16;  // channels a thread finishes
-        float o[PER];
-#pragma unroll
-        for (int k = 0; k < PER; k += 4) {
-          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float4 z = *reinterpret_cast<const float4 *>(s_meet + (w * 8 + c) * S::kPad + part * PER + k);
-            x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
-          }
-          o[k] = x.x, o[k + 1] = x.y, o[k + 2] = x.z, o[k + 3] = x.w;
-        }
-        const int ch = h * S::kMeetD + part * PER;  // the first of them
+        for (int w = 0; w < W; ++w) all += s_sum[w][c];
         if (whole) {
-          const int col = col0 + 8 * j + c;
-          if (col < cols && !lost) {
+          if (col < cols) {
             const int tok = col / A.G;
-            const float inv = total_sum == 0.0f ? 0.0f : A.out_mul / total_sum;
+            const float inv = all == 0.0f ? 0.0f : A.out_mul / all;
             bf16 *out = A.out + (((long long)g.b * A.T + tok) * A.hq + head * A.G + col - tok * A.G) * D + ch;
-            uint32_t z[PER / 2];
+            uint32_t z[S::kMt];
 #pragma unroll
-            for (int k = 0; k < PER / 2; ++k) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
-              z[k] = *reinterpret_cast<const uint32_t *>(&x);
+            for (int m = 0; m < S::kMt; ++m) {
+              const __nv_bfloat162 x = __floats2bfloat162_rn(acc[m][j][k] * inv, acc[m][j][k + 2] * inv);
+              z[m] = *reinterpret_cast<const uint32_t *>(&x);
             }
-            if constexpr (PER == 8)
+            if constexpr (S::kMt == 4)
               *reinterpret_cast<uint4 *>(out) = make_uint4(z[0], z[1], z[2], z[3]);
             else
               *reinterpret_cast<uint2 *>(out) = make_uint2(z[0], z[1]);
           }
         } else {
-          float *to = A.part + ((((long long)slot * NT + j) * (D / 64) + ch / 64) * 8 + c) * 64 + ch % 64;
+          float *part = A.part + ((long long)slot * S::N + c) * D + ch;
 #pragma unroll
-          for (int k = 0; k < PER; k += 4) *reinterpret_cast<float4 *>(to + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-          if (part == 0 && h == 0)
-            *reinterpret_cast<float2 *>(A.stats + ((long long)slot * S::N + 8 * j + c) * 2) =
-                make_float2(lost ? __int_as_float(0x7fffffff) : top, total_sum);
+          for (int m = 0; m < S::kMt; m += 2)
+            *reinterpret_cast<float4 *>(part + 2 * m) =
+                make_float4(acc[m][j][k], acc[m][j][k + 2], acc[m + 1][j][k], acc[m + 1][j][k + 2]);
+          if (row == 0 && warp == 0)
+            *reinterpret_cast<float2 *>(A.stats + ((long long)slot * S::N + c) * 2) =
+                make_float2(bad ? __int_as_float(0x7fffffff) : ref[j][k], all);
         }
-        __syncthreads();  // the meeting place and the queries are free again
       }
-    }
-    if (!whole && g.p == 0 && tid == 0) {
-      const int last = (int)((g.end * used + all - 1) / all) - 1;  // the last CTA whose share begins before the unit's end
-      A.header[cta] = {g.b, g.unit, last, 0};
-    }
-  }
-}
+    if (whole) continue;
 
-// The parts of a row that several shares held: CTA (i, slab) joins the one that
-// share i began; 8 columns by 64 channels, a part to a warp.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args A) {
-  constexpr int SLABS = NT * (D / 64);
-  __shared__ float s_top[8], s_wt[8][8];
-  __shared__ float4 s_o[8][128];
-  griddep_wait();
-  griddep_trigger();
-  const int i = blockIdx.x, slab = blockIdx.y, j = slab / (D / 64);
-  const Header H = A.header[i];
-  if (H.last < 0) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n = H.last - i + 1;
-  auto slot_of = [&](int k) { return k == 0 ? 2 * i + 1 : 2 * (i + k); };
-  // ---- the columns' largest reference: 8 lanes a part, warps over the parts
-  float top = kNone;
-  bool lost = false;
-  for (int k = tid >> 3; k < n; k += 32) {
-    const float r = A.stats[((long long)slot_of(k) * (8 * NT) + 8 * j + (tid & 7)) * 2];
-    lost |= r != r;
-    top = fmaxf(top, r);
-  }
+    // ---- the unit's parts: the last CTA of up to kFan joins theirs, the last of those the unit's
+    const int i0 = deal.owner(g.first), n = deal.owner(g.end - 1) - i0 + 1;  // the CTAs that hold one
+    auto slot_of = [&](int k) { return k == 0 ? 2 * i0 + 1 : 2 * (i0 + k); };
+    auto arrive = [&](int *count, int most) {  // true for the last
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const bool last = atomicAdd(count, 1) == most - 1;
+        if (last) *count = 0;
+        s_last = last;
+      }
+      __syncthreads();
+      const bool last = s_last;
+      if (last) __threadfence();
+      return last;
+    };
+    auto join = [&](int k0, int k1, int step, bool final) {  // parts k0, k0 + step .. below k1
+      bool lost = false;
+      constexpr int M = D / (16 * W);  // 16-byte pieces of 8 columns that a thread joins
+#pragma unroll 1
+      for (int j = 0; j < NT; ++j) {
+        float4 o[M];
+        float l[M], top[M];
 #pragma unroll
-  for (int o = 8; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane < 8) s_wt[warp][lane] = top;
-  if (__syncthreads_or(lost)) return;
-  if (tid < 8) {
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, s_wt[w][tid]);
-    s_top[tid] = top;
-  }
-  __syncthreads();
-  // ---- lane: columns lane / 16 + 2 m, channels 4 (lane % 16)
-  float4 o[4];
-  float l[4];
+        for (int m = 0; m < M; ++m) {
+          o[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          l[m] = 0.0f;
+          top[m] = kNone;
+        }
+#pragma unroll 4
+        for (int k = k0; k < k1; k += step)
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    o[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    l[m] = 0.0f;
-  }
-#pragma unroll 2
-  for (int k = warp; k < n; k += 8) {
-    const long long slot = slot_of(k);
-    const float4 *from = reinterpret_cast<const float4 *>(A.part + (slot * SLABS + slab) * 512);
+          for (int m = 0; m < M; ++m) {
+            const float r = __ldcg(A.stats + ((long long)slot_of(k) * S::N + 8 * j + (m * kThreads + tid) / (D / 4)) * 2);
+            lost |= r != r;
+            top[m] = fmaxf(top[m], r);
+          }
+#pragma unroll 4
+        for (int k = k0; k < k1; k += step) {
+          const long long slot_k = (long long)slot_of(k) * S::N + 8 * j;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int c = lane / 16 + 2 * m;
-      const float2 st = *reinterpret_cast<const float2 *>(A.stats + (slot * (8 * NT) + 8 * j + c) * 2);
-      const float4 x = from[32 * m + lane];
-      const float w = ex2(st.x - s_top[c]);
-      l[m] += st.y * w;
-      o[m].x += x.x * w, o[m].y += x.y * w, o[m].z += x.z * w, o[m].w += x.w * w;
-    }
-  }
-  __syncthreads();
+          for (int m = 0; m < M; ++m) {
+            const float2 st = __ldcg(reinterpret_cast<const float2 *>(A.stats) + slot_k + (m * kThreads + tid) / (D / 4));
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(A.part + slot_k * D) + m * kThreads + tid);
+            const float w = ex2(st.x - top[m]);
+            l[m] += st.y * w;
+            o[m].x += x.x * w, o[m].y += x.y * w, o[m].z += x.z * w, o[m].w += x.w * w;
+          }
+        }
+        __syncthreads();  // all have read the part that is written over
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    s_o[warp][32 * m + lane] = o[m];
-    if (lane % 16 == 0) s_wt[warp][lane / 16 + 2 * m] = l[m];
-  }
-  __syncthreads();
-  if (tid < 128) {
-    float4 x = s_o[0][tid];
-    const int c = tid / 16;
-    float total = s_wt[0][c];
-    for (int w = 1; w < 8; ++w) {
-      const float4 z = s_o[w][tid];
-      x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
-      total += s_wt[w][c];
-    }
-    const int head = H.unit / A.tiles, col = (H.unit - head * A.tiles) * (8 * NT) + 8 * j + c;
-    if (col < A.T * A.G) {
-      const int tok = col / A.G;
-      const float inv = total == 0.0f ? 0.0f : A.out_mul / total;
-      bf16 *out = A.out + (((long long)H.b * A.T + tok) * A.hq + head * A.G + col - tok * A.G) * D +
-                  slab % (D / 64) * 64 + tid % 16 * 4;
-      const __nv_bfloat162 a = __floats2bfloat162_rn(x.x * inv, x.y * inv), b = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-      *reinterpret_cast<uint2 *>(out) =
-          make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        for (int m = 0; m < M; ++m) {
+          const int c = 8 * j + (m * kThreads + tid) / (D / 4), at = (m * kThreads + tid) % (D / 4) * 4, col = col0 + c;
+          if (!final) {
+            const long long to = (long long)slot_of(k0) * S::N + c;
+            *reinterpret_cast<float4 *>(A.part + to * D + at) = o[m];
+            if (at == 0)
+              *reinterpret_cast<float2 *>(A.stats + to * 2) = make_float2(lost ? __int_as_float(0x7fffffff) : top[m], l[m]);
+          } else if (col < cols && !lost) {
+            const int tok = col / A.G;
+            const float inv = l[m] == 0.0f ? 0.0f : A.out_mul / l[m];
+            bf16 *out = A.out + (((long long)g.b * A.T + tok) * A.hq + head * A.G + col - tok * A.G) * D + at;
+            const __nv_bfloat162 a = __floats2bfloat162_rn(o[m].x * inv, o[m].y * inv);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[m].z * inv, o[m].w * inv);
+            *reinterpret_cast<uint2 *>(out) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+          }
+        }
+      }
+    };
+    const int k = cta - i0, k0 = k / kFan * kFan, k1 = min(n, k0 + kFan), groups = (n + kFan - 1) / kFan;
+    if (arrive(A.count + slot_of(k0), k1 - k0)) {
+      join(k0, k1, 1, groups == 1);
+      if (groups > 1 && arrive(A.count + 2 * kMaxCtas + slot_of(0), groups)) join(0, n, kFan, true);
     }
   }
 }
@@ -762,33 +773,34 @@ gdn_status check_dims(const gdn_attn_kv4_dims *d) {
     return fail(GDN_ERR_SHAPE, "k_exp and v_exp must be in [-32, 32]");
   if (d->q_stride % 8 != 0 || d->q_stride < (long long)d->n_q_heads * D || d->q_stride >= (1LL << 32))
     return fail(GDN_ERR_SHAPE, "q_stride must be a multiple of 8 elements that covers the heads, below 2^32");
-  if ((double)d->B * d->T * d->n_q_heads * d->max_pages > 1099511627776.0)
-    return fail(GDN_ERR_SHAPE, "B * T * n_q_heads * max_pages must be at most 2^40");
+  const double tiles = (d->T * (d->n_q_heads / d->n_kv_heads) + 7) / 8;
+  if (d->B * tiles * d->n_kv_heads * (d->max_pages + 2.0) > 1073741824.0)
+    return fail(GDN_ERR_SHAPE, "B * n_kv_heads * ceil(T * n_q_heads / n_kv_heads / 8) * (max_pages + 2) must be at most 2^30");
   if (!(fabs(ldexp((double)d->scale, d->k_exp) * 1.4426950408889634) <= 3.4e38))
     return fail(GDN_ERR_ARG, "|scale| 2^k_exp log2(e) must be finite");
   return GDN_OK;
 }
 
-// Query tiles of 8 columns that a CTA takes at once: what the columns fill, and the registers hold.
+// Query tiles of 8 columns that a CTA takes at once, as the columns fill them.
 int tiles_at_once(const gdn_attn_kv4_dims *d) {
   const int cols = d->T * (d->n_q_heads / d->n_kv_heads);
-  return cols <= 8 ? 1 : cols <= 16 || d->head_dim == 256 ? 2 : 4;
+  return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
 }
-size_t part_bytes(int D, int NT) { return (size_t)2 * kMaxCtas * 8 * NT * D * 4; }
+constexpr size_t kCountBytes = 4 * kMaxCtas * sizeof(int);
+static_assert(kCountBytes == GDN_ATTN_KV4_ZEROS, "the counters");
 size_t stats_bytes(int NT) { return (size_t)2 * kMaxCtas * 8 * NT * 8; }
+size_t part_bytes(int D, int NT) { return (size_t)2 * kMaxCtas * 8 * NT * D * 4; }
 
 template <int D, int NT>
-gdn_status launch(Args A, int sms, cudaStream_t stream) {
+gdn_status launch(const Args &A, int sms, cudaStream_t stream) {
   using S = Shape<D, NT>;
   if (cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
     return check_launch("attn_kv4");
-  // no more CTAs than the rows could fill with pages
-  const long long most = (long long)A.B * A.hk * A.tiles * A.max_pages;
+  // no more CTAs than the rows could fill
+  const long long most = (long long)A.B * A.hk * A.tiles * (A.max_pages + kSetup) / kLeast;
   int ctas = sms * S::kCtas < kMaxCtas ? sms * S::kCtas : kMaxCtas;
-  if (most < (long long)ctas * kLeast) ctas = most < 2 * kLeast ? 2 : (int)((most + kLeast - 1) / kLeast);
-  if (launch_pdl(attn_kernel<D, NT>, dim3(ctas), dim3(kThreads), S::kBytes, stream, A) != cudaSuccess)
-    return check_launch("attn_kv4");
-  launch_pdl(join_kernel<D, NT>, dim3(ctas, NT * (D / 64)), dim3(256), 0, stream, A);
+  if (most < ctas) ctas = (int)most;
+  launch_pdl(attn_kernel<D, NT>, dim3(ctas), dim3(S::kThreads), S::kBytes, stream, A);
   return check_launch("attn_kv4");
 }
 
@@ -800,8 +812,7 @@ using namespace gdn;
 extern "C" size_t gdn_attn_kv4_workspace_size(const gdn_attn_kv4_dims *dims) {
   if (attn_kv4::check_dims(dims) != GDN_OK) return 0;
   const int NT = attn_kv4::tiles_at_once(dims);
-  return attn_kv4::kMaxCtas * sizeof(attn_kv4::Header) + attn_kv4::stats_bytes(NT) +
-         attn_kv4::part_bytes(dims->head_dim, NT);
+  return attn_kv4::kCountBytes + attn_kv4::stats_bytes(NT) + attn_kv4::part_bytes(dims->head_dim, NT);
 }
 
 extern "C" gdn_status gdn_attn_kv4(const gdn_attn_kv4_dims *dims, const void *q, const void *pool,
@@ -839,16 +850,13 @@ extern "C" gdn_status gdn_attn_kv4(const gdn_attn_kv4_dims *dims, const void *q,
   A.kv_len = kv_len;
   A.q_len = q_len;
   A.out = static_cast<bf16 *>(out);
-  A.header = static_cast<attn_kv4::Header *>(workspace);
-  A.stats = reinterpret_cast<float *>(A.header + attn_kv4::kMaxCtas);
+  A.count = static_cast<int *>(workspace);
+  A.stats = reinterpret_cast<float *>(static_cast<char *>(workspace) + attn_kv4::kCountBytes);
   A.part = A.stats + attn_kv4::stats_bytes(NT) / 4;
   A.status = dev->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (D == 64)
-    return NT == 1 ? attn_kv4::launch<64, 1>(A, dev->sms, st)
-                   : NT == 2 ? attn_kv4::launch<64, 2>(A, dev->sms, st) : attn_kv4::launch<64, 4>(A, dev->sms, st);
-  if (D == 128)
-    return NT == 1 ? attn_kv4::launch<128, 1>(A, dev->sms, st)
-                   : NT == 2 ? attn_kv4::launch<128, 2>(A, dev->sms, st) : attn_kv4::launch<128, 4>(A, dev->sms, st);
-  return NT == 1 ? attn_kv4::launch<256, 1>(A, dev->sms, st) : attn_kv4::launch<256, 2>(A, dev->sms, st);
+  auto pick = [&](auto one, auto two, auto four) { return (NT == 1 ? one : NT == 2 ? two : four)(A, dev->sms, st); };
+  if (D == 64) return pick(attn_kv4::launch<64, 1>, attn_kv4::launch<64, 2>, attn_kv4::launch<64, 4>);
+  if (D == 128) return pick(attn_kv4::launch<128, 1>, attn_kv4::launch<128, 2>, attn_kv4::launch<128, 4>);
+  return pick(attn_kv4::launch<256, 1>, attn_kv4::launch<256, 2>, attn_kv4::launch<256, 4>);
 }

@@ -588,8 +588,8 @@ gdn_status gdn_kv4_load(const gdn_kv4_dims *dims, const void *pool, const int32_
  *   n_q_heads, n_kv_heads, head_dim   n_q_heads a multiple of n_kv_heads, at most
  *                    64 query heads per key head; head_dim one of 64, 128, 256
  *   n_pages          pages of the pool, at most 2^25 - 1
- *   max_pages        entries of a page table's line; B T n_q_heads max_pages at
- *                    most 2^40
+ *   max_pages        entries of a page table's line; B n_kv_heads
+ *                    ceil(T n_q_heads / n_kv_heads / 8) (max_pages + 2) at most 2^30
  *   k_exp, v_exp     the pool's exponents, in [-32, 32]
  *   scale            multiplies q.k before the softmax; finite, and so is
  *                    |scale| 2^k_exp log2(e)
@@ -608,9 +608,11 @@ typedef struct gdn_attn_kv4_dims {
  *               in the pool already); 0: the row's outputs are zeros
  *   q_len       int32 [B] in [0, T], the row's real tokens, or NULL (T each)
  *   out         bf16 [B][T][n_q_heads][head_dim]
- *   workspace   gdn_attn_kv4_workspace_size(dims) bytes, 256-byte aligned; its
- *               contents need not be preserved, and calls that may overlap (on
- *               several streams) need one each
+ *   workspace   gdn_attn_kv4_workspace_size(dims) bytes, 256-byte aligned. Its
+ *               first GDN_ATTN_KV4_ZEROS bytes are zero before a call and again
+ *               after it (zero them once; anew after GDN_ERR_TIMEOUT); the rest
+ *               need not be preserved. Calls that may overlap (on several
+ *               streams) need one each.
  * Token t sees keys j <= kv_len - q_len + t; a token that sees nothing, or with
  * t >= q_len, gets zeros. Keys and values enter the products exactly, queries
  * in fp16 relative to their head's largest channel (error below 2^-25 of it),
@@ -619,11 +621,12 @@ typedef struct gdn_attn_kv4_dims {
  * device error (GDN_ERR_INDEX): outputs of that row are not written. What the
  * last page holds behind the row's tokens is never used, whatever it is; values
  * that are not finite within a row may also reach its earlier tokens of the call. */
+#define GDN_ATTN_KV4_ZEROS 24576
 gdn_status gdn_attn_kv4(const gdn_attn_kv4_dims *dims, const void *q, const void *pool, const int32_t *page_table,
                         const int32_t *kv_len, const int32_t *q_len, void *out, void *workspace,
                         size_t workspace_bytes, void *stream);
 
-/* Workspace bytes of gdn_attn_kv4 on the current device (0 on invalid dims). */
+/* Workspace bytes of gdn_attn_kv4 (0 on invalid dims). */
 size_t gdn_attn_kv4_workspace_size(const gdn_attn_kv4_dims *dims);
 
 /* Sizes of a gdn_beam_select call.
