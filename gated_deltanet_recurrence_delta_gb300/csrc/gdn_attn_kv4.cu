@@ -76,7 +76,7 @@ struct Shape {
   static constexpr int kSubs = 4 / W;            // 16 keys each that a warp scores
   static constexpr int N = 8 * NT;               // query columns
   static constexpr bool kQRegs = NT == 1;        // the queries stay in registers
-  static constexpr int kStages = 3;
+  static constexpr int kStages = D == 128 && NT == 1 ? 2 : 3;
   static constexpr int kBlock = block_bytes(D);
   static constexpr int kSteps = D / 16;          // products of 16 channels
   static constexpr int kSlice = D / W;           // channels of a warp's output
@@ -85,7 +85,7 @@ struct Shape {
   static constexpr int kQ = kQRegs ? 0 : kSteps * NT * 32 * 8;
   static constexpr int kBytes = kStages * kBlock + kP + kQ;
   // on an SM, as shared memory and registers allow
-  static constexpr int kCtas = D == 256 ? (NT == 1 ? 3 : NT == 2 ? 3 : 2) : D == 128 ? (NT == 1 ? 7 : NT == 2 ? 6 : 4) : (NT == 1 ? 10 : NT == 2 ? 8 : 5);
+  static constexpr int kCtas = D == 256 ? (NT == 1 ? 3 : NT == 2 ? 3 : 2) : D == 128 ? (NT == 1 ? 8 : NT == 2 ? 6 : 4) : (NT == 1 ? 10 : NT == 2 ? 8 : 5);
 };
 
 // A row's tokens of the cache, -1 where its numbers are bad.
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
   __shared__ long long s_list[2 * kThreads];  // the blocks of the share's positions
   __shared__ int s_bad[S::kStages];           // the stage's page does not exist
   __shared__ float s_top[W][S::N], s_sum[W][S::N];
-  __shared__ int s_scan[W], s_rows[W], s_at[3], s_last;
+  __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 
   // ---- the share
   const int units = A.hk * A.tiles, N = gridDim.x, cta = blockIdx.x;
-  const int per = (A.B + kThreads - 1) / kThreads;
-  const int r0 = min(A.B, tid * per), r1 = min(A.B, r0 + per);
+  // every warp finds it by itself: a lane takes `per` rows
+  const int per = (A.B + 31) / 32;
+  const int r0 = min(A.B, lane * per), r1 = min(A.B, r0 + per);
   int mine = 0, rows = 0;
   for (int b = r0; b < r1; ++b) {
     const int c = row_cost(A, b);
@@ -240,43 +241,26 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
     if (lane >= o) upto += y;
   }
   rows = __reduce_add_sync(0xffffffffu, rows);
-  if (lane == 31) {
-    s_scan[warp] = upto;
-    s_rows[warp] = rows;
-  }
-  if (tid == 0) s_at[0] = -1;
-  __syncthreads();
-  int total = 0;
-  rows = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) upto += s_scan[w];
-    total += s_scan[w];
-    rows += s_rows[w];
-  }
-  total *= units;
+  const int total = __shfl_sync(0xffffffffu, upto, 31) * units;
   const Deal deal(total, min(min(N, total / kLeast), (int)min((long long)rows * units * kMostParts, (long long)N)));
   Walk share;
   share.x = cta < deal.used ? deal.start(cta) : 0;
   share.x1 = cta < deal.used ? deal.start(cta + 1) : 0;
-  if (share.x < share.x1 && share.x >= (upto - mine) * units && share.x < upto * units) {
-    int row0 = (upto - mine) * units;
-    for (int b = r0; b < r1; ++b) {
-      const int c = per == 1 ? mine : row_cost(A, b);
-      if (share.x < row0 + c * units) {
-        s_at[0] = b;
-        s_at[1] = c;
-        s_at[2] = row0;
-        break;
-      }
-      row0 += c * units;
-    }
-  }
-  __syncthreads();
   const int x0 = share.x, x1 = share.x1;
-  share.b = s_at[0];
-  share.cost = s_at[1];
-  share.row0 = s_at[2];
+  const bool any_share = x0 < x1;
+  if (any_share) {
+    const int owner = __ffs(__ballot_sync(0xffffffffu, x0 < upto * units)) - 1;
+    int at = r0, cost = mine, first = (upto - mine) * units;
+    if (per > 1 && lane == owner)
+      for (at = r0;; ++at) {
+        cost = row_cost(A, at);
+        if (x0 < first + cost * units) break;
+        first += cost * units;
+      }
+    share.b = __shfl_sync(0xffffffffu, at, owner);
+    share.cost = __shfl_sync(0xffffffffu, cost, owner);
+    share.row0 = __shfl_sync(0xffffffffu, first, owner);
+  }
 
   // ---- the blocks of the share, kThreads positions at a time
   Walk walk = share;
@@ -309,9 +293,28 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
       bulk_g2s(ring + stage * S::kBlock, A.pool + block * S::kBlock, S::kBlock, &s_full[stage]);
     }
   };
-  const bool any_share = s_at[0] >= 0;
+  // ---- the queries of a unit's tile: column `row`, channels t D/4 .. of it; the first unit's as early as may be
+  const int row = lane >> 2, t = lane & 3;  // the lane's place in the operands
+  const int cols = A.T * A.G;
+  uint32_t xq[D / 8];
+  auto load_q = [&](const Segment &g, int j) {
+    const int head = g.unit / A.tiles, c = (g.unit - head * A.tiles) * S::N + 8 * j + row, tok = c / A.G;
+    const bf16 *q = A.q + ((long long)g.b * A.T + tok) * A.qs + (head * A.G + c - tok * A.G) * D + t * (D / 4);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 y = c < cols ? *(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0, 0, 0, 0);
+      xq[4 * i] = y.x;
+      xq[4 * i + 1] = y.y;
+      xq[4 * i + 2] = y.z;
+      xq[4 * i + 3] = y.w;
+    }
+  };
+  Segment g;
+  bool more = false;
   if (any_share) {
     list(0);
+    more = next_segment(A, units, share, g);
+    if (more && NT == 1) load_q(g, 0);
     __syncthreads();
     if (tid == 0)
       for (int i = 0; i < S::kStages - 1; ++i) copy(i);
@@ -328,16 +331,25 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
   if (!any_share) return;
 
   // ---- the products
-  const int row = lane >> 2, t = lane & 3;  // the lane's place in the operands
   const int k_a = key_of(row), k_b = key_of(row + 8);
-  Segment g;
+  // offsets inside a block: the lane's codes of its two keys of the warp's first 16, and of its four keys of any 16 (the
+  // swizzle of D >= 128 does not depend on which 16)
+  const int sub0 = warp * S::kSubs;  // the warp's first 16 keys
+  constexpr int LB = D / (16 * W);   // a lane's bytes of a key's row in the second product: 8 channels, or 4
+  constexpr int k16 = 8 * D;         // bytes of 16 keys
+  const int at_a = sub0 * k16 + swizzle(k_a * (D / 2) + t * (D / 8)), at_b = sub0 * k16 + swizzle(k_b * (D / 2) + t * (D / 8));
+  const int at_s = scales_at(D, 0) + (sub0 * 16 + k_a) * (D / 16) + t * (D / 64);  // and the first key's scales
+  int at_v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) at_v[k] = codes_at(D, 1) + swizzle((4 * t + k) * (D / 2) + warp * (D / 2 / W) + row * LB);
+  const int at_z = scales_at(D, 1) + (warp * S::kSlice + row * (S::kSlice / 8)) / kGroup * kPage + 4 * t;
   int stage = 0, buf = 0, listed = kThreads;  // listed: positions whose blocks are known
   uint32_t parity = 0;  // of the ring's round
-  while (next_segment(A, units, share, g)) {
+  for (bool first = true; more; first = false) {
     int ql;
     const int len = row_len(A, g.b, ql);
-    const int head = g.unit / A.tiles, col0 = (g.unit - head * A.tiles) * S::N, cols = A.T * A.G;
-    // ---- the queries: column `row` of tile j, channels t D/4 .. of it
+    const int head = g.unit / A.tiles, col0 = (g.unit - head * A.tiles) * S::N;
+    // ---- the queries in fp16
     uint2 qf[S::kQRegs ? S::kSteps * NT : 1];
     float f[NT][2];    // scale of columns 2t, 2t + 1
     int sees[NT][2];   // keys that they see
@@ -345,19 +357,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float mul = A.scale;
-      const int c = col0 + 8 * j + row;
-      const bool real = c < cols;
-      const int tok = real ? c / A.G : 0;
-      const bf16 *q = A.q + ((long long)g.b * A.T + tok) * A.qs + (head * A.G + (real ? c - tok * A.G : 0)) * D + t * (D / 4);
-      uint32_t x[D / 8];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 y = real ? *(reinterpret_cast<const uint4 *>(q) + i) : make_uint4(0, 0, 0, 0);
-        x[4 * i] = y.x;
-        x[4 * i + 1] = y.y;
-        x[4 * i + 2] = y.z;
-        x[4 * i + 3] = y.w;
-      }
+      if (NT > 1 || !first) load_q(g, j);
+      const uint32_t *x = xq;
       uint32_t top2 = 0;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) top2 = __vmaxu2(top2, x[i] & 0x7fff7fffu);
@@ -422,7 +423,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 
       // ---- scores
       float s[S::kSubs][NT][4];
-      const int sub0 = warp * S::kSubs;  // the warp's first 16 keys
       const bool work = !bad && key0 + 16 * sub0 < len;
       if (work) {
 #pragma unroll
@@ -435,24 +435,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
         for (int c = 0; c < CHUNKS; ++c) {
           uint32_t wa[S::kSubs][CH / 8], wb[S::kSubs][CH / 8];
           __half2 sa[S::kSubs], sb[S::kSubs];
-          const int byte = t * (D / 8) + c * 16;
+          const uint8_t *pa = block + (c ? at_a ^ 16 : at_a), *pb = block + (c ? at_b ^ 16 : at_b), *ps = block + at_s + 2 * c;
 #pragma unroll
           for (int u = 0; u < S::kSubs; ++u) {
-            const int ka = (sub0 + u) * 16 + k_a, kb = (sub0 + u) * 16 + k_b;
-            if constexpr (D == 64) {
-              const uint2 x = *reinterpret_cast<const uint2 *>(block + swizzle(ka * 32 + byte));
-              const uint2 y = *reinterpret_cast<const uint2 *>(block + swizzle(kb * 32 + byte));
+            if constexpr (D == 64) {  // 16 keys further on the swizzle's bit 9 is the other one
+              const int other = (u & 1) << 6;
+              const uint2 x = *reinterpret_cast<const uint2 *>(block + ((at_a + u * k16) ^ other));
+              const uint2 y = *reinterpret_cast<const uint2 *>(block + ((at_b + u * k16) ^ other));
               wa[u][0] = x.x, wa[u][1] = x.y, wb[u][0] = y.x, wb[u][1] = y.y;
-              sa[u] = e4m3x2(block[scales_at(D, 0) + ka * 4 + t] * 0x101u);
-              sb[u] = e4m3x2(block[scales_at(D, 0) + kb * 4 + t] * 0x101u);
+              sa[u] = e4m3x2(ps[u * D] * 0x101u);
+              sb[u] = e4m3x2(ps[u * D + 2 * (D / 16)] * 0x101u);
             } else {
-              const uint4 x = *reinterpret_cast<const uint4 *>(block + swizzle(ka * (D / 2) + byte));
-              const uint4 y = *reinterpret_cast<const uint4 *>(block + swizzle(kb * (D / 2) + byte));
+              const uint4 x = *reinterpret_cast<const uint4 *>(pa + u * k16);
+              const uint4 y = *reinterpret_cast<const uint4 *>(pb + u * k16);
               wa[u][0] = x.x, wa[u][1] = x.y, wa[u][2] = x.z, wa[u][3] = x.w;
               wb[u][0] = y.x, wb[u][1] = y.y, wb[u][2] = y.z, wb[u][3] = y.w;
-              const uint8_t *at = block + scales_at(D, 0) + t * (D / 64) + c * 2;
-              sa[u] = e4m3x2(*reinterpret_cast<const unsigned short *>(at + ka * (D / 16)));
-              sb[u] = e4m3x2(*reinterpret_cast<const unsigned short *>(at + kb * (D / 16)));
+              sa[u] = e4m3x2(*reinterpret_cast<const unsigned short *>(ps + u * D));
+              sb[u] = e4m3x2(*reinterpret_cast<const unsigned short *>(ps + u * D + 2 * (D / 16)));
             }
           }
 #pragma unroll
@@ -579,9 +578,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
       }
       // ---- output: the warp's channels of 16 keys at a time
       if (!bad) {
-        const uint8_t *codes = block + codes_at(D, 1);
-        constexpr int LB = D / (16 * W);  // a lane's bytes of a key's row: 8 channels, or 4
-        const uint8_t *scales = block + scales_at(D, 1) + (warp * S::kSlice + row * (S::kSlice / 8)) / kGroup * kPage;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           if (key0 + 16 * ks >= len) break;
@@ -591,13 +587,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
           uint32_t wv[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint8_t *at = codes + swizzle((16 * ks + 4 * t + k) * (D / 2) + warp * (D / 2 / W) + row * LB);
+            const uint8_t *at = block + (D == 64 && ks & 1 ? (at_v[k] + ks * k16) ^ 64 : at_v[k] + ks * k16);
             if constexpr (LB == 4)
               wv[k] = *reinterpret_cast<const uint32_t *>(at);
             else
               wv[k] = *reinterpret_cast<const unsigned short *>(at);
           }
-          uint32_t e = *reinterpret_cast<const uint32_t *>(scales + 16 * ks + 4 * t);  // 4 keys' scales
+          uint32_t e = *reinterpret_cast<const uint32_t *>(block + at_z + 16 * ks);  // 4 keys' scales
           if (key0 + 16 * ks + 16 > len) {  // what the page holds behind the row's tokens may be anything
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -638,113 +634,150 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
         for (int o = 4; o < 32; o <<= 1) sum[j][k] += __shfl_xor_sync(0xffffffffu, sum[j][k], o);
         if (row == 0) s_sum[warp][8 * j + 2 * t + k] = sum[j][k];
       }
+    const Segment g0 = g;
+    more = next_segment(A, units, share, g);
     bad = __syncthreads_or(bad);
     const int ch = warp * S::kSlice + row * (S::kSlice / 8);  // the lane's first channel
-    const bool whole = g.p == 0 && g.x + g.count == g.end;
+    const bool whole = g0.p == 0 && g0.x + g0.count == g0.end;
     if (whole && bad) continue;
-    const int slot = 2 * cta + (g.p == 0);
+    const int slot = 2 * cta + (g0.p == 0);
+    bf16 *out = A.out + (long long)g0.b * A.T * A.hq * D + head * A.G * D;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int c = 8 * j + 2 * t + k, col = col0 + c;
+        if (col >= cols) continue;
         float all = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) all += s_sum[w][c];
         if (whole) {
-          if (col < cols) {
-            const int tok = col / A.G;
-            const float inv = all == 0.0f ? 0.0f : A.out_mul / all;
-            bf16 *out = A.out + (((long long)g.b * A.T + tok) * A.hq + head * A.G + col - tok * A.G) * D + ch;
-            uint32_t z[S::kMt];
+          const int tok = col / A.G;
+          const float inv = all == 0.0f ? 0.0f : A.out_mul / all;
+          bf16 *to = out + (tok * A.hq + col - tok * A.G) * D + ch;
+          uint32_t z[S::kMt];
 #pragma unroll
-            for (int m = 0; m < S::kMt; ++m) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(acc[m][j][k] * inv, acc[m][j][k + 2] * inv);
-              z[m] = *reinterpret_cast<const uint32_t *>(&x);
-            }
-            if constexpr (S::kMt == 4)
-              *reinterpret_cast<uint4 *>(out) = make_uint4(z[0], z[1], z[2], z[3]);
-            else
-              *reinterpret_cast<uint2 *>(out) = make_uint2(z[0], z[1]);
+          for (int m = 0; m < S::kMt; ++m) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[m][j][k] * inv, acc[m][j][k + 2] * inv);
+            z[m] = *reinterpret_cast<const uint32_t *>(&x);
           }
+          if constexpr (S::kMt == 4)
+            *reinterpret_cast<uint4 *>(to) = make_uint4(z[0], z[1], z[2], z[3]);
+          else
+            *reinterpret_cast<uint2 *>(to) = make_uint2(z[0], z[1]);
         } else {
           float *part = A.part + ((long long)slot * S::N + c) * D + ch;
 #pragma unroll
           for (int m = 0; m < S::kMt; m += 2)
-            *reinterpret_cast<float4 *>(part + 2 * m) =
-                make_float4(acc[m][j][k], acc[m][j][k + 2], acc[m + 1][j][k], acc[m + 1][j][k + 2]);
+            __stcg(reinterpret_cast<float4 *>(part + 2 * m),
+                   make_float4(acc[m][j][k], acc[m][j][k + 2], acc[m + 1][j][k], acc[m + 1][j][k + 2]));
           if (row == 0 && warp == 0)
-            *reinterpret_cast<float2 *>(A.stats + ((long long)slot * S::N + c) * 2) =
-                make_float2(bad ? __int_as_float(0x7fffffff) : ref[j][k], all);
+            __stcg(reinterpret_cast<float2 *>(A.stats + ((long long)slot * S::N + c) * 2),
+                   make_float2(bad ? __int_as_float(0x7fffffff) : ref[j][k], all));
         }
       }
     if (whole) continue;
 
     // ---- the unit's parts: the last CTA of up to kFan joins theirs, the last of those the unit's
-    const int i0 = deal.owner(g.first), n = deal.owner(g.end - 1) - i0 + 1;  // the CTAs that hold one
+    const int i0 = deal.owner(g0.first), n = deal.owner(g0.end - 1) - i0 + 1;  // the CTAs that hold one
     auto slot_of = [&](int k) { return k == 0 ? 2 * i0 + 1 : 2 * (i0 + k); };
     auto arrive = [&](int *count, int most) {  // true for the last
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const bool last = atomicAdd(count, 1) == most - 1;
-        if (last) *count = 0;
-        s_last = last;
+        int before;  // releases what the CTA has written, acquires what the others have
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
+        if (before == most - 1) *count = 0;
+        s_last = before == most - 1;
       }
       __syncthreads();
-      const bool last = s_last;
-      if (last) __threadfence();
-      return last;
+      return s_last != 0;
     };
     auto join = [&](int k0, int k1, int step, bool final) {  // parts k0, k0 + step .. below k1
+      constexpr int M = D / (16 * W);      // 16-byte pieces of 8 columns that a thread joins
+      constexpr int H = D == 256 ? 4 : 2;  // as the registers allow
       bool lost = false;
-      constexpr int M = D / (16 * W);  // 16-byte pieces of 8 columns that a thread joins
 #pragma unroll 1
-      for (int j = 0; j < NT; ++j) {
+      for (int j = 0; 8 * j < min(S::N, cols - col0); ++j) {
         float4 o[M];
-        float l[M], top[M];
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-          o[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          l[m] = 0.0f;
-          top[m] = kNone;
-        }
-#pragma unroll 4
-        for (int k = k0; k < k1; k += step)
+        for (int m = 0; m < M; ++m) o[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // lane: column lane % 8 of parts lane / 8 + 4 i, kFan parts at a time
+        const int c = lane & 7;
+        const bool real = col0 + 8 * j + c < cols;
+        float top = kNone, l = 0.0f;
+#pragma unroll 1
+        for (int kb = k0; kb < k1; kb += kFan * step) {
+          float2 st[kFan / 4];
+          float next = top;
+#pragma unroll
+          for (int i = 0; i < kFan / 4; ++i) {
+            const int k = kb + (lane / 8 + 4 * i) * step;
+            st[i] = make_float2(kNone, 0.0f);
+            if (k < k1 && real) st[i] = __ldcg(reinterpret_cast<const float2 *>(A.stats) + (long long)slot_of(k) * S::N + 8 * j + c);
+          }
+#pragma unroll
+          for (int i = 0; i < kFan / 4; ++i) {
+            lost |= st[i].x != st[i].x;
+            next = fmaxf(next, st[i].x);
+          }
+          next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 8));
+          next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 16));
+          const float fade = ex2(top - next);
+          top = next;
+          l *= fade;
+#pragma unroll
+          for (int i = 0; i < kFan / 4; ++i) {
+            st[i].x = ex2(st[i].x - next);
+            l += st[i].x * st[i].y;
+          }
 #pragma unroll
           for (int m = 0; m < M; ++m) {
-            const float r = __ldcg(A.stats + ((long long)slot_of(k) * S::N + 8 * j + (m * kThreads + tid) / (D / 4)) * 2);
-            lost |= r != r;
-            top[m] = fmaxf(top[m], r);
+            const float y = __shfl_sync(0xffffffffu, fade, (m * kThreads + tid) / (D / 4));
+            o[m].x *= y, o[m].y *= y, o[m].z *= y, o[m].w *= y;
           }
-#pragma unroll 4
-        for (int k = k0; k < k1; k += step) {
-          const long long slot_k = (long long)slot_of(k) * S::N + 8 * j;
 #pragma unroll
-          for (int m = 0; m < M; ++m) {
-            const float2 st = __ldcg(reinterpret_cast<const float2 *>(A.stats) + slot_k + (m * kThreads + tid) / (D / 4));
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(A.part + slot_k * D) + m * kThreads + tid);
-            const float w = ex2(st.x - top[m]);
-            l[m] += st.y * w;
-            o[m].x += x.x * w, o[m].y += x.y * w, o[m].z += x.z * w, o[m].w += x.w * w;
+          for (int i = 0; i < kFan / H; ++i) {  // the loads of H parts together
+            if (kb + H * i * step >= k1) break;
+            float4 x[H][M];
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int m = 0; m < M; ++m) {
+                const int k = kb + (H * i + h) * step, cm = (m * kThreads + tid) / (D / 4);
+                x[h][m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (k < k1 && col0 + 8 * j + cm < cols)
+                  x[h][m] = __ldcg(reinterpret_cast<const float4 *>(A.part + ((long long)slot_of(k) * S::N + 8 * j) * D) +
+                                   m * kThreads + tid);
+              }
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int m = 0; m < M; ++m) {
+                const float w = __shfl_sync(0xffffffffu, st[(H * i + h) / 4].x, 8 * ((H * i + h) % 4) + (m * kThreads + tid) / (D / 4));
+                o[m].x += x[h][m].x * w, o[m].y += x[h][m].y * w, o[m].z += x[h][m].z * w, o[m].w += x[h][m].w * w;
+              }
           }
         }
-        __syncthreads();  // all have read the part that is written over
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        lost = __any_sync(0xffffffffu, lost);
+        if (!final) __syncthreads();  // all have read the part that is written over
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-          const int c = 8 * j + (m * kThreads + tid) / (D / 4), at = (m * kThreads + tid) % (D / 4) * 4, col = col0 + c;
+          const int cm = (m * kThreads + tid) / (D / 4), at = (m * kThreads + tid) % (D / 4) * 4, col = col0 + 8 * j + cm;
+          const float all = __shfl_sync(0xffffffffu, l, cm), most = __shfl_sync(0xffffffffu, top, cm);
+          if (col >= cols) continue;
           if (!final) {
-            const long long to = (long long)slot_of(k0) * S::N + c;
-            *reinterpret_cast<float4 *>(A.part + to * D + at) = o[m];
+            const long long to = (long long)slot_of(k0) * S::N + 8 * j + cm;
+            __stcg(reinterpret_cast<float4 *>(A.part + to * D + at), o[m]);
             if (at == 0)
-              *reinterpret_cast<float2 *>(A.stats + to * 2) = make_float2(lost ? __int_as_float(0x7fffffff) : top[m], l[m]);
-          } else if (col < cols && !lost) {
+              __stcg(reinterpret_cast<float2 *>(A.stats) + to, make_float2(lost ? __int_as_float(0x7fffffff) : most, all));
+          } else if (!lost) {
             const int tok = col / A.G;
-            const float inv = l[m] == 0.0f ? 0.0f : A.out_mul / l[m];
-            bf16 *out = A.out + (((long long)g.b * A.T + tok) * A.hq + head * A.G + col - tok * A.G) * D + at;
+            const float inv = all == 0.0f ? 0.0f : A.out_mul / all;
             const __nv_bfloat162 a = __floats2bfloat162_rn(o[m].x * inv, o[m].y * inv);
             const __nv_bfloat162 b = __floats2bfloat162_rn(o[m].z * inv, o[m].w * inv);
-            *reinterpret_cast<uint2 *>(out) =
+            *reinterpret_cast<uint2 *>(out + (tok * A.hq + col - tok * A.G) * D + at) =
                 make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
           }
         }
@@ -794,8 +827,13 @@ size_t part_bytes(int D, int NT) { return (size_t)2 * kMaxCtas * 8 * NT * D * 4;
 template <int D, int NT>
 gdn_status launch(const Args &A, int sms, cudaStream_t stream) {
   using S = Shape<D, NT>;
-  if (cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
-    return check_launch("attn_kv4");
+  static std::atomic<uint64_t> ready{0};  // a bit a device: the attribute holds for the process
+  const uint64_t bit = 1ull << device_info().id;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
+      return check_launch("attn_kv4");
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   // no more CTAs than the rows could fill
   const long long most = (long long)A.B * A.hk * A.tiles * (A.max_pages + kSetup) / kLeast;
   int ctas = sms * S::kCtas < kMaxCtas ? sms * S::kCtas : kMaxCtas;
