@@ -76,6 +76,7 @@ struct Shape {
   static constexpr int kSubs = 4 / W;            // 16 keys each that a warp scores
   static constexpr int N = 8 * NT;               // query columns
   static constexpr bool kQRegs = NT == 1;        // the queries stay in registers
+  static constexpr int kTiles = kQRegs ? 1 : (NT + W - 1) / W;  // query tiles that a warp brings in
   static constexpr int kStages = D == 128 && NT == 1 ? 2 : 3;
   static constexpr int kBlock = block_bytes(D);
   static constexpr int kSteps = D / 16;          // products of 16 channels
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
   __shared__ __align__(8) uint64_t s_full[S::kStages];
   __shared__ long long s_list[2 * kThreads];  // the blocks of the share's positions
   __shared__ int s_bad[S::kStages];           // the stage's page does not exist
-  __shared__ float s_top[W][S::N], s_sum[W][S::N];
+  __shared__ float s_top[W][S::N], s_sum[W][S::N], s_f[S::N];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
   if (any_share) {
     list(0);
     more = next_segment(A, units, share, g);
-    if (more && NT == 1) load_q(g, 0);
+    if (more && (S::kQRegs || warp < NT)) load_q(g, S::kQRegs ? 0 : warp);
     __syncthreads();
     if (tid == 0)
       for (int i = 0; i < S::kStages - 1; ++i) copy(i);
@@ -350,56 +351,63 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
     const int len = row_len(A, g.b, ql);
     const int head = g.unit / A.tiles, col0 = (g.unit - head * A.tiles) * S::N;
     // ---- the queries in fp16
-    uint2 qf[S::kQRegs ? S::kSteps * NT : 1];
+    uint2 qf[S::kQRegs ? S::kSteps : 1];
     float f[NT][2];    // scale of columns 2t, 2t + 1
     int sees[NT][2];   // keys that they see
     if (!S::kQRegs) __syncthreads();  // the last unit's queries are used no more
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float mul = A.scale;
-      if (NT > 1 || !first) load_q(g, j);
-      const uint32_t *x = xq;
+    for (int i = 0; i < S::kTiles; ++i) {
+      const int j = S::kQRegs ? i : i * W + warp;  // each warp its own, or the tiles dealt out
+      if (j >= NT) break;
+      if (i > 0 || !first) load_q(g, j);
       uint32_t top2 = 0;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) top2 = __vmaxu2(top2, x[i] & 0x7fff7fffu);
+      for (int i = 0; i < D / 8; ++i) top2 = __vmaxu2(top2, xq[i] & 0x7fff7fffu);
       uint32_t top = max(top2 & 0xffffu, top2 >> 16) >> 7;  // the largest channel's exponent field
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = max(1, min(253, (int)top));  // 2^(e - 127) and its inverse are both normal
       const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-      mul *= __uint_as_float((uint32_t)e << 23);
-      if (S::kQRegs || j % W == warp) {
+      const float mul = A.scale * __uint_as_float((uint32_t)e << 23);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {  // 8 channels, two products
-          const uint32_t *y = x + 4 * i;
-          float ch[8];
+      for (int m = 0; m < D / 32; ++m) {  // 8 channels, two products
+        const uint32_t *y = xq + 4 * m;
+        float ch[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ch[2 * k] = __uint_as_float(y[k] << 16) * down;
-            ch[2 * k + 1] = __uint_as_float(y[k] & 0xffff0000u) * down;
-          }
+        for (int k = 0; k < 4; ++k) {
+          ch[2 * k] = __uint_as_float(y[k] << 16) * down;
+          ch[2 * k + 1] = __uint_as_float(y[k] & 0xffff0000u) * down;
+        }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint2 b;
-            b.x = bits(__floats2half2_rn(ch[2 * k], ch[2 * k + 4]));
-            b.y = bits(__floats2half2_rn(ch[2 * k + 1], ch[2 * k + 5]));
-            if constexpr (S::kQRegs)
-              qf[(2 * i + k) * NT + j] = b;
-            else
-              s_q[((2 * i + k) * NT + j) * 32 + lane] = b;
-          }
+        for (int k = 0; k < 2; ++k) {
+          uint2 b;
+          b.x = bits(__floats2half2_rn(ch[2 * k], ch[2 * k + 4]));
+          b.y = bits(__floats2half2_rn(ch[2 * k + 1], ch[2 * k + 5]));
+          if constexpr (S::kQRegs)
+            qf[2 * m + k] = b;
+          else
+            s_q[((2 * m + k) * NT + j) * 32 + lane] = b;
         }
       }
+      if constexpr (S::kQRegs) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) f[0][k] = __shfl_sync(0xffffffffu, mul, 4 * (2 * t + k));
+      } else if (t == 0) {
+        s_f[8 * j + row] = mul;
+      }
+    }
+    if (!S::kQRegs) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        f[j][k] = __shfl_sync(0xffffffffu, mul, 4 * (2 * t + k));
+        if (!S::kQRegs) f[j][k] = s_f[8 * j + 2 * t + k];
         const int c2 = col0 + 8 * j + 2 * t + k, tok2 = c2 / A.G;
         sees[j][k] = c2 >= cols ? len : tok2 < ql ? max(0, len - ql + tok2 + 1) : 0;  // a column of nobody's sees all
       }
     }
     // the tile's first token sees the fewest keys, unless tokens are missing
     const int least = (min(cols, col0 + S::N) - 1) / A.G < ql ? max(0, len - ql + col0 / A.G + 1) : 0;
-    if (!S::kQRegs) __syncthreads();
 
     float acc[S::kMt][NT][4], ref[NT][2], sum[NT][2];
 #pragma unroll
@@ -471,7 +479,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
                 for (int j = 0; j < NT; ++j) {
                   uint2 b;
                   if constexpr (S::kQRegs)
-                    b = qf[step * NT + j];
+                    b = qf[step];
                   else
                     b = s_q[(step * NT + j) * 32 + lane];
 #pragma unroll
@@ -694,7 +702,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
     };
     auto join = [&](int k0, int k1, int step, bool final) {  // parts k0, k0 + step .. below k1
       constexpr int M = D / (16 * W);      // 16-byte pieces of 8 columns that a thread joins
-      constexpr int H = D == 256 ? 4 : 2;  // as the registers allow
+      constexpr int H = NT == 4 ? 8 : D == 256 ? 4 : 2;  // as the registers allow
       bool lost = false;
 #pragma unroll 1
       for (int j = 0; 8 * j < min(S::N, cols - col0); ++j) {
