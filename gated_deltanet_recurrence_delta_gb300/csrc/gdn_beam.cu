@@ -44,17 +44,40 @@ struct Args {
 
 __device__ __forceinline__ bool better(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
 
-template <bool HALF>
-__device__ __forceinline__ float logit(const void *p, long long i) {
-  return HALF ? ldbf(static_cast<const bf16 *>(p) + i) : static_cast<const float *>(p)[i];
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Slice blockIdx.x of row blockIdx.y. A thread holds kPer / C runs of C logits
-// (16 bytes), run k at C (k kThreads + tid) from the slice's start.
+// 16 bytes of logits: 4 fp32, or 8 bf16 that stay packed.
 template <bool HALF>
-__global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__ Args A) {
-  constexpr int C = HALF ? 8 : 4, RUNS = kPer / C;
-  __shared__ float s_max[kParts], s_red[kWarps], s_sum[kWarps], s_cut;
+struct Run {
+  static constexpr int C = HALF ? 8 : 4;
+  uint4 w;
+  __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (HALF)
+      return __uint_as_float(i & 1 ? word(i / 2) & 0xffff0000u : word(i / 2) << 16);
+    else
+      return __uint_as_float(word(i));
+  }
+  __device__ __forceinline__ float top() const {  // a NaN is no maximum unless all are
+    if constexpr (HALF) {
+      auto h = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
+      const __nv_bfloat162 m = __hmax2(__hmax2(h(w.x), h(w.y)), __hmax2(h(w.z), h(w.w)));
+      return fmaxf(__low2float(m), __high2float(m));
+    } else {
+      return fmaxf(fmaxf(at(0), at(1)), fmaxf(at(2), at(3)));
+    }
+  }
+};
+
+// Slice blockIdx.x of row blockIdx.y: run k of a thread is run k kThreads + tid of the slice.
+template <bool HALF>
+__global__ void __launch_bounds__(kThreads, HALF ? 5 : 4) slice_kernel(const __grid_constant__ Args A) {
+  constexpr int C = Run<HALF>::C, RUNS = kPer / C, B = HALF ? 2 : 4;
+  __shared__ float s_max[kParts], s_red[kWarps], s_sum[kWarps];
   __shared__ float s_val[kList];
   __shared__ int s_at[kList], s_n, s_pick[kWarps];
   griddep_wait();
@@ -65,71 +88,82 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
   if (!(score > -INFINITY) || (A.done && A.done[row])) return;  // its logits give no candidates
   const long long runs = (A.V + C - 1) / C;  // 16 bytes each, dealt out evenly
   const int i0 = C * (int)(runs * slice / A.slices), i1 = min(A.V, C * (int)(runs * (slice + 1) / A.slices));
-  const long long base = row * A.stride;
-  const char *p = static_cast<const char *>(A.logits) + base * (HALF ? 2 : 4);
+  const char *p = static_cast<const char *>(A.logits) + row * A.stride * B;
   const bool aligned = (reinterpret_cast<uintptr_t>(p) & 15) == 0;  // and so is every run then
-  float v[kPer];
+  Run<HALF> v[RUNS];
 #pragma unroll
   for (int k = 0; k < RUNS; ++k) {
     const int i = i0 + C * (k * kThreads + tid);
     if (aligned && i + C <= i1) {
-      const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(p + (long long)i * (HALF ? 2 : 4)));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      v[k].w = __ldcs(reinterpret_cast<const uint4 *>(p + (long long)i * B));
+    } else if (HALF) {
+      uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (HALF) {
-          v[k * C + 2 * j] = __uint_as_float(w[j] << 16);
-          v[k * C + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        } else {
-          v[k * C + j] = __uint_as_float(w[j]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = i + j < i1 ? *reinterpret_cast<const unsigned short *>(p + (long long)(i + j) * 2) : 0xff80u;
+        if (j & 1) w[j / 2] |= x << 16;
+        else w[j / 2] = x;
       }
+      v[k].w = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
+      uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < C; ++j) v[k * C + j] = i + j < i1 ? logit<HALF>(p, i + j) : -INFINITY;
+      for (int j = 0; j < 4; ++j)
+        w[j] = i + j < i1 ? *reinterpret_cast<const uint32_t *>(p + (long long)(i + j) * 4) : 0xff800000u;
+      v[k].w = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   // ---- the slice's maximum and the parts' maxima (a NaN is no maximum, but reaches the sum)
-  float top = v[0];
+  float most[RUNS], top = -INFINITY;
 #pragma unroll
-  for (int j = 1; j < kPer; ++j) top = fmaxf(top, v[j]);
-  if (top != top) top = -INFINITY;
+  for (int k = 0; k < RUNS; ++k) {
+    most[k] = v[k].top();
+    top = fmaxf(top, most[k]);
+  }
   if (tid == 0) s_n = 0;
   float part = top;
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) part = fmaxf(part, __shfl_xor_sync(0xffffffffu, part, o));
   if (tid % kLanes == 0) s_max[tid / kLanes] = part;
-#pragma unroll
-  for (int o = kLanes; o < 32; o <<= 1) part = fmaxf(part, __shfl_xor_sync(0xffffffffu, part, o));
-  if (lane == 0) s_red[warp] = part;
   __syncthreads();
-  float m = s_red[0];
-#pragma unroll
-  for (int j = 1; j < kWarps; ++j) m = fmaxf(m, s_red[j]);
-  const float ref = m == -INFINITY ? 0.0f : m;
-  if (warp == 0) {  // the part whose maximum has beams - 1 better ones
+  float m = s_max[lane];
+  {  // the part whose maximum has beams - 1 better ones; every warp finds it
     static_assert(kParts == 32, "a part to a lane");
-    const float x = s_max[lane];
+    const float x = m;
     int rank = 0;
 #pragma unroll
     for (int j = 0; j < kParts; ++j) rank += better(__shfl_sync(0xffffffffu, x, j), j, x, lane);
-    if (rank == A.beams - 1) s_cut = x;
+    part = __shfl_sync(0xffffffffu, x, __ffs(__ballot_sync(0xffffffffu, rank == A.beams - 1)) - 1);
   }
-  __syncthreads();
-  const float cut = s_cut;
-  // ---- sum of exponentials, candidates
-  float sum = 0.0f;
+  const float cut = part;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    sum += exp2f((v[j] - ref) * 1.4426950408889634f);
-    if (v[j] >= cut && v[j] > -INFINITY) {
-      const int n = atomicAdd(&s_n, 1);
-      if (n < kList) {
-        s_val[n] = v[j];
-        s_at[n] = i0 + C * (j / C * kThreads + tid) + j % C;
+  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == -INFINITY ? 0.0f : m;
+  // ---- sum of exponentials, candidates
+  // 2^(v log2(e) + shift): what the shift's rounding loses is the same for all and put right in the sum
+  constexpr float log2e = 1.4426950408889634f;
+  const float shift = __fmul_rn(-ref, log2e), lost = fmaf(-ref, log2e, -shift);
+  float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k)
+#pragma unroll
+    for (int j = 0; j < C; ++j) sums[j & 3] += ex2(fmaf(v[k].at(j), log2e, shift));
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k)
+    if (most[k] >= cut) {  // few are
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const float x = v[k].at(j);
+        if (x >= cut && x > -INFINITY) {
+          const int n = atomicAdd(&s_n, 1);
+          if (n < kList) {
+            s_val[n] = x;
+            s_at[n] = i0 + C * (k * kThreads + tid) + j;
+          }
+        }
       }
     }
-  }
+  float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
@@ -137,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
   const long long at = row * A.slices + slice;
   if (tid == 0) {
     for (int j = 1; j < kWarps; ++j) sum += s_sum[j];
-    A.stats[at] = make_float2(m, sum);
+    A.stats[at] = make_float2(m, sum * ex2(lost));
   }
   const int n = s_n;
   float *best = A.best + at * A.beams;
@@ -164,13 +198,16 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
       float x = -INFINITY;
       int ix = 0x7fffffff;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int ij = i0 + C * (j / C * kThreads + tid) + j % C;
-        if (v[j] > -INFINITY && better(last, last_at, v[j], ij) && better(v[j], ij, x, ix)) {
-          x = v[j];
-          ix = ij;
+      for (int k = 0; k < RUNS; ++k)
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          const int ij = i0 + C * (k * kThreads + tid) + j;
+          const float y = v[k].at(j);
+          if (y > -INFINITY && better(last, last_at, y, ij) && better(y, ij, x, ix)) {
+            x = y;
+            ix = ij;
+          }
         }
-      }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float y = __shfl_xor_sync(0xffffffffu, x, o);
@@ -203,101 +240,138 @@ __global__ void __launch_bounds__(kThreads) slice_kernel(const __grid_constant__
 
 // A score as a whole number of the same order; 0 is below every candidate's.
 __device__ __forceinline__ unsigned long long key_of(double x) {
-  const long long b = __double_as_longlong(x);
+  const long long b = __double_as_longlong(x + 0.0);  // -0 is 0
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
 __device__ __forceinline__ double score_of(unsigned long long k) {
   return __longlong_as_double((long long)(k >> 63 ? k & 0x7fffffffffffffffull : ~k));
 }
+__device__ __forceinline__ uint32_t key_of(float x) {  // 0 for -inf; x is a logit that is a number
+  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 is 0
+  return x == -INFINITY ? 0 : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
 
-// Group blockIdx.x: joins its rows' slices, and takes its best candidates one
-// after the other.
+struct Place {  // of a row's list
+  float x;
+  int at;
+};
+
+// Group blockIdx.x. A warp joins a row's slices: their lists are in order, so the
+// row's best is always one of 32 heads (lists of higher tokens in higher lanes:
+// equal logits go to the lowest). Then the rows' lists meet, in 64 bits: the
+// fp64 units do two operations a cycle per SM, so that only the beams^2 scores
+// and one logarithm a beam are formed there. Candidates below the worst of the
+// rows' best are no one's, the others count how many are better.
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args A) {
+  extern __shared__ Place s_lists[];  // [kWarps][32][beams]: lane 0's is what has been joined so far
+  __shared__ Place s_row[kMaxBeams * kMaxBeams];
+  __shared__ unsigned long long s_key[kMaxBeams * kMaxBeams];
+  __shared__ int s_at[kMaxBeams * kMaxBeams], s_n;
   __shared__ double s_add[kMaxBeams];  // score - lse of a beam
-  __shared__ unsigned long long s_key[kWarps];
-  __shared__ int s_idx[kWarps];
+  __shared__ float s_m[kMaxBeams], s_sum[kMaxBeams];
+  __shared__ unsigned long long s_best[kMaxBeams];
   __shared__ uint8_t s_done[kMaxBeams];
   griddep_wait();
   griddep_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = A.beams, S = A.slices;
   const long long row0 = (long long)blockIdx.x * W;
+  Place *mine = s_lists + warp * 32 * W;
   for (int w = warp; w < W; w += kWarps) {
-    const float score = A.scores[row0 + w];
-    const bool over = A.done && A.done[row0 + w];
-    double add = -INFINITY;
-    if (over) {
-      add = score;
-    } else if (score > -INFINITY) {
-      const float2 *st = A.stats + (row0 + w) * S;
-      float m = -INFINITY;
-      for (int i = lane; i < S; i += 32) m = fmaxf(m, st[i].x);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      double sum = 0.0;
-      for (int i = lane; i < S; i += 32) sum += (double)st[i].y * exp((double)st[i].x - (double)m);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      add = (double)score - ((double)m + log(sum));
+    const long long row = row0 + w;
+    const float score = A.scores[row];
+    const bool over = A.done && A.done[row];
+    if (lane == 0) s_done[w] = over;
+    if (over || !(score > -INFINITY)) {
+      for (int i = lane; i < W; i += 32) s_row[w * W + i] = {-INFINITY, -1};
+      continue;
     }
+    const float2 *st = A.stats + row * S;
+    float m = -INFINITY, sum = 0.0f;
+    for (int i = lane; i < S; i += 32) m = fmaxf(m, st[i].x);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i = lane; i < S; i += 32) {
+      const float2 x = st[i];
+      sum += x.y * ex2((x.x - m) * 1.4426950408889634f);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
-      s_add[w] = add;
-      s_done[w] = over;
+      s_m[w] = m;
+      s_sum[w] = sum;
+    }
+    for (int s0 = 0; s0 < S; s0 += 31) {  // 31 slices at a time
+      const int n = min(31, S - s0) * W;
+      const float *bx = A.best + (row * S + s0) * W;
+      const int32_t *bi = A.best_at + (row * S + s0) * W;
+      for (int i = lane; i < n; i += 32) mine[W + i] = {bx[i], bi[i]};
+      for (int i = lane; i < W; i += 32) mine[i] = s0 == 0 ? Place{-INFINITY, -1} : s_row[w * W + i];
+      __syncwarp();
+      const bool list = lane == 0 || (lane - 1) * W < n;
+      int at = 0;
+      Place head = list ? mine[lane * W] : Place{-INFINITY, -1};
+      for (int r = 0; r < W; ++r) {
+        const uint32_t key = key_of(head.x), top = __reduce_max_sync(0xffffffffu, key);
+        const int from = __ffs(__ballot_sync(0xffffffffu, key == top)) - 1;
+        if (lane == from) {
+          s_row[w * W + r] = top ? head : Place{-INFINITY, -1};
+          ++at;
+          head = top && at < W ? mine[lane * W + at] : Place{-INFINITY, -1};
+        }
+      }
+      __syncwarp();
+    }
+  }
+  if (tid == 0) s_n = 0;
+  __syncthreads();
+  if (tid < W) {
+    const float score = A.scores[row0 + tid];
+    s_add[tid] = s_done[tid] ? (double)score
+                 : score > -INFINITY ? (double)score - ((double)s_m[tid] + log((double)s_sum[tid])) : -INFINITY;
+  }
+  __syncthreads();
+  auto key_at = [&](int w, int r) -> unsigned long long {  // 0: no candidate
+    double x = s_add[w];
+    if (s_done[w]) {
+      if (r > 0) return 0;
+    } else {
+      if (s_row[w * W + r].at < 0) return 0;
+      x += (double)s_row[w * W + r].x;
+    }
+    return x > -INFINITY ? key_of(x) : 0;  // not -inf, not NaN
+  };
+  if (tid < W) s_best[tid] = key_at(tid, 0);
+  __syncthreads();
+  unsigned long long cut = s_best[0];
+  for (int w = 1; w < W; ++w) cut = min(cut, s_best[w]);
+  for (int c = tid; c < W * W; c += kThreads) {
+    const int w = c / W, r = c - w * W;
+    const unsigned long long k = key_at(w, r);
+    if (k > 0 && k >= cut) {
+      const int i = atomicAdd(&s_n, 1);
+      s_key[i] = k;
+      s_at[i] = (w << 24) + (s_done[w] ? max(A.eos, 0) : s_row[c].at);
     }
   }
   __syncthreads();
-  // Candidate c < W S W: place c % W of slice c / W % S of beam c / (W S); its order among equals is (beam, token).
-  const int N = W * S * W;
-  unsigned long long last = ~0ull;  // the candidate taken last
-  int last_at = -1;
-  for (int r = 0; r < W; ++r) {
-    unsigned long long key = 0;
-    int at = 0x7fffffff;  // beam * 2^24 + token
-    auto offer = [&](double x, int ix) {
-      if (!(x > -INFINITY)) return;  // -inf, NaN
-      const unsigned long long k = key_of(x);
-      if ((k < last || (k == last && ix > last_at)) && (k > key || (k == key && ix < at))) {
-        key = k;
-        at = ix;
-      }
-    };
-    for (int c = tid; c < N; c += kThreads) {
-      const int w = c / (W * S);
-      if (s_done[w]) continue;
-      const int t = A.best_at[row0 * S * W + c];
-      if (s_add[w] > -INFINITY && t >= 0) offer(s_add[w] + (double)A.best[row0 * S * W + c], (w << 24) + t);
-    }
-    if (tid < W && s_done[tid]) offer(s_add[tid], (tid << 24) + max(A.eos, 0));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
-      const int i = __shfl_xor_sync(0xffffffffu, at, o);
-      if (k > key || (k == key && i < at)) {
-        key = k;
-        at = i;
-      }
-    }
-    __syncthreads();
-    if (lane == 0) {
-      s_key[warp] = key;
-      s_idx[warp] = at;
-    }
-    __syncthreads();
-    for (int j = 0; j < kWarps; ++j)
-      if (s_key[j] > key || (s_key[j] == key && s_idx[j] < at)) {
-        key = s_key[j];
-        at = s_idx[j];
-      }
-    last = key;
-    last_at = at;
-    if (tid == 0) {
-      const bool none = key == 0;
-      const int w = none ? r : at >> 24, t = none ? -1 : s_done[w] ? A.eos : at & 0xffffff;
-      A.parent[row0 + r] = (int)(row0 + w);
-      A.token[row0 + r] = t;
-      A.new_scores[row0 + r] = none ? -INFINITY : (float)score_of(key);
-      if (A.new_done) A.new_done[row0 + r] = !none && (s_done[w] || t == A.eos);
-    }
-    if (key == 0) last = 0;  // nothing is left
+  const int n = s_n;
+  for (int i = tid; i < n; i += kThreads) {
+    const unsigned long long k = s_key[i];
+    const int at = s_at[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += s_key[j] > k || (s_key[j] == k && s_at[j] < at);
+    if (rank >= W) continue;
+    const int w = at >> 24, t = s_done[w] ? A.eos : at & 0xffffff;
+    A.parent[row0 + rank] = (int)(row0 + w);
+    A.token[row0 + rank] = t;
+    A.new_scores[row0 + rank] = (float)score_of(k);
+    if (A.new_done) A.new_done[row0 + rank] = s_done[w] || t == A.eos;
+  }
+  for (int r = n + tid; r < W; r += kThreads) {  // places without a candidate
+    A.parent[row0 + r] = (int)(row0 + r);
+    A.token[row0 + r] = -1;
+    A.new_scores[row0 + r] = -INFINITY;
+    if (A.new_done) A.new_done[row0 + r] = 0;
   }
 }
 
@@ -347,7 +421,6 @@ extern "C" gdn_status gdn_beam_select(const gdn_beam_dims *dims, const void *log
     return fail(GDN_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdn_beam_workspace_size");
   const DeviceInfo *dev;
   GDN_TRY(current_device(&dev));
-  (void)dev;
   beam::Args A = {};
   A.groups = dims->n_groups;
   A.beams = dims->beams;
@@ -370,6 +443,15 @@ extern "C" gdn_status gdn_beam_select(const gdn_beam_dims *dims, const void *log
   const dim3 grid(A.slices, (unsigned)rows), block(beam::kThreads);
   if (launch_pdl(dims->half ? beam::slice_kernel<true> : beam::slice_kernel<false>, grid, block, 0, st, A) != cudaSuccess)
     return check_launch("beam_select");
-  launch_pdl(beam::join_kernel, dim3(A.groups), block, 0, st, A);
+  const size_t lists = (size_t)beam::kWarps * 32 * A.beams * sizeof(beam::Place);
+  static std::atomic<uint64_t> ready{0};  // a bit a device: the attribute holds for the process
+  const uint64_t bit = 1ull << dev->id;
+  if (lists > 16384 && !(ready.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(beam::join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             beam::kWarps * 32 * beam::kMaxBeams * (int)sizeof(beam::Place)) != cudaSuccess)
+      return check_launch("beam_select");
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  launch_pdl(beam::join_kernel, dim3(A.groups), block, lists, st, A);
   return check_launch("beam_select");
 }

@@ -77,7 +77,7 @@ def test_selection_matches_exact_arithmetic(G, W, V, half):
 def test_ties_go_to_the_lowest_place(V, half):
     """Equal logits in any number, equal beams, whole rows of one number."""
     dtype = torch.bfloat16 if half else torch.float32
-    for kind in range(5):
+    for kind in range(6):
         x = torch.zeros((2, 6, V), dtype=dtype, device="cuda")
         scores = torch.full((2, 6), -2.0, device="cuda")
         if kind == 1:
@@ -90,6 +90,9 @@ def test_ties_go_to_the_lowest_place(V, half):
             scores[:, 4] = -1.0
         elif kind == 4:  # a few values only
             x = torch.randint(0, 3, x.shape, generator=torch.Generator(device="cuda").manual_seed(V), device="cuda").to(dtype)
+        elif kind == 5:  # zeros of both signs are equal
+            x[:, :, 1::2] = -0.0
+            x[:, ::2, :V // 2] = -0.0
         _check(x, scores, None, -1, _select(x, scores))
 
 
