@@ -9,10 +9,10 @@
 // one pass; a second kernel joins a group's slices and ranks its candidates in
 // 64 bits, where alone different rows meet.
 //
-// A slice's best: a CTA's threads form 32 parts; every logit at or above the
-// `beams`-th largest of the parts' maxima is a candidate. At least `beams` logits
-// are, so the best are among them; for unordered logits hardly more than that
-// are. Each counts how many of them are better. Equal logits in numbers beyond
+// A slice's best: a CTA's threads form P >= `beams` parts (8, 16 or 32); every logit
+// at or above the smallest of the parts' maxima is a candidate. That is one a part
+// at least, so the best `beams` are among them, and P ln P or so of unordered
+// logits. Each counts how many of them are better. Equal logits in numbers beyond
 // the list are taken one round of the whole CTA each.
 #include <cuda_fp16.h>
 
@@ -50,6 +50,29 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 in one register pair, and the paired instructions.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(f2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // 16 bytes of logits: 4 fp32, or 8 bf16 that stay packed.
 template <bool HALF>
 struct Run {
@@ -78,8 +101,10 @@ template <bool HALF>
 __global__ void __launch_bounds__(kThreads, HALF ? 5 : 4) slice_kernel(const __grid_constant__ Args A) {
   constexpr int C = Run<HALF>::C, RUNS = kPer / C, B = HALF ? 2 : 4;
   __shared__ float s_max[kParts], s_red[kWarps], s_sum[kWarps];
+  __shared__ uint4 s_run[kList / C];
+  __shared__ int s_run_at[kList / C], s_runs, s_n, s_pick[kWarps];
   __shared__ float s_val[kList];
-  __shared__ int s_at[kList], s_n, s_pick[kWarps];
+  __shared__ int s_at[kList];
   griddep_wait();
   griddep_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = blockIdx.x;
@@ -96,20 +121,17 @@ __global__ void __launch_bounds__(kThreads, HALF ? 5 : 4) slice_kernel(const __g
     const int i = i0 + C * (k * kThreads + tid);
     if (aligned && i + C <= i1) {
       v[k].w = __ldcs(reinterpret_cast<const uint4 *>(p + (long long)i * B));
-    } else if (HALF) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t x = i + j < i1 ? *reinterpret_cast<const unsigned short *>(p + (long long)(i + j) * 2) : 0xff80u;
-        if (j & 1) w[j / 2] |= x << 16;
-        else w[j / 2] = x;
-      }
-      v[k].w = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = i + j < i1 ? *reinterpret_cast<const uint32_t *>(p + (long long)(i + j) * 4) : 0xff800000u;
+      for (int j = 0; j < C; ++j) {
+        if constexpr (HALF) {
+          const uint32_t x = i + j < i1 ? *reinterpret_cast<const unsigned short *>(p + (long long)(i + j) * 2) : 0xff80u;
+          w[j / 2] = j & 1 ? w[j / 2] | x << 16 : x;
+        } else {
+          w[j] = i + j < i1 ? *reinterpret_cast<const uint32_t *>(p + (long long)(i + j) * 4) : 0xff800000u;
+        }
+      }
       v[k].w = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
@@ -120,50 +142,52 @@ __global__ void __launch_bounds__(kThreads, HALF ? 5 : 4) slice_kernel(const __g
     most[k] = v[k].top();
     top = fmaxf(top, most[k]);
   }
-  if (tid == 0) s_n = 0;
   float part = top;
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) part = fmaxf(part, __shfl_xor_sync(0xffffffffu, part, o));
   if (tid % kLanes == 0) s_max[tid / kLanes] = part;
+  if (tid == 0) s_n = s_runs = 0;
   __syncthreads();
   float m = s_max[lane];
-  {  // the part whose maximum has beams - 1 better ones; every warp finds it
-    static_assert(kParts == 32, "a part to a lane");
-    const float x = m;
-    int rank = 0;
+  static_assert(kParts == 32, "a part to a lane");
+  float cut = m;  // every warp finds it: the smallest maximum of 8, 16 or 32 parts
+  if (A.beams <= 16) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, 1));
+  if (A.beams <= 8) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, 2));
 #pragma unroll
-    for (int j = 0; j < kParts; ++j) rank += better(__shfl_sync(0xffffffffu, x, j), j, x, lane);
-    part = __shfl_sync(0xffffffffu, x, __ffs(__ballot_sync(0xffffffffu, rank == A.beams - 1)) - 1);
+  for (int o = 1; o < 32; o <<= 1) cut = fminf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
+  if (cut == -INFINITY) {  // some parts hold nothing: the maximum that beams - 1 others of the 32 exceed
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < kParts; ++j) rank += better(__shfl_sync(0xffffffffu, m, j), j, m, lane);
+    cut = __shfl_sync(0xffffffffu, m, __ffs(__ballot_sync(0xffffffffu, rank == A.beams - 1)) - 1);
   }
-  const float cut = part;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = m == -INFINITY ? 0.0f : m;
-  // ---- sum of exponentials, candidates
+  // ---- the runs that hold candidates (few do), the sum of exponentials
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k)
+    if (most[k] >= cut && most[k] > -INFINITY) {
+      const int n = atomicAdd(&s_runs, 1);
+      if (n < kList / C) {
+        s_run[n] = v[k].w;
+        s_run_at[n] = i0 + C * (k * kThreads + tid);
+      }
+    }
   // 2^(v log2(e) + shift): what the shift's rounding loses is the same for all and put right in the sum
   constexpr float log2e = 1.4426950408889634f;
   const float shift = __fmul_rn(-ref, log2e), lost = fmaf(-ref, log2e, -shift);
-  float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const f2 slope = pair(log2e, log2e), shifts = pair(shift, shift);
+  f2 sums[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
   for (int k = 0; k < RUNS; ++k)
 #pragma unroll
-    for (int j = 0; j < C; ++j) sums[j & 3] += ex2(fmaf(v[k].at(j), log2e, shift));
-#pragma unroll
-  for (int k = 0; k < RUNS; ++k)
-    if (most[k] >= cut) {  // few are
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const float x = v[k].at(j);
-        if (x >= cut && x > -INFINITY) {
-          const int n = atomicAdd(&s_n, 1);
-          if (n < kList) {
-            s_val[n] = x;
-            s_at[n] = i0 + C * (k * kThreads + tid) + j;
-          }
-        }
-      }
+    for (int j = 0; j < C; j += 2) {
+      const float2 x = halves(fma2(pair(v[k].at(j), v[k].at(j + 1)), slope, shifts));
+      sums[j / 2 & 1] = add2(sums[j / 2 & 1], pair(ex2(x.x), ex2(x.y)));
     }
-  float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  const float2 both = halves(add2(sums[0], sums[1]));
+  float sum = both.x + both.y;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
@@ -173,10 +197,23 @@ __global__ void __launch_bounds__(kThreads, HALF ? 5 : 4) slice_kernel(const __g
     for (int j = 1; j < kWarps; ++j) sum += s_sum[j];
     A.stats[at] = make_float2(m, sum * ex2(lost));
   }
-  const int n = s_n;
   float *best = A.best + at * A.beams;
   int32_t *best_at = A.best_at + at * A.beams;
-  if (n <= kList) {  // each candidate's rank among them
+  const int listed = s_runs;
+  if (listed <= kList / C) {  // each candidate's rank among them
+    for (int i = tid; i < listed * C; i += kThreads) {
+      const Run<HALF> r = {s_run[i / C]};
+      float x = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < C; ++j) x = i % C == j ? r.at(j) : x;
+      if (x >= cut && x > -INFINITY) {
+        const int n = atomicAdd(&s_n, 1);
+        s_val[n] = x;
+        s_at[n] = s_run_at[i / C] + i % C;
+      }
+    }
+    __syncthreads();
+    const int n = s_n;
     for (int i = tid; i < n; i += kThreads) {
       const float x = s_val[i];
       const int ix = s_at[i];
@@ -238,6 +275,27 @@ __global__ void __launch_bounds__(kThreads, HALF ? 5 : 4) slice_kernel(const __g
   }
 }
 
+// log(x) of a float x >= 1 as a sum of two floats, to about 2^-40. x = 2^e m with m in
+// [2/3, 4/3): log m = 2 artanh(t), t = (m - 1) / (m + 1), |t| <= 1/5: 2 t is kept in two
+// floats, the rest of the series, below 2 t / 70, in one.
+__device__ __forceinline__ double log_of(float x) {
+  const int e = (int)((__float_as_uint(x) - 0x3f2aaaabu) >> 23);
+  const float m = __uint_as_float(__float_as_uint(x) - ((uint32_t)e << 23));
+  const float a = __fsub_rn(m, 1.0f);            // exact
+  const float b = __fadd_rn(m, 1.0f), bl = __fsub_rn(m, __fsub_rn(b, 1.0f));  // m + 1 = b + bl
+  const float t = __fdiv_rn(a, b);
+  const float tl = __fdiv_rn(__fsub_rn(fmaf(-t, b, a), __fmul_rn(t, bl)), b);  // what the quotient is short of
+  const float s = __fmul_rn(t, t);
+  float p = 2.0f / 13;
+  p = fmaf(p, s, 2.0f / 11);
+  p = fmaf(p, s, 2.0f / 9);
+  p = fmaf(p, s, 2.0f / 7);
+  p = fmaf(p, s, 2.0f / 5);
+  p = fmaf(p, s, 2.0f / 3);
+  const float rest = fmaf(__fmul_rn(p, s), t, 2.0f * tl);
+  return (double)e * 0.6931471805599453 + ((double)(2.0f * t) + (double)rest);
+}
+
 // A score as a whole number of the same order; 0 is below every candidate's.
 __device__ __forceinline__ unsigned long long key_of(double x) {
   const long long b = __double_as_longlong(x + 0.0);  // -0 is 0
@@ -259,8 +317,8 @@ struct Place {  // of a row's list
 // Group blockIdx.x. A warp joins a row's slices: their lists are in order, so the
 // row's best is always one of 32 heads (lists of higher tokens in higher lanes:
 // equal logits go to the lowest). Then the rows' lists meet, in 64 bits: the
-// fp64 units do two operations a cycle per SM, so that only the beams^2 scores
-// and one logarithm a beam are formed there. Candidates below the worst of the
+// fp64 units do two operations a cycle per SM, so that only the beams^2 scores are
+// formed there. Candidates below the worst of the
 // rows' best are no one's, the others count how many are better.
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args A) {
   extern __shared__ Place s_lists[];  // [kWarps][32][beams]: lane 0's is what has been joined so far
@@ -268,8 +326,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   __shared__ unsigned long long s_key[kMaxBeams * kMaxBeams];
   __shared__ int s_at[kMaxBeams * kMaxBeams], s_n;
   __shared__ double s_add[kMaxBeams];  // score - lse of a beam
-  __shared__ float s_m[kMaxBeams], s_sum[kMaxBeams];
-  __shared__ unsigned long long s_best[kMaxBeams];
   __shared__ uint8_t s_done[kMaxBeams];
   griddep_wait();
   griddep_trigger();
@@ -280,13 +336,22 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     const long long row = row0 + w;
     const float score = A.scores[row];
     const bool over = A.done && A.done[row];
-    if (lane == 0) s_done[w] = over;
+    if (lane == 0) {
+      s_done[w] = over;
+      s_add[w] = over ? (double)score : -INFINITY;
+    }
     if (over || !(score > -INFINITY)) {
       for (int i = lane; i < W; i += 32) s_row[w * W + i] = {-INFINITY, -1};
       continue;
     }
     const float2 *st = A.stats + row * S;
     float m = -INFINITY, sum = 0.0f;
+    const int n0 = min(31, S) * W;  // the first slices' lists
+    const float *bx0 = A.best + row * S * W;
+    const int32_t *bi0 = A.best_at + row * S * W;
+    for (int i = lane; i < W; i += 32) mine[i] = {-INFINITY, -1};
+#pragma unroll 4
+    for (int i = lane; i < n0; i += 32) mine[W + i] = {bx0[i], bi0[i]};
     for (int i = lane; i < S; i += 32) m = fmaxf(m, st[i].x);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -296,16 +361,16 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      s_m[w] = m;
-      s_sum[w] = sum;
-    }
+    // a sum that is not finite, or of nothing, makes every candidate NaN; else it is at least 1
+    if (lane == 0) s_add[w] = sum >= 0.75f && sum < INFINITY ? (double)score - ((double)m + log_of(sum)) : (double)NAN;
     for (int s0 = 0; s0 < S; s0 += 31) {  // 31 slices at a time
       const int n = min(31, S - s0) * W;
-      const float *bx = A.best + (row * S + s0) * W;
-      const int32_t *bi = A.best_at + (row * S + s0) * W;
-      for (int i = lane; i < n; i += 32) mine[W + i] = {bx[i], bi[i]};
-      for (int i = lane; i < W; i += 32) mine[i] = s0 == 0 ? Place{-INFINITY, -1} : s_row[w * W + i];
+      if (s0 > 0) {
+        const float *bx = bx0 + s0 * W;
+        const int32_t *bi = bi0 + s0 * W;
+        for (int i = lane; i < n; i += 32) mine[W + i] = {bx[i], bi[i]};
+        for (int i = lane; i < W; i += 32) mine[i] = s_row[w * W + i];
+      }
       __syncwarp();
       const bool list = lane == 0 || (lane - 1) * W < n;
       int at = 0;
@@ -324,12 +389,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   }
   if (tid == 0) s_n = 0;
   __syncthreads();
-  if (tid < W) {
-    const float score = A.scores[row0 + tid];
-    s_add[tid] = s_done[tid] ? (double)score
-                 : score > -INFINITY ? (double)score - ((double)s_m[tid] + log((double)s_sum[tid])) : -INFINITY;
-  }
-  __syncthreads();
   auto key_at = [&](int w, int r) -> unsigned long long {  // 0: no candidate
     double x = s_add[w];
     if (s_done[w]) {
@@ -340,10 +399,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     }
     return x > -INFINITY ? key_of(x) : 0;  // not -inf, not NaN
   };
-  if (tid < W) s_best[tid] = key_at(tid, 0);
-  __syncthreads();
-  unsigned long long cut = s_best[0];
-  for (int w = 1; w < W; ++w) cut = min(cut, s_best[w]);
+  unsigned long long cut = lane < W ? key_at(lane, 0) : ~0ull;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) cut = min(cut, __shfl_xor_sync(0xffffffffu, cut, o));
   for (int c = tid; c < W * W; c += kThreads) {
     const int w = c / W, r = c - w * W;
     const unsigned long long k = key_at(w, r);
