@@ -4,16 +4,18 @@
 //   the best `beams` of a group, ties to the lowest (w, x)
 //
 // Memory-bound: each logit is read once. Within a row candidates rank as their
-// logits do, so a slice of a row (at most 8192 logits, kept in registers)
-// yields its maximum, its sum of exponentials and its best `beams` logits in
-// one pass; a second kernel joins a group's slices and ranks its candidates in
-// 64 bits, where alone different rows meet.
+// logits do, so a slice of a row yields its maximum, its sum of exponentials (each
+// thread's own, against its own maximum so far) and its best `beams` logits in one
+// pass; a second kernel joins a group's slices and ranks its candidates in 64
+// bits, where alone different rows meet. (As the work of a group's last CTA the join
+// took 1 us longer: 1 us for the CTAs to agree, and its code is new to that SM.)
 //
-// A slice's best: a CTA's threads form P >= `beams` parts (8, 16 or 32); every logit
-// at or above the smallest of the parts' maxima is a candidate. That is one a part
-// at least, so the best `beams` are among them, and P ln P or so of unordered
-// logits. Each counts how many of them are better. Equal logits in numbers beyond
-// the list are taken one round of the whole CTA each.
+// A slice's best: a CTA's threads form P >= `beams` parts (8, 16 or 32). At least
+// `beams` logits reach the smallest of the parts' maxima over the first runs, so
+// only runs that reach it are listed. At the end the parts' maxima over the whole
+// slice give a tighter cut, which P ln P or so of unordered logits reach: each
+// counts how many of them are better. Equal logits in numbers beyond the list are
+// taken one after the other.
 #include <cuda_fp16.h>
 
 #include "gdn_check.h"
@@ -22,11 +24,11 @@ namespace gdn {
 namespace beam {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPer = 32;                  // logits a thread holds
-constexpr int kSlice = kThreads * kPer;   // logits of the largest slice
+constexpr int kRuns = 4;  // 16 bytes of logits each that a thread works on at a time
+constexpr int kLeast = 4096;  // logits that are worth a CTA
 constexpr int kMaxBeams = 32;
 constexpr int kParts = 32, kLanes = kThreads / kParts;
-constexpr int kList = 1024;
+constexpr int kList = 512;
 
 struct Args {
   int groups, beams, V, eos, slices;
@@ -62,9 +64,9 @@ __device__ __forceinline__ float2 halves(f2 x) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
   return r;
 }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ f2 add2(f2 a, f2 b) {
@@ -96,185 +98,6 @@ struct Run {
   }
 };
 
-// Slice blockIdx.x of row blockIdx.y: run k of a thread is run k kThreads + tid of the slice.
-template <bool HALF>
-__global__ void __launch_bounds__(kThreads, HALF ? 5 : 4) slice_kernel(const __grid_constant__ Args A) {
-  constexpr int C = Run<HALF>::C, RUNS = kPer / C, B = HALF ? 2 : 4;
-  __shared__ float s_max[kParts], s_red[kWarps], s_sum[kWarps];
-  __shared__ uint4 s_run[kList / C];
-  __shared__ int s_run_at[kList / C], s_runs, s_n, s_pick[kWarps];
-  __shared__ float s_val[kList];
-  __shared__ int s_at[kList];
-  griddep_wait();
-  griddep_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = blockIdx.x;
-  const long long row = blockIdx.y;
-  const float score = A.scores[row];
-  if (!(score > -INFINITY) || (A.done && A.done[row])) return;  // its logits give no candidates
-  const long long runs = (A.V + C - 1) / C;  // 16 bytes each, dealt out evenly
-  const int i0 = C * (int)(runs * slice / A.slices), i1 = min(A.V, C * (int)(runs * (slice + 1) / A.slices));
-  const char *p = static_cast<const char *>(A.logits) + row * A.stride * B;
-  const bool aligned = (reinterpret_cast<uintptr_t>(p) & 15) == 0;  // and so is every run then
-  Run<HALF> v[RUNS];
-#pragma unroll
-  for (int k = 0; k < RUNS; ++k) {
-    const int i = i0 + C * (k * kThreads + tid);
-    if (aligned && i + C <= i1) {
-      v[k].w = __ldcs(reinterpret_cast<const uint4 *>(p + (long long)i * B));
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-        if constexpr (HALF) {
-          const uint32_t x = i + j < i1 ? *reinterpret_cast<const unsigned short *>(p + (long long)(i + j) * 2) : 0xff80u;
-          w[j / 2] = j & 1 ? w[j / 2] | x << 16 : x;
-        } else {
-          w[j] = i + j < i1 ? *reinterpret_cast<const uint32_t *>(p + (long long)(i + j) * 4) : 0xff800000u;
-        }
-      }
-      v[k].w = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  // ---- the slice's maximum and the parts' maxima (a NaN is no maximum, but reaches the sum)
-  float most[RUNS], top = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < RUNS; ++k) {
-    most[k] = v[k].top();
-    top = fmaxf(top, most[k]);
-  }
-  float part = top;
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) part = fmaxf(part, __shfl_xor_sync(0xffffffffu, part, o));
-  if (tid % kLanes == 0) s_max[tid / kLanes] = part;
-  if (tid == 0) s_n = s_runs = 0;
-  __syncthreads();
-  float m = s_max[lane];
-  static_assert(kParts == 32, "a part to a lane");
-  float cut = m;  // every warp finds it: the smallest maximum of 8, 16 or 32 parts
-  if (A.beams <= 16) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, 1));
-  if (A.beams <= 8) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, 2));
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) cut = fminf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
-  if (cut == -INFINITY) {  // some parts hold nothing: the maximum that beams - 1 others of the 32 exceed
-    int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < kParts; ++j) rank += better(__shfl_sync(0xffffffffu, m, j), j, m, lane);
-    cut = __shfl_sync(0xffffffffu, m, __ffs(__ballot_sync(0xffffffffu, rank == A.beams - 1)) - 1);
-  }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.0f : m;
-  // ---- the runs that hold candidates (few do), the sum of exponentials
-#pragma unroll
-  for (int k = 0; k < RUNS; ++k)
-    if (most[k] >= cut && most[k] > -INFINITY) {
-      const int n = atomicAdd(&s_runs, 1);
-      if (n < kList / C) {
-        s_run[n] = v[k].w;
-        s_run_at[n] = i0 + C * (k * kThreads + tid);
-      }
-    }
-  // 2^(v log2(e) + shift): what the shift's rounding loses is the same for all and put right in the sum
-  constexpr float log2e = 1.4426950408889634f;
-  const float shift = __fmul_rn(-ref, log2e), lost = fmaf(-ref, log2e, -shift);
-  const f2 slope = pair(log2e, log2e), shifts = pair(shift, shift);
-  f2 sums[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
-#pragma unroll
-  for (int k = 0; k < RUNS; ++k)
-#pragma unroll
-    for (int j = 0; j < C; j += 2) {
-      const float2 x = halves(fma2(pair(v[k].at(j), v[k].at(j + 1)), slope, shifts));
-      sums[j / 2 & 1] = add2(sums[j / 2 & 1], pair(ex2(x.x), ex2(x.y)));
-    }
-  const float2 both = halves(add2(sums[0], sums[1]));
-  float sum = both.x + both.y;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  const long long at = row * A.slices + slice;
-  if (tid == 0) {
-    for (int j = 1; j < kWarps; ++j) sum += s_sum[j];
-    A.stats[at] = make_float2(m, sum * ex2(lost));
-  }
-  float *best = A.best + at * A.beams;
-  int32_t *best_at = A.best_at + at * A.beams;
-  const int listed = s_runs;
-  if (listed <= kList / C) {  // each candidate's rank among them
-    for (int i = tid; i < listed * C; i += kThreads) {
-      const Run<HALF> r = {s_run[i / C]};
-      float x = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < C; ++j) x = i % C == j ? r.at(j) : x;
-      if (x >= cut && x > -INFINITY) {
-        const int n = atomicAdd(&s_n, 1);
-        s_val[n] = x;
-        s_at[n] = s_run_at[i / C] + i % C;
-      }
-    }
-    __syncthreads();
-    const int n = s_n;
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = s_val[i];
-      const int ix = s_at[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += better(s_val[j], s_at[j], x, ix);
-      if (rank < A.beams) {
-        best[rank] = x;
-        best_at[rank] = ix;
-      }
-    }
-    for (int i = n + tid; i < A.beams; i += kThreads) {
-      best[i] = -INFINITY;
-      best_at[i] = -1;
-    }
-  } else {  // more candidates than the list holds: one after the other, the best behind the last one taken
-    float last = INFINITY;
-    int last_at = -1;
-    for (int r = 0; r < A.beams; ++r) {
-      float x = -INFINITY;
-      int ix = 0x7fffffff;
-#pragma unroll
-      for (int k = 0; k < RUNS; ++k)
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-          const int ij = i0 + C * (k * kThreads + tid) + j;
-          const float y = v[k].at(j);
-          if (y > -INFINITY && better(last, last_at, y, ij) && better(y, ij, x, ix)) {
-            x = y;
-            ix = ij;
-          }
-        }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_xor_sync(0xffffffffu, x, o);
-        const int iy = __shfl_xor_sync(0xffffffffu, ix, o);
-        if (better(y, iy, x, ix)) {
-          x = y;
-          ix = iy;
-        }
-      }
-      __syncthreads();
-      if (lane == 0) {
-        s_red[warp] = x;
-        s_pick[warp] = ix;
-      }
-      __syncthreads();
-      for (int j = 0; j < kWarps; ++j)
-        if (better(s_red[j], s_pick[j], x, ix)) {
-          x = s_red[j];
-          ix = s_pick[j];
-        }
-      last = x;
-      last_at = ix;
-      if (tid == 0) {
-        best[r] = x;
-        best_at[r] = x > -INFINITY ? ix : -1;
-      }
-    }
-  }
-}
-
 // log(x) of a float x >= 1 as a sum of two floats, to about 2^-40. x = 2^e m with m in
 // [2/3, 4/3): log m = 2 artanh(t), t = (m - 1) / (m + 1), |t| <= 1/5: 2 t is kept in two
 // floats, the rest of the series, below 2 t / 70, in one.
@@ -304,132 +127,397 @@ __device__ __forceinline__ unsigned long long key_of(double x) {
 __device__ __forceinline__ double score_of(unsigned long long k) {
   return __longlong_as_double((long long)(k >> 63 ? k & 0x7fffffffffffffffull : ~k));
 }
-__device__ __forceinline__ uint32_t key_of(float x) {  // 0 for -inf; x is a logit that is a number
-  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 is 0
-  return x == -INFINITY ? 0 : b & 0x80000000u ? ~b : b | 0x80000000u;
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_min(float x) {
+  float y;
+  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float part_max(float x) {  // over the lanes of a part
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
 }
 
-struct Place {  // of a row's list
-  float x;
-  int at;
-};
+// A number that `beams` of the parts' maxima (m: one to a lane) reach, by every warp: the smallest of 8, 16 or 32
+// parts, or, where some parts hold nothing, the one that beams - 1 others exceed.
+__device__ __forceinline__ float cut_of(float m, int beams, int lane) {
+  static_assert(kParts == 32, "a part to a lane");
+  float cut = m;
+  if (beams <= 16) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, 1));
+  if (beams <= 8) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, 2));
+  cut = warp_min(cut);
+  if (cut == -INFINITY) {
+    int rank = 0;
+#pragma unroll 1
+    for (int j = 0; j < kParts; ++j) rank += better(__shfl_sync(0xffffffffu, m, j), j, m, lane);
+    cut = __shfl_sync(0xffffffffu, m, __ffs(__ballot_sync(0xffffffffu, rank == beams - 1)) - 1);
+  }
+  return cut;
+}
 
-// Group blockIdx.x. A warp joins a row's slices: their lists are in order, so the
-// row's best is always one of 32 heads (lists of higher tokens in higher lanes:
-// equal logits go to the lowest). Then the rows' lists meet, in 64 bits: the
-// fp64 units do two operations a cycle per SM, so that only the beams^2 scores are
-// formed there. Candidates below the worst of the
-// rows' best are no one's, the others count how many are better.
+constexpr int kFinal = 1024;  // candidates that are ranked in 64 bits
+
+// Group blockIdx.x. A warp sums up a row's slices; then all
+// candidates of the rows' slices are compared in fp32 against the smallest maximum
+// of as many parts of the threads as there are beams, with what fp32 may be off by:
+// what remains, a few more than `beams`, counts in 64 bits how many are better.
+// (The fp64 units do two operations a cycle per SM.) Where more remain than the
+// list holds (rows of equal logits) they are taken one after the other.
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args A) {
-  extern __shared__ Place s_lists[];  // [kWarps][32][beams]: lane 0's is what has been joined so far
-  __shared__ Place s_row[kMaxBeams * kMaxBeams];
-  __shared__ unsigned long long s_key[kMaxBeams * kMaxBeams];
-  __shared__ int s_at[kMaxBeams * kMaxBeams], s_n;
-  __shared__ double s_add[kMaxBeams];  // score - lse of a beam
+  __shared__ unsigned long long s_key[kFinal];
+  __shared__ int s_at[kFinal], s_n, s_pick[kWarps];
+  __shared__ double s_add[kMaxBeams];  // score - lse
+  __shared__ unsigned long long s_top[kWarps];
+  __shared__ float s_max[32];
   __shared__ uint8_t s_done[kMaxBeams];
   griddep_wait();
   griddep_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = A.beams, S = A.slices;
   const long long row0 = (long long)blockIdx.x * W;
-  Place *mine = s_lists + warp * 32 * W;
+  const int each = S * W, N = W * each;  // candidates of a row, of all
+  const float *best = A.best + row0 * each;
+  const int32_t *best_at = A.best_at + row0 * each;
+  const int c0 = min(tid, N - 1);
+  const float x0 = __ldcg(best + c0);  // in flight meanwhile
+  const int at0 = __ldcg(best_at + c0);
+  if (tid == 0) s_n = 0;
+#pragma unroll 1
   for (int w = warp; w < W; w += kWarps) {
     const long long row = row0 + w;
+    const float2 *st = A.stats + row * S;
     const float score = A.scores[row];
     const bool over = A.done && A.done[row];
-    if (lane == 0) {
-      s_done[w] = over;
-      s_add[w] = over ? (double)score : -INFINITY;
+    float2 x = lane < S ? __ldcg(st + lane) : make_float2(-INFINITY, 0.0f);
+    for (int i = lane + 32; i < S; i += 32) {
+      const float2 y = __ldcg(st + i);
+      const float m = fmaxf(x.x, y.x), r = m == -INFINITY ? 0.0f : m;
+      x = make_float2(m, x.y * ex2((x.x - r) * 1.4426950408889634f) + y.y * ex2((y.x - r) * 1.4426950408889634f));
     }
-    if (over || !(score > -INFINITY)) {
-      for (int i = lane; i < W; i += 32) s_row[w * W + i] = {-INFINITY, -1};
-      continue;
-    }
-    const float2 *st = A.stats + row * S;
-    float m = -INFINITY, sum = 0.0f;
-    const int n0 = min(31, S) * W;  // the first slices' lists
-    const float *bx0 = A.best + row * S * W;
-    const int32_t *bi0 = A.best_at + row * S * W;
-    for (int i = lane; i < W; i += 32) mine[i] = {-INFINITY, -1};
-#pragma unroll 4
-    for (int i = lane; i < n0; i += 32) mine[W + i] = {bx0[i], bi0[i]};
-    for (int i = lane; i < S; i += 32) m = fmaxf(m, st[i].x);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int i = lane; i < S; i += 32) {
-      const float2 x = st[i];
-      sum += x.y * ex2((x.x - m) * 1.4426950408889634f);
-    }
+    const float m = warp_max(x.x);
+    float sum = x.y * ex2((x.x - m) * 1.4426950408889634f);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    // a sum that is not finite, or of nothing, makes every candidate NaN; else it is at least 1
-    if (lane == 0) s_add[w] = sum >= 0.75f && sum < INFINITY ? (double)score - ((double)m + log_of(sum)) : (double)NAN;
-    for (int s0 = 0; s0 < S; s0 += 31) {  // 31 slices at a time
-      const int n = min(31, S - s0) * W;
-      if (s0 > 0) {
-        const float *bx = bx0 + s0 * W;
-        const int32_t *bi = bi0 + s0 * W;
-        for (int i = lane; i < n; i += 32) mine[W + i] = {bx[i], bi[i]};
-        for (int i = lane; i < W; i += 32) mine[i] = s_row[w * W + i];
-      }
-      __syncwarp();
-      const bool list = lane == 0 || (lane - 1) * W < n;
-      int at = 0;
-      Place head = list ? mine[lane * W] : Place{-INFINITY, -1};
-      for (int r = 0; r < W; ++r) {
-        const uint32_t key = key_of(head.x), top = __reduce_max_sync(0xffffffffu, key);
-        const int from = __ffs(__ballot_sync(0xffffffffu, key == top)) - 1;
-        if (lane == from) {
-          s_row[w * W + r] = top ? head : Place{-INFINITY, -1};
-          ++at;
-          head = top && at < W ? mine[lane * W + at] : Place{-INFINITY, -1};
-        }
-      }
-      __syncwarp();
+    if (lane == 0) {
+      s_done[w] = over;
+      // a sum that is not finite, or of nothing, makes every candidate NaN; else it is at least 1
+      s_add[w] = over ? (double)score
+                 : score > -INFINITY && sum >= 0.75f && sum < INFINITY ? (double)score - ((double)m + log_of(sum)) : (double)NAN;
     }
   }
-  if (tid == 0) s_n = 0;
   __syncthreads();
-  auto key_at = [&](int w, int r) -> unsigned long long {  // 0: no candidate
-    double x = s_add[w];
-    if (s_done[w]) {
-      if (r > 0) return 0;
-    } else {
-      if (s_row[w * W + r].at < 0) return 0;
-      x += (double)s_row[w * W + r].x;
-    }
-    return x > -INFINITY ? key_of(x) : 0;  // not -inf, not NaN
+  // A candidate: c < N is place c % W of slice c / W % S of beam c / (W S), and stands for a finished beam if it is its
+  // first. false: it is none.
+  auto candidate = [&](int c, float &x, int t, int &w, int &at) {
+    w = c / each;
+    if (s_done[w]) x = 0.0f;
+    at = (w << 24) + (s_done[w] ? max(A.eos, 0) : t);
+    return s_done[w] ? c == w * each : t >= 0;
   };
-  unsigned long long cut = lane < W ? key_at(lane, 0) : ~0ull;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) cut = min(cut, __shfl_xor_sync(0xffffffffu, cut, o));
-  for (int c = tid; c < W * W; c += kThreads) {
-    const int w = c / W, r = c - w * W;
-    const unsigned long long k = key_at(w, r);
-    if (k > 0 && k >= cut) {
-      const int i = atomicAdd(&s_n, 1);
+  auto exact = [&](int w, float x) {
+    const double y = s_add[w] + (double)x;
+    return y > -INFINITY ? key_of(y) : 0ull;
+  };
+  auto close = [&](int w, float x, float side) {  // the score less (side -1) or more (1) than fp32 may be off by
+    const float a = (float)s_add[w], y = a + x + side * 2.4e-7f * (fabsf(a) + fabsf(x));  // 2^-22
+    return y > -INFINITY ? y : -INFINITY;  // NaN: none
+  };
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = tid; c < N; c += kThreads) {
+    float x = c == tid ? x0 : __ldcg(best + c);
+    int w, at;
+    if (candidate(c, x, c == tid ? at0 : __ldcg(best_at + c), w, at)) top = fmaxf(top, close(w, x, -1.0f));
+  }
+  top = part_max(top);
+  if (tid % kLanes == 0) s_max[tid / kLanes] = top;
+  __syncthreads();
+  const float cut = cut_of(s_max[lane], W, lane);
+#pragma unroll 1
+  for (int c = tid; c < N; c += kThreads) {
+    float x = c == tid ? x0 : __ldcg(best + c);
+    int w, at;
+    if (!candidate(c, x, c == tid ? at0 : __ldcg(best_at + c), w, at)) continue;
+    if (close(w, x, 1.0f) < cut) continue;
+    const unsigned long long k = exact(w, x);
+    if (k == 0) continue;
+    const int i = atomicAdd(&s_n, 1);
+    if (i < kFinal) {
       s_key[i] = k;
-      s_at[i] = (w << 24) + (s_done[w] ? max(A.eos, 0) : s_row[c].at);
+      s_at[i] = at;
     }
   }
   __syncthreads();
   const int n = s_n;
-  for (int i = tid; i < n; i += kThreads) {
-    const unsigned long long k = s_key[i];
-    const int at = s_at[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += s_key[j] > k || (s_key[j] == k && s_at[j] < at);
-    if (rank >= W) continue;
+  auto put = [&](int place, unsigned long long k, int at) {
     const int w = at >> 24, t = s_done[w] ? A.eos : at & 0xffffff;
-    A.parent[row0 + rank] = (int)(row0 + w);
-    A.token[row0 + rank] = t;
-    A.new_scores[row0 + rank] = (float)score_of(k);
-    if (A.new_done) A.new_done[row0 + rank] = s_done[w] || t == A.eos;
+    A.parent[row0 + place] = (int)(row0 + w);
+    A.token[row0 + place] = t;
+    A.new_scores[row0 + place] = (float)score_of(k);
+    if (A.new_done) A.new_done[row0 + place] = s_done[w] || t == A.eos;
+  };
+  if (n <= kFinal) {
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) {
+      const unsigned long long k = s_key[i];
+      const int at = s_at[i];
+      int rank = 0;
+#pragma unroll 2
+      for (int j = 0; j < n; ++j) rank += s_key[j] > k || (s_key[j] == k && s_at[j] < at);
+      if (rank < W) put(rank, k, at);
+    }
+  } else {
+    unsigned long long last = ~0ull;  // the candidate taken last
+    int last_at = -1;
+#pragma unroll 1
+    for (int r = 0; r < W; ++r) {
+      unsigned long long key = 0;
+      int at = 0x7fffffff;
+#pragma unroll 1
+      for (int c = tid; c < N; c += kThreads) {
+        float x = __ldcg(best + c);
+        int w, i;
+        if (!candidate(c, x, __ldcg(best_at + c), w, i)) continue;
+        const unsigned long long k = exact(w, x);
+        if (k > 0 && (k < last || (k == last && i > last_at)) && (k > key || (k == key && i < at))) {
+          key = k;
+          at = i;
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
+        const int i = __shfl_xor_sync(0xffffffffu, at, o);
+        if (k > key || (k == key && i < at)) {
+          key = k;
+          at = i;
+        }
+      }
+      __syncthreads();
+      if (lane == 0) {
+        s_top[warp] = key;
+        s_pick[warp] = at;
+      }
+      __syncthreads();
+      for (int j = 0; j < kWarps; ++j)
+        if (s_top[j] > key || (s_top[j] == key && s_pick[j] < at)) {
+          key = s_top[j];
+          at = s_pick[j];
+        }
+      last = key;  // n > kFinal >= W: there is one
+      last_at = at;
+      if (tid == 0) put(r, key, at);
+    }
   }
   for (int r = n + tid; r < W; r += kThreads) {  // places without a candidate
     A.parent[row0 + r] = (int)(row0 + r);
     A.token[row0 + r] = -1;
     A.new_scores[row0 + r] = -INFINITY;
     if (A.new_done) A.new_done[row0 + r] = 0;
+  }
+}
+
+// Slice blockIdx.x of row blockIdx.y, kRuns runs of a thread at a time, the next in
+// flight.
+template <bool HALF>
+__global__ void __launch_bounds__(kThreads, 4) slice_kernel(const __grid_constant__ Args A) {
+  constexpr int C = Run<HALF>::C, B = HALF ? 2 : 4, LIST = 512;
+  __shared__ float s_max[kParts], s_red[kWarps], s_sum[kWarps];
+  __shared__ uint4 s_run[LIST];  // the runs that may hold candidates, and where they begin
+  __shared__ int s_run_at[LIST], s_runs;
+  __shared__ float s_val[kList];  // the candidates
+  __shared__ int s_at[kList], s_n, s_pick[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = blockIdx.x;
+  if (tid == 0) s_runs = s_n = 0;
+  griddep_wait();
+  griddep_trigger();
+  const long long row = blockIdx.y;
+  const int all = (A.V + C - 1) / C;  // 16 bytes each, dealt out evenly
+  const int r0 = (int)((long long)all * slice / A.slices), r1 = (int)((long long)all * (slice + 1) / A.slices);
+  const char *p = static_cast<const char *>(A.logits) + row * A.stride * B;
+  const bool aligned = (reinterpret_cast<uintptr_t>(p) & 15) == 0;  // and so is every run then
+  auto fetch = [&](int r) {  // run r, -inf behind the row's end
+    Run<HALF> x;
+    if (aligned && r < r1 && (r + 1) * C <= A.V) {
+      x.w = __ldcs(reinterpret_cast<const uint4 *>(p) + r);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int i = r * C + j;
+        const bool in = r < r1 && i < A.V;
+        if constexpr (HALF) {
+          const uint32_t u = in ? *reinterpret_cast<const unsigned short *>(p + (long long)i * 2) : 0xff80u;
+          w[j / 2] = j & 1 ? w[j / 2] | u << 16 : u;
+        } else {
+          w[j] = in ? *reinterpret_cast<const uint32_t *>(p + (long long)i * 4) : 0xff800000u;
+        }
+      }
+      x.w = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return x;
+  };
+  Run<HALF> ahead[kRuns];
+  const float score = A.scores[row];
+  const bool over = A.done && A.done[row];
+  if (score > -INFINITY && !over) {  // else its logits give no candidates
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) ahead[k] = fetch(r0 + k * kThreads + tid);
+    constexpr float log2e = 1.4426950408889634f;
+    float m = -INFINITY, cut = -INFINITY;  // the thread's maximum so far; at least `beams` logits reach the cut
+    f2 sums = pair(0.0f, 0.0f);            // of exp(logit - m)
+    int turn = 0;
+    for (int rb = r0; rb < r1; rb += kRuns * kThreads, ++turn) {
+      Run<HALF> v[kRuns];
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k) {
+        v[k] = ahead[k];
+        if (rb + kRuns * kThreads < r1) ahead[k] = fetch(rb + (kRuns + k) * kThreads + tid);
+      }
+      float most[kRuns], top = m;  // a NaN is no maximum, but reaches the sum
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k) {
+        most[k] = v[k].top();
+        top = fmaxf(top, most[k]);
+      }
+      if ((turn & (turn + 1)) == 0 || cut == -INFINITY) {  // again each time that twice as much has been seen
+        const float part = part_max(top);
+        if (tid % kLanes == 0) s_max[tid / kLanes] = part;
+        __syncthreads();
+        cut = cut_of(s_max[lane], A.beams, lane);
+        __syncthreads();
+      }
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k)
+        if (most[k] >= cut && most[k] > -INFINITY) {  // few do
+          const int n = atomicAdd(&s_runs, 1);
+          if (n < LIST) {
+            s_run[n] = v[k].w;
+            s_run_at[n] = (rb + k * kThreads + tid) * C;
+          }
+        }
+      const float ref = top == -INFINITY ? 0.0f : top, fade = ex2((m - ref) * log2e);
+      m = top;
+      sums = mul2(sums, pair(fade, fade));
+      const f2 less = pair(-ref, -ref), slope = pair(log2e, log2e);
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k)
+#pragma unroll
+        for (int j = 0; j < C; j += 2) {
+          const float2 x = halves(mul2(add2(pair(v[k].at(j), v[k].at(j + 1)), less), slope));
+          sums = add2(sums, pair(ex2(x.x), ex2(x.y)));
+        }
+    }
+    // ---- the slice's maximum and sum; the cut of all its logits
+    const float part = part_max(m);
+    if (tid % kLanes == 0) s_max[tid / kLanes] = part;
+    __syncthreads();
+    const float far = s_max[lane], most = warp_max(far);
+    cut = cut_of(far, A.beams, lane);
+    const float2 both = halves(sums);
+    float sum = (both.x + both.y) * ex2((m - (most == -INFINITY ? 0.0f : most)) * log2e);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    const long long at = row * A.slices + slice;
+    if (tid == 0) {
+      for (int j = 1; j < kWarps; ++j) sum += s_sum[j];
+      A.stats[at] = make_float2(most, sum);
+    }
+    float *best = A.best + at * A.beams;
+    int32_t *best_at = A.best_at + at * A.beams;
+    const int listed = s_runs;
+    if (listed <= LIST) {  // the candidates
+#pragma unroll 1
+      for (int i = tid; i - lane < listed * C; i += kThreads) {
+        float x = -INFINITY;
+        if (i < listed * C) {
+          const Run<HALF> r = {s_run[i / C]};
+#pragma unroll
+          for (int j = 0; j < C; ++j) x = i % C == j ? r.at(j) : x;
+        }
+        const bool in = x >= cut && x > -INFINITY;
+        const uint32_t who = __ballot_sync(0xffffffffu, in);
+        if (who == 0) continue;
+        int k = 0;
+        if (lane == 0) k = atomicAdd(&s_n, __popc(who));
+        k = __shfl_sync(0xffffffffu, k, 0) + __popc(who & ((1u << lane) - 1));
+        if (in && k < kList) {
+          s_val[k] = x;
+          s_at[k] = s_run_at[i / C] + i % C;
+        }
+      }
+      __syncthreads();
+    }
+    const int n = listed <= LIST ? s_n : kList + 1;
+    if (n <= kList) {
+      for (int i = tid; i < n; i += kThreads) {  // each one's rank among them
+        const float x = s_val[i];
+        const int ix = s_at[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += better(s_val[j], s_at[j], x, ix);
+        if (rank < A.beams) {
+          best[rank] = x;
+          best_at[rank] = ix;
+        }
+      }
+      for (int i = n + tid; i < A.beams; i += kThreads) {
+        best[i] = -INFINITY;
+        best_at[i] = -1;
+      }
+    } else {  // more than the lists hold (equal logits): one after the other, the best behind the last one taken
+      float last = INFINITY;
+      int last_at = -1;
+#pragma unroll 1
+      for (int r = 0; r < A.beams; ++r) {
+        float x = -INFINITY;
+        int ix = 0x7fffffff;
+#pragma unroll 1
+        for (int k = r0 + tid; k < r1; k += kThreads) {
+          const Run<HALF> v = fetch(k);
+#pragma unroll
+          for (int j = 0; j < C; ++j) {
+            const float y = v.at(j);
+            if (y > -INFINITY && better(last, last_at, y, k * C + j) && better(y, k * C + j, x, ix)) {
+              x = y;
+              ix = k * C + j;
+            }
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_xor_sync(0xffffffffu, x, o);
+          const int iy = __shfl_xor_sync(0xffffffffu, ix, o);
+          if (better(y, iy, x, ix)) {
+            x = y;
+            ix = iy;
+          }
+        }
+        __syncthreads();
+        if (lane == 0) {
+          s_red[warp] = x;
+          s_pick[warp] = ix;
+        }
+        __syncthreads();
+        for (int j = 0; j < kWarps; ++j)
+          if (better(s_red[j], s_pick[j], x, ix)) {
+            x = s_red[j];
+            ix = s_pick[j];
+          }
+        last = x;
+        last_at = ix;
+        if (tid == 0) {
+          best[r] = x;
+          best_at[r] = x > -INFINITY ? ix : -1;
+        }
+      }
+    }
   }
 }
 
@@ -445,12 +533,11 @@ gdn_status check_dims(const gdn_beam_dims *d) {
   return GDN_OK;
 }
 
-// Slices of a row: as few as the registers allow, more where the rows alone would leave SMs idle.
+// Slices of a row: about three CTAs for each of 152 SMs in all (16 x 8 rows of 131072 bf16 logits: 608 CTAs 22 us, 456
+// 16.6 us, 304 17.1 us: what a slice costs besides its logits, the cuts and the ranking, is half of it).
 int slices_of(const gdn_beam_dims *d) {
-  const long long rows = (long long)d->n_groups * d->beams;
-  int n = (d->vocab + kSlice - 1) / kSlice;
-  while (rows * n < 304 && d->vocab / (2 * n) >= 2048) n *= 2;
-  return n;
+  const int rows = d->n_groups * d->beams, want = rows > 0 ? 456 / rows : 1, most = d->vocab / kLeast;
+  return want < 1 || most < 1 ? 1 : want < most ? want : most;
 }
 
 }  // namespace beam
@@ -501,15 +588,6 @@ extern "C" gdn_status gdn_beam_select(const gdn_beam_dims *dims, const void *log
   const dim3 grid(A.slices, (unsigned)rows), block(beam::kThreads);
   if (launch_pdl(dims->half ? beam::slice_kernel<true> : beam::slice_kernel<false>, grid, block, 0, st, A) != cudaSuccess)
     return check_launch("beam_select");
-  const size_t lists = (size_t)beam::kWarps * 32 * A.beams * sizeof(beam::Place);
-  static std::atomic<uint64_t> ready{0};  // a bit a device: the attribute holds for the process
-  const uint64_t bit = 1ull << dev->id;
-  if (lists > 16384 && !(ready.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(beam::join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             beam::kWarps * 32 * beam::kMaxBeams * (int)sizeof(beam::Place)) != cudaSuccess)
-      return check_launch("beam_select");
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
-  launch_pdl(beam::join_kernel, dim3(A.groups), block, lists, st, A);
+  launch_pdl(beam::join_kernel, dim3(A.groups), block, 0, st, A);
   return check_launch("beam_select");
 }

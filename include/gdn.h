@@ -650,7 +650,8 @@ typedef struct gdn_beam_dims {
  *   token       int32 [n_groups][beams]
  *   new_scores  fp32 [n_groups][beams], best first
  *   new_done    uint8 [n_groups][beams]: finished before or now; NULL iff done is
- *   workspace   gdn_beam_workspace_size(dims) bytes, 256-byte aligned
+ *   workspace   gdn_beam_workspace_size(dims) bytes, 256-byte aligned; its
+ *               contents need not be preserved. Calls that may overlap need one each.
  * Candidates: score + logit - log sum exp(logits) for every token of a beam that
  * is not finished; the beam itself, with token eos and its score unchanged, for
  * a finished one (its logits are not read). Candidates that are -inf or NaN (a
