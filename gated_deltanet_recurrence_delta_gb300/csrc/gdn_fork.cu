@@ -5,7 +5,8 @@
 // (which pages are used -> which are free -> who gets which -> where the tokens
 // go), so one CTA does it without leaving the SM: what is used stands as one bit
 // a page in shared memory, free pages are ranked by a scan of the bits' counts,
-// and the page of rank k goes to the row whose needs cover k. Latency bounds it.
+// and the page of rank k goes to the row whose needs cover k. Latency bounds it:
+// six barriers, and the chain parent -> length -> last page of dependent loads.
 //
 // slots_copy is an HBM copy of 16-byte vectors; a CTA takes one piece of one
 // slot of one layer, and a skipped pair's CTAs end at once.
@@ -29,132 +30,159 @@ struct Args {
   unsigned int *status;
 };
 
-// Inclusive scan over the CTA; `part` holds kWarps numbers.
-__device__ __forceinline__ int scan(int x, int *part) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();  // part may still be read by an earlier scan
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  int y = part[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int z = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) y += z;
-  }
-  y = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
-  return x + (warp > 0 ? y : 0);
-}
+constexpr int kFresh = 2048;  // new pages that shared memory holds (more: through the table)
 
 __device__ __forceinline__ int pages(int tokens) { return (tokens + kPage - 1) / kPage; }
 
 __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ Args A) {
   extern __shared__ uint32_t s_used[];  // a bit a page
   __shared__ int s_par[kMaxRows], s_len[kMaxRows], s_new[kMaxRows], s_first[kMaxRows];
+  __shared__ int s_tail[kMaxRows];  // the row's partly filled last page
   __shared__ int s_need[kMaxRows];  // pages of the rows up to this one
   __shared__ int s_dead[kMaxRows];  // rows without children, in order
+  __shared__ int s_fresh[kFresh];   // the new pages, in order
   __shared__ uint8_t s_copy[kMaxRows];
-  __shared__ int s_part[kWarps], s_total;
+  __shared__ int s_part[4][kWarps], s_most;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = A.rows;
+  s_first[tid] = kMaxRows;
+  s_copy[tid] = 0;
+  if (tid == 0) s_most = 0;
   griddep_wait();
   griddep_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = A.rows;
   const int words = (A.n_pages + 31) / 32;
   const long long most = (long long)A.width * kPage;
 
-  // ---- the rows
+  // ---- the rows, their last pages; pinned pages
   bool bad = false;
+  int par = -1, len = 0, take = 0, tail = -1;
   if (tid < R) {
-    int p = A.parent ? A.parent[tid] : tid, n = A.n_new ? A.n_new[tid] : A.T, len = 0;
-    if (p < -1 || p >= R) {
+    par = A.parent ? A.parent[tid] : tid;
+    take = A.n_new ? A.n_new[tid] : A.T;
+    if (par < -1 || par >= R) {
       bad = true;
-      p = -1;
+      par = -1;
     }
-    if (p >= 0) {
-      len = A.len[p];
+    if (take < 0 || take > A.T) {
+      bad = true;
+      take = 0;
+    }
+    if (par >= 0) {
+      len = A.len[par];
       if (len < 0 || len > most) {
         bad = true;
         len = 0;
       }
     }
-    if (n < 0 || n > A.T) {
-      bad = true;
-      n = 0;
+    if (len % kPage) {
+      tail = A.table[(long long)par * A.width + len / kPage];
+      if (tail < 0 || tail >= A.n_pages) tail = -1;
     }
-    s_par[tid] = p;
+    s_par[tid] = par;
     s_len[tid] = len;
-    s_new[tid] = n;
-    s_first[tid] = kMaxRows;
-    s_copy[tid] = 0;
+    s_new[tid] = take;
+    s_tail[tid] = tail;
   }
-  // ---- pinned pages
-  for (int w = tid; w < words; w += kThreads) {
-    uint32_t bits = w == words - 1 && A.n_pages % 32 ? ~0u << (A.n_pages % 32) : 0u;
-    if (A.pinned)
-      for (int i = 0; i < 32 && 32 * w + i < A.n_pages; ++i) bits |= (uint32_t)(A.pinned[32 * w + i] != 0) << i;
-    s_used[w] = bits;
+#pragma unroll 4
+  for (int w = warp; w < words; w += kWarps) {  // a page to a lane
+    const int page = 32 * w + lane;
+    const bool taken = page >= A.n_pages || (A.pinned && A.pinned[page]);
+    const uint32_t bits = __ballot_sync(0xffffffffu, taken);
+    if (lane == 0) s_used[w] = bits;
   }
   __syncthreads();
-  if (tid < R && s_par[tid] >= 0) atomicMin(&s_first[s_par[tid]], tid);  // the lowest child
-  // ---- the rows' pages: handed on and marked
-  for (int r = warp; r < R; r += kWarps) {
-    const int p = s_par[r], n = pages(s_len[r]);
-    if (p < 0) continue;
-    const int32_t *from = A.table + (long long)p * A.width;
-    int32_t *to = A.table_out + (long long)r * A.width;
-    for (int j = lane; j < n; j += 32) {
-      const int page = from[j];
-      to[j] = page;
-      if (page < 0 || page >= A.n_pages)
+  const int longest = __reduce_max_sync(0xffffffffu, pages(len));
+  if (lane == 0 && longest > 0) atomicMax(&s_most, longest);
+  if (par >= 0) atomicMin(&s_first[par], tid);  // the lowest child
+  __syncthreads();
+  // ---- the rows' pages: handed on and marked, 128 of a row at a time
+  const int blocks = (s_most + 127) / 128;
+  auto load = [&](int item, int (&x)[4]) {
+    const int r = item / max(blocks, 1), p = item < R * blocks ? s_par[r] : -1, j0 = (item - r * blocks) * 128 + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x[k] = p >= 0 && j0 + 32 * k < pages(s_len[r]) ? A.table[(long long)p * A.width + j0 + 32 * k] : 0;
+  };
+  auto mark = [&](int item, const int (&x)[4]) {
+    if (item >= R * blocks) return;
+    const int r = item / blocks, j0 = (item - r * blocks) * 128 + lane;
+    if (s_par[r] < 0) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (j0 + 32 * k >= pages(s_len[r])) break;
+      A.table_out[(long long)r * A.width + j0 + 32 * k] = x[k];
+      if (x[k] < 0 || x[k] >= A.n_pages)
         bad = true;
       else
-        atomicOr(&s_used[page >> 5], 1u << (page & 31));
+        atomicOr(&s_used[x[k] >> 5], 1u << (x[k] & 31));
     }
+  };
+  for (int item = warp; item < R * blocks; item += 2 * kWarps) {
+    int x[4], y[4];
+    load(item, x);
+    load(item + kWarps, y);
+    mark(item, x);
+    mark(item + kWarps, y);
   }
   // ---- partly filled last pages that are to be written, and are not the row's alone
   for (int r = warp; r < R; r += kWarps) {
-    const int len = s_len[r], at = len / kPage;
-    if (s_new[r] == 0 || len % kPage == 0) continue;
-    const int page = A.table[(long long)s_par[r] * A.width + at];
-    if (page < 0 || page >= A.n_pages) continue;
+    const int n = s_len[r], at = n / kPage, page = s_tail[r];
+    if (s_new[r] == 0 || page < 0) continue;
     bool other = A.pinned && A.pinned[page];
-    for (int x = lane; x < R; x += 32)
-      other |= x != r && pages(s_len[x]) > at && (s_len[x] > len || (s_len[x] == len && x < r)) &&
-               A.table[(long long)s_par[x] * A.width + at] == page;
+    for (int x = lane; x < R; x += 32) {
+      const int m = s_len[x];
+      if (x == r || pages(m) <= at || !(m > n || (m == n && x < r))) continue;
+      // the row's own last page stands there, or a full one
+      other |= (m / kPage == at ? s_tail[x] : A.table[(long long)s_par[x] * A.width + at]) == page;
+    }
     if (__any_sync(0xffffffffu, other) && lane == 0) s_copy[r] = 1;
   }
+  if (bad) set_status(A.status, GDN_ERR_INDEX);
   __syncthreads();
-  // ---- what each row needs
+  // ---- what each row needs, who has a state slot to give and to find, which pages are free: four scans at once
   int need = 0;
-  if (tid < R && s_new[tid] > 0) {
-    const long long after = (long long)s_len[tid] + s_new[tid];
-    if (after > most) {
-      need = -1;
-    } else {
-      need = s_copy[tid] + pages((int)after) - pages(s_len[tid]);
-    }
+  bool wide = false;  // more than a line of the table holds
+  if (take > 0) {
+    const long long after = (long long)len + take;
+    wide = after > most;
+    if (!wide) need = s_copy[tid] + pages((int)after) - pages(len);
   }
-  const bool wide = need < 0;  // more than a line of the table holds
-  need = max(need, 0);
-  const int upto = scan(need, s_part);
-  if (tid < R) s_need[tid] = upto;
-  // ---- free pages: this thread's run of words
+  const bool again = tid < R && (par < 0 || s_first[par] != tid), dead = tid < R && s_first[tid] == kMaxRows;
   const int per = (words + kThreads - 1) / kThreads, w0 = min(words, tid * per), w1 = min(words, w0 + per);
   int mine = 0;
   for (int w = w0; w < w1; ++w) mine += 32 - __popc(s_used[w]);
-  const int ahead = scan(mine, s_part);
-  if (tid == kThreads - 1) s_total = ahead;
+  int upto = need, ahead = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o), z = __shfl_up_sync(0xffffffffu, ahead, o);
+    if (lane >= o) {
+      upto += y;
+      ahead += z;
+    }
+  }
+  const uint32_t agains = __ballot_sync(0xffffffffu, again), deads = __ballot_sync(0xffffffffu, dead);
+  if (lane == 31) {
+    s_part[0][warp] = upto;
+    s_part[1][warp] = ahead;
+    s_part[2][warp] = __popc(agains);
+    s_part[3][warp] = __popc(deads);
+  }
   __syncthreads();
-  const int total = s_total, wanted = R > 0 ? s_need[R - 1] : 0;
-  int k = ahead - mine;  // rank of this thread's first free page
+  auto before = [&](int q) { return (int)__reduce_add_sync(0xffffffffu, lane < warp ? s_part[q][lane] : 0); };
+  upto += before(0);
+  ahead += before(1);
+  const int nth = before(2) + __popc(agains & ((1u << lane) - 1)), nth_dead = before(3) + __popc(deads & ((1u << lane) - 1));
+  const int wanted = __reduce_add_sync(0xffffffffu, s_part[0][lane]), total = __reduce_add_sync(0xffffffffu, s_part[1][lane]);
+  s_need[tid] = upto;
+  if (dead) s_dead[nth_dead] = tid;
+  __syncthreads();
+  // ---- the free pages of this thread's run of words, to the rows whose needs cover their ranks
+  int k = ahead - mine;
   if (k < wanted) {
     int r = -1;
     for (int w = w0; w < w1 && k < wanted; ++w) {
       for (uint32_t free = ~s_used[w]; free && k < wanted; free &= free - 1, ++k) {
         const int page = 32 * w + __ffs(free) - 1;
+        if (k < kFresh) s_fresh[k] = page;
         if (r < 0 || k >= s_need[r]) {  // the first row whose needs reach beyond k
           int lo = r + 1, hi = R - 1;
           while (lo < hi) {
@@ -166,50 +194,40 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
         }
         if (s_need[r] > total) continue;  // its pages do not all exist
         const int j = k - (r > 0 ? s_need[r - 1] : 0) - s_copy[r];  // -1: the copy
-        const int at = pages(s_len[r]) + j;
-        A.table_out[(long long)r * A.width + at] = page;
+        A.table_out[(long long)r * A.width + pages(s_len[r]) + j] = page;
         if (j < 0) A.page_dst[r] = page;
       }
     }
   }
   // ---- the rows' lengths and copies, the state slots
-  bool full = false;
-  int taken = 0, again = 0, dead = 0;
   if (tid < R) {
-    taken = s_new[tid];
-    full = wide || (taken > 0 && need > 0 && upto > total);
-    if (full) taken = 0;
-    A.len_out[tid] = s_len[tid] + taken;
+    const bool full = wide || (take > 0 && need > 0 && upto > total);
+    if (full) {
+      set_status(A.status, GDN_ERR_FULL);
+      s_new[tid] = 0;
+    }
+    A.len_out[tid] = len + (full ? 0 : take);
     const bool copy = s_copy[tid] && !full;
-    A.page_src[tid] = copy ? A.table[(long long)s_par[tid] * A.width + s_len[tid] / kPage] : -1;
+    A.page_src[tid] = copy ? tail : -1;
     if (!copy) A.page_dst[tid] = -1;
-    again = s_par[tid] < 0 || s_first[s_par[tid]] != tid;
-    dead = s_first[tid] == kMaxRows;
-  }
-  if (A.state) {
-    const int nth_dead = scan(dead, s_part);
-    if (dead) s_dead[nth_dead - 1] = tid;
-    const int nth = scan(again, s_part);
-    __syncthreads();
-    if (tid < R) {
-      const int from = s_par[tid] < 0 ? -1 : A.state[s_par[tid]];
-      const int to = again ? A.state[s_dead[nth - 1]] : from;
+    if (A.state) {
+      const int from = par < 0 ? -1 : A.state[par], to = again ? A.state[s_dead[nth]] : from;
       A.state_out[tid] = to;
       A.state_src[tid] = again ? from : -1;
-      A.state_dst[tid] = again && from >= 0 ? to : -1;
+      A.state_dst[tid] = again && par >= 0 ? to : -1;
     }
   }
-  if (__syncthreads_or(bad) && tid == 0) set_status(A.status, GDN_ERR_INDEX);
-  if (__syncthreads_or(full) && tid == 0) set_status(A.status, GDN_ERR_FULL);
-  // ---- the pool rows of the new tokens
-  if (tid < R) s_new[tid] = taken;
   __syncthreads();
+  // ---- the pool rows of the new tokens
   for (long long i = tid; i < (long long)R * A.T; i += kThreads) {
-    const int r = (int)(i / A.T), t = (int)(i - (long long)r * A.T), place = s_len[r] + t;
+    const int r = (int)(i / A.T), t = (int)(i - (long long)r * A.T), n = s_len[r], place = n + t;
     int row = -1;
     if (t < s_new[r]) {
-      const int page = A.table_out[(long long)r * A.width + place / kPage];
-      if (page >= 0 && page < A.n_pages) row = page * kPage + place % kPage;
+      const int at = place / kPage - pages(n) + s_copy[r];  // of the row's new pages; below 0: its last page
+      const int page = at < 0 ? s_tail[r]
+                       : wanted <= kFresh ? s_fresh[(r > 0 ? s_need[r - 1] : 0) + at]
+                                          : A.table_out[(long long)r * A.width + place / kPage];
+      if (page >= 0) row = page * kPage + place % kPage;
     }
     A.index[i] = row;
   }
@@ -305,10 +323,13 @@ extern "C" gdn_status gdn_cache_fork(const gdn_fork_dims *d, const int32_t *pare
   fork::Args A = {d->n_rows, d->T, d->max_pages, d->n_pages, parent, n_new, page_table, kv_len, pinned, page_table_out,
                   kv_len_out, kv_index, page_src, page_dst, state_idx, state_idx_out, state_src, state_dst, dev->status};
   const size_t smem = (size_t)(d->n_pages + 31) / 32 * 4;
-  if (smem > 16384) {  // always to the most, so that calls of several threads agree
+  static std::atomic<uint64_t> ready{0};  // a bit a device: the attribute holds for the process
+  const uint64_t bit = 1ull << dev->id;
+  if (smem > 8192 && !(ready.load(std::memory_order_relaxed) & bit)) {
     if (cudaFuncSetAttribute(fork::fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fork::kMaxPages / 8) !=
         cudaSuccess)
       return check_launch("cache_fork");
+    ready.fetch_or(bit, std::memory_order_relaxed);
   }
   launch_pdl(fork::fork_kernel, dim3(1), dim3(fork::kThreads), smem, static_cast<cudaStream_t>(stream), A);
   return check_launch("cache_fork");
