@@ -6,7 +6,7 @@
 // go), so one CTA does it without leaving the SM: what is used stands as one bit
 // a page in shared memory, free pages are ranked by a scan of the bits' counts,
 // and the page of rank k goes to the row whose needs cover k. Latency bounds it:
-// six barriers, and the chain parent -> length -> last page of dependent loads.
+// seven barriers, and the chain parent -> length -> last page of dependent loads.
 //
 // slots_copy is an HBM copy of 16-byte vectors; a CTA takes one piece of one
 // slot of one layer, and a skipped pair's CTAs end at once.
@@ -40,13 +40,13 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   __shared__ int s_tail[kMaxRows];  // the row's partly filled last page
   __shared__ int s_need[kMaxRows];  // pages of the rows up to this one
   __shared__ int s_dead[kMaxRows];  // rows without children, in order
+  __shared__ int s_state[kMaxRows];
   __shared__ int s_fresh[kFresh];   // the new pages, in order
   __shared__ uint8_t s_copy[kMaxRows];
-  __shared__ int s_part[4][kWarps], s_most;
+  __shared__ int s_part[4][kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = A.rows;
   s_first[tid] = kMaxRows;
   s_copy[tid] = 0;
-  if (tid == 0) s_most = 0;
   griddep_wait();
   griddep_trigger();
   const int words = (A.n_pages + 31) / 32;
@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
     s_len[tid] = len;
     s_new[tid] = take;
     s_tail[tid] = tail;
+    if (A.state) s_state[tid] = A.state[tid];
   }
 #pragma unroll 4
   for (int w = warp; w < words; w += kWarps) {  // a page to a lane
@@ -90,49 +91,52 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
     if (lane == 0) s_used[w] = bits;
   }
   __syncthreads();
-  const int longest = __reduce_max_sync(0xffffffffu, pages(len));
-  if (lane == 0 && longest > 0) atomicMax(&s_most, longest);
-  if (par >= 0) atomicMin(&s_first[par], tid);  // the lowest child
+  bool copy = tail >= 0 && (s_used[tail >> 5] >> (tail & 31) & 1);  // pinned
+  if (par >= 0) atomicMin(&s_first[par], tid);                          // the lowest child
   __syncthreads();
-  // ---- the rows' pages: handed on and marked, 128 of a row at a time
-  const int blocks = (s_most + 127) / 128;
-  auto load = [&](int item, int (&x)[4]) {
-    const int r = item / max(blocks, 1), p = item < R * blocks ? s_par[r] : -1, j0 = (item - r * blocks) * 128 + lane;
+  if (copy && take > 0) s_copy[tid] = 1;
+  // ---- the rows' pages: handed on and marked, 128 of each of two rows at a time
+  for (int ra = warp; ra < R; ra += 2 * kWarps) {
+    const int rb = ra + kWarps, na = pages(s_len[ra]), nb = rb < R ? pages(s_len[rb]) : 0;
+    const int32_t *from_a = A.table + (long long)max(s_par[ra], 0) * A.width;
+    const int32_t *from_b = nb ? A.table + (long long)s_par[rb] * A.width : from_a;
+    int32_t *to_a = A.table_out + (long long)ra * A.width, *to_b = A.table_out + (long long)rb * A.width;
+    for (int j0 = lane; j0 - lane < max(na, nb); j0 += 128) {
+      int x[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      x[k] = p >= 0 && j0 + 32 * k < pages(s_len[r]) ? A.table[(long long)p * A.width + j0 + 32 * k] : 0;
-  };
-  auto mark = [&](int item, const int (&x)[4]) {
-    if (item >= R * blocks) return;
-    const int r = item / blocks, j0 = (item - r * blocks) * 128 + lane;
-    if (s_par[r] < 0) return;
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + 32 * (k & 3);
+        x[k] = j < (k < 4 ? na : nb) ? (k < 4 ? from_a : from_b)[j] : -2;
+      }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (j0 + 32 * k >= pages(s_len[r])) break;
-      A.table_out[(long long)r * A.width + j0 + 32 * k] = x[k];
-      if (x[k] < 0 || x[k] >= A.n_pages)
-        bad = true;
-      else
-        atomicOr(&s_used[x[k] >> 5], 1u << (x[k] & 31));
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + 32 * (k & 3);
+        if (j >= (k < 4 ? na : nb)) continue;
+        (k < 4 ? to_a : to_b)[j] = x[k];
+        if (x[k] < 0 || x[k] >= A.n_pages)
+          bad = true;
+        else
+          atomicOr(&s_used[x[k] >> 5], 1u << (x[k] & 31));
+      }
     }
-  };
-  for (int item = warp; item < R * blocks; item += 2 * kWarps) {
-    int x[4], y[4];
-    load(item, x);
-    load(item + kWarps, y);
-    mark(item, x);
-    mark(item + kWarps, y);
   }
   // ---- partly filled last pages that are to be written, and are not the row's alone
   for (int r = warp; r < R; r += kWarps) {
     const int n = s_len[r], at = n / kPage, page = s_tail[r];
-    if (s_new[r] == 0 || page < 0) continue;
-    bool other = A.pinned && A.pinned[page];
-    for (int x = lane; x < R; x += 32) {
-      const int m = s_len[x];
-      if (x == r || pages(m) <= at || !(m > n || (m == n && x < r))) continue;
-      // the row's own last page stands there, or a full one
-      other |= (m / kPage == at ? s_tail[x] : A.table[(long long)s_par[x] * A.width + at]) == page;
+    if (s_new[r] == 0 || page < 0 || s_copy[r]) continue;
+    bool other = false;
+    for (int x0 = lane; x0 < R; x0 += 128) {  // four rows' loads together
+      int there[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = x0 + 32 * k, m = x < R ? s_len[x] : 0;
+        there[k] = -1;
+        if (x == r || pages(m) <= at || !(m > n || (m == n && x < r))) continue;
+        // the row's own last page stands there, or a full one
+        there[k] = m / kPage == at ? s_tail[x] : A.table[(long long)s_par[x] * A.width + at];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) other |= there[k] == page;
     }
     if (__any_sync(0xffffffffu, other) && lane == 0) s_copy[r] = 1;
   }
@@ -175,30 +179,28 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   s_need[tid] = upto;
   if (dead) s_dead[nth_dead] = tid;
   __syncthreads();
-  // ---- the free pages of this thread's run of words, to the rows whose needs cover their ranks
-  int k = ahead - mine;
-  if (k < wanted) {
-    int r = -1;
-    for (int w = w0; w < w1 && k < wanted; ++w) {
-      for (uint32_t free = ~s_used[w]; free && k < wanted; free &= free - 1, ++k) {
-        const int page = 32 * w + __ffs(free) - 1;
-        if (k < kFresh) s_fresh[k] = page;
-        if (r < 0 || k >= s_need[r]) {  // the first row whose needs reach beyond k
-          int lo = r + 1, hi = R - 1;
-          while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (s_need[mid] > k) hi = mid;
-            else lo = mid + 1;
-          }
-          r = lo;
-        }
-        if (s_need[r] > total) continue;  // its pages do not all exist
-        const int j = k - (r > 0 ? s_need[r - 1] : 0) - s_copy[r];  // -1: the copy
-        A.table_out[(long long)r * A.width + pages(s_len[r]) + j] = page;
-        if (j < 0) A.page_dst[r] = page;
-      }
+  // ---- the free pages: listed by rank, and rank k goes to the first row whose needs reach beyond k
+  auto give = [&](int k, int page) {
+    int lo = 0, hi = R - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (s_need[mid] > k) hi = mid;
+      else lo = mid + 1;
     }
-  }
+    if (s_need[lo] > total) return;  // its pages do not all exist
+    const int j = k - (lo > 0 ? s_need[lo - 1] : 0) - s_copy[lo];  // -1: the copy
+    A.table_out[(long long)lo * A.width + pages(s_len[lo]) + j] = page;
+    if (j < 0) A.page_dst[lo] = page;
+  };
+  int k = ahead - mine;  // of this thread's run of words
+  for (int w = w0; w < w1 && k < wanted; ++w)
+    for (uint32_t free = ~s_used[w]; free && k < wanted; free &= free - 1, ++k) {
+      const int page = 32 * w + __ffs(free) - 1;
+      if (k < kFresh) s_fresh[k] = page;
+      else give(k, page);
+    }
+  __syncthreads();
+  for (int i = tid; i < min(min(wanted, total), kFresh); i += kThreads) give(i, s_fresh[i]);
   // ---- the rows' lengths and copies, the state slots
   if (tid < R) {
     const bool full = wide || (take > 0 && need > 0 && upto > total);
@@ -207,11 +209,11 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
       s_new[tid] = 0;
     }
     A.len_out[tid] = len + (full ? 0 : take);
-    const bool copy = s_copy[tid] && !full;
+    copy = s_copy[tid] && !full;
     A.page_src[tid] = copy ? tail : -1;
     if (!copy) A.page_dst[tid] = -1;
     if (A.state) {
-      const int from = par < 0 ? -1 : A.state[par], to = again ? A.state[s_dead[nth]] : from;
+      const int from = par < 0 ? -1 : s_state[par], to = again ? s_state[s_dead[nth]] : from;
       A.state_out[tid] = to;
       A.state_src[tid] = again ? from : -1;
       A.state_dst[tid] = again && par >= 0 ? to : -1;

@@ -5,10 +5,10 @@
 //   s = e4m3(max|y| / 7, in [2^-9, 240]),  u = 8 + rint(y / s) in [1, 15]
 //
 // Memory-bound: 4 bytes a channel pair in, 9/8 out. A lane takes the 16
-// channels of one scale: 32 bytes of bf16, 8 bytes of codes, one scale. A warp
-// takes 8 groups of 4 tokens, so that a token's 8 code pieces and key scales
-// are contiguous, and the value scales of neighbouring tokens (which lie
-// together, [d/16][64]) meet in one sector.
+// channels of one scale of the keys and of the values: 32 bytes of bf16, 8 bytes of
+// codes, one scale each. A warp takes 8 groups of 4 tokens, so that a token's 8 code
+// pieces and key scales are contiguous, and the value scales of neighbouring tokens
+// (which lie together, [d/16][64]) meet in one sector.
 //
 // The quotient is rounded exactly without a division per channel. y has 8
 // significant bits, s at most 4: y/s is either k + 1/2 exactly or at least 2^-10
@@ -41,22 +41,18 @@ struct Args {
   unsigned int *status;
 };
 
-// This lane's token, kind (K or V) and group; false where there is none.
+// This lane's token and group; false where there is none.
 struct Place {
-  int t, kind, group;
+  int t, group;
 };
 __device__ __forceinline__ bool place_of(const Args &A, Place &p) {
   const int lane = threadIdx.x & 31;
-  const int octets = (A.groups + 7) / 8;
-  long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int octet = (int)(w % octets);
-  w /= octets;
-  p.kind = (int)(w & 1);
-  const long long t = (w >> 1) * 4 + (lane >> 3);
-  p.group = octet * 8 + (lane & 7);
-  if (t >= A.n || p.group >= A.groups) return false;
+  const uint32_t octets = (uint32_t)(A.groups + 7) / 8, w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t quad = w / octets;
+  const long long t = (long long)quad * 4 + (lane >> 3);
+  p.group = (int)(w - quad * octets) * 8 + (lane & 7);
   p.t = (int)t;
-  return true;
+  return t < A.n && p.group < A.groups;
 }
 
 // The token's pool row, or -1.
@@ -69,39 +65,37 @@ __device__ __forceinline__ long long row_of(const Args &A, int t) {
   return r;
 }
 
-// The block of the group's head; the 8 bytes of its codes and its scale byte.
+// The block of the group's head, and in it the 8 bytes of its keys' codes and their scale byte, and the values'.
 template <int D>
-__device__ __forceinline__ void addresses(const Args &A, const Place &p, long long row, uint8_t *&codes, uint8_t *&scale) {
-  constexpr int G = D / kGroup;
-  const int head = p.group / G, g = p.group % G, token = (int)(row % kPage);
-  uint8_t *block = A.pool + ((row / kPage) * A.hk + head) * (long long)block_bytes(D);
-  codes = block + codes_at(D, p.kind) + swizzle(token * (D / 2) + g * 8);
-  scale = block + scales_at(D, p.kind) + (p.kind == 0 ? token * G + g : g * kPage + token);
+struct Where {
+  uint8_t *codes, *k_scale, *v_scale;
+  __device__ __forceinline__ Where(const Args &A, const Place &p, long long row) {
+    constexpr int G = D / kGroup;
+    const int head = p.group / G, g = p.group % G, token = (int)(row % kPage);
+    uint8_t *block = A.pool + ((row / kPage) * A.hk + head) * (long long)block_bytes(D);
+    codes = block + swizzle(token * (D / 2) + g * 8);
+    k_scale = block + scales_at(D, 0) + token * G + g;
+    v_scale = block + scales_at(D, 1) + g * kPage + token;
+  }
+};
+
+__device__ __forceinline__ void load32(const bf16 *p, uint32_t (&w)[8]) {
+  *reinterpret_cast<uint4 *>(w) = __ldcs(reinterpret_cast<const uint4 *>(p));
+  *reinterpret_cast<uint4 *>(w + 4) = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__ Args A) {
-  griddep_wait();
-  griddep_trigger();
-  Place p;
-  if (!place_of(A, p)) return;
-  const long long row = row_of(A, p.t);
-  const bf16 *src = (p.kind == 0 ? A.k + p.t * A.ks : A.v + p.t * A.vs) + p.group * kGroup;
-  uint32_t w[8];
-  *reinterpret_cast<uint4 *>(w) = __ldcs(reinterpret_cast<const uint4 *>(src));
-  *reinterpret_cast<uint4 *>(w + 4) = __ldcs(reinterpret_cast<const uint4 *>(src) + 1);
-  if (row < 0) return;
+// 16 channels to their codes; returns the scale byte.
+__device__ __forceinline__ uint8_t quantise(const uint32_t (&w)[8], float mul, uint32_t (&code)[2]) {
   uint32_t top2 = 0;  // the largest magnitude's bits: an infinity or NaN is at least 0x7f80
 #pragma unroll
   for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, w[i] & 0x7fff7fffu);
   const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-  const float mul = p.kind == 0 ? A.k_mul : A.v_mul;
   const float amax = __uint_as_float(top << 16) * mul;
   const float wide = fminf(fmaxf(__fdiv_rn(amax, 7.0f), 0.001953125f), 240.0f);
-  __nv_fp8_storage_t byte = __nv_cvt_float_to_fp8(wide, __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8_storage_t byte = __nv_cvt_float_to_fp8(wide, __NV_SATFINITE, __NV_E4M3);
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)));
   const float r = mul * (1.0f / s);
-  uint32_t code[2] = {0, 0};
+  code[0] = code[1] = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float x = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
@@ -111,13 +105,41 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__
     code[i / 8] |= u << (4 * (i % 8));
   }
   if (top >= 0x7f80u) {
-    byte = 0x7f;  // e4m3 NaN: the group reads back as NaN
     code[0] = code[1] = 0x99999999u;
+    return 0x7f;  // e4m3 NaN: the group reads back as NaN
   }
-  uint8_t *codes, *scale;
-  addresses<D>(A, p, row, codes, scale);
-  *reinterpret_cast<uint2 *>(codes) = make_uint2(code[0], code[1]);
-  *scale = byte;
+  return byte;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__ Args A) {
+  griddep_wait();
+  griddep_trigger();
+  Place p;
+  if (!place_of(A, p)) return;
+  uint32_t k[8], v[8], code[2];
+  load32(A.k + p.t * A.ks + p.group * kGroup, k);
+  load32(A.v + p.t * A.vs + p.group * kGroup, v);
+  const long long row = row_of(A, p.t);
+  if (row < 0) return;
+  const Where<D> at(A, p, row);
+  *at.k_scale = quantise(k, A.k_mul, code);
+  *reinterpret_cast<uint2 *>(at.codes + codes_at(D, 0)) = make_uint2(code[0], code[1]);
+  *at.v_scale = quantise(v, A.v_mul, code);
+  *reinterpret_cast<uint2 *>(at.codes + codes_at(D, 1)) = make_uint2(code[0], code[1]);
+}
+
+__device__ __forceinline__ void expand(bf16 *to, uint2 code, float s) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t c = (i < 4 ? code.x : code.y) >> (8 * (i % 4));
+    const float a = (float)((int)(c & 15) - 8) * s, b = (float)((int)(c >> 4 & 15) - 8) * s;
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  __stcs(reinterpret_cast<uint4 *>(to), make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(reinterpret_cast<uint4 *>(to) + 1, make_uint4(w[4], w[5], w[6], w[7]));
 }
 
 template <int D>
@@ -128,21 +150,12 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   if (!place_of(A, p)) return;
   const long long row = row_of(A, p.t);
   if (row < 0) return;
-  uint8_t *codes, *scale;
-  addresses<D>(A, p, row, codes, scale);
-  const uint2 code = __ldcs(reinterpret_cast<const uint2 *>(codes));
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(*scale, __NV_E4M3))) * (p.kind == 0 ? A.k_mul : A.v_mul);
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t c = (i < 4 ? code.x : code.y) >> (8 * (i % 4));
-    const float a = (float)((int)(c & 15) - 8) * s, b = (float)((int)(c >> 4 & 15) - 8) * s;
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
-  bf16 *dst = (p.kind == 0 ? A.k + p.t * A.ks : A.v + p.t * A.vs) + p.group * kGroup;
-  *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  *(reinterpret_cast<uint4 *>(dst) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+  const Where<D> at(A, p, row);
+  const uint2 k = *reinterpret_cast<const uint2 *>(at.codes + codes_at(D, 0));
+  const uint2 v = *reinterpret_cast<const uint2 *>(at.codes + codes_at(D, 1));
+  const uint8_t sk = *at.k_scale, sv = *at.v_scale;
+  expand(A.k + p.t * A.ks + p.group * kGroup, k, __half2float(__half(__nv_cvt_fp8_to_halfraw(sk, __NV_E4M3))) * A.k_mul);
+  expand(A.v + p.t * A.vs + p.group * kGroup, v, __half2float(__half(__nv_cvt_fp8_to_halfraw(sv, __NV_E4M3))) * A.v_mul);
 }
 
 // The checks of both calls; A.n stays 0 where there is nothing to do.
@@ -162,8 +175,8 @@ gdn_status arguments(const gdn_kv4_dims *d, const void *k, const void *v, const 
   if (d->k_stride < width || d->v_stride < width) return fail(GDN_ERR_SHAPE, "token strides must cover the heads");
   if (d->k_stride >= (1LL << 32) || d->v_stride >= (1LL << 32))
     return fail(GDN_ERR_SHAPE, "token strides must be below 2^32 elements");
-  const long long warps = ((long long)d->n_tokens + 3) / 4 * 2 * ((width / kGroup + 7) / 8);
-  if ((warps + 7) / 8 > 0x7fffffffLL) return fail(GDN_ERR_SHAPE, "more tokens and heads than a grid holds");
+  const long long warps = ((long long)d->n_tokens + 3) / 4 * ((width / kGroup + 7) / 8);
+  if (warps > 0x7fffffffLL) return fail(GDN_ERR_SHAPE, "more tokens and heads than a grid holds");
   A = {};
   if (d->n_tokens == 0) return GDN_OK;  // empty tensors may have no address
   GDN_TRY(check_ptr(k, "k"));
@@ -189,7 +202,7 @@ gdn_status arguments(const gdn_kv4_dims *d, const void *k, const void *v, const 
 }
 
 void launch(const Args &A, int D, bool store, void *stream) {
-  const long long warps = ((long long)A.n + 3) / 4 * 2 * ((A.groups + 7) / 8);
+  const long long warps = ((long long)A.n + 3) / 4 * ((A.groups + 7) / 8);
   const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))), block(kThreads);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (D == 64) launch_pdl(store ? store_kernel<64> : load_kernel<64>, grid, block, 0, st, A);
