@@ -16,7 +16,7 @@
 // is at least 2^-10 s where |y| > 0.4 s). y times the reciprocal of s is off by
 // less than 2^-19 (|y/s| < 8), so rounding it to multiples of 2^-16 gives k + 1/2
 // exactly where the quotient is, and stays on the right side elsewhere; then it
-// is rounded to whole numbers, ties to even. max|y| / 7 is a true division: its
+// is rounded to whole numbers, ties to even: two operations, 192 + q first. max|y| / 7 is a true division: its
 // ties (max|y| = 7 times a number of 5 bits) are exact in fp32.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -28,10 +28,11 @@
 namespace gdn {
 namespace kv4 {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Args {
   int n, hk, groups;  // tokens, heads, scales of a token (hk d / 16)
+  bool wide;          // k and v allow accesses of 32 bytes
   long long rows;     // of the pool
   long long ks, vs;
   float k_mul, v_mul;  // 2^-exp (store), 2^exp (load)
@@ -79,10 +80,29 @@ struct Where {
   }
 };
 
-__device__ __forceinline__ void load32(const bf16 *p, uint32_t (&w)[8]) {
-  *reinterpret_cast<uint4 *>(w) = __ldcs(reinterpret_cast<const uint4 *>(p));
-  *reinterpret_cast<uint4 *>(w + 4) = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+// 32 bytes, as one access where every token's heads begin on such a boundary.
+__device__ __forceinline__ void load32(const bf16 *p, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    *reinterpret_cast<uint4 *>(w) = __ldcs(reinterpret_cast<const uint4 *>(p));
+    *reinterpret_cast<uint4 *>(w + 4) = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+  }
 }
+__device__ __forceinline__ void store32(bf16 *p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *(reinterpret_cast<uint4 *>(p) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+__device__ __forceinline__ float scale_of(uint8_t byte) { return __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3))); }
 
 // 16 channels to their codes; returns the scale byte.
 __device__ __forceinline__ uint8_t quantise(const uint32_t (&w)[8], float mul, uint32_t (&code)[2]) {
@@ -93,17 +113,27 @@ __device__ __forceinline__ uint8_t quantise(const uint32_t (&w)[8], float mul, u
   const float amax = __uint_as_float(top << 16) * mul;
   const float wide = fminf(fmaxf(__fdiv_rn(amax, 7.0f), 0.001953125f), 240.0f);
   const __nv_fp8_storage_t byte = __nv_cvt_float_to_fp8(wide, __NV_SATFINITE, __NV_E4M3);
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)));
-  const float r = mul * (1.0f / s);
-  code[0] = code[1] = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  const float s = scale_of(byte), r = mul * (1.0f / s);
+  // In fp32 1.5 * 2^23 + 8 + q has the code 8 + q as its last bits: the codes are shifted together as they are, and
+  // what the numbers' other bits add up to (modulo 2^32) is taken off at the end.
+  constexpr float kWhole = 12582912.0f;
+  constexpr uint32_t kRest = 0x4b400000u * 0x11111111u;
+  const auto code_of = [&](int i) {
     const float x = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    float q = __fsub_rn(__fmaf_rn(x, r, 192.0f), 192.0f);  // multiples of 2^-16 (beyond +-64 coarser, and clamped)
-    q = fminf(fmaxf(q, -7.0f), 7.0f);
-    const uint32_t u = __float_as_uint(__fadd_rn(q, 12582912.0f + 8.0f)) & 15u;  // 1.5 * 2^23: whole numbers, ties to even
-    code[i / 8] |= u << (4 * (i % 8));
+    return __fmaf_rn(x, r, 192.0f);  // 192 + q, to multiples of 2^-16
+  };
+  code[0] = code[1] = 0;
+  if (wide > 0.015625f && wide < 240.0f) {  // s is off by at most a 16th: |q| < 7.5
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      code[i / 8] += __float_as_uint(__fadd_rn(code_of(i), kWhole + 8.0f - 192.0f)) << (4 * (i % 8));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      code[i / 8] += __float_as_uint(__fadd_rn(fminf(fmaxf(code_of(i), 185.0f), 199.0f), kWhole + 8.0f - 192.0f)) << (4 * (i % 8));
   }
+  code[0] -= kRest;
+  code[1] -= kRest;
   if (top >= 0x7f80u) {
     code[0] = code[1] = 0x99999999u;
     return 0x7f;  // e4m3 NaN: the group reads back as NaN
@@ -118,8 +148,8 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__
   Place p;
   if (!place_of(A, p)) return;
   uint32_t k[8], v[8], code[2];
-  load32(A.k + p.t * A.ks + p.group * kGroup, k);
-  load32(A.v + p.t * A.vs + p.group * kGroup, v);
+  load32(A.k + p.t * A.ks + p.group * kGroup, A.wide, k);
+  load32(A.v + p.t * A.vs + p.group * kGroup, A.wide, v);
   const long long row = row_of(A, p.t);
   if (row < 0) return;
   const Where<D> at(A, p, row);
@@ -129,17 +159,27 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__
   *reinterpret_cast<uint2 *>(at.codes + codes_at(D, 1)) = make_uint2(code[0], code[1]);
 }
 
-__device__ __forceinline__ void expand(bf16 *to, uint2 code, float s) {
+// 16 codes times their scale to bf16. A nibble at the mantissa's bit 3 of 16 makes 16 + u; times s, less 24 s, that is
+// (u - 8) s exactly.
+__device__ __forceinline__ void expand(bf16 *to, bool wide, uint2 code, float s) {
+  auto bits = [](__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t *>(&h); };
+  const __nv_bfloat162 mul = __float2bfloat162_rn(s), add = __float2bfloat162_rn(-24.0f * s);
   uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t c = (i < 4 ? code.x : code.y) >> (8 * (i % 4));
-    const float a = (float)((int)(c & 15) - 8) * s, b = (float)((int)(c >> 4 & 15) - 8) * s;
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c = h ? code.y : code.x;
+    uint32_t v[4];  // channels i and i + 4
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = ((i == 0 ? c << 3 : c >> (4 * i - 3)) & 0x00780078u) | 0x41804180u;
+      v[i] = bits(__hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x), mul, add));
+    }
+    w[4 * h] = __byte_perm(v[0], v[1], 0x5410);
+    w[4 * h + 1] = __byte_perm(v[2], v[3], 0x5410);
+    w[4 * h + 2] = __byte_perm(v[0], v[1], 0x7632);
+    w[4 * h + 3] = __byte_perm(v[2], v[3], 0x7632);
   }
-  __stcs(reinterpret_cast<uint4 *>(to), make_uint4(w[0], w[1], w[2], w[3]));
-  __stcs(reinterpret_cast<uint4 *>(to) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  store32(to, wide, w);
 }
 
 template <int D>
@@ -154,8 +194,8 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
   const uint2 k = *reinterpret_cast<const uint2 *>(at.codes + codes_at(D, 0));
   const uint2 v = *reinterpret_cast<const uint2 *>(at.codes + codes_at(D, 1));
   const uint8_t sk = *at.k_scale, sv = *at.v_scale;
-  expand(A.k + p.t * A.ks + p.group * kGroup, k, __half2float(__half(__nv_cvt_fp8_to_halfraw(sk, __NV_E4M3))) * A.k_mul);
-  expand(A.v + p.t * A.vs + p.group * kGroup, v, __half2float(__half(__nv_cvt_fp8_to_halfraw(sv, __NV_E4M3))) * A.v_mul);
+  expand(A.k + p.t * A.ks + p.group * kGroup, A.wide, k, scale_of(sk) * A.k_mul);
+  expand(A.v + p.t * A.vs + p.group * kGroup, A.wide, v, scale_of(sv) * A.v_mul);
 }
 
 // The checks of both calls; A.n stays 0 where there is nothing to do.
@@ -195,6 +235,7 @@ gdn_status arguments(const gdn_kv4_dims *d, const void *k, const void *v, const 
   A.v_mul = ldexpf(1.0f, store ? -d->v_exp : d->v_exp);
   A.k = static_cast<bf16 *>(const_cast<void *>(k));
   A.v = static_cast<bf16 *>(const_cast<void *>(v));
+  A.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 | A.ks % 16 | A.vs % 16) == 0;
   A.index = kv_index;
   A.pool = static_cast<uint8_t *>(const_cast<void *>(pool));
   A.status = dev->status;
