@@ -1,5 +1,5 @@
-"""The full-attention layers of a hybrid stack beside its GDN layers, and the
-speculative step of both.
+"""The full-attention layers of a hybrid stack beside its GDN layers, the
+speculative step of both, and beam search over both.
 
 statecache.py (squad-0.8b, qev_fast): a hybrid model's layers are GDN layers,
 whose cache is a state slot, and full-attention layers, whose cache is the keys
@@ -14,6 +14,10 @@ one extent of pool rows; every row has an extent of its own behind it, with room
 for its continuation. Lengths live on the device, so a step can be captured: the
 class marshals buffers and issues the library's calls, as LayerStack does for the
 GDN layers.
+
+PagedAttentionLayers keeps them in 4-bit pages instead, in which a row grows page by
+page and rows that part later share what they have in common: what beam search
+needs, whose rows become copies of one another after every selection.
 """
 from __future__ import annotations
 
@@ -117,6 +121,161 @@ class AttentionLayers:
         """Every layer's caches keep the accepted tokens of the step: the next step overwrites the others."""
         with _on(stream):
             self.own_len[:accept_len.numel()] += accept_len
+
+
+class PagedAttentionLayers:
+    """n_layers full-attention layers of one head layout over n_pages pages of 64 tokens each, held in 4 bits (gdn.kv4_pool);
+    n_rows rows of at most max_pages pages each, all layers sharing the page table and the rows' lengths.
+
+    weights, inv_freq: as in AttentionLayers. k_exp, v_exp: the pools' exponents. pinned: uint8 [n_pages], the pages that
+    others hold (set by the caller; never taken or written). A step is take() -- rows become copies of other rows, get
+    pages for the tokens that they take now, and the copies of pages and states are made -- and then each layer's step().
+    Everything stays on the device, so that a step can be captured; what take() cannot give a page for takes no tokens and
+    is reported (GDN_ERR_FULL, gdn.check_status). A call given a stream does all its work on it."""
+
+    def __init__(self, n_q_heads, n_kv_heads, head_dim, weights, inv_freq, n_rows, n_pages, max_pages, k_exp=0, v_exp=0,
+                 device="cuda"):
+        self.hq, self.hk, self.d = n_q_heads, n_kv_heads, head_dim
+        self.weights, self.inv_freq, self.device = weights, inv_freq, device
+        self.n_layers, self.n_rows, self.n_pages, self.max_pages = len(weights), n_rows, n_pages, max_pages
+        self.k_exp, self.v_exp = k_exp, v_exp
+        self.pool = torch.zeros((self.n_layers, n_pages, n_kv_heads, 72 * head_dim), dtype=torch.uint8, device=device)
+        ints = lambda *n: torch.zeros(n, dtype=torch.int32, device=device)  # noqa: E731
+        self.table, self.kv_len, self.taken = ints(n_rows, max_pages), ints(n_rows), ints(n_rows)
+        self._table, self._kv_len = ints(n_rows, max_pages), ints(n_rows)
+        self.page_src, self.page_dst = ints(n_rows), ints(n_rows)
+        self.pinned = torch.zeros(n_pages, dtype=torch.uint8, device=device)
+        self.buffers = {}
+
+    def _buffer(self, name, shape, dtype, stream, zero=False):
+        key = (name, shape, gdn._stream(stream))
+        if key not in self.buffers:
+            make = torch.zeros if zero else torch.empty
+            self.buffers[key] = make(shape, dtype=dtype, device=self.device)
+        return self.buffers[key]
+
+    def take(self, T, parent=None, n_new=None, state_idx=None, stack=None, stream=None):
+        """Row r becomes a copy of row parent[r] (int32 [n_rows], -1: emptied; None: itself) and takes n_new[r] tokens
+        (int32 [n_rows] in [0, T]; None: T). With state_idx int32 [n_rows], the rows' slots of `stack` (a LayerStack), it
+        is brought along in place and the states and conv tails are copied too. Returns kv_index int32 [n_rows, T], the
+        tokens' pool rows; kv_len holds the rows' lengths with them."""
+        with _on(stream):
+            index = self._buffer("index", (self.n_rows, T), torch.int32, stream)
+            states = {}
+            if state_idx is not None:
+                names = ("state_idx_out", "state_src", "state_dst")
+                states = {n: self._buffer(n, (self.n_rows,), torch.int32, stream) for n in names}
+                states["state_idx"] = state_idx
+            gdn.cache_fork(self.table, self.kv_len, self._table, self._kv_len, index if T else None, self.page_src,
+                           self.page_dst, self.n_pages, parent=parent, n_new=n_new, pinned=self.pinned, stream=stream,
+                           **states)
+            pools = [(self.pool, self.page_src, self.page_dst)]
+            if state_idx is not None:
+                pools += [(p, states["state_src"], states["state_dst"]) for p in (stack.state_pool, stack.conv_pool)]
+            gdn.slots_copy(pools, stream)
+            if state_idx is not None:
+                state_idx.copy_(states["state_idx_out"])
+            self.table.copy_(self._table)
+            self.kv_len.copy_(self._kv_len)
+            if T:
+                torch.sum(index >= 0, 1, out=self.taken)
+            else:
+                self.taken.zero_()
+            return index
+
+    def _split(self, qkv):
+        hq, hk, d = self.hq, self.hk, self.d
+        return (qkv[:, :hq * d].unflatten(1, (hq, d)), qkv[:, hq * d:(hq + hk) * d].unflatten(1, (hk, d)),
+                qkv[:, (hq + hk) * d:].unflatten(1, (hk, d)))
+
+    def _norm_rope(self, layer, qkv, positions, q_out, k_out, v_out, kv_index, stream):
+        q, k, v = self._split(qkv)
+        dims = gdn.make_rope_dims(q, k, 2 * self.inv_freq.numel(), kv_rows=k_out.shape[0])
+        w = self.weights[layer]
+        gdn.head_norm_rope(dims, q, k, v, w["q_norm"], w["k_norm"], positions, self.inv_freq, q_out, k_out, v_out,
+                           kv_index=kv_index, stream=stream)
+
+    def step(self, layer, qkv, kv_index, q_buf, out, stream=None):
+        """A layer's decode (T = 1) or verify (T tokens) of all rows: qkv bf16 [n_rows, T, (hq + 2 hk) d], kv_index
+        take()'s; q_buf, out: bf16 [n_rows, T, hq, d]. A row's tokens behind the ones it took are none of it: their
+        outputs are zeros."""
+        with _on(stream):
+            R, T = q_buf.shape[:2]
+            first = self.kv_len - self.taken
+            positions = (first[:, None] + torch.arange(T, dtype=torch.int32, device=self.device)).reshape(1, -1)
+            k, v = (self._buffer(n, (R * T, self.hk, self.d), torch.bfloat16, stream) for n in ("k", "v"))
+            self._norm_rope(layer, qkv.flatten(0, 1), positions, q_buf, k, v, None, stream)
+            pool = self.pool[layer]
+            dims = gdn.make_kv4_dims(k, pool, k_exp=self.k_exp, v_exp=self.v_exp)
+            gdn.kv4_store(dims, k, v, kv_index, pool, stream)
+            dims = gdn.make_attn_kv4_dims(q_buf, pool, self.table, k_exp=self.k_exp, v_exp=self.v_exp)
+            size = (gdn.attn_kv4_workspace_size(dims),)
+            gdn.attn_kv4(dims, q_buf, pool, self.table, self.kv_len, out,
+                         self._buffer("workspace", size, torch.uint8, stream, zero=True), self.taken, stream)
+
+    def prefill(self, layer, qkv, rows, lens, past, kv_index, q_buf, out, stream=None):
+        """A layer's prompts, or further chunks of them: sequence i is lens[i] tokens of row rows[i], behind past[i] tokens
+        that its pages hold already (host lists); take() has given the rows their pages and kv_index is the tokens' of
+        it, int32 [n]. qkv bf16 [n, (hq + 2 hk) d]; q_buf, out bf16 [n, hq, d]. The new tokens attend in bf16; the past
+        ones as the pages hold them."""
+        with _on(stream):
+            dev, total = self.device, [a + b for a, b in zip(lens, past)]
+            ints = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+            places = torch.cat([torch.arange(p, p + n) for n, p in zip(lens, past)])
+            starts = [sum(total[:i]) for i in range(len(total))]
+            at = torch.cat([torch.arange(s + p, s + p + n) for s, n, p in zip(starts, lens, past)])
+            k, v = (torch.empty((sum(total), self.hk, self.d), dtype=torch.bfloat16, device=dev) for _ in range(2))
+            self._norm_rope(layer, qkv, places.int().to(dev)[None], q_buf, k, v, at.int().to(dev), stream)
+            pool = self.pool[layer]
+            new_k, new_v = (k, v) if not any(past) else (x[at.to(dev)] for x in (k, v))
+            gdn.kv4_store(gdn.make_kv4_dims(new_k, pool, k_exp=self.k_exp, v_exp=self.v_exp), new_k, new_v, kv_index, pool,
+                          stream)
+            if any(past):  # the cached tokens in front of them; -1: not loaded
+                old = torch.full((sum(total),), -1, dtype=torch.int32, device=dev)
+                for r, s, p in zip(rows, starts, past):
+                    j = torch.arange(p, device=dev)
+                    old[s:s + p] = self.table[r, j // gdn.PAGE_TOKENS] * gdn.PAGE_TOKENS + (j % gdn.PAGE_TOKENS).int()
+                gdn.kv4_load(gdn.make_kv4_dims(k, pool, k_exp=self.k_exp, v_exp=self.v_exp), pool, old, k, v, stream)
+            cu = ints([sum(lens[:i]) for i in range(len(lens) + 1)])
+            dims = gdn.make_attn_dims(q_buf, k, B=len(lens))
+            gdn.attn_prefill(dims, q_buf, k, v, cu, out, ints(starts), ints(total), stream)
+
+
+class Beams:
+    """What a beam search carries from step to step, [groups, beams] each: the scores (fp32, -inf: no beam), done (uint8),
+    and the last selection's parent (row numbers) and token. At the start each group has one beam, its first row."""
+
+    def __init__(self, groups, beams, device="cuda"):
+        new = lambda dtype, fill: torch.full((groups, beams), fill, dtype=dtype, device=device)  # noqa: E731
+        self.scores, self.done = new(torch.float32, float("-inf")), new(torch.uint8, 0)
+        self.scores[:, 0] = 0.0
+        self.parent = torch.arange(groups * beams, dtype=torch.int32, device=device).view(groups, beams)
+        self.token = new(torch.int32, -1)
+        self.workspace = None
+
+    def select(self, logits, eos=-1, stream=None):
+        """The best continuations, from the rows' logits [groups, beams, V] (fp32 or bf16)."""
+        if self.workspace is None:
+            self.workspace = gdn.beam_workspace(logits)
+        gdn.beam_select(logits, self.scores, self.parent, self.token, self.scores, self.workspace, done=self.done,
+                        new_done=self.done, eos=eos, stream=stream)
+
+
+def beam_step(stack, attention, beams, acts, qkv, logits, state_idx, buffers, eos=-1):
+    """One step of beam search over a hybrid stack, entirely on the device (and so capturable): the rows become what the
+    last selection made of them (pages shared, partly filled ones and the recurrent states copied), every layer decodes
+    one token a row, and the next selection is made.
+
+    stack: LayerStack; attention: PagedAttentionLayers; beams: Beams; acts / qkv: the layers' inputs (LayerStack.decode;
+    PagedAttentionLayers.step with T = 1); logits: [groups, beams, V]; state_idx int32 [n_rows], the rows' state slots;
+    buffers: dict with gdn_out (LayerStack.decode), q and attn_out [n_layers][n_rows][1][hq][d]. A finished beam takes no
+    tokens. The logits come from the layers' outputs; here they are given."""
+    n_new = (beams.done.flatten() == 0).to(torch.int32)
+    index = attention.take(1, beams.parent.flatten(), n_new, state_idx, stack)
+    stack.decode(acts, state_idx, buffers["gdn_out"])
+    for layer in range(attention.n_layers):
+        attention.step(layer, qkv[layer], index, buffers["q"], buffers["attn_out"][layer])
+    beams.select(logits, eos)
 
 
 def speculative_step(stack, attention, acts, qkv, state_idx, prompts, tokens, target_probs, draft_probs, uniform, buffers):
