@@ -25,9 +25,9 @@
 //     shared memory, moved from the scores' layout to the operand's by 8x8
 //     transposes between lanes. A lane holds 4 keys of 8 channels; byte permutes put
 //     two keys' nibbles of one channel into one register.
-//   - The running maximum is a reference that is only moved when a score exceeds
-//     it by 2^8 (fp16 holds the probabilities up to there): the barrier that hands
-//     the probabilities over also says whether any did.
+//   - The running maximum is a reference that is only moved, after the first page,
+//     when a score exceeds it by 2^8 (fp16 holds the probabilities up to there): the
+//     barrier that hands the probabilities over also says whether any did.
 //
 // A page's block of one head is contiguous: one bulk copy into a ring of stages. At
 // a page's barrier all warps have left the page before it, so its stage is filled
@@ -47,7 +47,7 @@ namespace attn_kv4 {
 using namespace kv4;
 
 constexpr int kMaxCtas = 1536;
-constexpr float kNone = -3.0e38f;  // a reference below every score
+constexpr float kNone = -3.0e38f;  // below every score
 constexpr float kLag = 8.0f;       // scores may exceed the reference by 2^8
 constexpr int kSetup = 2;          // pages that a unit's queries and output are worth
 constexpr int kLeast = 2;          // pages that are worth a CTA
@@ -412,12 +412,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
     float acc[S::kMt][NT][4], ref[NT][2], sum[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      ref[j][0] = ref[j][1] = kNone;
+      ref[j][0] = ref[j][1] = 0.0f;
       sum[j][0] = sum[j][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < S::kMt; ++i) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
     }
-    bool bad = false;
+    bool bad = false, first_page = true;
 
     for (int i = 0; i < g.count; ++i) {
       const int key0 = (g.p + i) * kPage;  // the page's first key
@@ -429,14 +429,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
       bad |= dead || s_bad[stage];
       const uint8_t *block = ring + stage * S::kBlock;
 
-      // ---- scores
-      float s[S::kSubs][NT][4];
-      const bool work = !bad && key0 + 16 * sub0 < len;
-      if (work) {
+      if (key0 + kPage > len) {  // what the page holds behind the row's tokens may be anything: values of zero
+        uint8_t *z = ring + stage * S::kBlock + scales_at(D, 1);
+        for (int k = tid; k < D / kGroup * kPage; k += kThreads)
+          if (key0 + k % kPage >= len) z[k] = 0;
+        fence_proxy_async_smem();  // before the stage is filled again
+      }
+      // ---- scores, times their scale, less the reference
+      float y[S::kSubs][NT][4];
+      bool over = first_page;
+      if (!bad) {
 #pragma unroll
         for (int u = 0; u < S::kSubs; ++u)
 #pragma unroll
-          for (int j = 0; j < NT; ++j) s[u][j][0] = s[u][j][1] = s[u][j][2] = s[u][j][3] = 0.0f;
+          for (int j = 0; j < NT; ++j) y[u][j][0] = y[u][j][1] = y[u][j][2] = y[u][j][3] = 0.0f;
         // a chunk of up to 32 channels (16 bytes) of each key at a time
         constexpr int CH = D < 128 ? 16 : 32, CHUNKS = D / 4 / CH;
 #pragma unroll
@@ -484,24 +490,38 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
                     b = s_q[(step * NT + j) * 32 + lane];
 #pragma unroll
                   for (int u = 0; u < S::kSubs; ++u)
-                    mma(s[u][j], va[u][2 * k], vb[u][2 * k], va[u][2 * k + 1], vb[u][2 * k + 1], b.x, b.y);
+                    mma(y[u][j], va[u][2 * k], vb[u][2 * k], va[u][2 * k + 1], vb[u][2 * k + 1], b.x, b.y);
                 }
               }
             }
           }
         }
+#pragma unroll
+        for (int u = 0; u < S::kSubs; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[u][j][k] = fmaf(y[u][j][k], f[j][k & 1], -ref[j][k & 1]);
+        if (key0 + kPage > least) {
+#pragma unroll
+          for (int u = 0; u < S::kSubs; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (key0 + (sub0 + u) * 16 + (k < 2 ? k_a : k_b) >= sees[j][k & 1]) y[u][j][k] = -INFINITY;
+        }
+        float top = y[0][0][0];
+#pragma unroll
+        for (int u = 0; u < S::kSubs; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, y[u][j][k]);
+        over = __any_sync(0xffffffffu, top > kLag) || first_page;
       }
       // ---- probabilities, to the warps that need them
       uint2 *to = s_p + buf * (4 * NT * 32);
-      const bool edge = key0 + 64 > least;
-      auto exponents = [&](int u, int j, float (&y)[4]) {
-        const int ja = key0 + (sub0 + u) * 16 + k_a, jb = key0 + (sub0 + u) * 16 + k_b;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          y[k] = fmaf(s[u][j][k], f[j][k & 1], -ref[j][k & 1]);
-          if (edge && (k < 2 ? ja : jb) >= sees[j][k & 1]) y[k] = -INFINITY;
-        }
-      };
       float add[NT][2];  // the lane's share of the sums
       auto hand_over = [&] {
 #pragma unroll
@@ -510,46 +530,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
         for (int u = 0; u < S::kSubs; ++u)
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            float y[4];
-            exponents(u, j, y);
+            float e[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = ex2(y[k]);
-            add[j][0] += y[0] + y[2];
-            add[j][1] += y[1] + y[3];
+            for (int k = 0; k < 4; ++k) e[k] = ex2(y[u][j][k]);
+            add[j][0] += e[0] + e[2];
+            add[j][1] += e[1] + e[3];
             uint2 p;
-            p.x = transpose(bits(__floats2half2_rn(y[0], y[1])));
-            p.y = transpose(bits(__floats2half2_rn(y[2], y[3])));
+            p.x = transpose(bits(__floats2half2_rn(e[0], e[1])));
+            p.y = transpose(bits(__floats2half2_rn(e[2], e[3])));
             to[((sub0 + u) * NT + j) * 32 + lane] = p;
           }
       };
-      bool over = false;
-      if (work) {
-#pragma unroll
-        for (int u = 0; u < S::kSubs; ++u)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            float y[4];
-            exponents(u, j, y);
-            over |= fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > kLag;
-          }
-        over = __any_sync(0xffffffffu, over);
-        if (!over) hand_over();
-      }
+      if (!bad && !over) hand_over();
       const bool moved = __syncthreads_or(over);
       if (tid == 0) copy(stage == 0 ? S::kStages - 1 : stage - 1);  // all warps have left the page before
-      if (moved) {  // the references move to the columns' maxima so far
+      if (moved) {  // the references move to the columns' maxima so far, always at a unit's first page here
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float top = ref[j][k];
-            if (work) {
+            float top = first_page ? kNone : 0.0f;
+            if (!bad) {
 #pragma unroll
-              for (int u = 0; u < S::kSubs; ++u) {
-                const int ja = key0 + (sub0 + u) * 16 + k_a, jb = key0 + (sub0 + u) * 16 + k_b;
-                if (!edge || ja < sees[j][k]) top = fmaxf(top, s[u][j][k] * f[j][k]);
-                if (!edge || jb < sees[j][k]) top = fmaxf(top, s[u][j][k + 2] * f[j][k]);
-              }
+              for (int u = 0; u < S::kSubs; ++u) top = fmaxf(top, fmaxf(y[u][j][k], y[u][j][k + 2]));
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             }
@@ -561,11 +564,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
           float fade[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float top = s_top[0][8 * j + 2 * t + k];
+            float up = s_top[0][8 * j + 2 * t + k];
 #pragma unroll
-            for (int w = 1; w < W; ++w) top = fmaxf(top, s_top[w][8 * j + 2 * t + k]);
-            fade[k] = ex2(ref[j][k] - top);
-            ref[j][k] = top;
+            for (int w = 1; w < W; ++w) up = fmaxf(up, s_top[w][8 * j + 2 * t + k]);
+            // a column that sees no key of a first page sees none at all
+            if (up == kNone) up = 0.0f;
+            fade[k] = first_page ? 1.0f : ex2(-up);
+            ref[j][k] += up;
+#pragma unroll
+            for (int u = 0; u < S::kSubs; ++u) {
+              y[u][j][k] -= up;
+              y[u][j][k + 2] -= up;
+            }
           }
 #pragma unroll
           for (int m = 0; m < S::kMt; ++m)
@@ -574,21 +584,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
           sum[j][0] *= fade[0];
           sum[j][1] *= fade[1];
         }
-        if (work) hand_over();
+        if (!bad) hand_over();
         __syncthreads();
       }
-      if (work) {
+      first_page = false;
+      // ---- output: the warp's channels of 16 keys at a time
+      if (!bad) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           sum[j][0] += add[j][0];
           sum[j][1] += add[j][1];
         }
-      }
-      // ---- output: the warp's channels of 16 keys at a time
-      if (!bad) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          if (key0 + 16 * ks >= len) break;
           uint2 p[NT];
 #pragma unroll
           for (int j = 0; j < NT; ++j) p[j] = to[(ks * NT + j) * 32 + lane];
@@ -601,12 +609,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
             else
               wv[k] = *reinterpret_cast<const unsigned short *>(at);
           }
-          uint32_t e = *reinterpret_cast<const uint32_t *>(block + at_z + 16 * ks);  // 4 keys' scales
-          if (key0 + 16 * ks + 16 > len) {  // what the page holds behind the row's tokens may be anything
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (key0 + 16 * ks + 4 * t + k >= len) e &= ~(0xffu << (8 * k));
-          }
+          const uint32_t e = *reinterpret_cast<const uint32_t *>(block + at_z + 16 * ks);  // 4 keys' scales
           const Scale z0(e4m3x2(e)), z1(e4m3x2(e >> 16));
 #pragma unroll
           for (int h = 0; h < LB / 2; ++h) {
@@ -681,7 +684,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
                    make_float4(acc[m][j][k], acc[m][j][k + 2], acc[m + 1][j][k], acc[m + 1][j][k + 2]));
           if (row == 0 && warp == 0)
             __stcg(reinterpret_cast<float2 *>(A.stats + ((long long)slot * S::N + c) * 2),
-                   make_float2(bad ? __int_as_float(0x7fffffff) : ref[j][k], all));
+                   make_float2(bad ? __int_as_float(0x7fffffff) : all == 0.0f ? kNone : ref[j][k], all));
         }
       }
     if (whole) continue;
