@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
   uint2 *s_p = reinterpret_cast<uint2 *>(smem + S::kStages * S::kBlock);  // [2][4][NT][32]
   uint2 *s_q = s_p + S::kP / 8;                                          // [kSteps][NT][32]
   __shared__ __align__(8) uint64_t s_full[S::kStages];
-  __shared__ long long s_list[2 * kThreads];  // the blocks of the share's positions
+  __shared__ long long s_list[2 * kThreads];  // where the blocks of the share's positions begin
   __shared__ int s_bad[S::kStages];           // the stage's page does not exist
   __shared__ float s_top[W][S::N], s_sum[W][S::N], s_f[S::N];
   __shared__ int s_last;
@@ -273,25 +273,27 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
       const int unit = (walk.x - walk.row0) / walk.cost, p = walk.x - walk.row0 - unit * walk.cost - kSetup;
       if (p >= 0) {
         const int page = A.table[(long long)walk.b * A.max_pages + p];
-        block = page >= 0 && page < A.n_pages ? (long long)page * A.hk + unit / A.tiles : kNoPage;
+        block = page >= 0 && page < A.n_pages ? ((long long)page * A.hk + unit / A.tiles) * S::kBlock : kNoPage;
       }
     }
     s_list[(i0 + tid) % (2 * kThreads)] = block;
   };
-  int ahead = 0;      // thread 0: the position whose block is copied next
-  bool dead = false;  // a wait has run out: no copy is started any more
+  uint32_t ahead = 0;  // thread 0: the position whose block is copied next
+  const uint32_t span = x1 - x0;
+  bool dead = false;   // a wait has run out: no copy is started any more
   auto copy = [&](int stage) {  // thread 0; the stage is free
-    long long block = kNothing;
-    if (dead) return;
-    while (block == kNothing && x0 + ahead < x1) block = s_list[ahead++ % (2 * kThreads)];
-    if (block == kNothing) return;
+    long long block;
+    do {
+      if (ahead >= span || dead) return;
+      block = s_list[ahead++ % (2 * kThreads)];
+    } while (block == kNothing);
     s_bad[stage] = block < 0;
     if (block < 0) {
       set_status(A.status, GDN_ERR_INDEX);
       mbar_arrive(&s_full[stage]);
     } else {
       mbar_arrive_expect_tx(&s_full[stage], S::kBlock);
-      bulk_g2s(ring + stage * S::kBlock, A.pool + block * S::kBlock, S::kBlock, &s_full[stage]);
+      bulk_g2s(ring + stage * S::kBlock, A.pool + block, S::kBlock, &s_full[stage]);
     }
   };
   // ---- the queries of a unit's tile: column `row`, channels t D/4 .. of it; the first unit's as early as may be
