@@ -510,9 +510,8 @@ def cache_fork(page_table, kv_len, page_table_out, kv_len_out, kv_index, page_sr
                n_new=None, pinned=None, state_idx=None, state_idx_out=None, state_src=None, state_dst=None, stream=None):
     """gdn_cache_fork: rows become copies of the rows parent int32 [R] and take n_new tokens (kv_index int32 [R, T]);
     page_src / page_dst and state_src / state_dst int32 [R] are slots_copy's."""
-    rows = page_table.shape[0]
-    width = _table(page_table)
-    if _table(page_table_out, rows) != width:
+    rows, width = page_table.shape[0], _table(page_table)
+    if page_table_out.shape != page_table.shape or _table(page_table_out) != width:
         raise ValueError("page_table and page_table_out must have one shape")
     T = 0 if kv_index is None else kv_index.shape[1]
     dims = ForkDims(rows, T, width, n_pages)
@@ -525,14 +524,16 @@ def cache_fork(page_table, kv_len, page_table_out, kv_len_out, kv_index, page_sr
 def slots_copy(pools, stream=None):
     """gdn_slots_copy: pools (at most MAX_SLOT_POOLS) of (tensor [n_layers, n_slots, ...], src, dst int32 [n]): in every
     layer slot src[i] is copied to slot dst[i]; -1 skips a pair."""
-    arr = (SlotPool * max(1, len(pools)))()
-    for a, (x, src, dst) in zip(arr, pools):
-        if not x.is_contiguous() or x.dim() < 2 or src.numel() != dst.numel():
+    args = []
+    for x, src, dst in pools:
+        shape, n = x.shape, src.numel()
+        if not x.is_contiguous() or len(shape) < 2 or n != dst.numel():
             raise ValueError("a pool must be a dense tensor [n_layers, n_slots, ...], src and dst of one length")
-        layers, n = x.shape[0], x.shape[1]
-        a.base, a.src, a.dst, a.n, a.n_layers, a.n_slots = _ptr(x), _ptr(src), _ptr(dst), src.numel(), layers, n
-        a.slot_bytes = x.numel() // max(1, layers * n) * x.element_size()
-    _check(load_library().gdn_slots_copy(arr, len(pools), _stream(stream)))
+        slot = 1
+        for d in shape[2:]:
+            slot *= d
+        args.append(SlotPool(x.data_ptr(), src.data_ptr(), dst.data_ptr(), slot * x.element_size(), n, shape[0], shape[1]))
+    _check(load_library().gdn_slots_copy((SlotPool * max(1, len(args)))(*args), len(args), _stream(stream)))
 
 
 def check_status(stream=None):
