@@ -327,7 +327,7 @@ extern "C" gdn_status gdn_cache_fork(const gdn_fork_dims *d, const int32_t *pare
   const size_t smem = (size_t)(d->n_pages + 31) / 32 * 4;
   static std::atomic<uint64_t> ready{0};  // a bit a device: the attribute holds for the process
   const uint64_t bit = 1ull << dev->id;
-  if (smem > 8192 && !(ready.load(std::memory_order_relaxed) & bit)) {
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {  // beside the kernel's own 41 KB the default allows 6
     if (cudaFuncSetAttribute(fork::fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fork::kMaxPages / 8) !=
         cudaSuccess)
       return check_launch("cache_fork");
