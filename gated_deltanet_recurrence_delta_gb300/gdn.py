@@ -28,6 +28,7 @@ EXPORTS = ("gdn_decode_step", "gdn_verify_with_checkpoints", "gdn_prefill_chunke
 MAX_OVERLAPPED_COPIES = 8
 MAX_SLOT_POOLS = 4
 PAGE_TOKENS = 64
+ATTN_KV4_ZEROS = 24576
 
 
 class GdnError(RuntimeError):

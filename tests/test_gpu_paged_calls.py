@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from gated_deltanet_recurrence_delta_gb300 import gdn
+from gated_deltanet_recurrence_delta_gb300.hybrid import PagedAttentionLayers
 
 pytestmark = pytest.mark.gpu
 PAGE = 64
@@ -40,3 +41,49 @@ gdn.check_status()
 assert (out.tolist(), new.tolist(), index.tolist()) == ([[7, 59999]], [65], [[59999 * 64]]), (out, new, index)
 """
     subprocess.run([sys.executable, "-c", code], check=True, cwd=Path(__file__).resolve().parents[1], timeout=300)
+
+
+def _layers(rows=3, hq=4, hk=2, d=64):
+    inv = 1e4 ** (-torch.arange(0, 32, 2, dtype=torch.float64, device="cuda") / 32)
+    weights = [dict(q_norm=None, k_norm=None)]
+    return PagedAttentionLayers(hq, hk, d, weights, inv, rows, 64, 16)
+
+
+def _prompts(att, lens, seed=5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    index = att.take(max(lens), n_new=_ints(lens))
+    kv_index = torch.cat([index[r, :n] for r, n in enumerate(lens)])
+    n = sum(lens)
+    qkv = torch.randn((n, (att.hq + 2 * att.hk) * att.d), generator=g, device="cuda").to(torch.bfloat16)
+    q, out = (torch.empty((n, att.hq, att.d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    att.prefill(0, qkv, list(range(len(lens))), lens, [0] * len(lens), kv_index, q, out)
+    gdn.check_status()
+    return out
+
+
+def test_graphs_that_share_a_workspace_replay_in_any_order():
+    """Two graphs captured from one stream before anything ran on it: the second is replayed first, its workspace's
+    counters full of ones."""
+    lens = [700, 64, 5]
+    eager, att = _layers(), _layers()
+    for x in (eager, att):
+        _prompts(x, lens)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    qkv = torch.randn((2, 3, 1, (att.hq + 2 * att.hk) * att.d), generator=g, device="cuda").to(torch.bfloat16)
+    new = lambda: torch.empty((2, 3, 1, att.hq, att.d), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    want, got, q = new(), new(), new()
+    for i in (1, 0):
+        eager.step(0, qkv[i], eager.take(1), q[i], want[i])
+    torch.cuda.synchronize()
+    graphs, side = [torch.cuda.CUDAGraph() for _ in range(2)], torch.cuda.Stream()
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph, stream=side):
+            att.step(0, qkv[i], att.take(1), q[i], got[i])
+    for key, x in att.buffers.items():
+        if key[0] == "workspace" and key[2] == side.cuda_stream:
+            x[:gdn.ATTN_KV4_ZEROS].view(torch.int32).fill_(1)
+    for i in (1, 0):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    gdn.check_status()
+    assert torch.equal(got, want) and torch.equal(att.kv_len, eager.kv_len)
