@@ -262,14 +262,16 @@ class Beams:
         self.scores[:, 0] = 0.0
         self.parent = torch.arange(groups * beams, dtype=torch.int32, device=device).view(groups, beams)
         self.token = new(torch.int32, -1)
-        self.workspace = None
+        self.workspaces = {}  # a captured step keeps the one of its logits
 
     def select(self, logits, eos=-1, stream=None):
         """The best continuations, from the rows' logits [groups, beams, V] (fp32 or bf16)."""
-        if self.workspace is None:
-            self.workspace = gdn.beam_workspace(logits)
-        gdn.beam_select(logits, self.scores, self.parent, self.token, self.scores, self.workspace, done=self.done,
-                        new_done=self.done, eos=eos, stream=stream)
+        if logits.shape[:2] != self.scores.shape:
+            raise ValueError(f"logits must be {list(self.scores.shape)} rows, they are {list(logits.shape[:2])}")
+        if logits.shape not in self.workspaces:
+            self.workspaces[logits.shape] = gdn.beam_workspace(logits)
+        gdn.beam_select(logits, self.scores, self.parent, self.token, self.scores, self.workspaces[logits.shape],
+                        done=self.done, new_done=self.done, eos=eos, stream=stream)
 
 
 def beam_step(stack, attention, beams, acts, qkv, logits, state_idx, buffers, eos=-1):

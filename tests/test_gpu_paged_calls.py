@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from gated_deltanet_recurrence_delta_gb300 import gdn
-from gated_deltanet_recurrence_delta_gb300.hybrid import PagedAttentionLayers
+from gated_deltanet_recurrence_delta_gb300.hybrid import Beams, PagedAttentionLayers
 
 pytestmark = pytest.mark.gpu
 PAGE = 64
@@ -87,3 +87,20 @@ def test_graphs_that_share_a_workspace_replay_in_any_order():
     torch.cuda.synchronize()
     gdn.check_status()
     assert torch.equal(got, want) and torch.equal(att.kv_len, eager.kv_len)
+
+
+def test_selections_over_vocabularies_of_several_sizes():
+    g = torch.Generator(device="cuda").manual_seed(7)
+    beams, single = Beams(2, 4), Beams(2, 4)
+    for V in (50, 40000, 9000, 40000):
+        logits = torch.randn((2, 4, V), generator=g, device="cuda")
+        fresh = Beams(2, 4)
+        fresh.scores.copy_(single.scores), fresh.done.copy_(single.done)
+        for b in (beams, fresh):
+            b.select(logits, eos=3)
+        gdn.check_status()
+        single = fresh
+        for n in ("scores", "done", "parent", "token"):
+            assert torch.equal(getattr(beams, n), getattr(fresh, n))
+    with pytest.raises(ValueError):
+        beams.select(logits[:, :3])
