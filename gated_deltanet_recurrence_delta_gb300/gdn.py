@@ -72,7 +72,6 @@ class AttnDims(ctypes.Structure):
 class Kv4Dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_kv_heads", "head_dim", "n_pages", "k_exp", "v_exp")] + [
         (n, ctypes.c_int64) for n in ("k_stride", "v_stride")]
-    _made_of = (None, None)
 
 
 class AttnKv4Dims(ctypes.Structure):
@@ -432,28 +431,20 @@ def kv4_pool(n_pages, n_kv_heads, head_dim, device="cuda") -> torch.Tensor:
 def make_kv4_dims(k, pool, v=None, k_exp=0, v_exp=0) -> Kv4Dims:
     """Sizes of a kv4_store / kv4_load call on k [n, Hk, d]; v's tokens are spaced as k's unless v is given."""
     n, hk, d, ks = _layout(k, "k")
-    dims = Kv4Dims(n, hk, d, _page_pool(pool, hk, d), k_exp, v_exp, ks, ks if v is None else _layout(v, "v")[3])
-    dims._made_of = k, v  # whose spacing has been looked at
-    return dims
-
-
-def _kv4_spaced(dims, k, v):
-    made_k, made_v = dims._made_of
-    if k is not made_k:
-        _spaced(k, dims.k_stride, "k")
-    if v is not made_v:
-        _spaced(v, dims.v_stride, "v")
+    return Kv4Dims(n, hk, d, _page_pool(pool, hk, d), k_exp, v_exp, ks, ks if v is None else _layout(v, "v")[3])
 
 
 def kv4_store(dims: Kv4Dims, k, v, kv_index, pool, stream=None):
     """gdn_kv4_store: k, v bf16 [n, Hk, d] into the pool rows kv_index int32 [n] (-1: not kept), 4 bits each."""
-    _kv4_spaced(dims, k, v)
+    _spaced(k, dims.k_stride, "k")
+    _spaced(v, dims.v_stride, "v")
     _check(load_library().gdn_kv4_store(ctypes.byref(dims), *_ptrs(k, v, kv_index, pool), _stream(stream)))
 
 
 def kv4_load(dims: Kv4Dims, pool, kv_index, k, v, stream=None):
     """gdn_kv4_load: pool rows kv_index int32 [n] to k, v bf16 [n, Hk, d], exactly as attn_kv4 uses them."""
-    _kv4_spaced(dims, k, v)
+    _spaced(k, dims.k_stride, "k")
+    _spaced(v, dims.v_stride, "v")
     _check(load_library().gdn_kv4_load(ctypes.byref(dims), *_ptrs(pool, kv_index, k, v), _stream(stream)))
 
 

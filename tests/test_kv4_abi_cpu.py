@@ -205,3 +205,15 @@ def test_plain_fork_by_hand():
     assert r["state_idx"] == [5, 7, 6] and r["state_src"] == [-1, 5, -1] and r["state_dst"] == [-1, 7, -1]
     r = kv4_plain.fork(table, lens, 5, 60, parent=[0, 1, 2], pinned=[0, 0, 0, 1, 0])
     assert r["full"] and r["kv_len"] == [130 - 60, 64, 63]  # both rows that need a page find none
+
+
+def test_binding_looks_at_strides_in_every_call():
+    """Also where the sizes were made from that very tensor, which has been laid out anew since."""
+    pool = torch.zeros((2, 2, 72 * 64), dtype=torch.uint8)
+    k = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    v, index = k.clone(), torch.zeros(4, dtype=torch.int32)
+    dims = gdn.make_kv4_dims(k, pool)
+    k.as_strided_((3, 2, 64), (144, 64, 1))
+    for call in (lambda: gdn.kv4_store(dims, k, v, index, pool), lambda: gdn.kv4_load(dims, pool, index, v, k)):
+        with pytest.raises(ValueError):
+            call()
