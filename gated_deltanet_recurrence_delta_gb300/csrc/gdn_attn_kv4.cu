@@ -426,6 +426,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
       if (!dead && !mbar_wait_bounded(&s_full[stage], parity)) {
         if (lane == 0) set_status(A.status, GDN_ERR_TIMEOUT);
         dead = true;
+        // let copies already in flight land before the CTA's memory is released
+        for (int k = 0; k < S::kStages - 1 && g.x + i + k < x1; ++k)
+          (void)mbar_wait_bounded(&s_full[(stage + k) % S::kStages], parity ^ (stage + k >= S::kStages));
       }
       dead = __any_sync(0xffffffffu, dead);
       bad |= dead || s_bad[stage];
