@@ -229,6 +229,8 @@ class PagedAttentionLayers:
         that its pages hold already (host lists); take() has given the rows their pages and kv_index is the tokens' of
         it, int32 [n]. qkv bf16 [n, (hq + 2 hk) d]; q_buf, out bf16 [n, hq, d]. The new tokens attend in bf16; the past
         ones as the pages hold them."""
+        if not sum(lens):
+            return
         with _on(stream):
             dev, total = self.device, [a + b for a, b in zip(lens, past)]
             ints = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731

@@ -104,3 +104,31 @@ def test_selections_over_vocabularies_of_several_sizes():
             assert torch.equal(getattr(beams, n), getattr(fresh, n))
     with pytest.raises(ValueError):
         beams.select(logits[:, :3])
+
+
+def test_prompts_without_tokens():
+    """A chunk of which some rows, or all, have none: the others' outputs are as without them, nothing else is written."""
+    a, b = _layers(), _layers()
+    want = _prompts(a, [70, 0, 9])
+    index = b.take(70, n_new=_ints([70, 0, 9]))
+    g = torch.Generator(device="cuda").manual_seed(5)
+    qkv = torch.randn((79, (b.hq + 2 * b.hk) * b.d), generator=g, device="cuda").to(torch.bfloat16)
+    q, out = (torch.empty((79, b.hq, b.d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    b.prefill(0, qkv, [0, 2], [70, 9], [0, 0], torch.cat((index[0], index[2, :9])), q, out)
+    gdn.check_status()
+    assert torch.equal(out, want) and torch.equal(a.pool, b.pool)
+    for x in (a, b):  # a second chunk, of the last row alone
+        n = 66
+        index = x.take(n, n_new=_ints([0, 0, n]))
+        qkv = torch.randn((n, (b.hq + 2 * b.hk) * b.d), generator=g.manual_seed(8), device="cuda").to(torch.bfloat16)
+        q, out = (torch.empty((n, b.hq, b.d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        rows, lens, past = ([0, 1, 2], [0, 0, n], [70, 0, 9]) if x is a else ([2], [n], [9])
+        x.prefill(0, qkv, rows, lens, past, index[2, :n].contiguous(), q, out)
+        gdn.check_status()
+        want = out if x is a else want
+    assert torch.equal(out, want) and torch.equal(a.pool, b.pool)
+    before, none = a.pool.clone(), torch.empty((0, b.hq, b.d), dtype=torch.bfloat16, device="cuda")
+    for rows, lens, past in (([], [], []), ([0, 1], [0, 0], [70, 0])):
+        a.prefill(0, qkv[:0], rows, lens, past, a.take(0).flatten(), none, none)
+    gdn.check_status()
+    assert torch.equal(a.pool, before) and a.kv_len.tolist() == [70, 0, 75]
