@@ -35,6 +35,15 @@
 // in equal shares to a CTA each, a unit's set-up counting as kSetup pages, so a share
 // may begin and end inside a unit: of the CTAs that hold parts of one, the last to
 // finish joins them.
+//
+// 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 122.5 us, 4.9 TB/s, 73% of
+// a copy's rate. A page of a head is 660 instructions of each of two warps, half of
+// them the codes' way into operands; 62% of the issue slots and half the ALU pipe's are
+// used, the rest goes to the page's chain (wait, scores, maximum, barrier, output),
+// which 16 warps an SM do not hide entirely. 16 verify rows of 8 tokens, 16/4 heads of
+// 256 (41.6 MB, 4.5 GFLOP): 35.3 us: 32 query columns take 255 registers, so that 8
+// warps an SM are all there are, and the joins are a quarter of it. 8 decode rows of up
+// to 2048 tokens: 12 us: start, three or four pages and the join in turn, all latency.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -49,6 +58,7 @@ using namespace kv4;
 constexpr int kMaxCtas = 1536;
 constexpr float kNone = -3.0e38f;  // below every score
 constexpr float kLag = 8.0f;       // scores may exceed the reference by 2^8
+// Shares: 1 and 3 in place of either 2 are slower or the same, on all of 8, 64 and 45 decode rows and 16 verify rows.
 constexpr int kSetup = 2;          // pages that a unit's queries and output are worth
 constexpr int kLeast = 2;          // pages that are worth a CTA
 constexpr int kMostParts = 64;     // of a unit, on the average
@@ -69,9 +79,14 @@ struct Args {
   unsigned int *status;
 };
 
+// The variant for head size D and tiles of 8 NT query columns (tiles_at_once: as few as hold a key head's columns,
+// since a page's codes are turned into operands once for all of them).
+// Stages and CTAs of an SM share its memory and registers. One column tile of 128: 2 stages and 8 CTAs (64 rows of
+// 8192 tokens 123 us; 3 stages and 6 CTAs 126; 10 CTAs, whose registers spill, 169). Four tiles of 256: 3 stages and 2
+// CTAs of 255 registers (16 verify rows 35 us; 3 CTAs, which spill, 71).
 template <int D, int NT>
 struct Shape {
-  static constexpr int W = D == 256 ? 4 : 2;     // warps
+  static constexpr int W = D == 256 ? 4 : 2;     // warps: each holds D / W channels' outputs in registers
   static constexpr int kThreads = 32 * W;
   static constexpr int kSubs = 4 / W;            // 16 keys each that a warp scores
   static constexpr int N = 8 * NT;               // query columns

