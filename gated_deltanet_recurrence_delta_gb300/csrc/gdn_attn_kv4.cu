@@ -33,17 +33,19 @@
 // a page's barrier all warps have left the page before it, so its stage is filled
 // again right behind it. The (row, key head, query tile, page) sequence is dealt out
 // in equal shares to a CTA each, a unit's set-up counting as kSetup pages, so a share
-// may begin and end inside a unit: of the CTAs that hold parts of one, the last to
-// finish joins them.
+// may begin and end inside a unit, whose parts a second kernel joins. (Joined by the
+// last CTA to finish, 16 verify rows take 35 us in place of 28.7, 8 decode rows 12.0 in
+// place of 10.7: one SM then reads all of a unit's parts, behind an exchange of
+// counters; 64 long decode rows, of few parts, are 1 us faster that way.)
 //
-// 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 122.5 us, 4.9 TB/s, 73% of
+// 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 123.4 us, 4.9 TB/s, 72% of
 // a copy's rate. A page of a head is 660 instructions of each of two warps, half of
 // them the codes' way into operands; 62% of the issue slots and half the ALU pipe's are
 // used, the rest goes to the page's chain (wait, scores, maximum, barrier, output),
 // which 16 warps an SM do not hide entirely. 16 verify rows of 8 tokens, 16/4 heads of
-// 256 (41.6 MB, 4.5 GFLOP): 35.3 us: 32 query columns take 255 registers, so that 8
-// warps an SM are all there are, and the joins are a quarter of it. 8 decode rows of up
-// to 2048 tokens: 12 us: start, three or four pages and the join in turn, all latency.
+// 256 (41.6 MB, 4.5 GFLOP): 28.7 us: 32 query columns take 249 registers, so that 8
+// warps an SM are all there are. 8 decode rows of up to 2048 tokens: 10.7 us: start,
+// two pages and the join in turn, all latency.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -62,7 +64,8 @@ constexpr float kLag = 8.0f;       // scores may exceed the reference by 2^8
 constexpr int kSetup = 2;          // pages that a unit's queries and output are worth
 constexpr int kLeast = 2;          // pages that are worth a CTA
 constexpr int kMostParts = 64;     // of a unit, on the average
-constexpr int kFan = 16;           // parts that are joined at a time
+constexpr int kJoin = 256;         // threads of a join, each with 4 channels of a column
+constexpr int kFan = 16;           // parts whose loads it has in flight: a lane of 16 has the statistics of each
 constexpr int kMargin = 16;        // positions that the copies may be ahead
 
 struct Args {
@@ -73,7 +76,7 @@ struct Args {
   const uint8_t *pool;
   const int32_t *table, *kv_len, *q_len;
   bf16 *out;
-  int *count;    // [2][2 kMaxCtas]: parts of a group, groups of a unit that are done; zero between calls
+  int ctas;      // of the attention kernel
   float *stats;  // [2 gridDim.x][columns][2]: reference, sum; a NaN reference: the row is bad
   float *part;   // [2 gridDim.x][columns][D]
   unsigned int *status;
@@ -161,6 +164,47 @@ struct Deal {
   }
 };
 
+// What all rows cost, found by each warp alone: a lane takes `per` of them.
+struct Rows {
+  int r0, per, mine, upto, real;  // the lane's first row, its rows' cost, that and all before, rows that have any
+  __device__ __forceinline__ Rows(const Args &A, int lane) {
+    per = (A.B + 31) / 32;
+    r0 = min(A.B, lane * per);
+    const int r1 = min(A.B, r0 + per);
+    mine = real = 0;
+    for (int b = r0; b < r1; ++b) {
+      const int c = row_cost(A, b);
+      mine += c;
+      real += c > 0;
+    }
+    upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    real = __reduce_add_sync(0xffffffffu, real);
+  }
+  __device__ __forceinline__ Deal deal(const Args &A, int units, int ctas) const {
+    const int total = __shfl_sync(0xffffffffu, upto, 31) * units;
+    return Deal(total, min(min(ctas, total / kLeast), (int)min((long long)real * units * kMostParts, (long long)ctas)));
+  }
+  // The row of position w.x, which is one of the sequence's.
+  __device__ __forceinline__ void find(const Args &A, int units, Walk &w) const {
+    const int owner = __ffs(__ballot_sync(0xffffffffu, w.x < upto * units)) - 1;
+    int at = r0, cost = mine, first = (upto - mine) * units;
+    if (per > 1 && (threadIdx.x & 31) == owner)
+      for (at = r0;; ++at) {
+        cost = row_cost(A, at);
+        if (w.x < first + cost * units) break;
+        first += cost * units;
+      }
+    w.b = __shfl_sync(0xffffffffu, at, owner);
+    w.cost = __shfl_sync(0xffffffffu, cost, owner);
+    w.row0 = __shfl_sync(0xffffffffu, first, owner);
+  }
+};
+
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   asm volatile(
@@ -228,7 +272,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
   __shared__ long long s_list[2 * kThreads];  // where the blocks of the share's positions begin
   __shared__ int s_bad[S::kStages];           // the stage's page does not exist
   __shared__ float s_top[W][S::N], s_sum[W][S::N], s_f[S::N];
-  __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -241,42 +284,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 
   // ---- the share
   const int units = A.hk * A.tiles, N = gridDim.x, cta = blockIdx.x;
-  // every warp finds it by itself: a lane takes `per` rows
-  const int per = (A.B + 31) / 32;
-  const int r0 = min(A.B, lane * per), r1 = min(A.B, r0 + per);
-  int mine = 0, rows = 0;
-  for (int b = r0; b < r1; ++b) {
-    const int c = row_cost(A, b);
-    mine += c;
-    rows += c > 0;
-  }
-  int upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  rows = __reduce_add_sync(0xffffffffu, rows);
-  const int total = __shfl_sync(0xffffffffu, upto, 31) * units;
-  const Deal deal(total, min(min(N, total / kLeast), (int)min((long long)rows * units * kMostParts, (long long)N)));
+  const Rows rows(A, lane);
+  const Deal deal = rows.deal(A, units, N);
   Walk share;
   share.x = cta < deal.used ? deal.start(cta) : 0;
   share.x1 = cta < deal.used ? deal.start(cta + 1) : 0;
   const int x0 = share.x, x1 = share.x1;
   const bool any_share = x0 < x1;
-  if (any_share) {
-    const int owner = __ffs(__ballot_sync(0xffffffffu, x0 < upto * units)) - 1;
-    int at = r0, cost = mine, first = (upto - mine) * units;
-    if (per > 1 && lane == owner)
-      for (at = r0;; ++at) {
-        cost = row_cost(A, at);
-        if (x0 < first + cost * units) break;
-        first += cost * units;
-      }
-    share.b = __shfl_sync(0xffffffffu, at, owner);
-    share.cost = __shfl_sync(0xffffffffu, cost, owner);
-    share.row0 = __shfl_sync(0xffffffffu, first, owner);
-  }
+  if (any_share) rows.find(A, units, share);
 
   // ---- the blocks of the share, kThreads positions at a time
   Walk walk = share;
@@ -707,118 +722,88 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
                    make_float2(bad ? __int_as_float(0x7fffffff) : all == 0.0f ? kNone : ref[j][k], all));
         }
       }
-    if (whole) continue;
+  }
+}
 
-    // ---- the unit's parts: the last CTA of up to kFan joins theirs, the last of those the unit's
-    const int i0 = deal.owner(g0.first), n = deal.owner(g0.end - 1) - i0 + 1;  // the CTAs that hold one
-    auto slot_of = [&](int k) { return k == 0 ? 2 * i0 + 1 : 2 * (i0 + k); };
-    auto arrive = [&](int *count, int most) {  // true for the last
-      __syncthreads();
-      if (tid == 0) {
-        int before;  // releases what the CTA has written, acquires what the others have
-        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
-        if (before == most - 1) *count = 0;
-        s_last = before == most - 1;
-      }
-      __syncthreads();
-      return s_last != 0;
-    };
-    auto join = [&](int k0, int k1, int step, bool final) {  // parts k0, k0 + step .. below k1
-      constexpr int M = D / (16 * W);      // 16-byte pieces of 8 columns that a thread joins
-      constexpr int H = NT == 4 ? 8 : D == 256 ? 4 : 2;  // as the registers allow
-      bool lost = false;
-#pragma unroll 1
-      for (int j = 0; 8 * j < min(S::N, cols - col0); ++j) {
-        float4 o[M];
-#pragma unroll
-        for (int m = 0; m < M; ++m) o[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        // lane: column lane % 8 of parts lane / 8 + 4 i, kFan parts at a time
-        const int c = lane & 7;
-        const bool real = col0 + 8 * j + c < cols;
-        float top = kNone, l = 0.0f;
-#pragma unroll 1
-        for (int kb = k0; kb < k1; kb += kFan * step) {
-          float2 st[kFan / 4];
-          float next = top;
-#pragma unroll
-          for (int i = 0; i < kFan / 4; ++i) {
-            const int k = kb + (lane / 8 + 4 * i) * step;
-            st[i] = make_float2(kNone, 0.0f);
-            if (k < k1 && real) st[i] = __ldcg(reinterpret_cast<const float2 *>(A.stats) + (long long)slot_of(k) * S::N + 8 * j + c);
-          }
-#pragma unroll
-          for (int i = 0; i < kFan / 4; ++i) {
-            lost |= st[i].x != st[i].x;
-            next = fmaxf(next, st[i].x);
-          }
-          next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 8));
-          next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 16));
-          const float fade = ex2(top - next);
-          top = next;
-          l *= fade;
-#pragma unroll
-          for (int i = 0; i < kFan / 4; ++i) {
-            st[i].x = ex2(st[i].x - next);
-            l += st[i].x * st[i].y;
-          }
-#pragma unroll
-          for (int m = 0; m < M; ++m) {
-            const float y = __shfl_sync(0xffffffffu, fade, (m * kThreads + tid) / (D / 4));
-            o[m].x *= y, o[m].y *= y, o[m].z *= y, o[m].w *= y;
-          }
-#pragma unroll
-          for (int i = 0; i < kFan / H; ++i) {  // the loads of H parts together
-            if (kb + H * i * step >= k1) break;
-            float4 x[H][M];
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-#pragma unroll
-              for (int m = 0; m < M; ++m) {
-                const int k = kb + (H * i + h) * step, cm = (m * kThreads + tid) / (D / 4);
-                x[h][m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (k < k1 && col0 + 8 * j + cm < cols)
-                  x[h][m] = __ldcg(reinterpret_cast<const float4 *>(A.part + ((long long)slot_of(k) * S::N + 8 * j) * D) +
-                                   m * kThreads + tid);
-              }
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-#pragma unroll
-              for (int m = 0; m < M; ++m) {
-                const float w = __shfl_sync(0xffffffffu, st[(H * i + h) / 4].x, 8 * ((H * i + h) % 4) + (m * kThreads + tid) / (D / 4));
-                o[m].x += x[h][m].x * w, o[m].y += x[h][m].y * w, o[m].z += x[h][m].z * w, o[m].w += x[h][m].w * w;
-              }
-          }
-        }
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        lost = __any_sync(0xffffffffu, lost);
-        if (!final) __syncthreads();  // all have read the part that is written over
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-          const int cm = (m * kThreads + tid) / (D / 4), at = (m * kThreads + tid) % (D / 4) * 4, col = col0 + 8 * j + cm;
-          const float all = __shfl_sync(0xffffffffu, l, cm), most = __shfl_sync(0xffffffffu, top, cm);
-          if (col >= cols) continue;
-          if (!final) {
-            const long long to = (long long)slot_of(k0) * S::N + 8 * j + cm;
-            __stcg(reinterpret_cast<float4 *>(A.part + to * D + at), o[m]);
-            if (at == 0)
-              __stcg(reinterpret_cast<float2 *>(A.stats) + to, make_float2(lost ? __int_as_float(0x7fffffff) : most, all));
-          } else if (!lost) {
-            const int tok = col / A.G;
-            const float inv = all == 0.0f ? 0.0f : A.out_mul / all;
-            const __nv_bfloat162 a = __floats2bfloat162_rn(o[m].x * inv, o[m].y * inv);
-            const __nv_bfloat162 b = __floats2bfloat162_rn(o[m].z * inv, o[m].w * inv);
-            *reinterpret_cast<uint2 *>(out + (tok * A.hq + col - tok * A.G) * D + at) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-          }
-        }
-      }
-    };
-    const int k = cta - i0, k0 = k / kFan * kFan, k1 = min(n, k0 + kFan), groups = (n + kFan - 1) / kFan;
-    if (arrive(A.count + slot_of(k0), k1 - k0)) {
-      join(k0, k1, 1, groups == 1);
-      if (groups > 1 && arrive(A.count + 2 * kMaxCtas + slot_of(0), groups)) join(0, n, kFan, true);
+// The parts of a unit that several CTAs worked on. Where there are more units than CTAs, job blockIdx.x is the unit that
+// CTA blockIdx.x begins and does not finish, else it is a unit; kJoin pieces of 4 channels of its columns. Which unit,
+// and whose parts, is found while the attention kernel still runs.
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoin, 3) join_kernel(const __grid_constant__ Args A) {
+  constexpr int N = 8 * NT, E = D / 4;
+  const int lane = threadIdx.x & 31, units = A.hk * A.tiles, job = blockIdx.x;
+  const Rows rows(A, lane);
+  const Deal deal = rows.deal(A, units, A.ctas);
+  Walk w;
+  int unit, i0, n = 0;
+  if (A.B * (long long)units <= A.ctas) {
+    w.b = job / units;
+    unit = job - w.b * units;
+    w.cost = row_cost(A, w.b);
+    w.row0 = 0;
+    if (w.cost > 0) {
+      const int lanes = w.b / rows.per;
+      w.row0 = __shfl_sync(0xffffffffu, rows.upto - rows.mine, lanes);
+      for (int b = lanes * rows.per; b < w.b; ++b) w.row0 += row_cost(A, b);
+      w.row0 *= units;
+      i0 = deal.owner(w.row0 + unit * w.cost + kSetup);
+      n = deal.owner(w.row0 + (unit + 1) * w.cost - 1) - i0 + 1;
     }
+  } else if (job + 1 < deal.used) {
+    w.x = deal.start(job + 1);
+    rows.find(A, units, w);
+    unit = (w.x - w.row0) / w.cost;
+    i0 = job;
+    const int first = w.row0 + unit * w.cost + kSetup;
+    if (first >= deal.start(job) && first < w.x) n = deal.owner(first - kSetup + w.cost - 1) - i0 + 1;
+  }
+  griddep_wait();
+  griddep_trigger();
+  if (n < 2) return;
+#pragma unroll 1
+  for (int piece = blockIdx.y * kJoin; piece < N * E; piece += gridDim.y * kJoin) {
+    const int head = unit / A.tiles, e = piece + threadIdx.x, c = e / E, col = (unit - head * A.tiles) * N + c;
+    if (c - lane / E >= N || col - lane / E >= A.T * A.G) return;  // the warp's first column
+    const bool real = c < N && col < A.T * A.G;
+    const float4 *part = reinterpret_cast<const float4 *>(A.part) + e;
+    const float2 *stats = reinterpret_cast<const float2 *>(A.stats) + c;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float top = kNone, l = 0.0f;
+    bool lost = false;
+    auto slot = [&](int k) { return 2 * (i0 + k) + (k == 0); };
+#pragma unroll 1
+    for (int k = 0; k < n; k += kFan) {
+      float4 x[kFan];
+      float2 st = make_float2(kNone, 0.0f);  // lane: its column of part k + lane % kFan
+      if (real && k + lane % kFan < n) st = __ldcg(stats + slot(k + lane % kFan) * N);
+#pragma unroll
+      for (int h = 0; h < kFan; ++h) {
+        x[h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (real && k + h < n) x[h] = __ldcg(part + slot(k + h) * (N * E));
+      }
+      lost |= st.x != st.x;
+      float next = fmaxf(top, st.x);
+#pragma unroll
+      for (int m = 1; m < kFan; m <<= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, m));
+      const float fade = ex2(top - next), mul = ex2(st.x - next);
+      top = next;
+      l = l * fade + mul * st.y;
+      o.x *= fade, o.y *= fade, o.z *= fade, o.w *= fade;
+#pragma unroll
+      for (int h = 0; h < kFan; ++h) {
+        const float y = __shfl_sync(0xffffffffu, mul, (lane & 16) + h);
+        o.x += x[h].x * y, o.y += x[h].y * y, o.z += x[h].z * y, o.w += x[h].w * y;
+      }
+    }
+#pragma unroll
+    for (int m = 1; m < kFan; m <<= 1) l += __shfl_xor_sync(0xffffffffu, l, m);
+    if (__any_sync(0xffffffffu, lost)) return;  // the row is bad: all its columns are
+    if (!real) continue;
+    const int tok = col / A.G;
+    const float inv = l == 0.0f ? 0.0f : A.out_mul / l;
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), y1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    bf16 *out = A.out + (((long long)w.b * A.T + tok) * A.hq + head * A.G + col - tok * A.G) * D + e % E * 4;
+    *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
   }
 }
 
@@ -850,13 +835,11 @@ int tiles_at_once(const gdn_attn_kv4_dims *d) {
   const int cols = d->T * (d->n_q_heads / d->n_kv_heads);
   return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
 }
-constexpr size_t kCountBytes = 4 * kMaxCtas * sizeof(int);
-static_assert(kCountBytes == GDN_ATTN_KV4_ZEROS, "the counters");
 size_t stats_bytes(int NT) { return (size_t)2 * kMaxCtas * 8 * NT * 8; }
 size_t part_bytes(int D, int NT) { return (size_t)2 * kMaxCtas * 8 * NT * D * 4; }
 
 template <int D, int NT>
-gdn_status launch(const Args &A, int sms, cudaStream_t stream) {
+gdn_status launch(Args A, int sms, cudaStream_t stream) {
   using S = Shape<D, NT>;
   static std::atomic<uint64_t> ready{0};  // a bit a device: the attribute holds for the process
   const uint64_t bit = 1ull << device_info().id;
@@ -866,10 +849,15 @@ gdn_status launch(const Args &A, int sms, cudaStream_t stream) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   // no more CTAs than the rows could fill
-  const long long most = (long long)A.B * A.hk * A.tiles * (A.max_pages + kSetup) / kLeast;
+  const long long units = (long long)A.B * A.hk * A.tiles, most = units * (A.max_pages + kSetup) / kLeast;
   int ctas = sms * S::kCtas < kMaxCtas ? sms * S::kCtas : kMaxCtas;
   if (most < ctas) ctas = (int)most;
-  launch_pdl(attn_kernel<D, NT>, dim3(ctas), dim3(S::kThreads), S::kBytes, stream, A);
+  A.ctas = ctas;
+  if (launch_pdl(attn_kernel<D, NT>, dim3(ctas), dim3(S::kThreads), S::kBytes, stream, A) != cudaSuccess)
+    return check_launch("attn_kv4");
+  // a CTA takes several pieces of a unit where all would not be on the SMs at once
+  const int jobs = units < ctas ? (int)units : ctas, pieces = (S::N * D / 4 + kJoin - 1) / kJoin, fit = 3 * sms / jobs;
+  launch_pdl(join_kernel<D, NT>, dim3(jobs, fit < 1 ? 1 : fit < pieces ? fit : pieces), dim3(kJoin), 0, stream, A);
   return check_launch("attn_kv4");
 }
 
@@ -881,7 +869,7 @@ using namespace gdn;
 extern "C" size_t gdn_attn_kv4_workspace_size(const gdn_attn_kv4_dims *dims) {
   if (attn_kv4::check_dims(dims) != GDN_OK) return 0;
   const int NT = attn_kv4::tiles_at_once(dims);
-  return attn_kv4::kCountBytes + attn_kv4::stats_bytes(NT) + attn_kv4::part_bytes(dims->head_dim, NT);
+  return attn_kv4::stats_bytes(NT) + attn_kv4::part_bytes(dims->head_dim, NT);
 }
 
 extern "C" gdn_status gdn_attn_kv4(const gdn_attn_kv4_dims *dims, const void *q, const void *pool,
@@ -919,8 +907,7 @@ extern "C" gdn_status gdn_attn_kv4(const gdn_attn_kv4_dims *dims, const void *q,
   A.kv_len = kv_len;
   A.q_len = q_len;
   A.out = static_cast<bf16 *>(out);
-  A.count = static_cast<int *>(workspace);
-  A.stats = reinterpret_cast<float *>(static_cast<char *>(workspace) + attn_kv4::kCountBytes);
+  A.stats = static_cast<float *>(workspace);
   A.part = A.stats + attn_kv4::stats_bytes(NT) / 4;
   A.status = dev->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

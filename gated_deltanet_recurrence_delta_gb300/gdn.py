@@ -28,7 +28,6 @@ EXPORTS = ("gdn_decode_step", "gdn_verify_with_checkpoints", "gdn_prefill_chunke
 MAX_OVERLAPPED_COPIES = 8
 MAX_SLOT_POOLS = 4
 PAGE_TOKENS = 64
-ATTN_KV4_ZEROS = 24576
 
 
 class GdnError(RuntimeError):
@@ -465,8 +464,8 @@ def attn_kv4_workspace_size(dims: AttnKv4Dims) -> int:
 
 
 def attn_kv4_workspace(dims: AttnKv4Dims, device="cuda") -> torch.Tensor:
-    """A workspace tensor for attn_kv4 (zeros, as the first call expects), reusable from call to call on one stream."""
-    return torch.zeros(max(attn_kv4_workspace_size(dims), 1), dtype=torch.uint8, device=device)
+    """A workspace tensor for attn_kv4, reusable from call to call on one stream."""
+    return torch.empty(max(attn_kv4_workspace_size(dims), 1), dtype=torch.uint8, device=device)
 
 
 def attn_kv4(dims: AttnKv4Dims, q, pool, page_table, kv_len, out, workspace, q_len=None, stream=None):

@@ -145,26 +145,12 @@ class PagedAttentionLayers:
         self._table, self._kv_len = ints(n_rows, max_pages), ints(n_rows)
         self.page_src, self.page_dst = ints(n_rows), ints(n_rows)
         self.pinned = torch.zeros(n_pages, dtype=torch.uint8, device=device)
-        self.buffers, self.made_in_capture = {}, set()
+        self.buffers = {}
 
     def _buffer(self, name, shape, dtype, stream):
         key = (name, shape, gdn._stream(stream))
         if key not in self.buffers:
             self.buffers[key] = torch.empty(shape, dtype=dtype, device=self.device)
-        return self.buffers[key]
-
-    def _workspace(self, dims, stream):
-        """attn_kv4's, whose counters are zero between calls. Those of one made while a graph was captured are zeroed by
-        every call: the first one's zeros are that graph's own, and another of the stream may be replayed before it."""
-        key = ("workspace", gdn.attn_kv4_workspace_size(dims), gdn._stream(stream))
-        if key not in self.buffers:
-            self.buffers[key] = torch.empty(key[1], dtype=torch.uint8, device=self.device)
-            if torch.cuda.is_current_stream_capturing():
-                self.made_in_capture.add(key)
-            else:
-                self.buffers[key][:gdn.ATTN_KV4_ZEROS].zero_()
-        if key in self.made_in_capture:
-            self.buffers[key][:gdn.ATTN_KV4_ZEROS].zero_()
         return self.buffers[key]
 
     def take(self, T, parent=None, n_new=None, state_idx=None, stack=None, stream=None):
@@ -222,7 +208,8 @@ class PagedAttentionLayers:
             dims = gdn.make_kv4_dims(k, pool, k_exp=self.k_exp, v_exp=self.v_exp)
             gdn.kv4_store(dims, k, v, kv_index, pool, stream)
             dims = gdn.make_attn_kv4_dims(q_buf, pool, self.table, k_exp=self.k_exp, v_exp=self.v_exp)
-            gdn.attn_kv4(dims, q_buf, pool, self.table, self.kv_len, out, self._workspace(dims, stream), self.taken, stream)
+            workspace = self._buffer("workspace", (gdn.attn_kv4_workspace_size(dims),), torch.uint8, stream)
+            gdn.attn_kv4(dims, q_buf, pool, self.table, self.kv_len, out, workspace, self.taken, stream)
 
     def prefill(self, layer, qkv, rows, lens, past, kv_index, q_buf, out, stream=None):
         """A layer's prompts, or further chunks of them: sequence i is lens[i] tokens of row rows[i], behind past[i] tokens

@@ -608,11 +608,9 @@ typedef struct gdn_attn_kv4_dims {
  *               in the pool already); 0: the row's outputs are zeros
  *   q_len       int32 [B] in [0, T], the row's real tokens, or NULL (T each)
  *   out         bf16 [B][T][n_q_heads][head_dim]
- *   workspace   gdn_attn_kv4_workspace_size(dims) bytes, 256-byte aligned. Its
- *               first GDN_ATTN_KV4_ZEROS bytes are zero before a call and again
- *               after it (zero them once; anew after GDN_ERR_TIMEOUT); the rest
- *               need not be preserved. Calls that may overlap (on several
- *               streams) need one each.
+ *   workspace   gdn_attn_kv4_workspace_size(dims) bytes, 256-byte aligned; its
+ *               contents need not be preserved. Calls that may overlap (on
+ *               several streams) need one each.
  * Token t sees keys j <= kv_len - q_len + t; a token that sees nothing, or with
  * t >= q_len, gets zeros. Keys and values enter the products exactly, queries
  * in fp16 relative to their head's largest channel (error below 2^-25 of it),
@@ -621,7 +619,6 @@ typedef struct gdn_attn_kv4_dims {
  * device error (GDN_ERR_INDEX): outputs of that row are not written. What the
  * last page holds behind the row's tokens is never used, whatever it is; values
  * that are not finite within a row may also reach its earlier tokens of the call. */
-#define GDN_ATTN_KV4_ZEROS 24576
 gdn_status gdn_attn_kv4(const gdn_attn_kv4_dims *dims, const void *q, const void *pool, const int32_t *page_table,
                         const int32_t *kv_len, const int32_t *q_len, void *out, void *workspace,
                         size_t workspace_bytes, void *stream);

@@ -279,8 +279,7 @@ def test_results_repeat_on_streams_and_in_graphs():
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     for _ in range(3):
-        assert not bool(ws[:24576].any())  # each call leaves its counters at zero
-        ws[24576:].random_(0, 256)  # and expects nothing of the rest
+        ws.random_(0, 256)  # a call expects nothing of it
         torch.cuda.synchronize()
         gdn.attn_kv4(dims, c["q"], c["pool"], c["table"], lens, out, ws, stream=side)
         side.synchronize()
@@ -290,7 +289,7 @@ def test_results_repeat_on_streams_and_in_graphs():
         gdn.attn_kv4(dims, c["q"], c["pool"], c["table"], lens, out, ws)
     for now in ([900, 64, 3000, 1], [5, 0, 2999, 1], [0, 0, 0, 0]):
         lens.copy_(_ints(now))
-        ws[24576:].fill_(255)
+        ws.random_(0, 256)
         out.fill_(9.0)
         graph.replay()
         gdn.check_status()
