@@ -9,7 +9,7 @@
 // pass; a second kernel joins a group's slices and ranks its candidates in 64
 // bits, where alone different rows meet. (As the work of a group's last CTA the join
 // cost more: 16 x 8 beams of 131072 bf16 logits took 22 to 28 us in the variants
-// tried, 16.6 to 22 as two kernels. Its code is new to that SM, and the registers
+// tried, 15.6 to 22 as two kernels. Its code is new to that SM, and the registers
 // of both parts are the slices'.)
 //
 // A slice's best: a CTA's threads form P >= `beams` parts (8, 16 or 32). At least
@@ -19,11 +19,11 @@
 // counts how many of them are better. Equal logits in numbers beyond the list are
 // taken one after the other.
 //
-// 16 x 8 beams of 131072 bf16 logits (33.6 MB, 4.9 us at the copy rate): 16.6 us as a
-// graph, 2 TB/s; slices about 11, join 5. A logit takes 12 instructions of a thread,
-// 5 us of the issue slots (54% of them used); a slice's cuts, lists and ranking and
-// the join are latency: dependent loads and barriers.
-// 4 x 4 beams of 32000 fp32 logits: 8.2 us, of which the two launches are 4.
+// 16 x 8 beams of 131072 bf16 logits (33.6 MB, 4.9 us at the copy rate): 15.6 us as a
+// graph, 2.2 TB/s; the logits' stream 5.7 of them, a slice's start and end 3, join 3.4. A slice's cuts, lists and
+// ranking and the join are latency: dependent loads, barriers, code that is new to its
+// SM.
+// 4 x 4 beams of 32000 fp32 logits: 7.1 us, of which the two launches are 4.
 #include <cuda_fp16.h>
 
 #include "gdn_check.h"
@@ -32,7 +32,9 @@ namespace gdn {
 namespace beam {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRuns = 4;  // 16 bytes of logits each that a thread works on at a time
+// 16 bytes of logits each that a thread works on at a time, and the next in flight: what three CTAs' registers hold (4 x 4
+// beams of 32000 fp32 logits 7.05 us, 16 x 8 of 131072 bf16 ones 15.6; 4 runs 7.6 and 15.6, 5 7.0 and 16.2, 8 7.3 and more)
+constexpr int kRuns = 6;
 constexpr int kLeast = 4096;  // logits that are worth a CTA
 constexpr int kMaxBeams = 32;
 constexpr int kParts = 32, kLanes = kThreads / kParts;
@@ -151,18 +153,19 @@ __device__ __forceinline__ float part_max(float x) {  // over the lanes of a par
   return x;
 }
 
-// A number that `beams` of the parts' maxima (m: one to a lane) reach, by every warp: the smallest of 8, 16 or 32
-// parts, or, where some parts hold nothing, the one that beams - 1 others exceed.
-__device__ __forceinline__ float cut_of(float m, int beams, int lane) {
+// A number that `beams` of the parts' maxima reach, by every warp: the smallest of 8, 16 or 32 parts, or, where some
+// parts hold nothing, the one that beams - 1 others exceed.
+__device__ __forceinline__ float cut_of(const float (&most)[kParts], int beams, int lane) {
   static_assert(kParts == 32, "a part to a lane");
+  const float m = most[lane];
   float cut = m;
   if (beams <= 16) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, 1));
   if (beams <= 8) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, 2));
   cut = warp_min(cut);
   if (cut == -INFINITY) {
     int rank = 0;
-#pragma unroll 1
-    for (int j = 0; j < kParts; ++j) rank += better(__shfl_sync(0xffffffffu, m, j), j, m, lane);
+#pragma unroll 8
+    for (int j = 0; j < kParts; ++j) rank += better(most[j], j, m, lane);
     cut = __shfl_sync(0xffffffffu, m, __ffs(__ballot_sync(0xffffffffu, rank == beams - 1)) - 1);
   }
   return cut;
@@ -170,16 +173,20 @@ __device__ __forceinline__ float cut_of(float m, int beams, int lane) {
 
 constexpr int kFinal = 1024;  // candidates that are ranked in 64 bits
 
-// Group blockIdx.x. A warp sums up a row's slices; then all
-// candidates of the rows' slices are compared in fp32 against the smallest maximum
-// of as many parts of the threads as there are beams, with what fp32 may be off by:
-// what remains, a few more than `beams`, counts in 64 bits how many are better.
-// (The fp64 units do two operations a cycle per SM.) Where more remain than the
-// list holds (rows of equal logits) they are taken one after the other.
+// Group blockIdx.x. A warp sums up a row's slices; then all candidates of the rows'
+// slices are compared in fp32 against the smallest maximum of as many parts of the
+// threads as there are beams, with what fp32 may be off by: what remains, a few more
+// than `beams`, counts in 64 bits how many are better. (The fp64 units do two
+// operations a cycle per SM.) Where more remain than the list holds (rows of equal
+// logits) they are taken one after the other.
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args A) {
   __shared__ unsigned long long s_key[kFinal];
   __shared__ int s_at[kFinal], s_n, s_pick[kWarps];
+  __shared__ float s_best[kFinal];     // the candidates' logits
   __shared__ double s_add[kMaxBeams];  // score - lse
+  __shared__ float s_close[kMaxBeams], s_off[kMaxBeams];  // that in fp32, and what it may be off by
+  __shared__ float s_row[3][kMaxBeams];                   // score, maximum, sum of exponentials
+  __shared__ uint8_t s_none[kMaxBeams];                   // the beam has no candidates
   __shared__ unsigned long long s_top[kWarps];
   __shared__ float s_max[32];
   __shared__ uint8_t s_done[kMaxBeams];
@@ -213,54 +220,69 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     if (lane == 0) {
       s_done[w] = over;
       // a sum that is not finite, or of nothing, makes every candidate NaN; else it is at least 1
-      s_add[w] = over ? (double)score
-                 : score > -INFINITY && sum >= 0.75f && sum < INFINITY ? (double)score - ((double)m + log_of(sum)) : (double)NAN;
+      s_none[w] = !(score > -INFINITY && (over || (sum >= 0.75f && sum < INFINITY)));
+      s_row[0][w] = score;
+      s_row[1][w] = m;
+      s_row[2][w] = sum;
+      // log2 is 2^-22 off, of itself or of 1, and each of three roundings 2^-24; too large for fp32: by anything
+      const float log = __log2f(fmaxf(sum, 0.75f)) * 0.693147182f;
+      const float size = fabsf(score) + (over ? 0.0f : fabsf(m) + fabsf(log) + 1.0f);
+      s_close[w] = over ? score : score - (m + log);
+      s_off[w] = size < 1e37f ? 3.6e-7f * size : INFINITY;
     }
   }
   __syncthreads();
+  if (warp == kWarps - 1 && lane < W) {  // one warp, the one with the fewest candidates, while the others look at theirs
+    // (an operation in 64 bits takes 16 cycles of the SM, however few lanes it has)
+    const double lse = s_done[lane] ? 0.0 : (double)s_row[1][lane] + log_of(s_row[2][lane]);
+    s_add[lane] = (double)s_row[0][lane] - lse;
+  }
   // A candidate: c < N is place c % W of slice c / W % S of beam c / (W S), and stands for a finished beam if it is its
   // first. false: it is none.
   auto candidate = [&](int c, float &x, int t, int &w, int &at) {
     w = c / each;
     if (s_done[w]) x = 0.0f;
     at = (w << 24) + (s_done[w] ? max(A.eos, 0) : t);
-    return s_done[w] ? c == w * each : t >= 0;
+    return !s_none[w] && (s_done[w] ? c == w * each : t >= 0);
   };
   auto exact = [&](int w, float x) {
     const double y = s_add[w] + (double)x;
     return y > -INFINITY ? key_of(y) : 0ull;
   };
-  auto close = [&](int w, float x, float side) {  // the score less (side -1) or more (1) than fp32 may be off by
-    const float a = (float)s_add[w], y = a + x + side * 2.4e-7f * (fabsf(a) + fabsf(x));  // 2^-22
-    return y > -INFINITY ? y : -INFINITY;  // NaN: none
+  auto close = [&](int w, float x, float side) {  // the score less (side -1) or more (1) than fp32 may be off by, or NaN
+    const float a = s_close[w];
+    return a + x + side * (s_off[w] + 2.4e-7f * (fabsf(a) + fabsf(x)));  // 2^-22
   };
   float top = -INFINITY;
 #pragma unroll 1
   for (int c = tid; c < N; c += kThreads) {
     float x = c == tid ? x0 : __ldcg(best + c);
     int w, at;
-    if (candidate(c, x, c == tid ? at0 : __ldcg(best_at + c), w, at)) top = fmaxf(top, close(w, x, -1.0f));
+    if (candidate(c, x, c == tid ? at0 : __ldcg(best_at + c), w, at))
+      top = fmaxf(top, close(w, x, -1.0f));  // a NaN is no maximum
   }
   top = part_max(top);
   if (tid % kLanes == 0) s_max[tid / kLanes] = top;
   __syncthreads();
-  const float cut = cut_of(s_max[lane], W, lane);
+  const float cut = cut_of(s_max, W, lane);
 #pragma unroll 1
   for (int c = tid; c < N; c += kThreads) {
     float x = c == tid ? x0 : __ldcg(best + c);
     int w, at;
     if (!candidate(c, x, c == tid ? at0 : __ldcg(best_at + c), w, at)) continue;
     if (close(w, x, 1.0f) < cut) continue;
-    const unsigned long long k = exact(w, x);
-    if (k == 0) continue;
     const int i = atomicAdd(&s_n, 1);
     if (i < kFinal) {
-      s_key[i] = k;
+      s_best[i] = x;
       s_at[i] = at;
     }
   }
   __syncthreads();
   const int n = s_n;
+  if (n <= kFinal) {
+    for (int i = tid; i < n; i += kThreads) s_key[i] = exact(s_at[i] >> 24, s_best[i]);
+    __syncthreads();
+  }
   auto put = [&](int place, unsigned long long k, int at) {
     const int w = at >> 24, t = s_done[w] ? A.eos : at & 0xffffff;
     A.parent[row0 + place] = (int)(row0 + w);
@@ -274,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
       const unsigned long long k = s_key[i];
       const int at = s_at[i];
       int rank = 0;
-#pragma unroll 2
+#pragma unroll 8
       for (int j = 0; j < n; ++j) rank += s_key[j] > k || (s_key[j] == k && s_at[j] < at);
       if (rank < W) put(rank, k, at);
     }
@@ -332,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 // Slice blockIdx.x of row blockIdx.y, kRuns runs of a thread at a time, the next in
 // flight.
 template <bool HALF>
-__global__ void __launch_bounds__(kThreads, 4) slice_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(kThreads, 3) slice_kernel(const __grid_constant__ Args A) {
   constexpr int C = Run<HALF>::C, B = HALF ? 2 : 4, LIST = 512;
   __shared__ float s_max[kParts], s_red[kWarps], s_sum[kWarps];
   __shared__ uint4 s_run[LIST];  // the runs that may hold candidates, and where they begin
@@ -372,9 +394,9 @@ __global__ void __launch_bounds__(kThreads, 4) slice_kernel(const __grid_constan
   Run<HALF> ahead[kRuns];
   const float score = A.scores[row];
   const bool over = A.done && A.done[row];
-  if (score > -INFINITY && !over) {  // else its logits give no candidates
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) ahead[k] = fetch(r0 + k * kThreads + tid);
+  for (int k = 0; k < kRuns; ++k) ahead[k] = fetch(r0 + k * kThreads + tid);
+  if (score > -INFINITY && !over) {  // else its logits give no candidates
     constexpr float log2e = 1.4426950408889634f;
     float m = -INFINITY, cut = -INFINITY;  // the thread's maximum so far; at least `beams` logits reach the cut
     f2 sums = pair(0.0f, 0.0f);            // of exp(logit - m)
@@ -396,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 4) slice_kernel(const __grid_constan
         const float part = part_max(top);
         if (tid % kLanes == 0) s_max[tid / kLanes] = part;
         __syncthreads();
-        cut = cut_of(s_max[lane], A.beams, lane);
+        cut = cut_of(s_max, A.beams, lane);
         __syncthreads();
       }
 #pragma unroll
@@ -424,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 4) slice_kernel(const __grid_constan
     const float part = part_max(m);
     if (tid % kLanes == 0) s_max[tid / kLanes] = part;
     __syncthreads();
-    const float far = s_max[lane], most = warp_max(far);
-    cut = cut_of(far, A.beams, lane);
+    const float most = warp_max(s_max[lane]);
+    cut = cut_of(s_max, A.beams, lane);
     const float2 both = halves(sums);
     float sum = (both.x + both.y) * ex2((m - (most == -INFINITY ? 0.0f : most)) * log2e);
 #pragma unroll
@@ -468,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 4) slice_kernel(const __grid_constan
         const float x = s_val[i];
         const int ix = s_at[i];
         int rank = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < n; ++j) rank += better(s_val[j], s_at[j], x, ix);
         if (rank < A.beams) {
           best[rank] = x;
@@ -542,7 +564,7 @@ gdn_status check_dims(const gdn_beam_dims *d) {
 }
 
 // Slices of a row: about three CTAs for each of 152 SMs in all (16 x 8 rows of 131072 bf16 logits: 608 CTAs 22 us, 456
-// 16.6 us, 304 17.1 us: what a slice costs besides its logits, the cuts and the ranking, is half of it).
+// 15.7 us, 304 16.4 us: what a slice costs besides its logits, the cuts and the ranking, is a third of it).
 int slices_of(const gdn_beam_dims *d) {
   const int rows = d->n_groups * d->beams, want = rows > 0 ? 456 / rows : 1, most = d->vocab / kLeast;
   return want < 1 || most < 1 ? 1 : want < most ? want : most;
@@ -594,6 +616,17 @@ extern "C" gdn_status gdn_beam_select(const gdn_beam_dims *dims, const void *log
   A.best_at = reinterpret_cast<int32_t *>(A.best + rows * A.slices * dims->beams);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(A.slices, (unsigned)rows), block(beam::kThreads);
+  static std::atomic<uint64_t> ready{0};  // a bit a device: the attributes hold for the process
+  const uint64_t bit = 1ull << dev->id;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    // one split of an SM's memory for both kernels, which follow one another on it: with the driver's own choices for
+    // each 16 x 8 beams take 19.1 us, with half of it shared 15.6, all 16.3
+    bool ok = true;
+    for (auto *k : {beam::slice_kernel<true>, beam::slice_kernel<false>, beam::join_kernel})
+      ok &= cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 50) == cudaSuccess;
+    if (!ok) return check_launch("beam_select");
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   if (launch_pdl(dims->half ? beam::slice_kernel<true> : beam::slice_kernel<false>, grid, block, 0, st, A) != cudaSuccess)
     return check_launch("beam_select");
   launch_pdl(beam::join_kernel, dim3(A.groups), block, 0, st, A);

@@ -132,3 +132,28 @@ def test_prompts_without_tokens():
         a.prefill(0, qkv[:0], rows, lens, past, a.take(0).flatten(), none, none)
     gdn.check_status()
     assert torch.equal(a.pool, before) and a.kv_len.tolist() == [70, 0, 75]
+
+
+def test_selections_at_the_ends_of_fp32():
+    """Scores and logits up to the largest numbers: sums that pass fp32's range in between rank as in 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    G, W, V = 6, 4, 700
+    sizes = torch.tensor([[1.0, 1e20, 1e37, 3e38, 1e38, 1e30], [3e38, 1e25, 1e37, 3e38, 1.0, 1e30]], device="cuda")
+    logits = (2 * torch.rand((G, W, V), generator=g, device="cuda") - 1) * sizes[0, :, None, None]
+    scores = (2 * torch.rand((G, W), generator=g, device="cuda") - 1) * sizes[1, :, None]
+    assert bool(logits.isfinite().all() and scores.isfinite().all())
+    ints = lambda: torch.zeros((G, W), dtype=torch.int32, device="cuda")  # noqa: E731
+    parent, token, new = ints(), ints(), torch.empty_like(scores)
+    gdn.beam_select(logits, scores, parent, token, new, gdn.beam_workspace(logits))
+    gdn.check_status()
+    x, s = logits.double(), scores.double()
+    cand = (x + (s - torch.logsumexp(x, -1))[..., None]).flatten(1)
+    for i in range(G):
+        order = sorted(range(W * V), key=lambda j: (-float(cand[i, j]), j))[:W + 1]
+        gap = min(float(cand[i, a] - cand[i, b]) for a, b in zip(order, order[1:]))
+        top = float(s[i].abs().max() + x[i].abs().max())
+        if gap > 2.0 ** -50 * top:  # apart in 64 bits
+            assert (parent[i] - W * i).tolist() == [j // V for j in order[:W]]
+            assert token[i].tolist() == [j % V for j in order[:W]]
+        want = cand[i, order[:W]].float()
+        assert bool(((new[i] == want) | ((new[i] - want).abs() <= 2.0 ** -22 * want.abs() + 1e-5)).all())
