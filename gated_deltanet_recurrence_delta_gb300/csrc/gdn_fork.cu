@@ -7,8 +7,8 @@
 // a page in shared memory, free pages are ranked by a scan of the bits' counts,
 // and the page of rank k goes to the row whose needs cover k. Latency bounds it:
 // seven barriers, and the chain parent -> length -> last page of dependent loads.
-// 64 rows of 4000 to 8192 tokens: 8.0 us (14 as one barrier after the other and pages
-// handed out row by row); 30 rows of up to 700: 5.9 us.
+// 64 rows of 4000 to 8192 tokens: 6.8 us (14 as one barrier after the other and pages
+// handed out row by row); 30 rows of up to 700: 5.2 us.
 //
 // slots_copy is an HBM copy of 16-byte vectors; a CTA takes one piece of one
 // slot of one layer, and a skipped pair's CTAs end at once. States and conv tails
@@ -124,25 +124,34 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
       }
     }
   }
-  // ---- partly filled last pages that are to be written, and are not the row's alone
-  for (int r = warp; r < R; r += kWarps) {
-    const int n = s_len[r], at = n / kPage, page = s_tail[r];
-    if (s_new[r] == 0 || page < 0 || s_copy[r]) continue;
-    bool other = false;
-    for (int x0 = lane; x0 < R; x0 += 128) {  // four rows' loads together
+  // ---- partly filled last pages that are to be written, and are not the row's alone: two rows at a time
+  for (int r0 = warp; r0 < R; r0 += 2 * kWarps) {
+    bool look[2], other[2] = {false, false};
+    int n[2], page[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = min(r0 + q * kWarps, R - 1);
+      n[q] = s_len[r];
+      page[q] = s_tail[r];
+      look[q] = r0 + q * kWarps < R && s_new[r] > 0 && page[q] >= 0 && !s_copy[r];
+    }
+    if (!look[0] && !look[1]) continue;
+    for (int x0 = lane; x0 < R; x0 += 64) {  // the loads of two others each together
       int there[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int x = x0 + 32 * k, m = x < R ? s_len[x] : 0;
+        const int q = k & 1, r = r0 + q * kWarps, at = n[q] / kPage, x = x0 + 32 * (k >> 1), m = x < R ? s_len[x] : 0;
         there[k] = -1;
-        if (x == r || pages(m) <= at || !(m > n || (m == n && x < r))) continue;
+        if (!look[q] || x == r || pages(m) <= at || !(m > n[q] || (m == n[q] && x < r))) continue;
         // the row's own last page stands there, or a full one
         there[k] = m / kPage == at ? s_tail[x] : A.table[(long long)s_par[x] * A.width + at];
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) other |= there[k] == page;
+      for (int k = 0; k < 4; ++k) other[k & 1] |= there[k] == page[k & 1];
     }
-    if (__any_sync(0xffffffffu, other) && lane == 0) s_copy[r] = 1;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (__any_sync(0xffffffffu, look[q] && other[q]) && lane == 0) s_copy[r0 + q * kWarps] = 1;
   }
   if (bad) set_status(A.status, GDN_ERR_INDEX);
   __syncthreads();
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   s_need[tid] = upto;
   if (dead) s_dead[nth_dead] = tid;
   __syncthreads();
-  // ---- the free pages: listed by rank, and rank k goes to the first row whose needs reach beyond k
+  // ---- the free pages: listed by rank. Beyond the list rank k goes to the first row whose needs reach beyond k
   auto give = [&](int k, int page) {
     int lo = 0, hi = R - 1;
     while (lo < hi) {
@@ -196,18 +205,39 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
     A.table_out[(long long)lo * A.width + pages(s_len[lo]) + j] = page;
     if (j < 0) A.page_dst[lo] = page;
   };
-  int k = ahead - mine;  // of this thread's run of words
-  for (int w = w0; w < w1 && k < wanted; ++w)
-    for (uint32_t free = ~s_used[w]; free && k < wanted; free &= free - 1, ++k) {
-      const int page = 32 * w + __ffs(free) - 1;
+  int first = ahead - mine;  // the rank of the first free page of this thread's words
+  for (int j = 0; j < per; ++j) {  // a warp takes its lanes' words one after the other, a page to a lane
+    const int w = w0 + j;
+    const uint32_t open = w < w1 ? ~s_used[w] : 0;
+    uint32_t turn = __ballot_sync(0xffffffffu, open && first < wanted);
+    for (; turn; turn &= turn - 1) {
+      const int who = __ffs(turn) - 1;
+      const uint32_t theirs = __shfl_sync(0xffffffffu, open, who);
+      const int page = 32 * __shfl_sync(0xffffffffu, w, who) + lane;
+      const int k = __shfl_sync(0xffffffffu, first, who) + __popc(theirs & ((1u << lane) - 1));
+      if (!(theirs >> lane & 1) || k >= wanted) continue;
       if (k < kFresh) s_fresh[k] = page;
       else give(k, page);
     }
+    first += __popc(open);
+  }
   __syncthreads();
-  for (int i = tid; i < min(min(wanted, total), kFresh); i += kThreads) give(i, s_fresh[i]);
+  const bool full = wide || (need > 0 && upto > total);
+  const int listed = full ? 0 : max(0, min(need, kFresh - (upto - need)));  // of the row's new pages
+  auto place = [&](int r, int k, int j, int copied) {  // new page j of row r, which is the list's k-th; a copy comes first
+    A.table_out[(long long)r * A.width + pages(s_len[r]) + j - copied] = s_fresh[k];
+    if (j < copied) A.page_dst[r] = s_fresh[k];
+  };
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (j < listed) place(tid, upto - need + j, j, s_copy[tid]);
+  for (uint32_t turn = __ballot_sync(0xffffffffu, listed > 2); turn; turn &= turn - 1) {  // many: a warp
+    const int who = __ffs(turn) - 1, r = 32 * warp + who, n = __shfl_sync(0xffffffffu, listed, who);
+    const int k = __shfl_sync(0xffffffffu, upto - need, who);
+    for (int j = 2 + lane; j < n; j += 32) place(r, k + j, j, s_copy[r]);
+  }
   // ---- the rows' lengths and copies, the state slots
   if (tid < R) {
-    const bool full = wide || (take > 0 && need > 0 && upto > total);
     if (full) {
       set_status(A.status, GDN_ERR_FULL);
       s_new[tid] = 0;
