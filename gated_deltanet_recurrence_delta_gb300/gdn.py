@@ -9,6 +9,7 @@ built, the first call raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import math
 from pathlib import Path
 
 import torch
@@ -90,6 +91,9 @@ class ForkDims(ctypes.Structure):
 class SlotPool(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("base", "src", "dst")] + [("slot_bytes", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ("n", "n_layers", "n_slots")]
+
+
+_pools_of = [SlotPool * max(1, n) for n in range(MAX_SLOT_POOLS + 1)]  # 0.4 us on the host when made in a call
 
 
 _lib = None
@@ -449,13 +453,16 @@ def kv4_load(dims: Kv4Dims, pool, kv_index, k, v, stream=None):
 
 def make_attn_kv4_dims(q, pool, page_table, scale=None, k_exp=0, v_exp=0) -> AttnKv4Dims:
     """Sizes of an attn_kv4 call: q [B, T, Hq, d], one layer's pool, page_table int32 [B, max_pages]."""
-    if q.dim() != 4:
-        raise ValueError("q must be [rows, tokens, heads, head_dim]")
-    one = q.shape[1] == 1 and q.stride(1) != q.stride(0)  # the stride of a dimension of one token says nothing
-    _, hq, d, qs = _layout(q[:, 0] if one else q, "q")
+    shape, st = q.shape, q.stride()
+    if q.dtype is not torch.bfloat16 or len(shape) != 4:
+        raise ValueError("q must be a bf16 tensor [rows, tokens, heads, head_dim]")
+    B, T, hq, d = shape
+    qs = st[0] if T == 1 else st[1]  # the stride of a dimension of one token says nothing
+    if st[3] != 1 or (st[2] != d and hq > 1) or (T > 1 and B > 1 and st[0] != T * qs):
+        raise ValueError("q must have dense heads and evenly spaced tokens")
     hk = pool.shape[1] if pool.dim() == 3 else 0
-    return AttnKv4Dims(q.shape[0], q.shape[1], hq, hk, d, _page_pool(pool, hk, d), _table(page_table, q.shape[0]), k_exp,
-                       v_exp, d ** -0.5 if scale is None else scale, qs)
+    return AttnKv4Dims(B, T, hq, hk, d, _page_pool(pool, hk, d), _table(page_table, B), k_exp, v_exp,
+                       d ** -0.5 if scale is None else scale, qs)
 
 
 def attn_kv4_workspace_size(dims: AttnKv4Dims) -> int:
@@ -472,7 +479,7 @@ def attn_kv4(dims: AttnKv4Dims, q, pool, page_table, kv_len, out, workspace, q_l
     """gdn_attn_kv4: q [B, T, Hq, d] over the pages of each row, kv_len int32 [B] tokens of it."""
     _check(load_library().gdn_attn_kv4(
         ctypes.byref(dims), *_ptrs(q, pool, page_table, kv_len, q_len, out, workspace),
-        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+        workspace.nbytes if workspace is not None else 0, _stream(stream)))
 
 
 def make_beam_dims(logits, eos=-1) -> BeamDims:
@@ -497,8 +504,8 @@ def beam_select(logits, scores, parent, token, new_scores, workspace, done=None,
     uint8 [groups, beams] -> parent (row numbers), token int32, new_scores, new_done [groups, beams]."""
     dims = make_beam_dims(logits, eos)
     _check(load_library().gdn_beam_select(
-        ctypes.byref(dims), *_ptrs(logits, scores, done, parent, token, new_scores, new_done, workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
-        _stream(stream)))
+        ctypes.byref(dims), *_ptrs(logits, scores, done, parent, token, new_scores, new_done, workspace),
+        workspace.nbytes if workspace is not None else 0, _stream(stream)))
 
 
 def cache_fork(page_table, kv_len, page_table_out, kv_len_out, kv_index, page_src, page_dst, n_pages, parent=None,
@@ -523,11 +530,12 @@ def slots_copy(pools, stream=None):
         shape, n = x.shape, src.numel()
         if not x.is_contiguous() or len(shape) < 2 or n != dst.numel():
             raise ValueError("a pool must be a dense tensor [n_layers, n_slots, ...], src and dst of one length")
-        slot = 1
-        for d in shape[2:]:
-            slot *= d
-        args.append(SlotPool(x.data_ptr(), src.data_ptr(), dst.data_ptr(), slot * x.element_size(), n, shape[0], shape[1]))
-    _check(load_library().gdn_slots_copy((SlotPool * max(1, len(args)))(*args), len(args), _stream(stream)))
+        layers, slots = shape[0], shape[1]
+        slot = x.nbytes // (layers * slots) if layers * slots else x.element_size() * math.prod(shape[2:])
+        args.append(SlotPool(x.data_ptr(), src.data_ptr(), dst.data_ptr(), slot, n, layers, slots))
+    n = len(args)
+    array = _pools_of[n] if n <= MAX_SLOT_POOLS else SlotPool * n
+    _check(load_library().gdn_slots_copy(array(*args), n, _stream(stream)))
 
 
 def check_status(stream=None):

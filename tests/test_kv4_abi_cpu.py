@@ -217,3 +217,24 @@ def test_binding_looks_at_strides_in_every_call():
     for call in (lambda: gdn.kv4_store(dims, k, v, index, pool), lambda: gdn.kv4_load(dims, pool, index, v, k)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_binding_reads_sizes_of_any_strides():
+    q = torch.zeros((3, 1, 6, 64), dtype=torch.bfloat16)
+    pool, table = torch.zeros((2, 2, 72 * 64), dtype=torch.uint8), torch.zeros((3, 5), dtype=torch.int32)
+    wide = torch.zeros((3, 1, 10, 64), dtype=torch.bfloat16)[:, :, 2:8]
+    for x, stride in ((q, 384), (wide, 640), (q.transpose(0, 1).contiguous().transpose(0, 1), 384)):
+        dims = gdn.make_attn_kv4_dims(x, pool, table)
+        assert (dims.B, dims.T, dims.n_q_heads, dims.n_kv_heads, dims.head_dim, dims.max_pages, dims.q_stride) == (
+            3, 1, 6, 2, 64, 5, stride)
+    rows = torch.zeros((3, 4, 10, 64), dtype=torch.bfloat16)
+    assert gdn.make_attn_kv4_dims(rows[:, :, :6], pool, table).q_stride == 640
+    for bad in (rows[:, :2], rows.transpose(2, 3), rows.float(), rows[0]):
+        with pytest.raises(ValueError):
+            gdn.make_attn_kv4_dims(bad, pool, table)
+    k = torch.zeros((4, 4, 64), dtype=torch.bfloat16)
+    dims = gdn.make_kv4_dims(k[:, :2], pool, v=torch.zeros((4, 2, 64), dtype=torch.bfloat16))
+    assert (dims.k_stride, dims.v_stride) == (256, 128)
+    assert gdn.make_kv4_dims(k[:, :2], pool, v=k[:, 2:]).v_stride == 256
+    with pytest.raises(ValueError):
+        gdn.make_kv4_dims(k[:, :2], pool, v=k[:, ::2])
