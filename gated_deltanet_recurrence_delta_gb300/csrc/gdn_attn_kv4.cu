@@ -40,7 +40,7 @@
 //
 // 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 123.4 us, 4.9 TB/s, 72% of
 // a copy's rate. A page of a head is 660 instructions of each of two warps, half of
-// them the codes' way into operands; 62% of the issue slots and half the ALU pipe's are
+// them the codes' way into operands; 64% of the issue slots and half the ALU pipe's are
 // used, the rest goes to the page's chain (wait, scores, maximum, barrier, output),
 // which 16 warps an SM do not hide entirely. 16 verify rows of 8 tokens, 16/4 heads of
 // 256 (41.6 MB, 4.5 GFLOP): 28.7 us: 32 query columns take 249 registers, so that 8
@@ -85,8 +85,8 @@ struct Args {
 // The variant for head size D and tiles of 8 NT query columns (tiles_at_once: as few as hold a key head's columns,
 // since a page's codes are turned into operands once for all of them).
 // Stages and CTAs of an SM share its memory and registers. One column tile of 128: 2 stages and 8 CTAs (64 rows of
-// 8192 tokens 123 us; 3 stages and 6 CTAs 126; 10 CTAs, whose registers spill, 169). Four tiles of 256: 3 stages and 2
-// CTAs of 255 registers (16 verify rows 35 us; 3 CTAs, which spill, 71).
+// 8192 tokens 123 us; 3 stages and 6 CTAs 126; 7 CTAs 136; 9, whose registers spill, 140). Four tiles of 256: 3 stages and
+// 2 CTAs of 249 registers (16 verify rows 29 us; 3 CTAs, which spill, twice that).
 template <int D, int NT>
 struct Shape {
   static constexpr int W = D == 256 ? 4 : 2;     // warps: each holds D / W channels' outputs in registers
@@ -830,7 +830,8 @@ gdn_status check_dims(const gdn_attn_kv4_dims *d) {
   return GDN_OK;
 }
 
-// Query tiles of 8 columns that a CTA takes at once, as the columns fill them.
+// Query tiles of 8 columns that a CTA takes at once, as the columns fill them (8 tokens of 4 heads a key head, 64 rows of
+// 8192 tokens: 234 us with four tiles, 294 with two at a time).
 int tiles_at_once(const gdn_attn_kv4_dims *d) {
   const int cols = d->T * (d->n_q_heads / d->n_kv_heads);
   return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
