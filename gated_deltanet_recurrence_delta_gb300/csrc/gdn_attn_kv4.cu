@@ -32,18 +32,18 @@
 // A page's block of one head is contiguous: one bulk copy into a ring of stages. At
 // a page's barrier all warps have left the page before it, so its stage is filled
 // again right behind it. The (row, key head, query tile, page) sequence is dealt out
-// in equal shares to a CTA each, a unit's set-up counting as kSetup pages, so a share
+// in equal shares to a CTA each, a unit's set-up counting as a few pages, so a share
 // may begin and end inside a unit, whose parts a second kernel joins. (Joined by the
 // last CTA to finish, 16 verify rows take 35 us in place of 28.7, 8 decode rows 12.0 in
 // place of 10.7: one SM then reads all of a unit's parts, behind an exchange of
 // counters; 64 long decode rows, of few parts, are 1 us faster that way.)
 //
-// 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 123.4 us, 4.9 TB/s, 72% of
+// 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 123.1 us, 4.9 TB/s, 72% of
 // a copy's rate. A page of a head is 660 instructions of each of two warps, half of
 // them the codes' way into operands; 64% of the issue slots and half the ALU pipe's are
 // used, the rest goes to the page's chain (wait, scores, maximum, barrier, output),
 // which 16 warps an SM do not hide entirely. 16 verify rows of 8 tokens, 16/4 heads of
-// 256 (41.6 MB, 4.5 GFLOP): 28.7 us: 32 query columns take 249 registers, so that 8
+// 256 (41.6 MB, 4.5 GFLOP): 28.3 us: 32 query columns take 249 registers, so that 8
 // warps an SM are all there are. 8 decode rows of up to 2048 tokens: 10.7 us: start,
 // two pages and the join in turn, all latency.
 #include <cuda_fp16.h>
@@ -60,9 +60,11 @@ using namespace kv4;
 constexpr int kMaxCtas = 1536;
 constexpr float kNone = -3.0e38f;  // below every score
 constexpr float kLag = 8.0f;       // scores may exceed the reference by 2^8
-// Shares: 1 and 3 in place of either 2 are slower or the same, on all of 8, 64 and 45 decode rows and 16 verify rows.
-constexpr int kSetup = 2;          // pages that a unit's queries and output are worth
-constexpr int kLeast = 2;          // pages that are worth a CTA
+constexpr int kLeast = 2;          // pages that are worth a CTA (8 and 45 decode rows: 1, 3 the same, 4 a us more)
+// Pages that a unit's queries and output are worth (45 odd decode rows 10.0 us with 1, 10.6 with 2; 16 verify rows, of four
+// tiles, 30.6 and 28.7, with 3 28.2).
+template <int NT>
+constexpr int kSetup = NT == 4 ? 3 : NT;
 constexpr int kMostParts = 64;     // of a unit, on the average
 constexpr int kJoin = 256;         // threads of a join, each with 4 channels of a column
 constexpr int kFan = 16;           // parts whose loads it has in flight: a lane of 16 has the statistics of each
@@ -114,20 +116,22 @@ __device__ __forceinline__ int row_len(const Args &A, int b, int &ql) {
   return len < 0 || len > (long long)A.max_pages * kPage || ql < 0 || ql > A.T ? -1 : len;
 }
 // Positions of each of a row's units: its pages and the set-up, none for a row without tokens.
+template <int SETUP>
 __device__ __forceinline__ int row_cost(const Args &A, int b) {
   int ql;
   const int len = row_len(A, b, ql);
-  return len > 0 ? (len + kPage - 1) / kPage + kSetup : 0;
+  return len > 0 ? (len + kPage - 1) / kPage + SETUP : 0;
 }
 
 // A walk over positions [x, x1) of the sequence of all rows' units.
+template <int SETUP>
 struct Walk {
   int x, x1, row0;  // row0: where row b begins
   int b, cost;      // the row, the positions of each of its units
   __device__ __forceinline__ void find_row(const Args &A, int units) {
     while (x >= row0 + cost * units) {  // rows without tokens are passed over
       row0 += cost * units;
-      cost = row_cost(A, ++b);
+      cost = row_cost<SETUP>(A, ++b);
     }
   }
 };
@@ -136,13 +140,14 @@ struct Segment {
   int b, unit, p, count, x;
   int first, end;  // the unit's first page's position, and behind its last
 };
-__device__ __forceinline__ bool next_segment(const Args &A, int units, Walk &w, Segment &g) {
+template <int SETUP>
+__device__ __forceinline__ bool next_segment(const Args &A, int units, Walk<SETUP> &w, Segment &g) {
   while (w.x < w.x1) {
     w.find_row(A, units);
     g.b = w.b;
     g.unit = (w.x - w.row0) / w.cost;
-    g.first = w.row0 + g.unit * w.cost + kSetup;
-    g.end = g.first - kSetup + w.cost;
+    g.first = w.row0 + g.unit * w.cost + SETUP;
+    g.end = g.first - SETUP + w.cost;
     g.x = max(w.x, g.first);
     const int to = min(g.end, w.x1);
     w.x = to;
@@ -165,6 +170,7 @@ struct Deal {
 };
 
 // What all rows cost, found by each warp alone: a lane takes `per` of them.
+template <int SETUP>
 struct Rows {
   int r0, per, mine, upto, real;  // the lane's first row, its rows' cost, that and all before, rows that have any
   __device__ __forceinline__ Rows(const Args &A, int lane) {
@@ -173,7 +179,7 @@ struct Rows {
     const int r1 = min(A.B, r0 + per);
     mine = real = 0;
     for (int b = r0; b < r1; ++b) {
-      const int c = row_cost(A, b);
+      const int c = row_cost<SETUP>(A, b);
       mine += c;
       real += c > 0;
     }
@@ -190,12 +196,12 @@ struct Rows {
     return Deal(total, min(min(ctas, total / kLeast), (int)min((long long)real * units * kMostParts, (long long)ctas)));
   }
   // The row of position w.x, which is one of the sequence's.
-  __device__ __forceinline__ void find(const Args &A, int units, Walk &w) const {
+  __device__ __forceinline__ void find(const Args &A, int units, Walk<SETUP> &w) const {
     const int owner = __ffs(__ballot_sync(0xffffffffu, w.x < upto * units)) - 1;
     int at = r0, cost = mine, first = (upto - mine) * units;
     if (per > 1 && (threadIdx.x & 31) == owner)
       for (at = r0;; ++at) {
-        cost = row_cost(A, at);
+        cost = row_cost<SETUP>(A, at);
         if (w.x < first + cost * units) break;
         first += cost * units;
       }
@@ -262,7 +268,7 @@ __device__ __forceinline__ constexpr int key_of(int r) { return 4 * ((r & 7) >> 
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) attn_kernel(const __grid_constant__ Args A) {
   using S = Shape<D, NT>;
-  constexpr int W = S::W, kThreads = S::kThreads;
+  constexpr int W = S::W, kThreads = S::kThreads, SETUP = kSetup<NT>;
   constexpr long long kNoPage = -1, kNothing = -2;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *ring = smem;
@@ -284,9 +290,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 
   // ---- the share
   const int units = A.hk * A.tiles, N = gridDim.x, cta = blockIdx.x;
-  const Rows rows(A, lane);
+  const Rows<SETUP> rows(A, lane);
   const Deal deal = rows.deal(A, units, N);
-  Walk share;
+  Walk<SETUP> share;
   share.x = cta < deal.used ? deal.start(cta) : 0;
   share.x1 = cta < deal.used ? deal.start(cta + 1) : 0;
   const int x0 = share.x, x1 = share.x1;
@@ -294,13 +300,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
   if (any_share) rows.find(A, units, share);
 
   // ---- the blocks of the share, kThreads positions at a time
-  Walk walk = share;
+  Walk<SETUP> walk = share;
   auto list = [&](int i0) {
     long long block = kNothing;
     walk.x = x0 + i0 + tid;
     if (walk.x < x1) {
       walk.find_row(A, units);
-      const int unit = (walk.x - walk.row0) / walk.cost, p = walk.x - walk.row0 - unit * walk.cost - kSetup;
+      const int unit = (walk.x - walk.row0) / walk.cost, p = walk.x - walk.row0 - unit * walk.cost - SETUP;
       if (p >= 0) {
         const int page = A.table[(long long)walk.b * A.max_pages + p];
         block = page >= 0 && page < A.n_pages ? ((long long)page * A.hk + unit / A.tiles) * S::kBlock : kNoPage;
@@ -730,23 +736,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 // and whose parts, is found while the attention kernel still runs.
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoin, 3) join_kernel(const __grid_constant__ Args A) {
-  constexpr int N = 8 * NT, E = D / 4;
+  constexpr int N = 8 * NT, E = D / 4, SETUP = kSetup<NT>;
   const int lane = threadIdx.x & 31, units = A.hk * A.tiles, job = blockIdx.x;
-  const Rows rows(A, lane);
+  const Rows<SETUP> rows(A, lane);
   const Deal deal = rows.deal(A, units, A.ctas);
-  Walk w;
+  Walk<SETUP> w;
   int unit, i0, n = 0;
   if (A.B * (long long)units <= A.ctas) {
     w.b = job / units;
     unit = job - w.b * units;
-    w.cost = row_cost(A, w.b);
+    w.cost = row_cost<SETUP>(A, w.b);
     w.row0 = 0;
     if (w.cost > 0) {
       const int lanes = w.b / rows.per;
       w.row0 = __shfl_sync(0xffffffffu, rows.upto - rows.mine, lanes);
-      for (int b = lanes * rows.per; b < w.b; ++b) w.row0 += row_cost(A, b);
+      for (int b = lanes * rows.per; b < w.b; ++b) w.row0 += row_cost<SETUP>(A, b);
       w.row0 *= units;
-      i0 = deal.owner(w.row0 + unit * w.cost + kSetup);
+      i0 = deal.owner(w.row0 + unit * w.cost + SETUP);
       n = deal.owner(w.row0 + (unit + 1) * w.cost - 1) - i0 + 1;
     }
   } else if (job + 1 < deal.used) {
@@ -754,8 +760,8 @@ __global__ void __launch_bounds__(kJoin, 3) join_kernel(const __grid_constant__ 
     rows.find(A, units, w);
     unit = (w.x - w.row0) / w.cost;
     i0 = job;
-    const int first = w.row0 + unit * w.cost + kSetup;
-    if (first >= deal.start(job) && first < w.x) n = deal.owner(first - kSetup + w.cost - 1) - i0 + 1;
+    const int first = w.row0 + unit * w.cost + SETUP;
+    if (first >= deal.start(job) && first < w.x) n = deal.owner(first - SETUP + w.cost - 1) - i0 + 1;
   }
   griddep_wait();
   griddep_trigger();
@@ -850,9 +856,9 @@ gdn_status launch(Args A, int sms, cudaStream_t stream) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   // no more CTAs than the rows could fill
-  const long long units = (long long)A.B * A.hk * A.tiles, most = units * (A.max_pages + kSetup) / kLeast;
+  const long long units = (long long)A.B * A.hk * A.tiles, most = units * (A.max_pages + kSetup<NT>) / kLeast;
   int ctas = sms * S::kCtas < kMaxCtas ? sms * S::kCtas : kMaxCtas;
-  if (most < ctas) ctas = (int)most;
+  if (most < ctas) ctas = most < 1 ? 1 : (int)most;
   A.ctas = ctas;
   if (launch_pdl(attn_kernel<D, NT>, dim3(ctas), dim3(S::kThreads), S::kBytes, stream, A) != cudaSuccess)
     return check_launch("attn_kv4");

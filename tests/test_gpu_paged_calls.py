@@ -157,3 +157,22 @@ def test_selections_at_the_ends_of_fp32():
             assert token[i].tolist() == [j % V for j in order[:W]]
         want = cand[i, order[:W]].float()
         assert bool(((new[i] == want) | ((new[i] - want).abs() <= 2.0 ** -22 * want.abs() + 1e-5)).all())
+
+
+@pytest.mark.parametrize("d,hq,hk,T", [(64, 1, 1, 1), (128, 8, 1, 2), (256, 8, 2, 8)])
+def test_attention_without_pages(d, hq, hk, T):
+    """Tables without entries, or pools without pages: rows without tokens give zeros, others are refused on the device."""
+    q = torch.ones((1, T, hq, d), dtype=torch.bfloat16, device="cuda")
+    for n_pages, width in ((0, 0), (3, 0), (0, 2), (1, 1)):
+        pool, table = gdn.kv4_pool(n_pages, hk, d), torch.zeros((1, width), dtype=torch.int32, device="cuda")
+        dims = gdn.make_attn_kv4_dims(q, pool, table)
+        out, work = torch.full_like(q, 7.0), gdn.attn_kv4_workspace(dims)
+        gdn.attn_kv4(dims, q, pool, table, _ints([0]), out, work)
+        gdn.check_status()
+        assert not bool(out.any())
+        if (n_pages, width) != (1, 1):
+            out.fill_(7.0)
+            gdn.attn_kv4(dims, q, pool, table, _ints([5]), out, work)
+            with pytest.raises(gdn.GdnError, match="INDEX"):
+                gdn.check_status()
+            assert bool((out == 7.0).all())
