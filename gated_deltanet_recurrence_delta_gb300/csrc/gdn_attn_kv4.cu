@@ -35,16 +35,16 @@
 // in equal shares to a CTA each, a unit's set-up counting as a few pages, so a share
 // may begin and end inside a unit, whose parts a second kernel joins. (Joined by the
 // last CTA to finish, 16 verify rows take 35 us in place of 28.7, 8 decode rows 12.0 in
-// place of 10.7: one SM then reads all of a unit's parts, behind an exchange of
+// place of 10.8: one SM then reads all of a unit's parts, behind an exchange of
 // counters; 64 long decode rows, of few parts, are 1 us faster that way.)
 //
-// 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 123.1 us, 4.9 TB/s, 72% of
+// 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 121.3 us, 5.0 TB/s, 74% of
 // a copy's rate. A page of a head is 660 instructions of each of two warps, half of
 // them the codes' way into operands; 64% of the issue slots and half the ALU pipe's are
 // used, the rest goes to the page's chain (wait, scores, maximum, barrier, output),
 // which 16 warps an SM do not hide entirely. 16 verify rows of 8 tokens, 16/4 heads of
 // 256 (41.6 MB, 4.5 GFLOP): 28.3 us: 32 query columns take 249 registers, so that 8
-// warps an SM are all there are. 8 decode rows of up to 2048 tokens: 10.7 us: start,
+// warps an SM are all there are. 8 decode rows of up to 2048 tokens: 10.8 us: start,
 // two pages and the join in turn, all latency.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -169,45 +169,83 @@ struct Deal {
   }
 };
 
-// What all rows cost, found by each warp alone: a lane takes `per` of them.
+// What all rows cost, found by each warp alone: 32 rows at a time, of which a lane keeps the sums of `per` in a row. (With
+// neighbouring rows to a lane each load is 32 lines: 1000 rows of 150 tokens 84 us in place of 59, 20000 of 60 557 in
+// place of 341.)
 template <int SETUP>
 struct Rows {
-  int r0, per, mine, upto, real;  // the lane's first row, its rows' cost, that and all before, rows that have any
-  __device__ __forceinline__ Rows(const Args &A, int lane) {
-    per = (A.B + 31) / 32;
-    r0 = min(A.B, lane * per);
-    const int r1 = min(A.B, r0 + per);
-    mine = real = 0;
-    for (int b = r0; b < r1; ++b) {
-      const int c = row_cost<SETUP>(A, b);
-      mine += c;
-      real += c > 0;
-    }
-    upto = mine;
+  int chunks, per, c0, mine, upto, real;  // the lane's cost in the first 32; its sums, and all before; rows of any cost
+  __device__ __forceinline__ int cost(const Args &A, int i, int lane) const {
+    const int b = 32 * i + lane;
+    return b < A.B ? row_cost<SETUP>(A, b) : 0;
+  }
+  __device__ __forceinline__ static int scan(int x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    real = __reduce_add_sync(0xffffffffu, real);
+    return x;
+  }
+  __device__ __forceinline__ Rows(const Args &A, int lane) {
+    chunks = (A.B + 31) / 32;
+    per = (chunks + 31) / 32;
+    c0 = cost(A, 0, lane);
+    mine = __reduce_add_sync(0xffffffffu, c0);
+    if (lane > 0) mine = 0;
+    int some = c0 > 0;
+    if (per == 1) {
+#pragma unroll 4
+      for (int i = 1; i < chunks; ++i) {
+        const int c = cost(A, i, lane), sum = __reduce_add_sync(0xffffffffu, c);
+        some += c > 0;
+        if (lane == i) mine = sum;
+      }
+    } else {
+      for (int g = 0; g * per < chunks; ++g) {
+        int c = 0;
+#pragma unroll 4
+        for (int i = max(1, g * per); i < min(chunks, (g + 1) * per); ++i) {
+          const int x = cost(A, i, lane);
+          c += x;
+          some += x > 0;
+        }
+        const int sum = __reduce_add_sync(0xffffffffu, c);
+        if (lane == g) mine += sum;
+      }
+    }
+    real = __reduce_add_sync(0xffffffffu, some);
+    upto = scan(mine, lane);
   }
   __device__ __forceinline__ Deal deal(const Args &A, int units, int ctas) const {
     const int total = __shfl_sync(0xffffffffu, upto, 31) * units;
     return Deal(total, min(min(ctas, total / kLeast), (int)min((long long)real * units * kMostParts, (long long)ctas)));
   }
   // The row of position w.x, which is one of the sequence's.
-  __device__ __forceinline__ void find(const Args &A, int units, Walk<SETUP> &w) const {
+  __device__ __forceinline__ void find(const Args &A, int units, int lane, Walk<SETUP> &w) const {
     const int owner = __ffs(__ballot_sync(0xffffffffu, w.x < upto * units)) - 1;
-    int at = r0, cost = mine, first = (upto - mine) * units;
-    if (per > 1 && (threadIdx.x & 31) == owner)
-      for (at = r0;; ++at) {
-        cost = row_cost<SETUP>(A, at);
-        if (w.x < first + cost * units) break;
-        first += cost * units;
+    int first = __shfl_sync(0xffffffffu, upto - mine, owner);
+    for (int i = owner * per; i < chunks; ++i) {
+      const int c = i == 0 ? c0 : cost(A, i, lane), sum = scan(c, lane);
+      const uint32_t hit = __ballot_sync(0xffffffffu, w.x < (first + sum) * units);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        w.b = 32 * i + l;
+        w.cost = __shfl_sync(0xffffffffu, c, l);
+        w.row0 = (first + __shfl_sync(0xffffffffu, sum, l) - w.cost) * units;
+        return;
       }
-    w.b = __shfl_sync(0xffffffffu, at, owner);
-    w.cost = __shfl_sync(0xffffffffu, cost, owner);
-    w.row0 = __shfl_sync(0xffffffffu, first, owner);
+      first += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  // Row w.b: its cost and where it begins.
+  __device__ __forceinline__ void place(const Args &A, int units, int lane, Walk<SETUP> &w) const {
+    const int at = w.b / 32, owner = at / per, l = w.b % 32;
+    int first = __shfl_sync(0xffffffffu, upto - mine, owner);
+    for (int i = owner * per; i < at; ++i) first += __reduce_add_sync(0xffffffffu, cost(A, i, lane));
+    const int c = at == 0 ? c0 : cost(A, at, lane);
+    w.cost = __shfl_sync(0xffffffffu, c, l);
+    w.row0 = (first + __reduce_add_sync(0xffffffffu, lane < l ? c : 0)) * units;
   }
 };
 
@@ -297,7 +335,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
   share.x1 = cta < deal.used ? deal.start(cta + 1) : 0;
   const int x0 = share.x, x1 = share.x1;
   const bool any_share = x0 < x1;
-  if (any_share) rows.find(A, units, share);
+  if (any_share) rows.find(A, units, lane, share);
 
   // ---- the blocks of the share, kThreads positions at a time
   Walk<SETUP> walk = share;
@@ -737,32 +775,40 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoin, 3) join_kernel(const __grid_constant__ Args A) {
   constexpr int N = 8 * NT, E = D / 4, SETUP = kSetup<NT>;
-  const int lane = threadIdx.x & 31, units = A.hk * A.tiles, job = blockIdx.x;
-  const Rows<SETUP> rows(A, lane);
-  const Deal deal = rows.deal(A, units, A.ctas);
-  Walk<SETUP> w;
-  int unit, i0, n = 0;
-  if (A.B * (long long)units <= A.ctas) {
-    w.b = job / units;
-    unit = job - w.b * units;
-    w.cost = row_cost<SETUP>(A, w.b);
-    w.row0 = 0;
-    if (w.cost > 0) {
-      const int lanes = w.b / rows.per;
-      w.row0 = __shfl_sync(0xffffffffu, rows.upto - rows.mine, lanes);
-      for (int b = lanes * rows.per; b < w.b; ++b) w.row0 += row_cost<SETUP>(A, b);
-      w.row0 *= units;
-      i0 = deal.owner(w.row0 + unit * w.cost + SETUP);
-      n = deal.owner(w.row0 + (unit + 1) * w.cost - 1) - i0 + 1;
+  __shared__ int s_job[4];  // the row, its unit, the CTA with the first part, and how many there are
+  const int lane = threadIdx.x & 31, units = A.hk * A.tiles;
+  if (threadIdx.x < 32) {
+    const int job = blockIdx.x;
+    const Rows<SETUP> rows(A, lane);
+    const Deal deal = rows.deal(A, units, A.ctas);
+    Walk<SETUP> w;
+    w.b = 0;
+    int unit = 0, i0 = 0, n = 0;
+    if (A.B * (long long)units <= A.ctas) {
+      w.b = job / units;
+      unit = job - w.b * units;
+      rows.place(A, units, lane, w);
+      if (w.cost > 0) {
+        i0 = deal.owner(w.row0 + unit * w.cost + SETUP);
+        n = deal.owner(w.row0 + (unit + 1) * w.cost - 1) - i0 + 1;
+      }
+    } else if (job + 1 < deal.used) {
+      w.x = deal.start(job + 1);
+      rows.find(A, units, lane, w);
+      unit = (w.x - w.row0) / w.cost;
+      i0 = job;
+      const int first = w.row0 + unit * w.cost + SETUP;
+      if (first >= deal.start(job) && first < w.x) n = deal.owner(first - SETUP + w.cost - 1) - i0 + 1;
     }
-  } else if (job + 1 < deal.used) {
-    w.x = deal.start(job + 1);
-    rows.find(A, units, w);
-    unit = (w.x - w.row0) / w.cost;
-    i0 = job;
-    const int first = w.row0 + unit * w.cost + SETUP;
-    if (first >= deal.start(job) && first < w.x) n = deal.owner(first - SETUP + w.cost - 1) - i0 + 1;
+    if (lane == 0) {
+      s_job[0] = w.b;
+      s_job[1] = unit;
+      s_job[2] = i0;
+      s_job[3] = n;
+    }
   }
+  __syncthreads();
+  const int b = s_job[0], unit = s_job[1], i0 = s_job[2], n = s_job[3];
   griddep_wait();
   griddep_trigger();
   if (n < 2) return;
@@ -808,7 +854,7 @@ __global__ void __launch_bounds__(kJoin, 3) join_kernel(const __grid_constant__ 
     const int tok = col / A.G;
     const float inv = l == 0.0f ? 0.0f : A.out_mul / l;
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), y1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    bf16 *out = A.out + (((long long)w.b * A.T + tok) * A.hq + head * A.G + col - tok * A.G) * D + e % E * 4;
+    bf16 *out = A.out + (((long long)b * A.T + tok) * A.hq + head * A.G + col - tok * A.G) * D + e % E * 4;
     *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
   }
 }
