@@ -39,11 +39,11 @@
 // counters; 64 long decode rows, of few parts, are 1 us faster that way.)
 //
 // 64 decode rows of 8192 tokens, 32/8 heads of 128 (605 MB): 121.3 us, 5.0 TB/s, 74% of
-// a copy's rate. A page of a head is 660 instructions of each of two warps, half of
-// them the codes' way into operands; 64% of the issue slots and half the ALU pipe's are
+// a copy's rate. A page of a head is 650 instructions of each of two warps, half of
+// them the codes' way into operands; 63% of the issue slots and half the ALU pipe's are
 // used, the rest goes to the page's chain (wait, scores, maximum, barrier, output),
 // which 16 warps an SM do not hide entirely. 16 verify rows of 8 tokens, 16/4 heads of
-// 256 (41.6 MB, 4.5 GFLOP): 28.3 us: 32 query columns take 249 registers, so that 8
+// 256 (41.6 MB, 4.5 GFLOP): 28.3 us: 32 query columns take 244 registers, so that 8
 // warps an SM are all there are. 8 decode rows of up to 2048 tokens: 10.8 us: start,
 // two pages and the join in turn, all latency.
 #include <cuda_fp16.h>
@@ -88,7 +88,7 @@ struct Args {
 // since a page's codes are turned into operands once for all of them).
 // Stages and CTAs of an SM share its memory and registers. One column tile of 128: 2 stages and 8 CTAs (64 rows of
 // 8192 tokens 123 us; 3 stages and 6 CTAs 126; 7 CTAs 136; 9, whose registers spill, 140). Four tiles of 256: 3 stages and
-// 2 CTAs of 249 registers (16 verify rows 29 us; 3 CTAs, which spill, twice that).
+// 2 CTAs of 244 registers (16 verify rows 29 us; 3 CTAs, which spill, twice that).
 template <int D, int NT>
 struct Shape {
   static constexpr int W = D == 256 ? 4 : 2;     // warps: each holds D / W channels' outputs in registers
