@@ -9,6 +9,7 @@ import torch
 
 from gated_deltanet_recurrence_delta_gb300 import gdn
 from gated_deltanet_recurrence_delta_gb300.hybrid import Beams, PagedAttentionLayers
+from tests.test_gpu_kv4 import _case, _compare, _run
 
 pytestmark = pytest.mark.gpu
 PAGE = 64
@@ -176,3 +177,16 @@ def test_attention_without_pages(d, hq, hk, T):
             with pytest.raises(gdn.GdnError, match="INDEX"):
                 gdn.check_status()
             assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("rows,T,hq,hk,d", [(31, 1, 4, 2, 128), (33, 2, 8, 2, 256), (64, 1, 4, 4, 64), (65, 8, 4, 1, 256),
+                                            (1024, 1, 1, 1, 64), (1025, 1, 1, 1, 64), (1150, 1, 2, 1, 64), (1100, 1, 2, 2, 128)])
+def test_long_rows_among_many(rows, T, hq, hk, d):
+    """Rows whose pages many CTAs share, at the ends of every 32 and every 1024 rows, among short and empty ones."""
+    lens = [(7 * i) % 90 if i % 5 else 0 for i in range(rows)]
+    for i in {0, rows // 2, rows - 1, min(rows - 1, 31), min(rows - 1, 32), min(rows - 1, 1023)}:
+        lens[i] = 1500 + 64 * (i % 3) + i % 64
+    lens = [n if n == 0 else max(n, T) for n in lens]
+    c = _case(lens, T, hq, hk, d, seed=rows)
+    _compare(c, _run(c))
+    gdn.check_status()
