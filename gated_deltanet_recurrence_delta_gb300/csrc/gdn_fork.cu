@@ -95,10 +95,9 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
     if (lane == 0) s_used[w] = bits;
   }
   __syncthreads();
-  bool copy = tail >= 0 && (s_used[tail >> 5] >> (tail & 31) & 1);  // pinned
-  if (par >= 0) atomicMin(&s_first[par], tid);                          // the lowest child
-  __syncthreads();
-  if (copy && take > 0) s_copy[tid] = 1;
+  if (take > 0 && tail >= 0 && (s_used[tail >> 5] >> (tail & 31) & 1)) s_copy[tid] = 1;  // pinned
+  if (par >= 0) atomicMin(&s_first[par], tid);                                            // the lowest child
+  __syncthreads();  // what the votes below read of other rows is written in front of it
   // ---- the rows' pages: handed on and marked, 128 of each of two rows at a time
   for (int ra = warp; ra < R; ra += 2 * kWarps) {
     const int rb = ra + kWarps, na = pages(s_len[ra]), nb = rb < R ? pages(s_len[rb]) : 0;
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
       s_new[tid] = 0;
     }
     A.len_out[tid] = len + (full ? 0 : take);
-    copy = s_copy[tid] && !full;
+    const bool copy = s_copy[tid] && !full;
     A.page_src[tid] = copy ? tail : -1;
     if (!copy) A.page_dst[tid] = -1;
     if (A.state) {

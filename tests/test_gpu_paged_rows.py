@@ -1,0 +1,50 @@
+"""Rows of the paged 4-bit cache where a rule of one row depends on the others: forks of rows whose last pages are pinned."""
+import random
+
+import pytest
+import torch
+
+from gated_deltanet_recurrence_delta_gb300 import gdn
+from tests import kv4_plain
+from tests.test_gpu_beam import _check_fork, _fork
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from gated_deltanet_recurrence_delta_gb300 import build
+    build.build()
+    gdn.load_library()
+
+
+@pytest.mark.parametrize("R", [2, 33, 64, 200, 1024])
+def test_fork_of_pinned_last_pages(R):
+    """Last pages that are pinned, shared, both or neither, in rows of very different lengths (whose warps come to the
+    look at the other rows at different times): who copies is decided the same way every time."""
+    for seed in range(3):
+        rng = random.Random(R + seed)
+        n_pages, width = 40 * R + 64, 20
+        order = list(range(n_pages))
+        rng.shuffle(order)
+        table, lens, pinned = [], [], [0] * n_pages
+        for r in range(R):
+            if r and rng.random() < 0.5:  # a copy of a row
+                p = rng.randrange(r)
+                table.append(list(table[p]))
+                lens.append(lens[p])
+                continue
+            n = rng.choice((1, 5, 70, 18 * PAGE + 3, rng.randint(1, 18 * PAGE)))
+            used = -(-n // PAGE)
+            table.append([order.pop() for _ in range(used)] + [-3] * (width - used))
+            lens.append(n)
+            pinned[table[r][used - 1]] = int(rng.random() < 0.5)
+        n_new = [rng.choice((0, 1, 1, 2)) for _ in range(R)]
+        want = kv4_plain.fork(table, lens, n_pages, 2, n_new=n_new, pinned=pinned)
+        assert not want["full"] and (R == 2 or any(p >= 0 for p in want["page_src"]))
+        for _ in range(10):
+            _check_fork(_fork(table, lens, n_pages, 2, n_new=n_new, pinned=pinned), want)
+    gdn.check_status()
