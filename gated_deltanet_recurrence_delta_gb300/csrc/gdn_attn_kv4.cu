@@ -26,8 +26,10 @@
 //     transposes between lanes. A lane holds 4 keys of 8 channels; byte permutes put
 //     two keys' nibbles of one channel into one register.
 //   - The running maximum is a reference that is only moved, after the first page,
-//     when a score exceeds it by 2^8 (fp16 holds the probabilities up to there): the
-//     barrier that hands the probabilities over also says whether any did.
+//     when a probability would exceed 2^15 (fp16 ends at 2^16): the barrier that hands
+//     the probabilities over also says whether any did. It is moved to 7 below the
+//     maximum: fp16 rounds numbers to no finer than half of 2^-24, which is then 2^-32 of
+//     the largest probability. The factor 2^7 is in the products and the sums alike.
 //
 // A page's block of one head is contiguous: one bulk copy into a ring of stages. At
 // a page's barrier all warps have left the page before it, so its stage is filled
@@ -59,7 +61,8 @@ using namespace kv4;
 
 constexpr int kMaxCtas = 1536;
 constexpr float kNone = -3.0e38f;  // below every score
-constexpr float kLag = 8.0f;       // scores may exceed the reference by 2^8
+constexpr float kTop = 7.0f;       // where a move of the reference leaves the largest score
+constexpr float kLag = 15.0f;      // scores may lie above it by this much: fp16 holds probabilities up to 2^16
 constexpr int kLeast = 2;          // pages that are worth a CTA (8 and 45 decode rows: 1, 3 the same, 4 a us more)
 // Pages that a unit's queries and output are worth (45 odd decode rows 10.0 us with 1, 10.6 with 2; 16 verify rows, of four
 // tiles, 30.6 and 28.7, with 3 28.2).
@@ -623,12 +626,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
       if (!bad && !over) hand_over();
       const bool moved = __syncthreads_or(over);
       if (tid == 0) copy(stage == 0 ? S::kStages - 1 : stage - 1);  // all warps have left the page before
-      if (moved) {  // the references move to the columns' maxima so far, always at a unit's first page here
+      if (moved) {  // the references move to kTop below the columns' maxima so far, always at a unit's first page here
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float top = first_page ? kNone : 0.0f;
+            float top = first_page ? kNone : kTop;
             if (!bad) {
 #pragma unroll
               for (int u = 0; u < S::kSubs; ++u) top = fmaxf(top, fmaxf(y[u][j][k], y[u][j][k + 2]));
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 #pragma unroll
             for (int w = 1; w < W; ++w) up = fmaxf(up, s_top[w][8 * j + 2 * t + k]);
             // a column that sees no key of a first page sees none at all
-            if (up == kNone) up = 0.0f;
+            up = up == kNone ? 0.0f : up - kTop;
             fade[k] = first_page ? 1.0f : ex2(-up);
             ref[j][k] += up;
 #pragma unroll

@@ -614,7 +614,10 @@ typedef struct gdn_attn_kv4_dims {
  * Token t sees keys j <= kv_len - q_len + t; a token that sees nothing, or with
  * t >= q_len, gets zeros. Keys and values enter the products exactly, queries
  * in fp16 relative to their head's largest channel (error below 2^-25 of it),
- * probabilities in fp16; statistics and accumulators are fp32. A length outside
+ * probabilities in fp16 relative to 2^-7 of the largest: each is off by 2^-11 of
+ * itself, or, where that is more, by 2^-32 of the largest (keys that together
+ * matter although each is 22 nats below another one are lost); statistics and
+ * accumulators are fp32. A length outside
  * [0, 64 max_pages], a q_len outside [0, T] or a page outside [0, n_pages) is a
  * device error (GDN_ERR_INDEX): outputs of that row are not written. What the
  * last page holds behind the row's tokens is never used, whatever it is; values
