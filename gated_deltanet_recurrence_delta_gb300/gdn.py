@@ -170,7 +170,7 @@ def _ptr(t):
 
 
 def _ptrs(*tensors):
-    """_ptr of each: 0.13 us a tensor on the host, one by one 0.25 (a call of gdn_cache_fork has 15)."""
+    """_ptr of each: 0.13 us a tensor on the host, one by one 0.25."""
     return [t if t is None or t.__class__ is int else t.data_ptr() for t in tensors]
 
 
@@ -187,6 +187,32 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _arrays(dtype, size, names, *arrays):
+    """_ptr of each array that a kernel indexes by position alone: refuses a tensor of another type, of fewer than `size`
+    bytes or with gaps (0.2 us a tensor on the host). What has no tensor to look at (None, a raw address) passes."""
+    return [x if x is None or x.__class__ is int
+            else x.data_ptr() if x.dtype is dtype and x.nbytes >= size and x.is_contiguous()
+            else _refuse(x, dtype, size, names[i]) for i, x in enumerate(arrays)]
+
+
+def _refuse(x, dtype, size, name):
+    raise ValueError(f"{name} must be a dense {dtype} tensor of {size // dtype.itemsize} elements or more, it is {x.dtype} "
+                     f"{list(x.shape)} with strides {list(x.stride())}")
+
+
+def _here(x, name):
+    """Refuses a tensor that is not on the current device, on which the kernels run."""
+    if isinstance(x, torch.Tensor):
+        device = x.get_device()
+        if device < 0 or device != (_device() if _device is not None else torch.cuda.current_device()):
+            raise ValueError(f"{name} must be on the current device, it is on {x.device}")
+
+
+def _flags(x):
+    """Truth values as the bytes that they are."""
+    return x.view(torch.uint8) if isinstance(x, torch.Tensor) and x.dtype is torch.bool else x
 
 
 def make_dims(B, T, nk, nv, dk, dv, n_slots, conv_k=4, scale=None, l2_eps=1e-6, rms_eps=1e-6) -> Dims:
@@ -441,14 +467,18 @@ def kv4_store(dims: Kv4Dims, k, v, kv_index, pool, stream=None):
     """gdn_kv4_store: k, v bf16 [n, Hk, d] into the pool rows kv_index int32 [n] (-1: not kept), 4 bits each."""
     _spaced(k, dims.k_stride, "k")
     _spaced(v, dims.v_stride, "v")
-    _check(load_library().gdn_kv4_store(ctypes.byref(dims), *_ptrs(k, v, kv_index, pool), _stream(stream)))
+    _here(pool, "pool")
+    index, = _arrays(torch.int32, 4 * dims.n_tokens, ("kv_index",), kv_index)
+    _check(load_library().gdn_kv4_store(ctypes.byref(dims), *_ptrs(k, v), index, _ptr(pool), _stream(stream)))
 
 
 def kv4_load(dims: Kv4Dims, pool, kv_index, k, v, stream=None):
     """gdn_kv4_load: pool rows kv_index int32 [n] to k, v bf16 [n, Hk, d], exactly as attn_kv4 uses them."""
     _spaced(k, dims.k_stride, "k")
     _spaced(v, dims.v_stride, "v")
-    _check(load_library().gdn_kv4_load(ctypes.byref(dims), *_ptrs(pool, kv_index, k, v), _stream(stream)))
+    _here(pool, "pool")
+    index, = _arrays(torch.int32, 4 * dims.n_tokens, ("kv_index",), kv_index)
+    _check(load_library().gdn_kv4_load(ctypes.byref(dims), _ptr(pool), index, *_ptrs(k, v), _stream(stream)))
 
 
 def make_attn_kv4_dims(q, pool, page_table, scale=None, k_exp=0, v_exp=0) -> AttnKv4Dims:
@@ -477,8 +507,11 @@ def attn_kv4_workspace(dims: AttnKv4Dims, device="cuda") -> torch.Tensor:
 
 def attn_kv4(dims: AttnKv4Dims, q, pool, page_table, kv_len, out, workspace, q_len=None, stream=None):
     """gdn_attn_kv4: q [B, T, Hq, d] over the pages of each row, kv_len int32 [B] tokens of it."""
+    _here(pool, "pool")
+    table, = _arrays(torch.int32, 4 * dims.B * dims.max_pages, ("page_table",), page_table)
+    lens = _arrays(torch.int32, 4 * dims.B, ("kv_len", "q_len"), kv_len, q_len)
     _check(load_library().gdn_attn_kv4(
-        ctypes.byref(dims), *_ptrs(q, pool, page_table, kv_len, q_len, out, workspace),
+        ctypes.byref(dims), *_ptrs(q, pool), table, *lens, *_ptrs(out, workspace),
         workspace.nbytes if workspace is not None else 0, _stream(stream)))
 
 
@@ -503,23 +536,38 @@ def beam_select(logits, scores, parent, token, new_scores, workspace, done=None,
     """gdn_beam_select: the best continuations of each group's beams; logits [groups, beams, V], scores fp32 and done
     uint8 [groups, beams] -> parent (row numbers), token int32, new_scores, new_done [groups, beams]."""
     dims = make_beam_dims(logits, eos)
+    _here(logits, "logits")
+    rows = dims.n_groups * dims.beams
+    scores, new_scores = _arrays(torch.float32, 4 * rows, ("scores", "new_scores"), scores, new_scores)
+    done, new_done = _arrays(torch.uint8, rows, ("done", "new_done"), _flags(done), _flags(new_done))
+    parent, token = _arrays(torch.int32, 4 * rows, ("parent", "token"), parent, token)
     _check(load_library().gdn_beam_select(
-        ctypes.byref(dims), *_ptrs(logits, scores, done, parent, token, new_scores, new_done, workspace),
+        ctypes.byref(dims), _ptr(logits), scores, done, parent, token, new_scores, new_done, _ptr(workspace),
         workspace.nbytes if workspace is not None else 0, _stream(stream)))
+
+
+_FORK_ROWS = ("parent", "n_new", "kv_len", "kv_len_out", "page_src", "page_dst", "state_idx", "state_idx_out", "state_src",
+              "state_dst")
 
 
 def cache_fork(page_table, kv_len, page_table_out, kv_len_out, kv_index, page_src, page_dst, n_pages, parent=None,
                n_new=None, pinned=None, state_idx=None, state_idx_out=None, state_src=None, state_dst=None, stream=None):
     """gdn_cache_fork: rows become copies of the rows parent int32 [R] and take n_new tokens (kv_index int32 [R, T]);
     page_src / page_dst and state_src / state_dst int32 [R] are slots_copy's."""
-    rows, width = page_table.shape[0], _table(page_table)
-    if page_table_out.shape != page_table.shape or _table(page_table_out) != width:
-        raise ValueError("page_table and page_table_out must have one shape")
+    if page_table.dim() != 2 or page_table_out.shape != page_table.shape:
+        raise ValueError("page_table and page_table_out must be of one shape [rows, max_pages]")
+    rows, width = page_table.shape
     T = 0 if kv_index is None else kv_index.shape[1]
     dims = ForkDims(rows, T, width, n_pages)
-    _check(load_library().gdn_cache_fork(
-        ctypes.byref(dims), *_ptrs(parent, n_new, page_table, kv_len, pinned, page_table_out, kv_len_out, kv_index, page_src,
-                                   page_dst, state_idx, state_idx_out, state_src, state_dst), _stream(stream)))
+    _here(page_table, "page_table")
+    table, table_out = _arrays(torch.int32, 4 * rows * width, ("page_table", "page_table_out"), page_table, page_table_out)
+    index, = _arrays(torch.int32, 4 * rows * T, ("kv_index",), kv_index)
+    pins, = _arrays(torch.uint8, n_pages, ("pinned",), _flags(pinned))
+    parent, n_new, kv_len, kv_len_out, *copies = _arrays(
+        torch.int32, 4 * rows, _FORK_ROWS, parent, n_new, kv_len, kv_len_out, page_src, page_dst, state_idx, state_idx_out,
+        state_src, state_dst)
+    _check(load_library().gdn_cache_fork(ctypes.byref(dims), parent, n_new, table, kv_len, pins, table_out, kv_len_out, index,
+                                         *copies, _stream(stream)))
 
 
 def slots_copy(pools, stream=None):
@@ -532,7 +580,8 @@ def slots_copy(pools, stream=None):
             raise ValueError("a pool must be a dense tensor [n_layers, n_slots, ...], src and dst of one length")
         layers, slots = shape[0], shape[1]
         slot = x.nbytes // (layers * slots) if layers * slots else x.element_size() * math.prod(shape[2:])
-        args.append(SlotPool(x.data_ptr(), src.data_ptr(), dst.data_ptr(), slot, n, layers, slots))
+        _here(x, "a pool")
+        args.append(SlotPool(x.data_ptr(), *_arrays(torch.int32, 4 * n, ("src", "dst"), src, dst), slot, n, layers, slots))
     n = len(args)
     array = _pools_of[n] if n <= MAX_SLOT_POOLS else SlotPool * n
     _check(load_library().gdn_slots_copy(array(*args), n, _stream(stream)))
