@@ -169,11 +169,6 @@ def _ptr(t):
     return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
-def _ptrs(*tensors):
-    """_ptr of each: 0.13 us a tensor on the host, one by one 0.25."""
-    return [t if t is None or t.__class__ is int else t.data_ptr() for t in tensors]
-
-
 # torch.cuda.current_stream() builds a Stream object (3 us); a small call's kernel takes 5
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", None)
@@ -208,6 +203,15 @@ def _here(x, name):
         device = x.get_device()
         if device < 0 or device != (_device() if _device is not None else torch.cuda.current_device()):
             raise ValueError(f"{name} must be on the current device, it is on {x.device}")
+
+
+def _space(workspace):
+    """Address and bytes of a workspace tensor, which is dense."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be dense")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _flags(x):
@@ -371,6 +375,19 @@ def _spaced(x, stride, name):
             raise ValueError(f"{name}'s tokens are {st[-3]} elements apart, the sizes say {stride}")
 
 
+def _tokens(x, n, heads, d, stride, name):
+    """_ptr of x, which must be n tokens (or more) of `heads` heads of d, `stride` elements apart, as the sizes say."""
+    if x is None or x.__class__ is int:
+        return x
+    # the usual case at once: 0.3 us on the host in place of 1
+    if x.stride() != (stride, d, 1) or x.shape != (n, heads, d) or x.dtype is not torch.bfloat16:
+        tokens, h, dim, apart = _layout(x, name)
+        if tokens < n or h != heads or dim != d or (apart != stride and n > 1):
+            raise ValueError(f"{name} is {tokens} tokens of {h} heads of {dim}, {apart} elements apart, the sizes say {n}, "
+                             f"{heads}, {d}, {stride}")
+    return x.data_ptr()
+
+
 def make_rope_dims(q, k, rot_dim, n_axes=1, kv_rows=None, adjacent=False, eps=1e-6, v=None) -> RopeDims:
     """Sizes and token strides of a head_norm_rope call on q [n, Hq, d] and k [n, Hk, d]; v's tokens are spaced as
     k's unless v is given. kv_rows: rows of the pools (n when they hold the tokens themselves)."""
@@ -463,26 +480,29 @@ def make_kv4_dims(k, pool, v=None, k_exp=0, v_exp=0) -> Kv4Dims:
     return Kv4Dims(n, hk, d, _page_pool(pool, hk, d), k_exp, v_exp, ks, ks if v is None else _layout(v, "v")[3])
 
 
+def _kv4_arguments(dims, k, v, kv_index, pool):
+    """The four addresses of a kv4_store or kv4_load call."""
+    n, heads, d = dims.n_tokens, dims.n_kv_heads, dims.head_dim
+    _here(pool, "pool")
+    return (_tokens(k, n, heads, d, dims.k_stride, "k"), _tokens(v, n, heads, d, dims.v_stride, "v"),
+            *_arrays(torch.int32, 4 * n, ("kv_index",), kv_index),
+            *_arrays(torch.uint8, dims.n_pages * heads * 72 * d, ("pool",), pool))
+
+
 def kv4_store(dims: Kv4Dims, k, v, kv_index, pool, stream=None):
     """gdn_kv4_store: k, v bf16 [n, Hk, d] into the pool rows kv_index int32 [n] (-1: not kept), 4 bits each."""
-    _spaced(k, dims.k_stride, "k")
-    _spaced(v, dims.v_stride, "v")
-    _here(pool, "pool")
-    index, = _arrays(torch.int32, 4 * dims.n_tokens, ("kv_index",), kv_index)
-    _check(load_library().gdn_kv4_store(ctypes.byref(dims), *_ptrs(k, v), index, _ptr(pool), _stream(stream)))
+    args = _kv4_arguments(dims, k, v, kv_index, pool)
+    _check(load_library().gdn_kv4_store(ctypes.byref(dims), *args, _stream(stream)))
 
 
 def kv4_load(dims: Kv4Dims, pool, kv_index, k, v, stream=None):
     """gdn_kv4_load: pool rows kv_index int32 [n] to k, v bf16 [n, Hk, d], exactly as attn_kv4 uses them."""
-    _spaced(k, dims.k_stride, "k")
-    _spaced(v, dims.v_stride, "v")
-    _here(pool, "pool")
-    index, = _arrays(torch.int32, 4 * dims.n_tokens, ("kv_index",), kv_index)
-    _check(load_library().gdn_kv4_load(ctypes.byref(dims), _ptr(pool), index, *_ptrs(k, v), _stream(stream)))
+    to_k, to_v, index, pages = _kv4_arguments(dims, k, v, kv_index, pool)
+    _check(load_library().gdn_kv4_load(ctypes.byref(dims), pages, index, to_k, to_v, _stream(stream)))
 
 
-def make_attn_kv4_dims(q, pool, page_table, scale=None, k_exp=0, v_exp=0) -> AttnKv4Dims:
-    """Sizes of an attn_kv4 call: q [B, T, Hq, d], one layer's pool, page_table int32 [B, max_pages]."""
+def _row_tokens(q):
+    """(rows, tokens, heads, head_dim, elements between tokens) of a bf16 tensor [rows, tokens, heads, head_dim]."""
     shape, st = q.shape, q.stride()
     if q.dtype is not torch.bfloat16 or len(shape) != 4:
         raise ValueError("q must be a bf16 tensor [rows, tokens, heads, head_dim]")
@@ -490,6 +510,12 @@ def make_attn_kv4_dims(q, pool, page_table, scale=None, k_exp=0, v_exp=0) -> Att
     qs = st[0] if T == 1 else st[1]  # the stride of a dimension of one token says nothing
     if st[3] != 1 or (st[2] != d and hq > 1) or (T > 1 and B > 1 and st[0] != T * qs):
         raise ValueError("q must have dense heads and evenly spaced tokens")
+    return B, T, hq, d, qs
+
+
+def make_attn_kv4_dims(q, pool, page_table, scale=None, k_exp=0, v_exp=0) -> AttnKv4Dims:
+    """Sizes of an attn_kv4 call: q [B, T, Hq, d], one layer's pool, page_table int32 [B, max_pages]."""
+    B, T, hq, d, qs = _row_tokens(q)
     hk = pool.shape[1] if pool.dim() == 3 else 0
     return AttnKv4Dims(B, T, hq, hk, d, _page_pool(pool, hk, d), _table(page_table, B), k_exp, v_exp,
                        d ** -0.5 if scale is None else scale, qs)
@@ -507,12 +533,21 @@ def attn_kv4_workspace(dims: AttnKv4Dims, device="cuda") -> torch.Tensor:
 
 def attn_kv4(dims: AttnKv4Dims, q, pool, page_table, kv_len, out, workspace, q_len=None, stream=None):
     """gdn_attn_kv4: q [B, T, Hq, d] over the pages of each row, kv_len int32 [B] tokens of it."""
+    B, T, hq, hk, d = dims.B, dims.T, dims.n_q_heads, dims.n_kv_heads, dims.head_dim
+    if q is not None and q.__class__ is not int:
+        qs = dims.q_stride
+        if q.stride() != (T * qs, qs, d, 1) or q.shape != (B, T, hq, d) or q.dtype is not torch.bfloat16:  # not the usual case
+            rows, *sizes, stride = _row_tokens(q)
+            if rows < B or sizes != [T, hq, d] or (stride != qs and B * T > 1):
+                raise ValueError(f"q is {[rows, *sizes]}, its tokens {stride} elements apart, the sizes say {[B, T, hq, d]}, "
+                                 f"{qs}")
     _here(pool, "pool")
-    table, = _arrays(torch.int32, 4 * dims.B * dims.max_pages, ("page_table",), page_table)
-    lens = _arrays(torch.int32, 4 * dims.B, ("kv_len", "q_len"), kv_len, q_len)
-    _check(load_library().gdn_attn_kv4(
-        ctypes.byref(dims), *_ptrs(q, pool), table, *lens, *_ptrs(out, workspace),
-        workspace.nbytes if workspace is not None else 0, _stream(stream)))
+    pages, = _arrays(torch.uint8, dims.n_pages * hk * 72 * d, ("pool",), pool)
+    table, = _arrays(torch.int32, 4 * B * dims.max_pages, ("page_table",), page_table)
+    lens = _arrays(torch.int32, 4 * B, ("kv_len", "q_len"), kv_len, q_len)
+    to, = _arrays(torch.bfloat16, 2 * B * T * hq * d, ("out",), out)
+    space, size = _space(workspace)
+    _check(load_library().gdn_attn_kv4(ctypes.byref(dims), _ptr(q), pages, table, *lens, to, space, size, _stream(stream)))
 
 
 def make_beam_dims(logits, eos=-1) -> BeamDims:
@@ -542,8 +577,8 @@ def beam_select(logits, scores, parent, token, new_scores, workspace, done=None,
     done, new_done = _arrays(torch.uint8, rows, ("done", "new_done"), _flags(done), _flags(new_done))
     parent, token = _arrays(torch.int32, 4 * rows, ("parent", "token"), parent, token)
     _check(load_library().gdn_beam_select(
-        ctypes.byref(dims), _ptr(logits), scores, done, parent, token, new_scores, new_done, _ptr(workspace),
-        workspace.nbytes if workspace is not None else 0, _stream(stream)))
+        ctypes.byref(dims), _ptr(logits), scores, done, parent, token, new_scores, new_done, *_space(workspace),
+        _stream(stream)))
 
 
 _FORK_ROWS = ("parent", "n_new", "kv_len", "kv_len_out", "page_src", "page_dst", "state_idx", "state_idx_out", "state_src",

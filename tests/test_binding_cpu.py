@@ -84,6 +84,41 @@ def test_tensors_of_another_device(call):
         CALLS[call]()[1]()
 
 
+def _others(x):
+    """What is not x's layout: other types, fewer tokens, heads or channels, other strides."""
+    wide = torch.zeros((*x.shape[:-1], 2 * x.shape[-1]), dtype=x.dtype)
+    return [x.float(), x[:-1], x[..., :-1, :].contiguous(), x[..., : x.shape[-1] // 2].contiguous(),
+            wide[..., :x.shape[-1]], wide[..., ::2], x[:1].expand(x.shape)]
+
+
+@pytest.mark.parametrize("call,names", [("kv4_store", "kv"), ("kv4_load", "kv"), ("attn_kv4", ("q", "out"))])
+def test_tokens_that_are_not_as_the_sizes_say(call, names, monkeypatch):
+    a, run, _ = CALLS[call]()
+    monkeypatch.setattr(gdn, "_here", lambda x, name: None)
+    for n in names:
+        for b in _others(a[n]):
+            with pytest.raises(ValueError):
+                run(**{n: b})
+
+
+@pytest.mark.parametrize("call", ["kv4_store", "kv4_load", "attn_kv4"])
+def test_pools_that_are_not_as_the_sizes_say(call, monkeypatch):
+    a, run, _ = CALLS[call]()
+    monkeypatch.setattr(gdn, "_here", lambda x, name: None)
+    pool = a["pool"]
+    for b in (pool.int(), pool[:-1], pool[:, :1], pool[..., ::2], pool[:1].expand(pool.shape)):
+        with pytest.raises(ValueError):
+            run(pool=b)
+
+
+@pytest.mark.parametrize("call", ["attn_kv4", "beam_select"])
+def test_workspaces_with_gaps(call, monkeypatch):
+    a, run, _ = CALLS[call]()
+    monkeypatch.setattr(gdn, "_here", lambda x, name: None)
+    with pytest.raises(ValueError):
+        run(workspace=torch.zeros((1 << 20, 2), dtype=torch.uint8)[:, 0])
+
+
 def test_arrays_that_pass(monkeypatch):
     x = _ints(2, 3)
     assert gdn._arrays(torch.int32, 20, "abc", None, 1 << 20, x) == [None, 1 << 20, x.data_ptr()]
