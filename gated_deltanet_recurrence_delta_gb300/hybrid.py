@@ -27,6 +27,8 @@ import torch
 
 from . import gdn
 
+_STEP = 64  # the most tokens of a row that a step over pages takes (gdn.attn_kv4)
+
 
 def _on(stream):
     """The context in which torch's own operations and allocations belong to `stream` (a stream or its handle; None: the
@@ -157,9 +159,13 @@ class PagedAttentionLayers:
         """Row r becomes a copy of row parent[r] (int32 [n_rows], -1: emptied; None: itself) and takes n_new[r] tokens
         (int32 [n_rows] in [0, T]; None: T). With state_idx int32 [n_rows], the rows' slots of `stack` (a LayerStack), it
         is brought along in place and the states and conv tails are copied too. Returns kv_index int32 [n_rows, T], the
-        tokens' pool rows; kv_len holds the rows' lengths with them."""
+        tokens' pool rows (up to the 64 tokens of a step it is the same tensor every time, which the stream's next take()
+        of T tokens writes anew; a prompt's is the caller's); kv_len holds the rows' lengths with them."""
         with _on(stream):
-            index = self._buffer("index", (self.n_rows, T), torch.int32, stream)
+            if T <= _STEP:
+                index = self._buffer("index", (self.n_rows, T), torch.int32, stream)
+            else:  # prompts are of any length: one kept for each would be without end
+                index = torch.empty((self.n_rows, T), dtype=torch.int32, device=self.device)
             states = {}
             if state_idx is not None:
                 names = ("state_idx_out", "state_src", "state_dst")

@@ -1,0 +1,53 @@
+"""What the paged layers of hybrid.py and its beams keep and hand to the library, without a GPU: the library's calls are
+replaced by recorders."""
+import types
+
+import pytest
+import torch
+
+from gated_deltanet_recurrence_delta_gb300 import gdn, hybrid
+
+HQ, HK, D, ROWS = 4, 2, 64, 3
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The recorded calls: (name, arguments by name)."""
+    seen = []
+
+    def fork(page_table, kv_len, page_table_out, kv_len_out, kv_index, page_src, page_dst, n_pages, parent=None, n_new=None,
+             **kw):
+        T = 0 if kv_index is None else kv_index.shape[1]
+        new = torch.full_like(kv_len, T) if n_new is None else n_new
+        copy = lambda x: None if x is None else x.clone()  # noqa: E731
+        seen.append(("fork", types.SimpleNamespace(T=T, parent=copy(parent), n_new=copy(n_new), **kw)))
+        page_table_out.copy_(page_table)
+        kv_len_out.copy_(kv_len + new)
+        if T:
+            kv_index.copy_(torch.where(torch.arange(T) < new[:, None], len(seen), -1))
+
+    monkeypatch.setattr(gdn, "cache_fork", fork)
+    monkeypatch.setattr(gdn, "slots_copy", lambda pools, stream=None: seen.append(("copy", len(pools))))
+    monkeypatch.setattr(gdn, "_stream", lambda s: 0 if s is None else s if isinstance(s, int) else s.cuda_stream)
+    return seen
+
+
+def _layers():
+    weights = [dict(q_norm=None, k_norm=None)]
+    return hybrid.PagedAttentionLayers(HQ, HK, D, weights, torch.ones(16, dtype=torch.float64), ROWS, 20, 300, device="cpu")
+
+
+def _ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def test_prompts_of_any_length_leave_nothing_behind(calls):
+    """The rows of a prompt's tokens are the caller's: no later take() writes them, none is kept."""
+    att = _layers()
+    first = att.take(1000)
+    for T in (1, 64, *range(65, 400, 7), 1000):
+        att.take(T)
+    assert bool((first == 1).all())
+    assert sum(x.nbytes for x in att.buffers.values()) == 4 * ROWS * (1 + 64)
+    step = att.take(8)
+    assert att.take(8) is step and att.take(0).shape == (ROWS, 0)
