@@ -257,15 +257,18 @@ class Beams:
         self.scores[:, 0] = 0.0
         self.parent = torch.arange(groups * beams, dtype=torch.int32, device=device).view(groups, beams)
         self.token = new(torch.int32, -1)
-        self.workspaces = {}  # a captured step keeps the one of its logits
+        self.workspaces = {}  # for each shape of logits and stream: a captured step keeps its own
 
     def select(self, logits, eos=-1, stream=None):
-        """The best continuations, from the rows' logits [groups, beams, V] (fp32 or bf16)."""
+        """The best continuations, from the rows' logits [groups, beams, V] (fp32 or bf16). A call given a stream does all
+        its work on it."""
         if logits.shape[:2] != self.scores.shape:
             raise ValueError(f"logits must be {list(self.scores.shape)} rows, they are {list(logits.shape[:2])}")
-        if logits.shape not in self.workspaces:
-            self.workspaces[logits.shape] = gdn.beam_workspace(logits)
-        gdn.beam_select(logits, self.scores, self.parent, self.token, self.scores, self.workspaces[logits.shape],
+        key = (logits.shape, gdn._stream(stream))
+        if key not in self.workspaces:
+            with _on(stream):  # of that stream's memory: a block of another one's may still be in use there
+                self.workspaces[key] = gdn.beam_workspace(logits)
+        gdn.beam_select(logits, self.scores, self.parent, self.token, self.scores, self.workspaces[key],
                         done=self.done, new_done=self.done, eos=eos, stream=stream)
 
 

@@ -1,10 +1,12 @@
-"""Rows of the paged 4-bit cache where a rule of one row depends on the others: forks of rows whose last pages are pinned."""
+"""Rows of the paged 4-bit cache and beams where one depends on what others do: forks of rows whose last pages are pinned,
+streams beside one another."""
 import random
 
 import pytest
 import torch
 
 from gated_deltanet_recurrence_delta_gb300 import gdn
+from gated_deltanet_recurrence_delta_gb300.hybrid import Beams
 from tests import kv4_plain
 from tests.test_gpu_beam import _check_fork, _fork
 
@@ -48,3 +50,28 @@ def test_fork_of_pinned_last_pages(R):
         for _ in range(10):
             _check_fork(_fork(table, lens, n_pages, 2, n_new=n_new, pinned=pinned), want)
     gdn.check_status()
+
+
+def test_a_first_selection_on_a_stream_beside_a_busy_one():
+    """The current stream still writes to memory that torch has taken back: a selection's workspace on another stream is
+    none of it."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.randn((16, 8, 50000), generator=g, device="cuda")
+    want = Beams(16, 8)
+    want.select(logits)
+    gdn.check_status()
+    n = gdn.beam_workspace(logits).numel()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        got = Beams(16, 8)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(2_000_000)  # 1 ms
+        x = torch.empty(n, dtype=torch.uint8, device="cuda")
+        for _ in range(200):
+            x.fill_(255)
+        del x
+        got.select(logits, stream=side)
+        torch.cuda.synchronize()
+        gdn.check_status()
+        for name in ("scores", "parent", "token", "done"):
+            assert torch.equal(getattr(got, name), getattr(want, name))

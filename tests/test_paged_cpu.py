@@ -51,3 +51,31 @@ def test_prompts_of_any_length_leave_nothing_behind(calls):
     assert sum(x.nbytes for x in att.buffers.values()) == 4 * ROWS * (1 + 64)
     step = att.take(8)
     assert att.take(8) is step and att.take(0).shape == (ROWS, 0)
+
+
+def test_a_selection_takes_its_workspace_from_its_stream(calls, monkeypatch):
+    """One for each shape and stream, made while that stream is torch's own."""
+    on, used = [None], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            on.append(self.stream)
+
+        def __exit__(self, *_):
+            on.pop()
+
+    def select(logits, scores, parent, token, new_scores, workspace, done=None, new_done=None, eos=-1, stream=None):
+        used.append((workspace, stream))
+
+    monkeypatch.setattr(hybrid, "_on", On)
+    monkeypatch.setattr(gdn, "beam_workspace", lambda logits: (tuple(logits.shape), on[-1]))
+    monkeypatch.setattr(gdn, "beam_select", select)
+    beams, shape = hybrid.Beams(2, 3, device="cpu"), (2, 3, 50)
+    for stream in (None, 7, 9, None, 7):
+        beams.select(torch.zeros(shape), stream=stream)
+    assert used == [((shape, s), s) for s in (None, 7, 9, None, 7)] and len(beams.workspaces) == 3
+    with pytest.raises(ValueError):
+        beams.select(torch.zeros((2, 4, 50)))
