@@ -249,14 +249,15 @@ class PagedAttentionLayers:
 
 class Beams:
     """What a beam search carries from step to step, [groups, beams] each: the scores (fp32, -inf: no beam), done (uint8),
-    and the last selection's parent (row numbers) and token. At the start each group has one beam, its first row."""
+    and the last selection's parent (row numbers) and token (-1: a place that it left without a beam; -2: none was made
+    yet). At the start each group has one beam, its first row."""
 
     def __init__(self, groups, beams, device="cuda"):
         new = lambda dtype, fill: torch.full((groups, beams), fill, dtype=dtype, device=device)  # noqa: E731
         self.scores, self.done = new(torch.float32, float("-inf")), new(torch.uint8, 0)
         self.scores[:, 0] = 0.0
         self.parent = torch.arange(groups * beams, dtype=torch.int32, device=device).view(groups, beams)
-        self.token = new(torch.int32, -1)
+        self.token = new(torch.int32, -2)
         self.workspaces = {}  # for each shape of logits and stream: a captured step keeps its own
 
     def select(self, logits, eos=-1, stream=None):
@@ -280,9 +281,11 @@ def beam_step(stack, attention, beams, acts, qkv, logits, state_idx, buffers, eo
     stack: LayerStack; attention: PagedAttentionLayers; beams: Beams; acts / qkv: the layers' inputs (LayerStack.decode;
     PagedAttentionLayers.step with T = 1); logits: [groups, beams, V]; state_idx int32 [n_rows], the rows' state slots;
     buffers: dict with gdn_out (LayerStack.decode), q and attn_out [n_layers][n_rows][1][hq][d]. A finished beam takes no
-    tokens. The logits come from the layers' outputs; here they are given."""
-    n_new = (beams.done.flatten() == 0).to(torch.int32)
-    index = attention.take(1, beams.parent.flatten(), n_new, state_idx, stack)
+    tokens. The row of a place that the last selection left without a beam is emptied and takes none: nobody reads it, and
+    its pages are the others'. The logits come from the layers' outputs; here they are given."""
+    going, none = (beams.done == 0).flatten(), (beams.token == -1).flatten()
+    n_new = (going > none).to(torch.int32)
+    index = attention.take(1, beams.parent.flatten().masked_fill(going & none, -1), n_new, state_idx, stack)
     stack.decode(acts, state_idx, buffers["gdn_out"])
     for layer in range(attention.n_layers):
         attention.step(layer, qkv[layer], index, buffers["q"], buffers["attn_out"][layer])

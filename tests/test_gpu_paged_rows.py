@@ -1,14 +1,15 @@
 """Rows of the paged 4-bit cache and beams where one depends on what others do: forks of rows whose last pages are pinned,
-streams beside one another."""
+streams beside one another, places without a beam."""
 import random
 
 import pytest
 import torch
 
 from gated_deltanet_recurrence_delta_gb300 import gdn
-from gated_deltanet_recurrence_delta_gb300.hybrid import Beams
+from gated_deltanet_recurrence_delta_gb300.hybrid import Beams, beam_step
 from tests import kv4_plain
 from tests.test_gpu_beam import _check_fork, _fork
+from tests.test_gpu_beam_search import _World
 
 pytestmark = pytest.mark.gpu
 PAGE = 64
@@ -75,3 +76,25 @@ def test_a_first_selection_on_a_stream_beside_a_busy_one():
         gdn.check_status()
         for name in ("scores", "parent", "token", "done"):
             assert torch.equal(getattr(got, name), getattr(want, name))
+
+
+def test_places_without_a_beam_leave_their_pages_to_the_others():
+    """One allowed token a row and step: each group has one beam of four for 70 steps, in a pool of as many pages as the
+    first step takes. The other rows would need a second page each after 64 steps."""
+    w = _World(W=4, layers=1, n_pages=11)  # 4 pages of prompts, one for the second's next token, 6 rows' first ones
+    att, W, R, V = w.att, w.W, w.R, 200
+    beams, acts, s = Beams(2, W), w.stack.static_acts(R, 1), w.shape
+    qkv = [w.rand(R, 1, (w.hq + 2 * w.hk) * w.d)]
+    buf = dict(gdn_out=torch.empty((2, R, 1, s.nv, s.dv), dtype=torch.bfloat16, device="cuda"),
+               q=torch.empty((R, 1, w.hq, w.d), dtype=torch.bfloat16, device="cuda"),
+               attn_out=torch.empty((1, R, 1, w.hq, w.d), dtype=torch.bfloat16, device="cuda"))
+    for i in range(70):
+        logits = torch.full((2, W, V), -float("inf"), device="cuda")
+        logits[:, :, (17 * i) % V] = 0.5
+        beam_step(w.stack, att, beams, acts, qkv, logits, w.state_idx, buf)
+        gdn.check_status()
+        other = 1 if i == 0 else 0
+        assert att.kv_len.tolist() == [131 + i, *[other] * 3, 65 + i, *[other] * 3]
+        assert beams.token.tolist() == [[(17 * i) % V, -1, -1, -1]] * 2
+        assert sorted(w.state_idx.tolist()) == list(range(R))
+    assert bool((buf["attn_out"][0, [0, W]] != 0).any()) and not bool(buf["attn_out"][0, [1, 2, 3]].any())

@@ -79,3 +79,23 @@ def test_a_selection_takes_its_workspace_from_its_stream(calls, monkeypatch):
     assert used == [((shape, s), s) for s in (None, 7, 9, None, 7)] and len(beams.workspaces) == 3
     with pytest.raises(ValueError):
         beams.select(torch.zeros((2, 4, 50)))
+
+
+def test_places_without_a_beam_take_nothing(calls):
+    """At the start every row takes a token; what a selection left without a beam (token -1) is emptied and takes none, and
+    a finished beam keeps its row as it is, whatever its token."""
+    att, beams = _layers(), hybrid.Beams(1, ROWS, device="cpu")
+    att.step = lambda *a, **k: None
+    select = types.SimpleNamespace(next=None)
+    beams.select = lambda logits, eos: [getattr(beams, n).copy_(torch.tensor([x])) for n, x in select.next.items()]
+    stack = types.SimpleNamespace(decode=lambda *a: None, state_pool=None, conv_pool=None)
+    buf = dict(gdn_out=None, q=None, attn_out=[None])
+    inf = float("inf")
+    chosen = [dict(parent=[0, 1, 2], token=[7, -1, -1], scores=[-1.0, -inf, -inf], done=[0, 0, 0]),
+              dict(parent=[0, 0, 2], token=[5, -1, -1], scores=[-1.0, -2.0, -inf], done=[0, 1, 0]),
+              dict(parent=[1, 0, 0], token=[3, 9, 5], scores=[-2.0, -3.0, -4.0], done=[1, 0, 0]), {}]
+    want = [([0, 1, 2], [1, 1, 1]), ([0, -1, -1], [1, 0, 0]), ([0, 0, -1], [1, 0, 0]), ([1, 0, 0], [0, 1, 1])]
+    for select.next, (parent, n_new) in zip(chosen, want):
+        hybrid.beam_step(stack, att, beams, None, [None], None, None, buf)
+        got = [x for kind, x in calls if kind == "fork"][-1]
+        assert (got.parent.tolist(), got.n_new.tolist()) == (parent, n_new) and got.parent.dtype == torch.int32
