@@ -701,12 +701,14 @@ typedef struct gdn_fork_dims {
  * tokens among those that hold it (ties: the lowest row), unless it is pinned;
  * every other row that takes tokens gets a copy. New pages are the
  * lowest-numbered free ones, in the order of the rows, for a row its copy first.
- * A row whose pages do not exist any more (none free, or more than max_pages)
- * takes no tokens (kv_len_out = L, kv_index -1), which is a device error
- * (GDN_ERR_FULL). A page that several rows hold stands at the same place in
- * all of them, as copies of a row have it. The lowest child of a row keeps that
- * row's state slot; other children, and emptied rows, take the slots of rows
- * without children, in order. A parent outside [-1, n_rows), a length outside
+ * A row that would have more than max_pages takes no tokens (kv_len_out = L,
+ * kv_index -1). So do the first row for which the free pages do not suffice and
+ * every row behind it that needs pages, however few (what is left over stays
+ * free: a row waits for those in front of it); rows that need none take theirs.
+ * Either is a device error (GDN_ERR_FULL). A page that several rows hold stands
+ * at the same place in all of them, as copies of a row have it. The lowest child
+ * of a row keeps that row's state slot; other children, and emptied rows, take the
+ * slots of rows without children, in order. A parent outside [-1, n_rows), a length outside
  * [0, 64 max_pages], an n_new outside [0, T] or a used page outside
  * [0, n_pages) is a device error (GDN_ERR_INDEX), taken as -1, 0, 0, and a page
  * that nothing is copied from. */

@@ -98,3 +98,21 @@ def test_places_without_a_beam_leave_their_pages_to_the_others():
         assert beams.token.tolist() == [[(17 * i) % V, -1, -1, -1]] * 2
         assert sorted(w.state_idx.tolist()) == list(range(R))
     assert bool((buf["attn_out"][0, [0, W]] != 0).any()) and not bool(buf["attn_out"][0, [1, 2, 3]].any())
+
+
+def test_rows_wait_for_those_in_front_of_them():
+    """Three free pages, of which row 1 needs five: it takes nothing, nor does row 2 behind it, which needs one; row 3 needs
+    none and takes its tokens, as row 0 in front does. Without row 1's tokens row 2 is served."""
+    table, lens = [[0, 1, -3, -3, -3, -3], [2, -3, -3, -3, -3, -3], [3, -3, -3, -3, -3, -3], [4, -3, -3, -3, -3, -3]], [
+        128, 64, 64, 10]
+    got = _fork(table, lens, 9, 300, n_new=[1, 300, 1, 2])
+    with pytest.raises(gdn.GdnError, match="GDN_ERR_FULL"):
+        gdn.check_status()
+    assert got["kv_len"] == [129, 64, 64, 12]
+    index = [[x for x in row if x >= 0] for row in got["kv_index"]]
+    assert index == [[5 * PAGE], [], [], [4 * PAGE + 10, 4 * PAGE + 11]]
+    assert got["page_src"] == got["page_dst"] == [-1] * 4
+    assert [row[:2] for row in got["table"]] == [[0, 1], [2, -77], [3, -77], [4, -77]] and got["table"][0][2] == 5
+    got = _fork(table, lens, 9, 300, n_new=[1, 0, 1, 2])
+    gdn.check_status()
+    assert got["kv_len"] == [129, 64, 65, 12] and got["table"][2][:2] == [3, 6] and got["kv_index"][2][0] == 6 * PAGE
