@@ -158,7 +158,8 @@ class PagedAttentionLayers:
     def take(self, T, parent=None, n_new=None, state_idx=None, stack=None, stream=None):
         """Row r becomes a copy of row parent[r] (int32 [n_rows], -1: emptied; None: itself) and takes n_new[r] tokens
         (int32 [n_rows] in [0, T]; None: T). With state_idx int32 [n_rows], the rows' slots of `stack` (a LayerStack), it
-        is brought along in place and the states and conv tails are copied too. Returns kv_index int32 [n_rows, T], the
+        is brought along in place and the states and conv tails are copied too (an emptied row's slot, state_idx[r], holds
+        what its last row left there: set it to zeros before a new sequence starts in it). Returns kv_index int32 [n_rows, T], the
         tokens' pool rows (up to the 64 tokens of a step it is the same tensor every time, which the stream's next take()
         of T tokens writes anew; a prompt's is the caller's); kv_len holds the rows' lengths with them."""
         with _on(stream):

@@ -708,10 +708,12 @@ typedef struct gdn_fork_dims {
  * Either is a device error (GDN_ERR_FULL). A page that several rows hold stands
  * at the same place in all of them, as copies of a row have it. The lowest child
  * of a row keeps that row's state slot; other children, and emptied rows, take the
- * slots of rows without children, in order. A parent outside [-1, n_rows), a length outside
- * [0, 64 max_pages], an n_new outside [0, T] or a used page outside
- * [0, n_pages) is a device error (GDN_ERR_INDEX), taken as -1, 0, 0, and a page
- * that nothing is copied from. */
+ * slots of rows without children, in order. Nothing is copied to an emptied row's
+ * slot: it holds what its last row left there, and whoever starts a new sequence
+ * in it sets its state and conv tail to zeros first. A parent outside
+ * [-1, n_rows), a length outside [0, 64 max_pages], an n_new outside [0, T] or a
+ * used page outside [0, n_pages) is a device error (GDN_ERR_INDEX), taken as -1,
+ * 0, 0, and a page that nothing is copied from. */
 gdn_status gdn_cache_fork(const gdn_fork_dims *dims, const int32_t *parent, const int32_t *n_new,
                           const int32_t *page_table, const int32_t *kv_len, const uint8_t *pinned,
                           int32_t *page_table_out, int32_t *kv_len_out, int32_t *kv_index, int32_t *page_src,
