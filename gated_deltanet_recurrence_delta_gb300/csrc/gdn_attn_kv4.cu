@@ -774,7 +774,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) a
 
 // The parts of a unit that several CTAs worked on. Where there are more units than CTAs, job blockIdx.x is the unit that
 // CTA blockIdx.x begins and does not finish, else it is a unit; kJoin pieces of 4 channels of its columns. Which unit,
-// and whose parts, is found while the attention kernel still runs.
+// and whose parts, is found while the attention kernel still runs: this one is launched when every CTA of that one has
+// passed its own wait, so that whatever wrote the lengths is complete, and no kernel of the call writes them.
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoin, 3) join_kernel(const __grid_constant__ Args A) {
   constexpr int N = 8 * NT, E = D / 4, SETUP = kSetup<NT>;

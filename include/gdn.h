@@ -25,10 +25,11 @@
  *     may start while the kernel before it in the stream is finishing, and it
  *     waits (griddepcontrol.wait) for that kernel to complete before it reads
  *     or writes any caller tensor; it then lets the next kernel in the stream
- *     start early (griddepcontrol.launch_dependents). Inside one prefill call
- *     a kernel may read workspace data of an earlier kernel of the same call
- *     before its wait, once an earlier wait or a flag (release / acquire at
- *     GPU scope) has ordered it. Stream order is preserved for ordinary
+ *     start early (griddepcontrol.launch_dependents). Inside one call a kernel
+ *     behind its first may read workspace data of an earlier kernel of that
+ *     call (prefill), or lengths that no kernel of the call writes
+ *     (gdn_attn_kv4), before its wait, once an earlier wait or a flag (release
+ *     / acquire at GPU scope) has ordered it. Stream order is preserved for ordinary
  *     kernels; a caller's kernel that itself opts into programmatic launch
  *     after a libgdn call must wait before reading libgdn's outputs, as with
  *     any programmatic dependent.

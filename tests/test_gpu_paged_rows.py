@@ -116,3 +116,41 @@ def test_rows_wait_for_those_in_front_of_them():
     got = _fork(table, lens, 9, 300, n_new=[1, 0, 1, 2])
     gdn.check_status()
     assert got["kv_len"] == [129, 64, 65, 12] and got["table"][2][:2] == [3, 6] and got["kv_index"][2][0] == 6 * PAGE
+
+
+def test_lengths_that_change_between_calls():
+    """Lengths written anew by the kernel in front of every call, among calls of few CTAs (a part of the GPU's SMs): the
+    parts of each call are joined by the lengths that it has, 300 calls on end without a wait, eager and as a graph."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    R, width = 5, 40
+    pool = torch.randint(0, 256, (R * width, 2, 72 * 128), generator=g, device="cuda", dtype=torch.uint8)
+    pool[:, :, 64 * 128:] = 0x38  # scales of one
+    table = torch.randperm(R * width, generator=g, device="cuda").int().view(R, width)
+    q = torch.randn((R, 1, 8, 128), generator=g, device="cuda").to(torch.bfloat16)
+    dims = gdn.make_attn_kv4_dims(q, pool, table)
+    work, lens = gdn.attn_kv4_workspace(dims), torch.zeros(R, dtype=torch.int32, device="cuda")
+    sets = torch.randint(0, width * PAGE + 1, (300, R), generator=g, device="cuda").int()
+    want, got = (torch.zeros((300, *q.shape), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def run(out):
+        for i in range(300):
+            lens.copy_(sets[i])
+            gdn.attn_kv4(dims, q, pool, table, lens, out[i], work)
+
+    for i in range(300):
+        lens.copy_(sets[i])
+        torch.cuda.synchronize()
+        gdn.attn_kv4(dims, q, pool, table, lens, want[i], work)
+        torch.cuda.synchronize()
+    assert bool(want.isfinite().all())
+    run(got)
+    gdn.check_status()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(got)
+    for _ in range(5):
+        got.fill_(7.0)
+        graph.replay()
+        gdn.check_status()
+        assert torch.equal(got, want)
