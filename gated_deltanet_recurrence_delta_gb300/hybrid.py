@@ -205,8 +205,11 @@ class PagedAttentionLayers:
         """A layer's decode (T = 1) or verify (T tokens) of all rows: qkv bf16 [n_rows, T, (hq + 2 hk) d], kv_index
         take()'s; q_buf, out: bf16 [n_rows, T, hq, d]. A row's tokens behind the ones it took are none of it: their
         outputs are zeros."""
+        R, T = q_buf.shape[:2]
+        if qkv.shape[:2] != (R, T) or kv_index.numel() != R * T:
+            raise ValueError(f"qkv and kv_index must be of q_buf's {R} rows of {T} tokens, they are {list(qkv.shape)} and "
+                             f"{list(kv_index.shape)}")
         with _on(stream):
-            R, T = q_buf.shape[:2]
             first = self.kv_len - self.taken
             positions = (first[:, None] + torch.arange(T, dtype=torch.int32, device=self.device)).reshape(1, -1)
             k, v = (self._buffer(n, (R * T, self.hk, self.d), torch.bfloat16, stream) for n in ("k", "v"))
@@ -223,6 +226,9 @@ class PagedAttentionLayers:
         that its pages hold already (host lists); take() has given the rows their pages and kv_index is the tokens' of
         it, int32 [n]. qkv bf16 [n, (hq + 2 hk) d]; q_buf, out bf16 [n, hq, d]. The new tokens attend in bf16; the past
         ones as the pages hold them."""
+        if qkv.shape[0] != sum(lens) or kv_index.numel() != sum(lens):
+            raise ValueError(f"qkv and kv_index must be of {sum(lens)} tokens, they are {list(qkv.shape)} and "
+                             f"{list(kv_index.shape)}")
         if not sum(lens):
             return
         with _on(stream):

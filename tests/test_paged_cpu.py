@@ -99,3 +99,17 @@ def test_places_without_a_beam_take_nothing(calls):
         hybrid.beam_step(stack, att, beams, None, [None], None, None, buf)
         got = [x for kind, x in calls if kind == "fork"][-1]
         assert (got.parent.tolist(), got.n_new.tolist()) == (parent, n_new) and got.parent.dtype == torch.int32
+
+
+def test_steps_and_prompts_refuse_another_number_of_tokens(calls):
+    """The pool rows of another take(), or all rows' where one prompt's are meant: tokens would go to others' places."""
+    att, new = _layers(), lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    qkv, q = new(ROWS, 2, (HQ + 2 * HK) * D), new(ROWS, 2, HQ, D)
+    for index, x in ((att.take(4), qkv), (att.take(1), qkv), (att.take(2), qkv[:, :1]), (att.take(2), qkv[:2])):
+        with pytest.raises(ValueError, match="kv_index"):
+            att.step(0, x, index, q, q.clone())
+    index = att.take(100, n_new=_ints(0, 100, 0))
+    qkv, q = new(100, (HQ + 2 * HK) * D), new(100, HQ, D)
+    for at, x in ((index, qkv), (index[1, :99], qkv), (index[1], qkv[:99])):
+        with pytest.raises(ValueError, match="kv_index"):
+            att.prefill(0, x, [1], [100], [0], at, q, q.clone())
