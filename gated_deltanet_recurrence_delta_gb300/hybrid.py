@@ -290,9 +290,9 @@ def beam_step(stack, attention, beams, acts, qkv, logits, state_idx, buffers, eo
     buffers: dict with gdn_out (LayerStack.decode), q and attn_out [n_layers][n_rows][1][hq][d]. A finished beam takes no
     tokens. The row of a place that the last selection left without a beam is emptied and takes none: nobody reads it, and
     its pages are the others'. The logits come from the layers' outputs; here they are given."""
-    going, none = (beams.done == 0).flatten(), (beams.token == -1).flatten()
-    n_new = (going > none).to(torch.int32)
-    index = attention.take(1, beams.parent.flatten().masked_fill(going & none, -1), n_new, state_idx, stack)
+    none = (beams.token == -1) & (beams.scores == float("-inf"))
+    n_new = ((beams.done == 0) > none).flatten().to(torch.int32)
+    index = attention.take(1, beams.parent.masked_fill(none, -1).flatten(), n_new, state_idx, stack)
     stack.decode(acts, state_idx, buffers["gdn_out"])
     for layer in range(attention.n_layers):
         attention.step(layer, qkv[layer], index, buffers["q"], buffers["attn_out"][layer])

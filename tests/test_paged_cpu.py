@@ -93,8 +93,10 @@ def test_places_without_a_beam_take_nothing(calls):
     inf = float("inf")
     chosen = [dict(parent=[0, 1, 2], token=[7, -1, -1], scores=[-1.0, -inf, -inf], done=[0, 0, 0]),
               dict(parent=[0, 0, 2], token=[5, -1, -1], scores=[-1.0, -2.0, -inf], done=[0, 1, 0]),
-              dict(parent=[1, 0, 0], token=[3, 9, 5], scores=[-2.0, -3.0, -4.0], done=[1, 0, 0]), {}]
-    want = [([0, 1, 2], [1, 1, 1]), ([0, -1, -1], [1, 0, 0]), ([0, 0, -1], [1, 0, 0]), ([1, 0, 0], [0, 1, 1])]
+              dict(parent=[1, 0, 0], token=[3, 9, 5], scores=[-2.0, -3.0, -4.0], done=[1, 0, 0]),
+              dict(parent=[0, 1, 2], token=[-1, -1, -1], scores=[0.0, -inf, -inf], done=[0, 0, 0]), {}]  # set back by hand
+    want = [([0, 1, 2], [1, 1, 1]), ([0, -1, -1], [1, 0, 0]), ([0, 0, -1], [1, 0, 0]), ([1, 0, 0], [0, 1, 1]),
+            ([0, -1, -1], [1, 0, 0])]
     for select.next, (parent, n_new) in zip(chosen, want):
         hybrid.beam_step(stack, att, beams, None, [None], None, None, buf)
         got = [x for kind, x in calls if kind == "fork"][-1]
