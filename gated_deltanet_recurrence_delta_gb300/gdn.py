@@ -27,6 +27,7 @@ EXPORTS = ("gdn_decode_step", "gdn_verify_with_checkpoints", "gdn_prefill_chunke
            "gdn_accept_draft", "gdn_kv4_store", "gdn_kv4_load", "gdn_attn_kv4", "gdn_attn_kv4_workspace_size",
            "gdn_beam_select", "gdn_beam_workspace_size", "gdn_cache_fork", "gdn_slots_copy")
 MAX_OVERLAPPED_COPIES = 8
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8  # 30 ns each when looked up in a call
 MAX_SLOT_POOLS = 4
 PAGE_TOKENS = 64
 
@@ -184,17 +185,22 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _arrays(dtype, size, names, *arrays):
-    """_ptr of each array that a kernel indexes by position alone: refuses a tensor of another type, of fewer than `size`
-    bytes or with gaps (0.2 us a tensor on the host). What has no tensor to look at (None, a raw address) passes."""
-    return [x if x is None or x.__class__ is int
-            else x.data_ptr() if x.dtype is dtype and x.nbytes >= size and x.is_contiguous()
-            else _refuse(x, dtype, size, names[i]) for i, x in enumerate(arrays)]
-
-
-def _refuse(x, dtype, size, name):
+def _array(x, dtype, size, name):
+    """_ptr of an array that a kernel indexes by position alone: refuses a tensor of another type, of fewer than `size`
+    bytes or with gaps (0.3 us on the host). What has no tensor to look at (None, a raw address) passes."""
+    if x is None or x.__class__ is int:
+        return x
+    if x.dtype is dtype and x.nbytes >= size and x.is_contiguous():
+        return x.data_ptr()
     raise ValueError(f"{name} must be a dense {dtype} tensor of {size // dtype.itemsize} elements or more, it is {x.dtype} "
                      f"{list(x.shape)} with strides {list(x.stride())}")
+
+
+def _arrays(dtype, size, names, *arrays):
+    """_array of each, in one go."""
+    return [x if x is None or x.__class__ is int
+            else x.data_ptr() if x.dtype is dtype and x.nbytes >= size and x.is_contiguous()
+            else _array(x, dtype, size, names[i]) for i, x in enumerate(arrays)]
 
 
 def _here(x, name):
@@ -216,7 +222,7 @@ def _space(workspace):
 
 def _flags(x):
     """Truth values as the bytes that they are."""
-    return x.view(torch.uint8) if isinstance(x, torch.Tensor) and x.dtype is torch.bool else x
+    return x if x is None or x.__class__ is int or x.dtype is not torch.bool else x.view(_U8)
 
 
 def make_dims(B, T, nk, nv, dk, dv, n_slots, conv_k=4, scale=None, l2_eps=1e-6, rms_eps=1e-6) -> Dims:
@@ -358,7 +364,9 @@ def _layout(x, name):
     [rows, tokens, heads, head_dim] whose heads lie together and whose tokens are evenly spaced."""
     shape, st = x.shape, x.stride()
     rank = len(shape)
-    if x.dtype is not torch.bfloat16 or not 3 <= rank <= 4:
+    if rank == 3 and st[1:] == (shape[2], 1) and x.dtype is _BF16:  # the usual case: 0.5 us on the host in place of 0.9
+        return *shape, st[0]
+    if x.dtype is not _BF16 or not 3 <= rank <= 4:
         raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, head_dim] or [rows, tokens, heads, head_dim]")
     heads, d = shape[-2], shape[-1]
     n = shape[0] if rank == 3 else shape[0] * shape[1]
@@ -380,7 +388,7 @@ def _tokens(x, n, heads, d, stride, name):
     if x is None or x.__class__ is int:
         return x
     # the usual case at once: 0.3 us on the host in place of 1
-    if x.stride() != (stride, d, 1) or x.shape != (n, heads, d) or x.dtype is not torch.bfloat16:
+    if x.stride() != (stride, d, 1) or x.shape != (n, heads, d) or x.dtype is not _BF16:
         tokens, h, dim, apart = _layout(x, name)
         if tokens < n or h != heads or dim != d or (apart != stride and n > 1):
             raise ValueError(f"{name} is {tokens} tokens of {h} heads of {dim}, {apart} elements apart, the sizes say {n}, "
@@ -454,19 +462,11 @@ def accept_draft(tokens, target_probs, draft_probs, uniform, accept_len, next_to
 
 
 def _page_pool(pool, heads, d):
-    """Pages of a pool uint8 [n_pages, heads, 72 d]."""
+    """(pages, heads) of a pool uint8 [n_pages, heads, 72 d]; heads None: any. Calls look at its strides."""
     shape = pool.shape
-    if pool.dtype is not torch.uint8 or len(shape) != 3 or shape[1] != heads or shape[2] != 72 * d or not pool.is_contiguous():
-        raise ValueError(f"the pool must be a dense uint8 tensor [n_pages, {heads}, {72 * d}]")
-    return shape[0]
-
-
-def _table(page_table, rows=None):
-    """Entries of a line of a page table int32 [rows, max_pages]."""
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous() or (
-            rows is not None and page_table.shape[0] != rows):
-        raise ValueError("page tables must be dense int32 tensors [rows, max_pages]")
-    return page_table.shape[1]
+    if pool.dtype is not _U8 or len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != 72 * d:
+        raise ValueError(f"the pool must be a dense uint8 tensor [n_pages, {heads or 'heads'}, {72 * d}]")
+    return shape[0], shape[1]
 
 
 def kv4_pool(n_pages, n_kv_heads, head_dim, device="cuda") -> torch.Tensor:
@@ -477,7 +477,7 @@ def kv4_pool(n_pages, n_kv_heads, head_dim, device="cuda") -> torch.Tensor:
 def make_kv4_dims(k, pool, v=None, k_exp=0, v_exp=0) -> Kv4Dims:
     """Sizes of a kv4_store / kv4_load call on k [n, Hk, d]; v's tokens are spaced as k's unless v is given."""
     n, hk, d, ks = _layout(k, "k")
-    return Kv4Dims(n, hk, d, _page_pool(pool, hk, d), k_exp, v_exp, ks, ks if v is None else _layout(v, "v")[3])
+    return Kv4Dims(n, hk, d, _page_pool(pool, hk, d)[0], k_exp, v_exp, ks, ks if v is None else _layout(v, "v")[3])
 
 
 def _kv4_arguments(dims, k, v, kv_index, pool):
@@ -485,8 +485,7 @@ def _kv4_arguments(dims, k, v, kv_index, pool):
     n, heads, d = dims.n_tokens, dims.n_kv_heads, dims.head_dim
     _here(pool, "pool")
     return (_tokens(k, n, heads, d, dims.k_stride, "k"), _tokens(v, n, heads, d, dims.v_stride, "v"),
-            *_arrays(torch.int32, 4 * n, ("kv_index",), kv_index),
-            *_arrays(torch.uint8, dims.n_pages * heads * 72 * d, ("pool",), pool))
+            _array(kv_index, _I32, 4 * n, "kv_index"), _array(pool, _U8, dims.n_pages * heads * 72 * d, "pool"))
 
 
 def kv4_store(dims: Kv4Dims, k, v, kv_index, pool, stream=None):
@@ -504,7 +503,7 @@ def kv4_load(dims: Kv4Dims, pool, kv_index, k, v, stream=None):
 def _row_tokens(q):
     """(rows, tokens, heads, head_dim, elements between tokens) of a bf16 tensor [rows, tokens, heads, head_dim]."""
     shape, st = q.shape, q.stride()
-    if q.dtype is not torch.bfloat16 or len(shape) != 4:
+    if q.dtype is not _BF16 or len(shape) != 4:
         raise ValueError("q must be a bf16 tensor [rows, tokens, heads, head_dim]")
     B, T, hq, d = shape
     qs = st[0] if T == 1 else st[1]  # the stride of a dimension of one token says nothing
@@ -516,9 +515,11 @@ def _row_tokens(q):
 def make_attn_kv4_dims(q, pool, page_table, scale=None, k_exp=0, v_exp=0) -> AttnKv4Dims:
     """Sizes of an attn_kv4 call: q [B, T, Hq, d], one layer's pool, page_table int32 [B, max_pages]."""
     B, T, hq, d, qs = _row_tokens(q)
-    hk = pool.shape[1] if pool.dim() == 3 else 0
-    return AttnKv4Dims(B, T, hq, hk, d, _page_pool(pool, hk, d), _table(page_table, B), k_exp, v_exp,
-                       d ** -0.5 if scale is None else scale, qs)
+    pages, hk = _page_pool(pool, None, d)
+    table = page_table.shape
+    if page_table.dtype is not _I32 or len(table) != 2 or table[0] != B:
+        raise ValueError("the page table must be a dense int32 tensor [rows, max_pages]")
+    return AttnKv4Dims(B, T, hq, hk, d, pages, table[1], k_exp, v_exp, d ** -0.5 if scale is None else scale, qs)
 
 
 def attn_kv4_workspace_size(dims: AttnKv4Dims) -> int:
@@ -536,29 +537,29 @@ def attn_kv4(dims: AttnKv4Dims, q, pool, page_table, kv_len, out, workspace, q_l
     B, T, hq, hk, d = dims.B, dims.T, dims.n_q_heads, dims.n_kv_heads, dims.head_dim
     if q is not None and q.__class__ is not int:
         qs = dims.q_stride
-        if q.stride() != (T * qs, qs, d, 1) or q.shape != (B, T, hq, d) or q.dtype is not torch.bfloat16:  # not the usual case
+        if q.stride() != (T * qs, qs, d, 1) or q.shape != (B, T, hq, d) or q.dtype is not _BF16:  # not the usual case
             rows, *sizes, stride = _row_tokens(q)
             if rows < B or sizes != [T, hq, d] or (stride != qs and B * T > 1):
                 raise ValueError(f"q is {[rows, *sizes]}, its tokens {stride} elements apart, the sizes say {[B, T, hq, d]}, "
                                  f"{qs}")
     _here(pool, "pool")
-    pages, = _arrays(torch.uint8, dims.n_pages * hk * 72 * d, ("pool",), pool)
-    table, = _arrays(torch.int32, 4 * B * dims.max_pages, ("page_table",), page_table)
-    lens = _arrays(torch.int32, 4 * B, ("kv_len", "q_len"), kv_len, q_len)
-    to, = _arrays(torch.bfloat16, 2 * B * T * hq * d, ("out",), out)
-    space, size = _space(workspace)
-    _check(load_library().gdn_attn_kv4(ctypes.byref(dims), _ptr(q), pages, table, *lens, to, space, size, _stream(stream)))
+    _check(load_library().gdn_attn_kv4(
+        ctypes.byref(dims), _ptr(q), _array(pool, _U8, dims.n_pages * hk * 72 * d, "pool"),
+        _array(page_table, _I32, 4 * B * dims.max_pages, "page_table"), _array(kv_len, _I32, 4 * B, "kv_len"),
+        _array(q_len, _I32, 4 * B, "q_len"), _array(out, _BF16, 2 * B * T * hq * d, "out"), *_space(workspace),
+        _stream(stream)))
 
 
 def make_beam_dims(logits, eos=-1) -> BeamDims:
     """Sizes of a beam_select call on logits [groups, beams, V], fp32 or bf16, rows evenly spaced."""
-    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.dim() != 3:
+    shape, st, half = logits.shape, logits.stride(), logits.dtype is _BF16
+    if len(shape) != 3 or not (half or logits.dtype is _F32):
         raise ValueError("logits must be fp32 or bf16 [groups, beams, vocab]")
-    (g, w, v), st = logits.shape, logits.stride()
+    g, w, v = shape
     stride = st[1] if w > 1 else st[0] if g > 1 else v
     if (v > 1 and st[2] != 1) or (g > 1 and w > 1 and st[0] != w * st[1]):
         raise ValueError("logits must have dense rows, evenly spaced")
-    return BeamDims(g, w, v, int(logits.dtype is torch.bfloat16), -1 if eos is None else eos, stride)
+    return BeamDims(g, w, v, half, -1 if eos is None else eos, stride)
 
 
 def beam_workspace(logits) -> torch.Tensor:
@@ -573,12 +574,11 @@ def beam_select(logits, scores, parent, token, new_scores, workspace, done=None,
     dims = make_beam_dims(logits, eos)
     _here(logits, "logits")
     rows = dims.n_groups * dims.beams
-    scores, new_scores = _arrays(torch.float32, 4 * rows, ("scores", "new_scores"), scores, new_scores)
-    done, new_done = _arrays(torch.uint8, rows, ("done", "new_done"), _flags(done), _flags(new_done))
-    parent, token = _arrays(torch.int32, 4 * rows, ("parent", "token"), parent, token)
+    size = 4 * rows
     _check(load_library().gdn_beam_select(
-        ctypes.byref(dims), _ptr(logits), scores, done, parent, token, new_scores, new_done, *_space(workspace),
-        _stream(stream)))
+        ctypes.byref(dims), _ptr(logits), _array(scores, _F32, size, "scores"), _array(_flags(done), _U8, rows, "done"),
+        _array(parent, _I32, size, "parent"), _array(token, _I32, size, "token"), _array(new_scores, _F32, size, "new_scores"),
+        _array(_flags(new_done), _U8, rows, "new_done"), *_space(workspace), _stream(stream)))
 
 
 _FORK_ROWS = ("parent", "n_new", "kv_len", "kv_len_out", "page_src", "page_dst", "state_idx", "state_idx_out", "state_src",
@@ -589,20 +589,20 @@ def cache_fork(page_table, kv_len, page_table_out, kv_len_out, kv_index, page_sr
                n_new=None, pinned=None, state_idx=None, state_idx_out=None, state_src=None, state_dst=None, stream=None):
     """gdn_cache_fork: rows become copies of the rows parent int32 [R] and take n_new tokens (kv_index int32 [R, T]);
     page_src / page_dst and state_src / state_dst int32 [R] are slots_copy's."""
-    if page_table.dim() != 2 or page_table_out.shape != page_table.shape:
+    shape = page_table.shape
+    if len(shape) != 2 or page_table_out.shape != shape:
         raise ValueError("page_table and page_table_out must be of one shape [rows, max_pages]")
-    rows, width = page_table.shape
+    rows, width = shape
     T = 0 if kv_index is None else kv_index.shape[1]
     dims = ForkDims(rows, T, width, n_pages)
     _here(page_table, "page_table")
-    table, table_out = _arrays(torch.int32, 4 * rows * width, ("page_table", "page_table_out"), page_table, page_table_out)
-    index, = _arrays(torch.int32, 4 * rows * T, ("kv_index",), kv_index)
-    pins, = _arrays(torch.uint8, n_pages, ("pinned",), _flags(pinned))
+    table, table_out = _arrays(_I32, 4 * rows * width, ("page_table", "page_table_out"), page_table, page_table_out)
     parent, n_new, kv_len, kv_len_out, *copies = _arrays(
-        torch.int32, 4 * rows, _FORK_ROWS, parent, n_new, kv_len, kv_len_out, page_src, page_dst, state_idx, state_idx_out,
-        state_src, state_dst)
-    _check(load_library().gdn_cache_fork(ctypes.byref(dims), parent, n_new, table, kv_len, pins, table_out, kv_len_out, index,
-                                         *copies, _stream(stream)))
+        _I32, 4 * rows, _FORK_ROWS, parent, n_new, kv_len, kv_len_out, page_src, page_dst, state_idx, state_idx_out, state_src,
+        state_dst)
+    _check(load_library().gdn_cache_fork(
+        ctypes.byref(dims), parent, n_new, table, kv_len, _array(_flags(pinned), _U8, n_pages, "pinned"), table_out, kv_len_out,
+        _array(kv_index, _I32, 4 * rows * T, "kv_index"), *copies, _stream(stream)))
 
 
 def slots_copy(pools, stream=None):
@@ -616,7 +616,7 @@ def slots_copy(pools, stream=None):
         layers, slots = shape[0], shape[1]
         slot = x.nbytes // (layers * slots) if layers * slots else x.element_size() * math.prod(shape[2:])
         _here(x, "a pool")
-        args.append(SlotPool(x.data_ptr(), *_arrays(torch.int32, 4 * n, ("src", "dst"), src, dst), slot, n, layers, slots))
+        args.append(SlotPool(x.data_ptr(), _array(src, _I32, 4 * n, "src"), _array(dst, _I32, 4 * n, "dst"), slot, n, layers, slots))
     n = len(args)
     array = _pools_of[n] if n <= MAX_SLOT_POOLS else SlotPool * n
     _check(load_library().gdn_slots_copy(array(*args), n, _stream(stream)))
