@@ -23,7 +23,10 @@
 // graph, 2.2 TB/s; the logits' stream 5.7 of them, a slice's start and end 3, join 3.4. A slice's cuts, lists and
 // ranking and the join are latency: dependent loads, barriers, code that is new to its
 // SM.
-// 4 x 4 beams of 32000 fp32 logits: 7.1 us, of which the two launches are 4.
+// 4 x 4 beams of 32000 fp32 logits: 6.9 us, of which the two launches are 4.
+// Slow, and right: logits of which all but a few are one finite number (masks of the type's lowest value), whose lists
+// overflow (16 x 8 beams of 131072: 199 us fp32, 125 us bf16); 32 beams, whose parts in the join each see a few places of
+// all slices only, so that their cut is low (4 x 32 beams of 131072: 783 and 633 us).
 #include <cuda_fp16.h>
 
 #include "gdn_check.h"
