@@ -25,8 +25,9 @@
 // SM.
 // 4 x 4 beams of 32000 fp32 logits: 6.9 us, of which the two launches are 4.
 // Slow, and right: logits of which all but a few are one finite number (masks of the type's lowest value), whose lists
-// overflow (16 x 8 beams of 131072: 199 us fp32, 125 us bf16); 32 beams, whose parts in the join each see a few places of
-// all slices only, so that their cut is low (4 x 32 beams of 131072: 783 and 633 us).
+// overflow (16 x 8 beams of 131072: 199 us fp32, 125 us bf16); 32 beams, whose cuts are low: some slices' lists overflow,
+// and in the join, where 32 divides the threads, a part sees a few places of all slices only (4 x 32 beams of 131072:
+// slices 500 us, join 290).
 #include <cuda_fp16.h>
 
 #include "gdn_check.h"
